@@ -1,5 +1,6 @@
-"""ctypes binding of libadaln.so: the C ABI of include/adaln.h with the same
-entry-point names, taking PyTorch CUDA tensors.
+"""ctypes binding of libadaln.so: the C ABI of include/adaln.h and
+include/adaln_ops.h with the same entry-point names, taking PyTorch CUDA
+tensors.
 
 This layer only marshals arguments: it checks dtypes, devices and shapes,
 allocates missing outputs and workspaces with PyTorch's allocator, copies an
@@ -12,6 +13,7 @@ no fallback path.  If the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -50,6 +52,26 @@ _SIGNATURES = {
     "adaln_out_fwd_proj": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _P]),
     "adaln_device_error": (_I, []),
 }
+
+# include/adaln_ops.h
+_HEADS_FWD = (_I, [_P] * 7 + [_I] + [_P] * 2 + [_I] * 8 + [_F, _P])
+_HEADS_BWD = (_I, [_P] * 9 + [_I] + [_P] * 4 + [_I, _P, _SZ] + [_I] * 8 + [_F, _P])
+_EMBED_FWD = (_I, [_P, _I, _P, _F, _P, _I, _I, _I, _P])
+_SIGNATURES.update({
+    "adaln_qk_norm_rope_fwd": _HEADS_FWD,
+    "adaln_f32_qk_norm_rope_fwd": _HEADS_FWD,
+    "adaln_qk_norm_rope_bwd_workspace_bytes": (_SZ, [_I] * 5),
+    "adaln_qk_norm_rope_bwd": _HEADS_BWD,
+    "adaln_f32_qk_norm_rope_bwd": _HEADS_BWD,
+    "adaln_embed_fwd": _EMBED_FWD,
+    "adaln_f32_embed_fwd": _EMBED_FWD,
+    "adaln_embed_bwd_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "adaln_embed_bwd": (_I, [_P, _P, _I, _F, _P, _P, _I, _P, _SZ, _I, _I, _I, _P]),
+    "adaln_f32_embed_bwd": (_I, [_P, _P, _I, _F, _P, _I, _P, _SZ, _I, _I, _I, _P]),
+    "adaln_grad_norm_workspace_bytes": (_SZ, [_P, _I]),
+    "adaln_grad_norm": (_I, [_P, _I, _P, _P, _SZ, _P]),
+    "adaln_grad_clip": (_I, [_P, _P, _I, ctypes.c_double, _P, _P, _SZ, _P]),
+})
 
 _lib = None
 
@@ -442,3 +464,343 @@ def adaln_proj_wgrad_rows(d_emb, u, n0, n1, dW_acc=None, db_acc=None, dW=None, d
                                                             _ptr(db_acc), _ptr(dW), _ptr(db), int(bool(accumulate)),
                                                             B, D, _stream(stream)))
     return dW_acc, db_acc, dW, db
+
+
+# ---------------------------------------------------------------------------
+# include/adaln_ops.h: norm of queries and keys with rotation, embedding,
+# gradient norm
+#
+# A call given a `stream` runs as a whole on it: the copies and allocations made
+# here belong to that stream too.  Tensors must be on the current device.
+# ---------------------------------------------------------------------------
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", _P), ("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [("data", _P), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+def _on_stream(call):
+    """Let the call's `stream` be the current stream while it runs."""
+    @functools.wraps(call)
+    def wrapped(*args, stream=None, **kwargs):
+        if stream is None:
+            return call(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return call(*args, **kwargs)
+    return wrapped
+
+
+def _here(t, dtypes, name):
+    """The tensor's device index, after the checks of its kind."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is {torch.cuda.current_device()}")
+    return t
+
+
+def _flat(t, dtypes, shape, name):
+    """A dense 16-byte aligned input: t, or a copy of it."""
+    _here(t, dtypes, name)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        return t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _result(t, dtype, shape, name, device):
+    """A dense 16-byte aligned output: t, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _here(t, (dtype,), name)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous() or t.data_ptr() % 16:
+        raise ValueError(f"{name}: must be contiguous and 16-byte aligned")
+    return t
+
+
+def _scratch(ws, need, device):
+    """A workspace of `need` bytes: ws, or a new one."""
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("workspace: expected a contiguous CUDA tensor")
+    if ws.get_device() != torch.cuda.current_device():
+        raise ValueError(f"workspace: on {ws.device}, but the current device is {torch.cuda.current_device()}")
+    if ws.numel() * ws.element_size() < need:
+        raise ValueError(f"workspace: {need} bytes needed")
+    return ws
+
+
+def _head_rows(t, dtype, shape, name, copy):
+    """(tensor, _Heads) of head rows [B, S, H, Dh]: t itself when its channels
+    are dense and its rows 16-byte aligned, else a copy (inputs only)."""
+    _here(t, (dtype,), name)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    st, step = t.stride(), 16 // t.element_size()
+    if t.numel() and ((st[3] != 1 and shape[3] > 1) or t.data_ptr() % 16
+                      or any(s % step and n > 1 for s, n in zip(st, shape[:3]))):
+        if not copy:
+            raise ValueError(f"{name}: channels must be dense and rows 16-byte aligned")
+        t = t.clone(memory_format=torch.contiguous_format)
+        st = t.stride()
+    return t, _Heads(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _head_out(t, dtype, shape, name, device):
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+    return _head_rows(t, dtype, shape, name, False)
+
+
+def _head_common(q, k, wq, wk, cos, sin, pos, dtype):
+    """Sizes and the arguments that forward and backward share; `keep` holds the
+    tensors behind the pointers."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q: expected a tensor [B, S, H, Dh]")
+    B, S, Hq, Dh = q.shape
+    if k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 4):
+        raise ValueError("k: expected a tensor [B, S, H, Dh]")
+    Hk = 0 if k is None else k.shape[2]
+    wq = None if wq is None else _flat(wq, (dtype,), (Dh,), "wq")
+    wk = None if wk is None or k is None else _flat(wk, (dtype,), (Dh,), "wk")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos, sin: give both or neither")
+    P, Dr = (1 << 31) - 1, 0
+    if cos is not None:
+        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+            raise ValueError("cos: expected a tensor [P, Dr / 2]")
+        P, half = cos.shape
+        Dr = 2 * half
+        cos = _flat(cos, (torch.float32,), cos.shape, "cos")
+        sin = _flat(sin, (torch.float32,), cos.shape, "sin")
+    is64 = 0
+    if pos is not None:
+        pos = _flat(pos, (torch.int32, torch.int64), (B, S), "pos")
+        is64 = int(pos.dtype == torch.int64)
+    return (B, S, Hq, Hk, Dh, Dr, P), (wq, wk, cos, sin, pos), is64
+
+
+def _qk_fwd(name, dtype, q, k, wq, wk, cos, sin, pos, q_out, k_out, eps, interleaved):
+    L = load()
+    sizes, flat, is64 = _head_common(q, k, wq, wk, cos, sin, pos, dtype)
+    B, S, Hq, Hk, Dh = sizes[:5]
+    q, qs = _head_rows(q, dtype, (B, S, Hq, Dh), "q", True)
+    q_out, qo = _head_out(q_out, dtype, (B, S, Hq, Dh), "q_out", q.device)
+    ks = ko = None
+    if k is not None:
+        k, ks = _head_rows(k, dtype, (B, S, Hk, Dh), "k", True)
+        k_out, ko = _head_out(k_out, dtype, (B, S, Hk, Dh), "k_out", q.device)
+    _check(name, getattr(L, name)(ctypes.byref(qs), ks and ctypes.byref(ks), *map(_ptr, flat), is64, ctypes.byref(qo),
+                                  ko and ctypes.byref(ko), *sizes, int(bool(interleaved)), eps, _stream(None)))
+    return q_out, k_out
+
+
+@_on_stream
+def adaln_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos=None, q_out=None, k_out=None, eps=1e-6, interleaved=True):
+    """RMS norm of the head rows q [B,S,Hq,Dh] and k [B,S,Hk,Dh] (bf16, any
+    strides with dense channels; k may be None, wk is not used then) with weights wq, wk [Dh] (or
+    None), then the rotation of their first Dr channels by the rows pos [B,S]
+    (default: 0 .. S-1) of cos, sin [P,Dr/2] fp32.  A row whose position is
+    outside [0, P) is padding: zero.  q_out may be q and k_out k (in place), or
+    any rows of the same shape.  Returns (q_out, k_out)."""
+    return _qk_fwd("adaln_qk_norm_rope_fwd", torch.bfloat16, q, k, wq, wk, cos, sin, pos, q_out, k_out, eps,
+                   interleaved)
+
+
+@_on_stream
+def adaln_f32_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos=None, q_out=None, k_out=None, eps=1e-6, interleaved=True):
+    """adaln_qk_norm_rope_fwd on fp32 head rows and weights."""
+    return _qk_fwd("adaln_f32_qk_norm_rope_fwd", torch.float32, q, k, wq, wk, cos, sin, pos, q_out, k_out, eps,
+                   interleaved)
+
+
+def adaln_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hk, Dh):
+    return load().adaln_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hk, Dh)
+
+
+def _qk_bwd(name, dtype, d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos, d_q, d_k, dwq_acc, dwk_acc, accumulate,
+            want_w, workspace, eps, interleaved):
+    L = load()
+    sizes, flat, is64 = _head_common(q, k, wq, wk, cos, sin, pos, dtype)
+    B, S, Hq, Hk, Dh = sizes[:5]
+    dev = q.device
+    q, qs = _head_rows(q, dtype, (B, S, Hq, Dh), "q", True)
+    d_q_out, gq = _head_rows(d_q_out, dtype, (B, S, Hq, Dh), "d_q_out", True)
+    d_q, oq = _head_out(d_q, dtype, (B, S, Hq, Dh), "d_q", dev)
+    ks = gk = ok = None
+    if k is not None:
+        k, ks = _head_rows(k, dtype, (B, S, Hk, Dh), "k", True)
+        d_k_out, gk = _head_rows(d_k_out, dtype, (B, S, Hk, Dh), "d_k_out", True)
+        d_k, ok = _head_out(d_k, dtype, (B, S, Hk, Dh), "d_k", dev)
+    ws, nws = None, 0
+    if want_w:
+        if accumulate and (dwq_acc is None or (k is not None and dwk_acc is None)):
+            raise ValueError("accumulate: dwq_acc and dwk_acc must be given")
+        dwq_acc = _result(dwq_acc, torch.float32, (Dh,), "dwq_acc", dev)
+        if Hk:
+            dwk_acc = _result(dwk_acc, torch.float32, (Dh,), "dwk_acc", dev)
+        nws = L.adaln_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hk, Dh)
+        ws = _scratch(workspace, nws, dev)
+    _check(name, getattr(L, name)(ctypes.byref(gq), gk and ctypes.byref(gk), ctypes.byref(qs), ks and ctypes.byref(ks),
+                                  *map(_ptr, flat), is64, ctypes.byref(oq), ok and ctypes.byref(ok),
+                                  _ptr(dwq_acc) if want_w else None, _ptr(dwk_acc) if want_w and Hk else None,
+                                  int(bool(accumulate)), _ptr(ws), nws, *sizes, int(bool(interleaved)), eps,
+                                  _stream(None)))
+    return d_q, d_k, dwq_acc, dwk_acc
+
+
+@_on_stream
+def adaln_qk_norm_rope_bwd(d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos=None, d_q=None, d_k=None, dwq_acc=None,
+                           dwk_acc=None, accumulate=False, want_w=True, workspace=None, eps=1e-6, interleaved=True):
+    """Backward of adaln_qk_norm_rope_fwd from its inputs: (d_q, d_k, dwq_acc,
+    dwk_acc).  d_q may be d_q_out and d_k d_k_out (in place).  The weight
+    gradients are fp32 [Dh], allocated here when not given and want_w; accumulate
+    adds to given ones."""
+    return _qk_bwd("adaln_qk_norm_rope_bwd", torch.bfloat16, d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos, d_q, d_k,
+                   dwq_acc, dwk_acc, accumulate, want_w, workspace, eps, interleaved)
+
+
+@_on_stream
+def adaln_f32_qk_norm_rope_bwd(d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos=None, d_q=None, d_k=None, dwq_acc=None,
+                               dwk_acc=None, accumulate=False, want_w=True, workspace=None, eps=1e-6,
+                               interleaved=True):
+    """adaln_qk_norm_rope_bwd on fp32 head rows, gradients and weights."""
+    return _qk_bwd("adaln_f32_qk_norm_rope_bwd", torch.float32, d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos, d_q,
+                   d_k, dwq_acc, dwk_acc, accumulate, want_w, workspace, eps, interleaved)
+
+
+def _embed_fwd(name, dtype, tokens, table, scale, out):
+    L = load()
+    tokens = _flat(tokens, (torch.int32, torch.int64), tokens.shape, "tokens")
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table: expected a tensor [V, D]")
+    V, D = table.shape
+    table = _flat(table, (dtype,), (V, D), "table")
+    out = _result(out, dtype, (*tokens.shape, D), "out", table.device)
+    _check(name, getattr(L, name)(_ptr(tokens), int(tokens.dtype == torch.int64), _ptr(table), scale, _ptr(out),
+                                  tokens.numel(), V, D, _stream(None)))
+    return out
+
+
+@_on_stream
+def adaln_embed_fwd(tokens, table, scale=1.0, out=None):
+    """out[..., :] = bf16(scale * table[tokens, :]); tokens int32 or int64 of
+    any shape, table [V,D] bf16.  A token outside [0, V) gives a zero row."""
+    return _embed_fwd("adaln_embed_fwd", torch.bfloat16, tokens, table, scale, out)
+
+
+@_on_stream
+def adaln_f32_embed_fwd(tokens, table, scale=1.0, out=None):
+    """adaln_embed_fwd on an fp32 table."""
+    return _embed_fwd("adaln_f32_embed_fwd", torch.float32, tokens, table, scale, out)
+
+
+def adaln_embed_bwd_workspace_bytes(n, V, D):
+    return load().adaln_embed_bwd_workspace_bytes(n, V, D)
+
+
+def _embed_args(d_out, tokens, dtype, workspace, V):
+    tokens = _flat(tokens, (torch.int32, torch.int64), tokens.shape, "tokens")
+    if not isinstance(d_out, torch.Tensor) or d_out.dim() < 1:
+        raise ValueError("d_out: expected a tensor [..., D]")
+    D = d_out.shape[-1]
+    d_out = _flat(d_out, (dtype,), (*tokens.shape, D), "d_out")
+    need = load().adaln_embed_bwd_workspace_bytes(tokens.numel(), V, D)
+    return tokens, d_out, D, _scratch(workspace, need, d_out.device), need
+
+
+@_on_stream
+def adaln_embed_bwd(d_out, tokens, V, scale=1.0, d_table_acc=None, d_table=None, accumulate=False, workspace=None):
+    """Gradient of a table [V,D] from d_out [..., D] bf16: scale times the sum of
+    d_out over each token's occurrences, into d_table_acc (fp32, the default; +=
+    with accumulate) or d_table (bf16).  Returns the one written."""
+    tokens, d_out, D, ws, need = _embed_args(d_out, tokens, torch.bfloat16, workspace, V)
+    if d_table is None:
+        if accumulate and d_table_acc is None:
+            raise ValueError("accumulate: d_table_acc must be given")
+        d_table_acc = _result(d_table_acc, torch.float32, (V, D), "d_table_acc", d_out.device)
+    else:
+        d_table = _result(d_table, torch.bfloat16, (V, D), "d_table", d_out.device)
+    _check("adaln_embed_bwd",
+           load().adaln_embed_bwd(_ptr(d_out), _ptr(tokens), int(tokens.dtype == torch.int64), scale,
+                                  _ptr(d_table_acc), _ptr(d_table), int(bool(accumulate)), _ptr(ws), need,
+                                  tokens.numel(), V, D, _stream(None)))
+    return d_table_acc if d_table is None else d_table
+
+
+@_on_stream
+def adaln_f32_embed_bwd(d_out, tokens, V, scale=1.0, d_table_acc=None, accumulate=False, workspace=None):
+    """adaln_embed_bwd on an fp32 d_out.  Returns d_table_acc."""
+    tokens, d_out, D, ws, need = _embed_args(d_out, tokens, torch.float32, workspace, V)
+    if accumulate and d_table_acc is None:
+        raise ValueError("accumulate: d_table_acc must be given")
+    d_table_acc = _result(d_table_acc, torch.float32, (V, D), "d_table_acc", d_out.device)
+    _check("adaln_f32_embed_bwd",
+           load().adaln_f32_embed_bwd(_ptr(d_out), _ptr(tokens), int(tokens.dtype == torch.int64), scale,
+                                      _ptr(d_table_acc), int(bool(accumulate)), _ptr(ws), need, tokens.numel(), V, D,
+                                      _stream(None)))
+    return d_table_acc
+
+
+_GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _tensor_list(tensors, name):
+    """A host array of adaln_tensor: the tensors' elements in place."""
+    arr = (_Tensor * len(tensors))()
+    here = torch.cuda.current_device()
+    for a, t in zip(arr, tensors):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _GRAD_DTYPES:
+            raise TypeError(f"{name}: expected CUDA tensors of float32 or bfloat16")
+        if t.get_device() != here:
+            raise ValueError(f"{name}: a tensor on {t.device}, but the current device is {here}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensors must be contiguous")
+        a.data, a.numel, a.dtype = t.data_ptr(), t.numel(), _GRAD_DTYPES[t.dtype]
+    return arr
+
+
+@_on_stream
+def adaln_grad_norm(grads, norm=None, workspace=None):
+    """The global norm sqrt(sum x^2) over a list of fp32 and bf16 tensors, as a
+    device tensor [1] fp32 (nothing is synchronized)."""
+    L = load()
+    arr, n = _tensor_list(grads, "grads"), len(grads)
+    dev = torch.device("cuda", torch.cuda.current_device())
+    norm = _result(norm, torch.float32, (1,), "norm", dev)
+    need = L.adaln_grad_norm_workspace_bytes(arr, n)
+    ws = _scratch(workspace, need, dev)
+    _check("adaln_grad_norm", L.adaln_grad_norm(arr, n, _ptr(norm), _ptr(ws), need, _stream(None)))
+    return norm
+
+
+@_on_stream
+def adaln_grad_clip(grads, max_norm, outs=None, stats=None, workspace=None):
+    """outs[i] = coef * grads[i] with coef = min(1, max_norm / (norm + 1e-6)) of
+    the list's global norm; outs=grads scales in place, None allocates.  Returns
+    (outs, stats), stats = [norm, coef] on the device."""
+    L = load()
+    arr, n = _tensor_list(grads, "grads"), len(grads)
+    if outs is None:
+        outs = [torch.empty_like(g) for g in grads]
+    if len(outs) != n:
+        raise ValueError("outs: expected as many tensors as grads")
+    to = arr if outs is grads else _tensor_list(outs, "outs")
+    dev = torch.device("cuda", torch.cuda.current_device())
+    stats = _result(stats, torch.float32, (2,), "stats", dev)
+    need = L.adaln_grad_norm_workspace_bytes(arr, n)
+    ws = _scratch(workspace, need, dev)
+    _check("adaln_grad_clip", L.adaln_grad_clip(arr, to, n, float(max_norm), _ptr(stats), _ptr(ws), need,
+                                                _stream(None)))
+    return outs, stats

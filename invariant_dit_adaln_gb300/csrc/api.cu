@@ -10,6 +10,7 @@
 #include <unordered_map>
 
 #include "adaln.h"
+#include "checks.h"
 #include "common.cuh"
 #include "internal.h"
 
@@ -17,46 +18,12 @@ namespace adaln {
 
 namespace {
 
-struct Buf {
-    const void *p;
-    size_t bytes;
-};
-
-bool overlaps(const Buf &a, const Buf &b) {
-    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-// Every output against every input, every other output and the workspace.
-bool any_alias(const Buf *outs, int nout, const Buf *ins, int nin) {
-    for (int i = 0; i < nout; ++i) {
-        for (int j = 0; j < nin; ++j)
-            if (overlaps(outs[i], ins[j])) return true;
-        for (int j = i + 1; j < nout; ++j)
-            if (overlaps(outs[i], outs[j])) return true;
-    }
-    return false;
-}
-
-bool aligned16(const void *p) { return p == nullptr || ((uintptr_t)p & 15u) == 0; }
-
-// a buffer with bytes > 0 needs a pointer
-bool missing(const Buf &b) { return b.bytes > 0 && b.p == nullptr; }
-bool any_missing(const Buf *bufs, int n) {
-    for (int i = 0; i < n; ++i)
-        if (missing(bufs[i])) return true;
-    return false;
-}
-
 bool valid_D(int D) { return D >= 8 && D <= kMaxD && D % 8 == 0; }
 
 bool valid_BS(int B, int S, int D) {
     if (B < 0 || S < 0 || S > kMaxS || B > 65535) return false;
     return (long double)B * S * D < 1099511627776.0L;  // 2^40
 }
-
-size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 std::mutex g_mu;
 
@@ -89,12 +56,6 @@ adaln_status current_device(DeviceInfo *info) {
     }
     *info = d;
     return (d.cc_major == 10 && d.cc_minor == 3) ? ADALN_OK : ADALN_ERR_DEVICE;
-}
-
-adaln_status from_cuda(cudaError_t e) {
-    if (e == cudaSuccess) return ADALN_OK;
-    cudaGetLastError();  // clear a non-sticky launch error
-    return ADALN_ERR_CUDA;
 }
 
 size_t tiles(int S) { return (size_t)((S + kTile - 1) / kTile); }

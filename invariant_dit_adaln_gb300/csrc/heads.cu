@@ -1,0 +1,503 @@
+// RMS norm of query and key heads with the position rotation, forward and
+// backward (contract: include/adaln_ops.h).
+//
+// Mathematics, for one head row x of Dh channels with weights w:
+//   r = 1 / sqrt(sum x^2 / Dh + eps),  n = x r w,  y = R n
+// R turns channel pairs by the angles of the row's position (orthogonal), so
+//   g = R^T dy,  h = g w,  dx = r (h - x r^2 (sum h x) / Dh),  dw = sum g x r.
+// Neither direction needs anything but its tensors once: the backward forms r
+// again from x.
+//
+// Layout: a row is held by LPR = Dh/8 lanes, rounded up to a power of two (at least 4), 8
+// channels a lane, so both reductions are butterflies inside the row's lanes.
+// A lane's 8 channels are chosen so that both members of every pair it touches
+// are its own: interleaved, channels 8l .. 8l+7; halves, channels 4l .. 4l+3
+// and Dr/2 + 4l .. Dr/2 + 4l + 3.  The rotation therefore exchanges nothing
+// between lanes, and lane l needs the angles 4l .. 4l+3 in either form.
+#include "common.cuh"
+#include "ops.h"
+
+namespace adaln {
+
+namespace {
+
+constexpr int kWarps = 8;  // warps of a CTA
+
+struct HeadsArgs {
+    const void *x[2], *dy[2];
+    void *out[2];
+    const void *w[2];
+    long long xs[2][3], dys[2][3], os[2][3];  // batch, token, head strides in elements
+    const float *cos, *sin;
+    const void *pos;
+    int pos_is_64;
+    int S, H[2], Dh, Dr, P;
+    int chunks[2];      // groups of heads of a token: q's, k's
+    long long tokens;   // B * S
+    float eps;
+    // backward
+    float *part;        // [B][tiles][2][Dh]
+    int tile, tiles;    // tokens of a tile, tiles of a sample
+};
+
+__device__ __forceinline__ long long position(const HeadsArgs &a, long long token, int s) {
+    if (a.pos == nullptr) return s;
+    return a.pos_is_64 ? static_cast<const long long *>(a.pos)[token] : static_cast<const int *>(a.pos)[token];
+}
+
+// The 8 channels of a lane: two runs of four, at lo and hi.
+struct Slot {
+    int lo, hi;
+    bool live, turned;
+};
+template <bool INTER>
+__device__ __forceinline__ Slot lane_slot(int l, int Dh, int Dr) {
+    Slot s;
+    s.live = 8 * l < Dh;
+    s.turned = 8 * l < Dr;
+    s.lo = (INTER || !s.turned) ? 8 * l : 4 * l;
+    s.hi = (INTER || !s.turned) ? 8 * l + 4 : Dr / 2 + 4 * l;
+    return s;
+}
+
+// Plain (coherent) loads: in place, a row is read by the lanes that write it.
+template <bool INTER>
+__device__ __forceinline__ void load8(float (&v)[8], const uint16_t *p, const Slot &s) {
+    uint2 a, b;
+    if (INTER) {
+        const uint4 t = *reinterpret_cast<const uint4 *>(p + s.lo);
+        a = make_uint2(t.x, t.y);
+        b = make_uint2(t.z, t.w);
+    } else {
+        a = *reinterpret_cast<const uint2 *>(p + s.lo);
+        b = *reinterpret_cast<const uint2 *>(p + s.hi);
+    }
+    v[0] = bf16lo(a.x), v[1] = bf16hi(a.x), v[2] = bf16lo(a.y), v[3] = bf16hi(a.y);
+    v[4] = bf16lo(b.x), v[5] = bf16hi(b.x), v[6] = bf16lo(b.y), v[7] = bf16hi(b.y);
+}
+template <bool INTER>
+__device__ __forceinline__ void load8(float (&v)[8], const float *p, const Slot &s) {
+    const float4 a = *reinterpret_cast<const float4 *>(p + s.lo);
+    const float4 b = *reinterpret_cast<const float4 *>(p + s.hi);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+template <bool INTER>
+__device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8], const Slot &s) {
+    const uint2 a = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    const uint2 b = make_uint2(pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    if (INTER) {
+        *reinterpret_cast<uint4 *>(p + s.lo) = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+        *reinterpret_cast<uint2 *>(p + s.lo) = a;
+        *reinterpret_cast<uint2 *>(p + s.hi) = b;
+    }
+}
+template <bool INTER>
+__device__ __forceinline__ void store8(float *p, const float (&v)[8], const Slot &s) {
+    *reinterpret_cast<float4 *>(p + s.lo) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(p + s.hi) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// Turn the lane's four pairs by its angles (BACK: by the negative angles).
+template <bool INTER, bool BACK>
+__device__ __forceinline__ void turn(float (&v)[8], const float (&c)[4], const float (&s)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + 4;
+        const float a = v[ia], b = v[ib];
+        const float sn = BACK ? -s[i] : s[i];
+        v[ia] = __fmaf_rn(a, c[i], -__fmul_rn(b, sn));
+        v[ib] = __fmaf_rn(a, sn, __fmul_rn(b, c[i]));
+    }
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
+    return v;
+}
+
+__device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
+    float t = __fmul_rn(a[0], b[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t = __fmaf_rn(a[i], b[i], t);
+    return t;
+}
+
+// --------------------------------------------------------------------------
+// Forward: a warp takes U * 32/LPR heads of one token, so the token's angles
+// are loaded once for them.
+// --------------------------------------------------------------------------
+template <typename T, int LPR, int U, bool INTER>
+__global__ void __launch_bounds__(32 * kWarps) heads_fwd_kernel(const __grid_constant__ HeadsArgs a) {
+    constexpr int RPW = 32 / LPR;
+    const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+    const Slot slot = lane_slot<INTER>(l, a.Dh, a.Dr);
+    const int nchunk = a.chunks[0] + a.chunks[1];
+    const long long total = a.tokens * nchunk;
+    const float inv = __fdiv_rn(1.0f, (float)a.Dh);
+    pdl_wait();
+    pdl_trigger();
+    for (long long task = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); task < total;
+         task += (long long)gridDim.x * kWarps) {
+        const long long token = task / nchunk;
+        int chunk = (int)(task - token * nchunk);
+        const int t = chunk >= a.chunks[0];
+        if (t) chunk -= a.chunks[0];
+        const long long b = token / a.S;
+        const int s = (int)(token - b * a.S);
+        const int h0 = chunk * (U * RPW) + sub;
+        const T *x = static_cast<const T *>(a.x[t]) + b * a.xs[t][0] + s * a.xs[t][1];
+        T *o = static_cast<T *>(a.out[t]) + b * a.os[t][0] + s * a.os[t][1];
+
+        const long long p = position(a, token, s);
+        const bool real = p >= 0 && p < a.P;
+        float v[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * RPW;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+            if (slot.live && h < a.H[t]) load8<INTER>(v[u], x + h * a.xs[t][2], slot);
+        }
+        float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (slot.turned && real) {
+            const long long at = p * (a.Dr / 2) + 4 * l;
+            const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
+            const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
+            c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
+            sn[0] = sv.x, sn[1] = sv.y, sn[2] = sv.z, sn[3] = sv.w;
+        }
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+        if (slot.live && a.w[t] != nullptr) load8<INTER>(w, static_cast<const T *>(a.w[t]), slot);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float ss = row_sum<LPR>(dot8(v[u], v[u]));
+            const float r = __frsqrt_rn(__fmaf_rn(ss, inv, a.eps));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] = __fmul_rn(__fmul_rn(v[u][i], r), w[i]);
+            if (slot.turned) turn<INTER, false>(v[u], c, sn);
+            if (!real) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+            }
+            const int h = h0 + u * RPW;
+            if (slot.live && h < a.H[t]) store8<INTER>(o + h * a.os[t][2], v[u], slot);
+        }
+    }
+}
+
+// --------------------------------------------------------------------------
+// Backward: one CTA per (sample, tile of tokens, q or k).  Its warps take the
+// tile's (token, heads) tasks in turn; each lane keeps the dw sums of its 8
+// channels, joined over the CTA in a fixed order into the tile's partial.
+// --------------------------------------------------------------------------
+template <typename T, int LPR, int U, bool INTER>
+__global__ void __launch_bounds__(32 * kWarps) heads_bwd_kernel(const __grid_constant__ HeadsArgs a) {
+    constexpr int RPW = 32 / LPR;
+    __shared__ float red[kWarps][LPR * 8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+    const Slot slot = lane_slot<INTER>(l, a.Dh, a.Dr);
+    const int t = blockIdx.y;
+    const int nchunk = a.chunks[t];
+    if (nchunk == 0) return;  // no keys
+    const float inv = __fdiv_rn(1.0f, (float)a.Dh);
+    const int s0 = blockIdx.x * a.tile;
+    const int ntask = min(a.tile, a.S - s0) * nchunk;
+    const long long b = blockIdx.z;
+    const T *xb = static_cast<const T *>(a.x[t]) + b * a.xs[t][0];
+    const T *gb = static_cast<const T *>(a.dy[t]) + b * a.dys[t][0];
+    T *ob = static_cast<T *>(a.out[t]) + b * a.os[t][0];
+    float dw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[i] = 0.0f;
+    pdl_wait();
+    pdl_trigger();
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    if (slot.live && a.w[t] != nullptr) load8<INTER>(w, static_cast<const T *>(a.w[t]), slot);
+    for (int task = warp; task < ntask; task += kWarps) {
+        const int s = s0 + task / nchunk;
+        const int h0 = (task % nchunk) * (U * RPW) + sub;
+        const long long p = position(a, b * a.S + s, s);
+        const bool real = p >= 0 && p < a.P;
+        const T *x = xb + s * a.xs[t][1];
+        const T *dy = gb + s * a.dys[t][1];
+        T *o = ob + s * a.os[t][1];
+        float v[U][8], g[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * RPW;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] = g[u][i] = 0.0f;
+            if (slot.live && h < a.H[t]) {
+                load8<INTER>(v[u], x + h * a.xs[t][2], slot);
+                load8<INTER>(g[u], dy + h * a.dys[t][2], slot);
+            }
+        }
+        float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (slot.turned && real) {
+            const long long at = p * (a.Dr / 2) + 4 * l;
+            const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
+            const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
+            c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
+            sn[0] = sv.x, sn[1] = sv.y, sn[2] = sv.z, sn[3] = sv.w;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * RPW;
+            if (slot.turned) turn<INTER, true>(g[u], c, sn);
+            float hx = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) hx = __fmaf_rn(__fmul_rn(g[u][i], w[i]), v[u][i], hx);
+            const float ss = row_sum<LPR>(dot8(v[u], v[u]));
+            hx = row_sum<LPR>(hx);
+            const float r = __frsqrt_rn(__fmaf_rn(ss, inv, a.eps));
+            const float k = __fmul_rn(__fmul_rn(__fmul_rn(r, r), inv), hx);
+            float dx[8];
+            const bool mine = slot.live && h < a.H[t];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dx[i] = real ? __fmul_rn(r, __fmaf_rn(-v[u][i], k, __fmul_rn(g[u][i], w[i]))) : 0.0f;
+                if (real && mine) dw[i] = __fmaf_rn(g[u][i], __fmul_rn(v[u][i], r), dw[i]);
+            }
+            if (mine) store8<INTER>(o + h * a.os[t][2], dx, slot);
+        }
+    }
+    if (a.part == nullptr) return;
+    // the warp's row groups, then the warps in ascending order
+#pragma unroll
+    for (int off = LPR; off < 32; off <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[i] = __fadd_rn(dw[i], __shfl_xor_sync(0xFFFFFFFFu, dw[i], off));
+    }
+    if (sub == 0 && slot.live) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            red[warp][slot.lo + i] = dw[i];
+            red[warp][slot.hi + i] = dw[4 + i];
+        }
+    }
+    __syncthreads();
+    float *part = a.part + ((b * a.tiles + blockIdx.x) * 2 + t) * a.Dh;
+    for (int d = threadIdx.x; d < a.Dh; d += 32 * kWarps) {
+        float sum = red[0][d];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) sum = __fadd_rn(sum, red[i][d]);
+        part[d] = sum;
+    }
+}
+
+// --------------------------------------------------------------------------
+// dw of a sample: its tiles' partials.  32 columns and 32 groups of tiles a
+// CTA: group g adds the tiles g, g + 32, ... in order, then the groups are
+// added in order.  Fixed by the number of tiles, that is by S, H, Dh.
+//   DIRECT: a CTA takes the samples one after the other and adds them onto the
+//   accumulator itself; otherwise blockIdx.z is the sample and its sum goes to
+//   sums [B][2][Dh].
+// --------------------------------------------------------------------------
+struct FoldArgs {
+    const float *part;
+    float *sums;
+    float *dw[2];
+    int B, tiles, Dh, accumulate;
+};
+
+template <bool DIRECT>
+__global__ void __launch_bounds__(1024) heads_fold_kernel(const FoldArgs a) {
+    __shared__ float red[32][33];
+    const int col = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int t = blockIdx.y, d = blockIdx.x * 32 + col;
+    pdl_wait();
+    pdl_trigger();
+    float *dw = a.dw[t];
+    if (dw == nullptr) return;
+    float acc = 0.0f;
+    if (DIRECT && grp == 0 && d < a.Dh && a.accumulate) acc = dw[d];
+    const long long b0 = DIRECT ? 0 : blockIdx.z, b1 = DIRECT ? a.B : b0 + 1;
+    for (long long b = b0; b < b1; ++b) {
+        const float *p = a.part + (b * a.tiles * 2 + t) * a.Dh + d;
+        float sum = 0.0f;
+        if (d < a.Dh) {
+#pragma unroll 8
+            for (int i = grp; i < a.tiles; i += 32) sum = __fadd_rn(sum, __ldcg(p + (long long)i * 2 * a.Dh));
+        }
+        red[grp][col] = sum;
+        __syncthreads();
+        if (grp == 0 && d < a.Dh) {
+            sum = red[0][col];
+#pragma unroll
+            for (int i = 1; i < 32; ++i) sum = __fadd_rn(sum, red[i][col]);
+            if (DIRECT)
+                acc = __fadd_rn(acc, sum);
+            else
+                a.sums[(b * 2 + t) * a.Dh + d] = sum;
+        }
+        __syncthreads();
+    }
+    if (DIRECT && grp == 0 && d < a.Dh) dw[d] = acc;
+}
+
+// the samples' sums onto the accumulators, in ascending order
+__global__ void __launch_bounds__(256) heads_samples_kernel(const FoldArgs a) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    if (i >= 2 * a.Dh) return;
+    float *dw = a.dw[i / a.Dh];
+    if (dw == nullptr) return;
+    float acc = a.accumulate ? dw[i % a.Dh] : 0.0f;
+#pragma unroll 16
+    for (long long b = 0; b < a.B; ++b) acc = __fadd_rn(acc, __ldcg(a.sums + b * 2 * a.Dh + i));
+    dw[i % a.Dh] = acc;
+}
+
+int lanes_per_row(int Dh) {
+    int l = 4;  // smaller rows leave lanes idle
+    while (8 * l < Dh) l *= 2;
+    return l;
+}
+
+HeadsArgs make_args(const HeadsCall &c, int group) {
+    HeadsArgs a = {};
+    for (int t = 0; t < 2; ++t) {
+        a.x[t] = c.x[t].data;
+        a.dy[t] = c.dy[t].data;
+        a.out[t] = c.out[t].data;
+        a.w[t] = c.w[t];
+        a.H[t] = c.H[t];
+        a.chunks[t] = (c.H[t] + group - 1) / group;
+        const adaln_heads *h[3] = {&c.x[t], &c.dy[t], &c.out[t]};
+        long long *s[3] = {a.xs[t], a.dys[t], a.os[t]};
+        for (int i = 0; i < 3; ++i) {
+            s[i][0] = h[i]->batch;
+            s[i][1] = h[i]->token;
+            s[i][2] = h[i]->head;
+        }
+    }
+    a.cos = c.cos;
+    a.sin = c.sin;
+    a.pos = c.pos;
+    a.pos_is_64 = c.pos_is_64;
+    a.S = c.S;
+    a.Dh = c.Dh;
+    a.Dr = c.Dr;
+    // without positions and without a rotation every row is real
+    a.P = (c.pos == nullptr && c.Dr == 0) ? 0x7FFFFFFF : c.P;
+    a.tokens = (long long)c.B * c.S;
+    a.eps = c.eps;
+    return a;
+}
+
+// heads of a backward task: 4 rows a lane where a token has that many heads
+int bwd_rows(int Hq, int Hk, int Dh) {
+    const int rpw = 32 / lanes_per_row(Dh), h = Hq > Hk ? Hq : Hk;
+    return h > 2 * rpw ? 4 : h > rpw ? 2 : 1;
+}
+
+template <typename T, int LPR, int U>
+cudaError_t run_fwd(const HeadsCall &c, cudaStream_t stream) {
+    const HeadsArgs a = make_args(c, U * (32 / LPR));
+    const long long tasks = a.tokens * (a.chunks[0] + a.chunks[1]);
+    const long long ctas = (tasks + kWarps - 1) / kWarps;
+    const dim3 grid((unsigned)(ctas < (1ll << 30) ? ctas : (1ll << 30)));
+    return c.interleaved ? launch_pdl(heads_fwd_kernel<T, LPR, U, true>, grid, dim3(32 * kWarps), 0, stream, a)
+                         : launch_pdl(heads_fwd_kernel<T, LPR, U, false>, grid, dim3(32 * kWarps), 0, stream, a);
+}
+
+template <typename T, int LPR>
+cudaError_t pick_fwd(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &dev) {
+    // 4 rows a lane where that still gives every SM 16 warps; few rows go one
+    // a lane, for the shortest path through the kernel
+    const long long rows = (long long)c.B * c.S * (c.H[0] + c.H[1]);
+    return rows / (4 * (32 / LPR)) >= 16ll * dev.sm_count ? run_fwd<T, LPR, 4>(c, stream)
+                                                          : run_fwd<T, LPR, 1>(c, stream);
+}
+
+template <typename T, int LPR, int U>
+cudaError_t run_bwd(const HeadsCall &c, cudaStream_t stream) {
+    HeadsArgs a = make_args(c, U * (32 / LPR));
+    a.tile = heads_tile_tokens(c.H[0], c.H[1], c.Dh);
+    a.tiles = (c.S + a.tile - 1) / a.tile;
+    a.part = (c.dw[0] || c.dw[1]) ? c.ws : nullptr;
+    const dim3 grid(a.tiles, 2, c.B);
+    return c.interleaved ? launch_pdl(heads_bwd_kernel<T, LPR, U, true>, grid, dim3(32 * kWarps), 0, stream, a)
+                         : launch_pdl(heads_bwd_kernel<T, LPR, U, false>, grid, dim3(32 * kWarps), 0, stream, a);
+}
+
+template <typename T, int LPR>
+cudaError_t pick_bwd(const HeadsCall &c, cudaStream_t stream) {
+    switch (bwd_rows(c.H[0], c.H[1], c.Dh)) {
+        case 4: return run_bwd<T, LPR, 4>(c, stream);
+        case 2: return run_bwd<T, LPR, 2>(c, stream);
+        default: return run_bwd<T, LPR, 1>(c, stream);
+    }
+}
+
+}  // namespace
+
+int heads_tile_tokens(int Hq, int Hk, int Dh) {
+    // about 24 tasks a CTA, 3 a warp: enough rows to pay for joining dw, and
+    // enough CTAs (1024 at B = 2, S = 4096, 24 + 24 heads of 128)
+    const int group = bwd_rows(Hq, Hk, Dh) * (32 / lanes_per_row(Dh)), h = Hq > Hk ? Hq : Hk;
+    const int chunks = (h + group - 1) / group;
+    return chunks >= 24 ? 1 : 24 / chunks;
+}
+
+// Samples up to this many are added by the fold itself.
+constexpr int kDirectSamples = 4;
+
+size_t heads_bwd_ws_floats(int B, int S, int Hq, int Hk, int Dh) {
+    const int tile = heads_tile_tokens(Hq, Hk, Dh);
+    const size_t tiles = ((size_t)S + tile - 1) / tile;
+    return (size_t)B * (tiles + 1) * 2 * Dh;
+}
+
+template <typename T>
+cudaError_t launch_heads_fwd(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &dev) {
+    switch (lanes_per_row(c.Dh)) {
+        case 4: return pick_fwd<T, 4>(c, stream, dev);
+        case 8: return pick_fwd<T, 8>(c, stream, dev);
+        case 16: return pick_fwd<T, 16>(c, stream, dev);
+        default: return pick_fwd<T, 32>(c, stream, dev);
+    }
+}
+
+template <typename T>
+cudaError_t launch_heads_bwd(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &) {
+    cudaError_t e;
+    switch (lanes_per_row(c.Dh)) {
+        case 4: e = pick_bwd<T, 4>(c, stream); break;
+        case 8: e = pick_bwd<T, 8>(c, stream); break;
+        case 16: e = pick_bwd<T, 16>(c, stream); break;
+        default: e = pick_bwd<T, 32>(c, stream); break;
+    }
+    if (e != cudaSuccess || (!c.dw[0] && !c.dw[1])) return e;
+    FoldArgs f = {};
+    f.part = c.ws;
+    f.dw[0] = c.dw[0];
+    f.dw[1] = c.dw[1];
+    f.B = c.B;
+    f.Dh = c.Dh;
+    f.accumulate = c.accumulate;
+    const int tile = heads_tile_tokens(c.H[0], c.H[1], c.Dh);
+    f.tiles = (c.S + tile - 1) / tile;
+    f.sums = c.ws + (size_t)c.B * f.tiles * 2 * c.Dh;
+    const unsigned cols = (c.Dh + 31) / 32;
+    if (c.B <= kDirectSamples) return launch_pdl(heads_fold_kernel<true>, dim3(cols, 2), dim3(1024), 0, stream, f);
+    e = launch_pdl(heads_fold_kernel<false>, dim3(cols, 2, c.B), dim3(1024), 0, stream, f);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(heads_samples_kernel, dim3((2 * c.Dh + 255) / 256), dim3(256), 0, stream, f);
+}
+
+template cudaError_t launch_heads_fwd<uint16_t>(const HeadsCall &, cudaStream_t, const DeviceInfo &);
+template cudaError_t launch_heads_fwd<float>(const HeadsCall &, cudaStream_t, const DeviceInfo &);
+template cudaError_t launch_heads_bwd<uint16_t>(const HeadsCall &, cudaStream_t, const DeviceInfo &);
+template cudaError_t launch_heads_bwd<float>(const HeadsCall &, cudaStream_t, const DeviceInfo &);
+
+}  // namespace adaln
