@@ -33,8 +33,10 @@ struct HeadsArgs {
     int pos_is_64;
     int S, H[2], Dh, Dr, P;
     int chunks[2];      // groups of heads of a token: q's, k's
-    long long tokens;   // B * S
     float eps;
+    // forward: the tokens of this launch, of all B * S
+    long long token0;
+    unsigned ntok;
     // backward
     float *part;        // [B][tiles][2][Dh]
     int tile, tiles;    // tokens of a tile, tiles of a sample
@@ -60,27 +62,39 @@ __device__ __forceinline__ Slot lane_slot(int l, int Dh, int Dr) {
     return s;
 }
 
-// Plain (coherent) loads: in place, a row is read by the lanes that write it.
-template <bool INTER>
-__device__ __forceinline__ void load8(float (&v)[8], const uint16_t *p, const Slot &s) {
+// A lane's 8 channels as they lie in memory, and their values.  Plain
+// (coherent) loads: in place, a row is read by the lanes that write it.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
     uint2 a, b;
+};
+template <>
+struct Raw<float> {
+    float4 a, b;
+};
+template <bool INTER>
+__device__ __forceinline__ Raw<uint16_t> load8(const uint16_t *p, const Slot &s) {
     if (INTER) {
         const uint4 t = *reinterpret_cast<const uint4 *>(p + s.lo);
-        a = make_uint2(t.x, t.y);
-        b = make_uint2(t.z, t.w);
-    } else {
-        a = *reinterpret_cast<const uint2 *>(p + s.lo);
-        b = *reinterpret_cast<const uint2 *>(p + s.hi);
+        return {make_uint2(t.x, t.y), make_uint2(t.z, t.w)};
     }
-    v[0] = bf16lo(a.x), v[1] = bf16hi(a.x), v[2] = bf16lo(a.y), v[3] = bf16hi(a.y);
-    v[4] = bf16lo(b.x), v[5] = bf16hi(b.x), v[6] = bf16lo(b.y), v[7] = bf16hi(b.y);
+    return {*reinterpret_cast<const uint2 *>(p + s.lo), *reinterpret_cast<const uint2 *>(p + s.hi)};
 }
 template <bool INTER>
-__device__ __forceinline__ void load8(float (&v)[8], const float *p, const Slot &s) {
-    const float4 a = *reinterpret_cast<const float4 *>(p + s.lo);
-    const float4 b = *reinterpret_cast<const float4 *>(p + s.hi);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ Raw<float> load8(const float *p, const Slot &s) {
+    return {*reinterpret_cast<const float4 *>(p + s.lo), *reinterpret_cast<const float4 *>(p + s.hi)};
+}
+__device__ __forceinline__ void clear(Raw<uint16_t> &r) { r.a = r.b = make_uint2(0, 0); }
+__device__ __forceinline__ void clear(Raw<float> &r) { r.a = r.b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+__device__ __forceinline__ void values(float (&v)[8], const Raw<uint16_t> &r) {
+    v[0] = bf16lo(r.a.x), v[1] = bf16hi(r.a.x), v[2] = bf16lo(r.a.y), v[3] = bf16hi(r.a.y);
+    v[4] = bf16lo(r.b.x), v[5] = bf16hi(r.b.x), v[6] = bf16lo(r.b.y), v[7] = bf16hi(r.b.y);
+}
+__device__ __forceinline__ void values(float (&v)[8], const Raw<float> &r) {
+    v[0] = r.a.x, v[1] = r.a.y, v[2] = r.a.z, v[3] = r.a.w;
+    v[4] = r.b.x, v[5] = r.b.y, v[6] = r.b.z, v[7] = r.b.w;
 }
 template <bool INTER>
 __device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8], const Slot &s) {
@@ -97,6 +111,23 @@ template <bool INTER>
 __device__ __forceinline__ void store8(float *p, const float (&v)[8], const Slot &s) {
     *reinterpret_cast<float4 *>(p + s.lo) = make_float4(v[0], v[1], v[2], v[3]);
     *reinterpret_cast<float4 *>(p + s.hi) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// the lane's weights (1 without weights, and in idle lanes)
+template <typename T, bool INTER>
+__device__ __forceinline__ void load_weights(float (&w)[8], const void *p, const Slot &s) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    if (s.live && p != nullptr) values(w, load8<INTER>(static_cast<const T *>(p), s));
+}
+
+// the lane's angles at position p (0 <= p < P)
+__device__ __forceinline__ void load_angles(float (&c)[4], float (&s)[4], const HeadsArgs &a, long long p, int l) {
+    const long long at = p * (a.Dr / 2) + 4 * l;
+    const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
+    const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
+    c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
+    s[0] = sv.x, s[1] = sv.y, s[2] = sv.z, s[3] = sv.w;
 }
 
 // Turn the lane's four pairs by its angles (BACK: by the negative angles).
@@ -128,66 +159,58 @@ __device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) 
 
 // --------------------------------------------------------------------------
 // Forward: a warp takes U * 32/LPR heads of one token, so the token's angles
-// are loaded once for them.
+// are loaded once for them, and all their loads are in flight together.
 // --------------------------------------------------------------------------
 template <typename T, int LPR, int U, bool INTER>
 __global__ void __launch_bounds__(32 * kWarps) heads_fwd_kernel(const __grid_constant__ HeadsArgs a) {
     constexpr int RPW = 32 / LPR;
     const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
     const Slot slot = lane_slot<INTER>(l, a.Dh, a.Dr);
-    const int nchunk = a.chunks[0] + a.chunks[1];
-    const long long total = a.tokens * nchunk;
-    const float inv = __fdiv_rn(1.0f, (float)a.Dh);
+    const unsigned nchunk = a.chunks[0] + a.chunks[1];
+    const unsigned task = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const unsigned tk = task / nchunk;
+    int chunk = (int)(task - tk * nchunk);
+    const int t = chunk >= a.chunks[0];
+    if (t) chunk -= a.chunks[0];
+    const long long token = a.token0 + tk;
+    const long long b = (token >> 32) ? token / a.S : (unsigned)token / (unsigned)a.S;
+    const int s = (int)(token - b * a.S);
+    const int h0 = chunk * (U * RPW) + sub;
+    const T *x = static_cast<const T *>(a.x[t]) + b * a.xs[t][0] + s * a.xs[t][1] + h0 * a.xs[t][2];
+    T *o = static_cast<T *>(a.out[t]) + b * a.os[t][0] + s * a.os[t][1] + h0 * a.os[t][2];
+    const int rows = slot.live ? (a.H[t] - h0 + RPW - 1) / RPW : 0;  // the lane's heads: u < rows
     pdl_wait();
     pdl_trigger();
-    for (long long task = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); task < total;
-         task += (long long)gridDim.x * kWarps) {
-        const long long token = task / nchunk;
-        int chunk = (int)(task - token * nchunk);
-        const int t = chunk >= a.chunks[0];
-        if (t) chunk -= a.chunks[0];
-        const long long b = token / a.S;
-        const int s = (int)(token - b * a.S);
-        const int h0 = chunk * (U * RPW) + sub;
-        const T *x = static_cast<const T *>(a.x[t]) + b * a.xs[t][0] + s * a.xs[t][1];
-        T *o = static_cast<T *>(a.out[t]) + b * a.os[t][0] + s * a.os[t][1];
-
-        const long long p = position(a, token, s);
-        const bool real = p >= 0 && p < a.P;
-        float v[U][8];
+    if (tk >= a.ntok) return;
+    const long long p = position(a, token, s);
+    Raw<T> raw[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * RPW;
+    for (int u = 0; u < U; ++u) {
+        clear(raw[u]);
+        if (u < rows) raw[u] = load8<INTER>(x + u * RPW * a.xs[t][2], slot);
+    }
+    float w[8];
+    load_weights<T, INTER>(w, a.w[t], slot);
+    if (p < 0 || p >= a.P) {  // padding
+        const float zero[8] = {};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
-            if (slot.live && h < a.H[t]) load8<INTER>(v[u], x + h * a.xs[t][2], slot);
-        }
-        float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (slot.turned && real) {
-            const long long at = p * (a.Dr / 2) + 4 * l;
-            const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
-            const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
-            c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
-            sn[0] = sv.x, sn[1] = sv.y, sn[2] = sv.z, sn[3] = sv.w;
-        }
-        float w[8];
+        for (int u = 0; u < U; ++u)
+            if (u < rows) store8<INTER>(o + u * RPW * a.os[t][2], zero, slot);
+        return;
+    }
+    float c[4], sn[4];
+    if (slot.turned) load_angles(c, sn, a, p, l);
+    const float inv = __fdiv_rn(1.0f, (float)a.Dh);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-        if (slot.live && a.w[t] != nullptr) load8<INTER>(w, static_cast<const T *>(a.w[t]), slot);
+    for (int u = 0; u < U; ++u) {
+        float v[8];
+        values(v, raw[u]);
+        const float ss = row_sum<LPR>(dot8(v, v));
+        const float r = __frsqrt_rn(__fmaf_rn(ss, inv, a.eps));
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const float ss = row_sum<LPR>(dot8(v[u], v[u]));
-            const float r = __frsqrt_rn(__fmaf_rn(ss, inv, a.eps));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = __fmul_rn(__fmul_rn(v[u][i], r), w[i]);
-            if (slot.turned) turn<INTER, false>(v[u], c, sn);
-            if (!real) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
-            }
-            const int h = h0 + u * RPW;
-            if (slot.live && h < a.H[t]) store8<INTER>(o + h * a.os[t][2], v[u], slot);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], r), w[i]);
+        if (slot.turned) turn<INTER, false>(v, c, sn);
+        if (u < rows) store8<INTER>(o + u * RPW * a.os[t][2], v, slot);
     }
 }
 
@@ -218,55 +241,53 @@ __global__ void __launch_bounds__(32 * kWarps) heads_bwd_kernel(const __grid_con
     pdl_wait();
     pdl_trigger();
     float w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-    if (slot.live && a.w[t] != nullptr) load8<INTER>(w, static_cast<const T *>(a.w[t]), slot);
+    load_weights<T, INTER>(w, a.w[t], slot);
     for (int task = warp; task < ntask; task += kWarps) {
         const int s = s0 + task / nchunk;
         const int h0 = (task % nchunk) * (U * RPW) + sub;
+        const int rows = slot.live ? (a.H[t] - h0 + RPW - 1) / RPW : 0;  // the lane's heads: u < rows
+        const T *x = xb + s * a.xs[t][1] + h0 * a.xs[t][2];
+        const T *dy = gb + s * a.dys[t][1] + h0 * a.dys[t][2];
+        T *o = ob + s * a.os[t][1] + h0 * a.os[t][2];
         const long long p = position(a, b * a.S + s, s);
-        const bool real = p >= 0 && p < a.P;
-        const T *x = xb + s * a.xs[t][1];
-        const T *dy = gb + s * a.dys[t][1];
-        T *o = ob + s * a.os[t][1];
-        float v[U][8], g[U][8];
+        Raw<T> rx[U], rg[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * RPW;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = g[u][i] = 0.0f;
-            if (slot.live && h < a.H[t]) {
-                load8<INTER>(v[u], x + h * a.xs[t][2], slot);
-                load8<INTER>(g[u], dy + h * a.dys[t][2], slot);
+            clear(rx[u]);
+            clear(rg[u]);
+            if (u < rows) {
+                rx[u] = load8<INTER>(x + u * RPW * a.xs[t][2], slot);
+                rg[u] = load8<INTER>(dy + u * RPW * a.dys[t][2], slot);
             }
         }
-        float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (slot.turned && real) {
-            const long long at = p * (a.Dr / 2) + 4 * l;
-            const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
-            const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
-            c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
-            sn[0] = sv.x, sn[1] = sv.y, sn[2] = sv.z, sn[3] = sv.w;
+        if (p < 0 || p >= a.P) {  // padding
+            const float zero[8] = {};
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u < rows) store8<INTER>(o + u * RPW * a.os[t][2], zero, slot);
+            continue;
         }
+        float c[4], sn[4];
+        if (slot.turned) load_angles(c, sn, a, p, l);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * RPW;
-            if (slot.turned) turn<INTER, true>(g[u], c, sn);
-            float hx = 0.0f;
+            float v[8], g[8], h[8];
+            values(v, rx[u]);
+            values(g, rg[u]);
+            if (slot.turned) turn<INTER, true>(g, c, sn);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) hx = __fmaf_rn(__fmul_rn(g[u][i], w[i]), v[u][i], hx);
-            const float ss = row_sum<LPR>(dot8(v[u], v[u]));
-            hx = row_sum<LPR>(hx);
-            const float r = __frsqrt_rn(__fmaf_rn(ss, inv, a.eps));
+            for (int i = 0; i < 8; ++i) h[i] = __fmul_rn(g[i], w[i]);
+            const float ss = row_sum<LPR>(dot8(v, v));
+            const float hx = row_sum<LPR>(dot8(h, v));
+            // lanes without a row: 0, where r would be infinite at eps = 0
+            const float r = u < rows ? __frsqrt_rn(__fmaf_rn(ss, inv, a.eps)) : 0.0f;
             const float k = __fmul_rn(__fmul_rn(__fmul_rn(r, r), inv), hx);
-            float dx[8];
-            const bool mine = slot.live && h < a.H[t];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                dx[i] = real ? __fmul_rn(r, __fmaf_rn(-v[u][i], k, __fmul_rn(g[u][i], w[i]))) : 0.0f;
-                if (real && mine) dw[i] = __fmaf_rn(g[u][i], __fmul_rn(v[u][i], r), dw[i]);
+                dw[i] = __fmaf_rn(g[i], __fmul_rn(v[i], r), dw[i]);
+                h[i] = __fmul_rn(r, __fmaf_rn(-v[i], k, h[i]));
             }
-            if (mine) store8<INTER>(o + h * a.os[t][2], dx, slot);
+            if (u < rows) store8<INTER>(o + u * RPW * a.os[t][2], h, slot);
         }
     }
     if (a.part == nullptr) return;
@@ -389,7 +410,6 @@ HeadsArgs make_args(const HeadsCall &c, int group) {
     a.Dr = c.Dr;
     // without positions and without a rotation every row is real
     a.P = (c.pos == nullptr && c.Dr == 0) ? 0x7FFFFFFF : c.P;
-    a.tokens = (long long)c.B * c.S;
     a.eps = c.eps;
     return a;
 }
@@ -402,12 +422,18 @@ int bwd_rows(int Hq, int Hk, int Dh) {
 
 template <typename T, int LPR, int U>
 cudaError_t run_fwd(const HeadsCall &c, cudaStream_t stream) {
-    const HeadsArgs a = make_args(c, U * (32 / LPR));
-    const long long tasks = a.tokens * (a.chunks[0] + a.chunks[1]);
-    const long long ctas = (tasks + kWarps - 1) / kWarps;
-    const dim3 grid((unsigned)(ctas < (1ll << 30) ? ctas : (1ll << 30)));
-    return c.interleaved ? launch_pdl(heads_fwd_kernel<T, LPR, U, true>, grid, dim3(32 * kWarps), 0, stream, a)
-                         : launch_pdl(heads_fwd_kernel<T, LPR, U, false>, grid, dim3(32 * kWarps), 0, stream, a);
+    HeadsArgs a = make_args(c, U * (32 / LPR));
+    // tasks of a launch are counted in 31 bits
+    const long long tokens = (long long)c.B * c.S, nchunk = a.chunks[0] + a.chunks[1];
+    const long long most = 0x7FFFFFFFll / nchunk;
+    for (; a.token0 < tokens; a.token0 += a.ntok) {
+        a.ntok = (unsigned)(tokens - a.token0 < most ? tokens - a.token0 : most);
+        const dim3 grid((unsigned)((a.ntok * nchunk + kWarps - 1) / kWarps)), block(32 * kWarps);
+        const cudaError_t e = c.interleaved ? launch_pdl(heads_fwd_kernel<T, LPR, U, true>, grid, block, 0, stream, a)
+                                            : launch_pdl(heads_fwd_kernel<T, LPR, U, false>, grid, block, 0, stream, a);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 template <typename T, int LPR>

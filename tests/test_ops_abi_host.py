@@ -223,8 +223,13 @@ def test_embed_bwd_checks(L):
 
 # --- gradient norm ------------------------------------------------------------
 
+class Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 def tensors(*specs):
-    arr = (binding._Tensor * len(specs))()
+    arr = (Tensor * len(specs))()
     for a, (p, n, d) in zip(arr, specs):
         a.data, a.numel, a.dtype = p, n, d
     return arr
