@@ -155,7 +155,7 @@ adaln_status adaln_f32_embed_fwd(const void *tokens, int tokens_are_64, const fl
                                  int n, int V, int D, void *stream);
 
 /* Workspace bytes adaln_embed_bwd and adaln_f32_embed_bwd need: the sorted
- * tokens, the list of pieces, and fp32 partial sums of long pieces. */
+ * tokens, the list of pieces, and fp32 partial sums of long runs. */
 size_t adaln_embed_bwd_workspace_bytes(int n, int V, int D);
 
 /*
@@ -167,9 +167,10 @@ size_t adaln_embed_bwd_workspace_bytes(int n, int V, int D);
  *
  * The occurrences of a token are taken in ascending order of i, in pieces of
  * 32, each summed from +0; the pieces of a token with more than 32 occurrences
- * are added in an order fixed by their number.  The order therefore depends
- * on the number of the token's occurrences alone: not on n, on the places or on the
- * other tokens.  Padding tokens (outside [0, V)) add nothing.
+ * are the leaves of a tree of fan-out 32, each node the sum of its children in
+ * order from +0.  The order therefore depends on the number of the token's
+ * occurrences alone: not on n, on the places or on the other tokens.  Padding
+ * tokens (outside [0, V)) add nothing.
  *
  *   d_out       [n, D]  bf16
  *   d_table_acc [V, D]  fp32 in/out, or NULL
@@ -203,15 +204,16 @@ typedef struct adaln_tensor {
     int32_t reserved;
 } adaln_tensor;
 
-/* Workspace bytes adaln_grad_norm and adaln_grad_clip need: an fp64 partial sum
- * for each 32 KB of each tensor.  0 for a list that the calls refuse. */
+/* Workspace bytes adaln_grad_norm and adaln_grad_clip need: 8 bytes for each
+ * 32 KB of each tensor.  0 for a list that the calls refuse. */
 size_t adaln_grad_norm_workspace_bytes(const adaln_tensor *grads, int count);
 
 /*
  * adaln_grad_norm — norm[0] = sqrt(sum over all elements of all tensors of x^2).
  *
  * Squares are summed in fp32 within 32 KB of a tensor (in fp64 where fp32 would
- * overflow or lose them), then in fp64.  The order is fixed by the list's sizes
+ * overflow or lose them), then in pairs of fp32 with the additions' errors (or in
+ * fp64).  The order is fixed by the list's sizes
  * and types alone, not by addresses.  The result is infinite or NaN exactly as
  * the exact norm (rounded to fp32) is.
  *

@@ -4,18 +4,21 @@
 //   out[i] = scale * table[t_i];   dT[v] = scale * sum over i, t_i = v, of d_out[i]
 //
 // Both are bound by HBM: rows read and rows written.  The gradient groups the
-// tokens first, so that every row of d_out is read once, every row of dT is
-// written once by one owner, and no floating-point atomic decides an order:
-//   1. a stable radix sort of (token, place), 8 bits a pass, as many passes as
-//      V has bytes;  n <= kSmall: one CTA, in shared memory, otherwise a
-//      histogram and a scatter kernel per pass;
+// tokens first, so that every row of d_out is read once, every row of dT has
+// one owner, and no floating-point atomic decides an order:
+//   1. a stable radix sort of (token, place), at most 8 bits a pass: in the
+//      shared memory of one CTA where a token and a place fit 32 bits together
+//      and n <= kCtaTokens, otherwise by a histogram and a scatter kernel a pass;
 //   2. the runs of equal tokens cut into pieces of 32 places.  Which list entry
 //      a piece gets is left to an integer atomic: it decides who computes
 //      the piece, not what;
-//   3. a warp per (piece, group of columns) adds the piece's rows in ascending order;
-//      a token with one piece is written at once, the pieces of longer runs
-//      go to partial sums.  The same kernel writes the zero rows;
-//   4. the partial sums of the long runs.
+//   3. a warp per (piece, 256 columns) adds the piece's rows in ascending order.
+//      A token with one piece is written at once.  The pieces of longer runs
+//      are the leaves of a 32-way tree: whoever brings the last child of a node
+//      adds the children in order (a ticket per node; nobody waits).
+// Sorting is a chain of latencies that leaves the memory idle, so the table is
+// zeroed meanwhile, by the other CTAs of the sorting launches; step 3 then
+// writes the rows of tokens that occur.
 #include "common.cuh"
 #include "ops.h"
 
@@ -23,22 +26,37 @@ namespace adaln {
 
 namespace {
 
-constexpr int kSmall = 4096;      // tokens that one CTA sorts
+constexpr int kCtaThreads = 1024;
+// Tokens that one CTA sorts, four a thread (11 us at 4096, most of it latency).
+// With 32 a thread one CTA took 67 us for 32768 tokens; the kernels that share
+// them among CTAs take about 25 us at any such size.
+constexpr int kCtaTokens = 4 * kCtaThreads;
 constexpr int kPiece = 32;        // places of a piece
-constexpr int kDigits = 256;      // 8 bits a pass
-constexpr int kTileMin = 2048;    // tokens of a sorting CTA
+constexpr int kFan = 32;          // children of a node
+constexpr int kDigits = 256;      // at most 8 bits a pass
+constexpr int kTileMin = 1024;    // tokens of a sorting CTA
 constexpr int kMaxTiles = 256;    // ... and the number of such CTAs
 
-struct Piece {
-    int token, start, len;
-    int slot;  // partial sum, or -1: the token's only piece
-};
-struct Run {
-    int token, slot, pieces;
+// One piece of a token's run.  A run of several pieces has a partial sum for
+// every piece and every node below the root, level by level from `slot`, and a
+// ticket (per column group) for every node, level by level from `node`.
+struct __align__(16) Piece {
+    int token, start, len, index;  // index: which piece of the run; -1: the only one
+    int pieces, slot, node, unused;
 };
 struct Counts {
-    int pieces, runs, slots;
+    int singles, pieces, slots, nodes;  // runs of one piece; pieces, partial sums and nodes of the longer runs
 };
+
+// partial sums and nodes of a run of np > 1 pieces
+__host__ __device__ inline void tree_size(int np, int &slots, int &nodes) {
+    slots = nodes = 0;
+    for (int n = np; n > 1;) {
+        slots += n;
+        n = (n + kFan - 1) / kFan;
+        nodes += n;
+    }
+}
 
 __device__ __forceinline__ uint32_t token_key(const void *tokens, int is64, int i, int V) {
     const long long t = is64 ? static_cast<const long long *>(tokens)[i] : static_cast<const int *>(tokens)[i];
@@ -90,172 +108,231 @@ embed_fwd_kernel(const void *tokens, int is64, const T *__restrict__ table, floa
     }
 }
 
+// The lanes whose digit equals this lane's, by one ballot a bit.  (With
+// match.any the one-CTA sort of 4096 tokens took 13.5 us instead of 10.5.)
+__device__ __forceinline__ unsigned same_digit(int digit, int digit_bits) {
+    unsigned peers = 0xFFFFFFFFu;
+    for (int k = 0; k < digit_bits; ++k) {
+        const bool one = (digit >> k) & 1;
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, one);
+        peers &= one ? m : ~m;
+    }
+    return peers;
+}
+
 // --------------------------------------------------------------------------
-// sorting
+// zeroing: CTAs [first, gridDim.x) of a sorting launch write their share
 // --------------------------------------------------------------------------
-// lanes of the warp with the same digit (among the lanes of `active`)
-__device__ __forceinline__ unsigned same_digit(unsigned active, int digit) { return __match_any_sync(active, digit); }
-
-// Exclusive scan of one value per thread over the first 256 threads of a CTA
-// (all threads call it; the others pass 0 and ignore the result).
-__device__ int scan256(int v, int *warp_sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int inc = v;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
-        if (lane >= off) inc += o;
-    }
-    if (warp < 8 && lane == 31) warp_sums[warp] = inc;
-    __syncthreads();
-    int before = 0;
-    for (int i = 0; i < warp && i < 8; ++i) before += warp_sums[i];
-    __syncthreads();
-    return before + inc - v;
+struct Fill {
+    uint4 *p;
+    long long vecs;  // of 16 bytes; 0: nothing to zero
+};
+__device__ void fill_zero(const Fill &f, int cta, int ctas) {
+    const long long step = (long long)ctas * blockDim.x;
+    for (long long i = (long long)cta * blockDim.x + threadIdx.x; i < f.vecs; i += step)
+        f.p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// First index of keys[0, n) (ascending) whose key is >= k.
-__device__ __forceinline__ int lower_bound(const uint32_t *keys, int n, uint32_t k) {
-    int lo = 0, hi = n;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (keys[mid] < k)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
-// Pieces of the run that begins at sorted place i, if one does.  Called by
-// whole warps: long runs are written by all lanes together.
-__device__ void plan_place(const uint32_t *keys, int n, int V, int i, Piece *pieces, Run *runs, Counts *counts) {
-    const int lane = threadIdx.x & 31;
-    int len = 0;
-    uint32_t key = (uint32_t)V;
-    if (i < n) {
-        key = keys[i];
-        if (key < (uint32_t)V && (i == 0 || keys[i - 1] != key)) {
-            // the end: nearby for most tokens, otherwise by bisection
-            int e = i + 1;
-            while (e < n && e < i + 4 && keys[e] == key) ++e;
-            if (e == i + 4 && e < n && keys[e] == key) e += lower_bound(keys + e, n - e, key + 1);
-            len = e - i;
-        }
-    }
-    const int np = (len + kPiece - 1) / kPiece;
-    // one atomic per warp and counter
-    int inc = np, slots = np > 1 ? np : 0;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int a = __shfl_up_sync(0xFFFFFFFFu, inc, off), b = __shfl_up_sync(0xFFFFFFFFu, slots, off);
-        if (lane >= off) inc += a, slots += b;
-    }
-    const int all = __shfl_sync(0xFFFFFFFFu, inc, 31), all_slots = __shfl_sync(0xFFFFFFFFu, slots, 31);
-    if (all == 0) return;
-    const unsigned longs = __ballot_sync(0xFFFFFFFFu, np > 1);
-    int base = 0, slot_base = 0, run_base = 0;
-    if (lane == 0) {
-        base = atomicAdd(&counts->pieces, all);
-        if (longs) {
-            slot_base = atomicAdd(&counts->slots, all_slots);
-            run_base = atomicAdd(&counts->runs, __popc(longs));
-        }
-    }
-    base = __shfl_sync(0xFFFFFFFFu, base, 0) + inc - np;
-    slot_base = __shfl_sync(0xFFFFFFFFu, slot_base, 0) + slots - (np > 1 ? np : 0);
-    run_base = __shfl_sync(0xFFFFFFFFu, run_base, 0) + __popc(longs & ((1u << lane) - 1));
-    if (np == 1) pieces[base] = Piece{(int)key, i, len, -1};
-    if (np > 1) runs[run_base] = Run{(int)key, slot_base, np};
-    for (unsigned m = longs; m; m &= m - 1) {
-        const int src = __ffs(m) - 1;
-        const int token = __shfl_sync(0xFFFFFFFFu, (int)key, src), start = __shfl_sync(0xFFFFFFFFu, i, src);
-        const int n_p = __shfl_sync(0xFFFFFFFFu, np, src), length = __shfl_sync(0xFFFFFFFFu, len, src);
-        const int at = __shfl_sync(0xFFFFFFFFu, base, src), slot = __shfl_sync(0xFFFFFFFFu, slot_base, src);
-        for (int p = lane; p < n_p; p += 32)
-            pieces[at + p] = Piece{token, start + p * kPiece, min(kPiece, length - p * kPiece), slot + p};
-    }
-}
-
-// n <= kSmall: sort and plan in one CTA of 32 warps, 4 places a thread, warp w
-// holding the places [128 w, 128 w + 128) of every pass.
-struct SmallShared {
-    uint32_t keys[kSmall];
-    int idx[kSmall];
-    int cnt[32][kDigits];
-    int warp_sums[8];
+// --------------------------------------------------------------------------
+// pieces of the sorted tokens
+// --------------------------------------------------------------------------
+struct PackedKeys {  // token << bits | place
+    const uint32_t *items;
+    int bits;
+    __device__ uint32_t operator()(int i) const { return items[i] >> bits; }
+};
+struct PlainKeys {
+    const uint32_t *keys;
+    __device__ uint32_t operator()(int i) const { return keys[i]; }
 };
 
-__global__ void __launch_bounds__(1024)
-embed_sort_small_kernel(const void *tokens, int is64, int n, int V, int passes, uint32_t *keys_out, int *idx_out,
-                        Piece *pieces, Run *runs, Counts *counts) {
+// The first place >= from whose key is not `key` (or n), by all lanes: the next
+// 32 places, then a search by 32nds.
+template <typename Keys>
+__device__ int run_end(const Keys &keys, int n, int from, uint32_t key) {
+    const int lane = threadIdx.x & 31;
+    int lo = from, hi = min(n, from + 32);
+    int c = __popc(__ballot_sync(0xFFFFFFFFu, lo + lane < hi && keys(lo + lane) == key));
+    if (lo + c < hi || hi == n) return lo + c;
+    lo = hi;
+    hi = n;
+    while (hi - lo > 32) {
+        const int step = (hi - lo + 31) / 32, p = lo + lane * step;
+        c = __popc(__ballot_sync(0xFFFFFFFFu, p < hi && keys(p) == key));
+        if (c == 0) return lo;
+        hi = min(hi, lo + c * step);
+        lo += (c - 1) * step + 1;
+    }
+    return lo + __popc(__ballot_sync(0xFFFFFFFFu, lo + lane < hi && keys(lo + lane) == key));
+}
+
+// The pieces of the runs that begin at the warp's 32 places base + lane.
+template <typename Keys>
+__device__ void plan_places(const Keys &keys, int n, int V, int base, int groups, Piece *pieces, int *tickets,
+                            Counts *counts) {
+    if (base >= n) return;
+    const int lane = threadIdx.x & 31, i = base + lane;
+    const uint32_t key = i < n ? keys(i) : 0xFFFFFFFFu;
+    uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, key, 1);
+    if (lane == 0 && i > 0) prev = keys(i - 1);
+    const bool edge = i >= n || i == 0 || key != prev;
+    const bool head = edge && i < n && key < (uint32_t)V;
+    const unsigned edges = __ballot_sync(0xFFFFFFFFu, edge);
+    int len = 0;
+    if (edges != 0) {
+        // the last run may go on behind the warp's places
+        const int last = 31 - __clz(edges);
+        const int last_head = __shfl_sync(0xFFFFFFFFu, (int)head, last);
+        int behind = base + 32;
+        if (last_head) behind = run_end(keys, n, base + 32, __shfl_sync(0xFFFFFFFFu, key, last));
+        const unsigned next = lane < 31 ? edges & (0xFFFFFFFEu << lane) : 0u;
+        if (head) len = (next ? base + __ffs(next) - 1 : behind) - i;
+    }
+    const int np = (len + kPiece - 1) / kPiece;
+    int slots = 0, nodes = 0;
+    if (np > 1) tree_size(np, slots, nodes);
+    // one atomic per warp and counter.  Long runs fill the list from the front,
+    // so that their trees are begun first; the others from the back.
+    const unsigned longs = __ballot_sync(0xFFFFFFFFu, np > 1), ones = __ballot_sync(0xFFFFFFFFu, np == 1);
+    int4 *out = reinterpret_cast<int4 *>(pieces);
+    if (ones) {
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&counts->singles, __popc(ones));
+        at = n - 1 - __shfl_sync(0xFFFFFFFFu, at, 0) - __popc(ones & ((1u << lane) - 1));
+        if (np == 1) out[2 * at] = make_int4((int)key, i, len, -1);
+    }
+    if (longs == 0) return;
+    const int mine = np > 1 ? np : 0;
+    int at = mine, slot = slots, node = nodes;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, at, off), y = __shfl_up_sync(0xFFFFFFFFu, slot, off),
+                  z = __shfl_up_sync(0xFFFFFFFFu, node, off);
+        if (lane >= off) at += x, slot += y, node += z;
+    }
+    int at0 = 0, slot0 = 0, node0 = 0;
+    if (lane == 31) {
+        at0 = atomicAdd(&counts->pieces, at);
+        slot0 = atomicAdd(&counts->slots, slot);
+        node0 = atomicAdd(&counts->nodes, node);
+    }
+    at += __shfl_sync(0xFFFFFFFFu, at0, 31) - mine;
+    slot += __shfl_sync(0xFFFFFFFFu, slot0, 31) - slots;
+    node += __shfl_sync(0xFFFFFFFFu, node0, 31) - nodes;
+    for (unsigned m = longs; m; m &= m - 1) {  // long runs: by all lanes
+        const int src = __ffs(m) - 1;
+        const int l_token = __shfl_sync(0xFFFFFFFFu, (int)key, src), l_start = __shfl_sync(0xFFFFFFFFu, i, src);
+        const int l_len = __shfl_sync(0xFFFFFFFFu, len, src), l_np = __shfl_sync(0xFFFFFFFFu, np, src);
+        const int l_at = __shfl_sync(0xFFFFFFFFu, at, src), l_slot = __shfl_sync(0xFFFFFFFFu, slot, src);
+        const int l_node = __shfl_sync(0xFFFFFFFFu, node, src), l_nodes = __shfl_sync(0xFFFFFFFFu, nodes, src);
+        for (int p = lane; p < l_np; p += 32) {
+            out[2 * (l_at + p)] = make_int4(l_token, l_start + p * kPiece, min(kPiece, l_len - p * kPiece), p);
+            out[2 * (l_at + p) + 1] = make_int4(l_np, l_slot, l_node, 0);
+        }
+        for (long long k = lane; k < (long long)l_nodes * groups; k += 32) tickets[(long long)l_node * groups + k] = 0;
+    }
+}
+
+// --------------------------------------------------------------------------
+// sorting in one CTA: 32 warps, IPT items a thread; warp w holds the places
+// [32 IPT w, 32 IPT (w + 1)) of every pass.  An item is token << bits | place.
+// --------------------------------------------------------------------------
+constexpr int kCntStride = kDigits + 1;  // keeps the scan's reads in different banks
+struct CtaShared {
+    int cnt[32][kCntStride];  // per warp and digit: the count, then the next place
+    int sums[32];
+    Counts counts;
+    uint32_t items[1];  // [IPT * 1024]
+};
+
+template <int IPT>
+__global__ void __launch_bounds__(kCtaThreads)
+embed_sort_cta_kernel(const void *tokens, int is64, int n, int V, int bits, int digit_bits, int passes, int groups,
+                      int *idx_out, Piece *pieces, int *tickets, Counts *counts, Fill fill) {
     extern __shared__ __align__(16) unsigned char raw[];
-    SmallShared &sh = *reinterpret_cast<SmallShared *>(raw);
+    CtaShared &sh = *reinterpret_cast<CtaShared *>(raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    if (threadIdx.x == 0) *counts = Counts{0, 0, 0};
-    uint32_t key[4];
-    int idx[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        idx[j] = warp * 128 + j * 32 + lane;
-        key[j] = idx[j] < n ? token_key(tokens, is64, idx[j], V) : 0xFFFFFFFFu;  // behind the end: sorts last
+    if (blockIdx.x > 0) {
+        fill_zero(fill, blockIdx.x - 1, gridDim.x - 1);
+        return;
     }
-    for (int pass = 0; pass < passes; ++pass) {
-        for (int d = lane; d < kDigits; d += 32) sh.cnt[warp][d] = 0;
-        __syncwarp();
-        int rank[4];
+    const int base = warp * (32 * IPT) + lane;
+    const int nd = 1 << digit_bits;
+    uint32_t item[IPT];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int digit = (key[j] >> (8 * pass)) & 255;
-            const unsigned peers = same_digit(0xFFFFFFFFu, digit);
-            const int before = __popc(peers & ((1u << lane) - 1));
-            const int base = sh.cnt[warp][digit];
-            __syncwarp();
-            if (before == 0) sh.cnt[warp][digit] = base + __popc(peers);
-            __syncwarp();
-            rank[j] = base + before;
-        }
+    for (int j = 0; j < IPT; ++j) {
+        const int i = base + 32 * j;
+        item[j] = i < n ? token_key(tokens, is64, i, V) << bits | i : 0xFFFFFFFFu;  // behind the end: last
+    }
+    if (threadIdx.x == 0) sh.counts = Counts{0, 0, 0, 0};
+    for (int pass = 0; pass < passes; ++pass) {
+        const int shift = bits + pass * digit_bits;
+        for (int d = lane; d < nd; d += 32) sh.cnt[warp][d] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < IPT; ++j) atomicAdd(&sh.cnt[warp][(item[j] >> shift) & (nd - 1)], 1);
         __syncthreads();
-        // counts of a digit over the warps, then the digits
-        int total = 0;
-        if (threadIdx.x < kDigits) {
-            for (int w = 0; w < 32; ++w) {
-                const int c = sh.cnt[w][threadIdx.x];
-                sh.cnt[w][threadIdx.x] = total;
-                total += c;
+        // exclusive scan over (digit, warp): thread 4 d + q has the warps 8 q ..
+        const int d = threadIdx.x >> 2, q = threadIdx.x & 3;
+        int c[8], sum = 0;
+        if (d < nd) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) c[k] = sh.cnt[8 * q + k][d];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += c[k];
+        }
+        int inc = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+            if (lane >= off) inc += o;
+        }
+        if (lane == 31) sh.sums[warp] = inc;
+        __syncthreads();
+        int before = lane < warp ? sh.sums[lane] : 0;
+        before = __reduce_add_sync(0xFFFFFFFFu, before) + inc - sum;
+        if (d < nd) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                sh.cnt[8 * q + k][d] = before;
+                before += c[k];
             }
         }
-        const int first = scan256(total, sh.warp_sums);
-        if (threadIdx.x < kDigits)
-            for (int w = 0; w < 32; ++w) sh.cnt[w][threadIdx.x] += first;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int at = sh.cnt[warp][(key[j] >> (8 * pass)) & 255] + rank[j];
-            sh.keys[at] = key[j];
-            sh.idx[at] = idx[j];
+        for (int j = 0; j < IPT; ++j) {
+            const int digit = (item[j] >> shift) & (nd - 1);
+            const unsigned peers = same_digit(digit, digit_bits);
+            const int rank = __popc(peers & ((1u << lane) - 1));
+            const int at = sh.cnt[warp][digit];
+            __syncwarp();
+            if (rank == 0) sh.cnt[warp][digit] = at + __popc(peers);
+            __syncwarp();
+            sh.items[at + rank] = item[j];
         }
         __syncthreads();
         if (pass + 1 < passes) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                key[j] = sh.keys[warp * 128 + j * 32 + lane];
-                idx[j] = sh.idx[warp * 128 + j * 32 + lane];
-            }
+            for (int j = 0; j < IPT; ++j) item[j] = sh.items[base + 32 * j];
             __syncthreads();
         }
     }
-    for (int i = threadIdx.x; i < n; i += 1024) {
-        keys_out[i] = sh.keys[i];
-        idx_out[i] = sh.idx[i];
-    }
-    for (int i0 = 0; i0 < n; i0 += 1024) plan_place(sh.keys, n, V, i0 + threadIdx.x, pieces, runs, counts);
+    const uint32_t mask = (1u << bits) - 1u;
+    for (int i = threadIdx.x; i < n; i += kCtaThreads) idx_out[i] = (int)(sh.items[i] & mask);
+    const PackedKeys keys{sh.items, bits};
+    for (int i0 = warp * 32; i0 < n; i0 += kCtaThreads)
+        plan_places(keys, n, V, i0, groups, pieces, tickets, &sh.counts);
+    __syncthreads();
+    if (threadIdx.x == 0) *counts = sh.counts;
 }
 
-// larger n: pass by pass.  CTA b holds the places [b * tile, (b + 1) * tile),
-// its warp w an eighth of them; hist [tiles][256].
+// --------------------------------------------------------------------------
+// larger sorts: pass by pass.  CTA b holds the places [b * tile, (b + 1) *
+// tile), its warp w an eighth of them; hist [tiles][256].  The CTAs from
+// `tiles` on zero their share of the table.
+// --------------------------------------------------------------------------
 struct SortArgs {
     const void *tokens;  // the first pass reads the tokens themselves
     int is64;
@@ -269,71 +346,106 @@ struct SortArgs {
 };
 
 __device__ __forceinline__ uint32_t sort_key(const SortArgs &a, int i) {
-    return a.keys_in ? a.keys_in[i] : token_key(a.tokens, a.is64, i, a.V);
+    return a.keys_in ? __ldcg(a.keys_in + i) : token_key(a.tokens, a.is64, i, a.V);
 }
 
-__global__ void __launch_bounds__(256) embed_hist_kernel(const SortArgs a) {
+__global__ void __launch_bounds__(256) embed_hist_kernel(const SortArgs a, const Fill fill) {
     __shared__ int cnt[kDigits];
     cnt[threadIdx.x] = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.counts = Counts{0, 0, 0};
+    if ((int)blockIdx.x >= a.tiles) {
+        fill_zero(fill, blockIdx.x - a.tiles, gridDim.x - a.tiles);
+        return;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.counts = Counts{0, 0, 0, 0};
     const int i1 = min(a.n, (int)(blockIdx.x + 1) * a.tile);
+#pragma unroll 4
     for (int i = blockIdx.x * a.tile + threadIdx.x; i < i1; i += 256)
         atomicAdd(&cnt[(sort_key(a, i) >> a.shift) & 255], 1);
     __syncthreads();
     a.hist[blockIdx.x * kDigits + threadIdx.x] = cnt[threadIdx.x];
 }
 
-__global__ void __launch_bounds__(256) embed_scatter_kernel(const SortArgs a) {
-    __shared__ int cnt[8][kDigits];  // next place of a digit, per warp
-    __shared__ int warp_sums[8];
+__global__ void __launch_bounds__(256) embed_scatter_kernel(const SortArgs a, const Fill fill) {
+    constexpr int J = 4;             // places of a lane in flight
+    __shared__ int cnt[8][kDigits];  // per warp and digit: the count, then the next place
+    __shared__ int sums[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = threadIdx.x;
     for (int w = 0; w < 8; ++w) cnt[w][d] = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
+    if ((int)blockIdx.x >= a.tiles) {
+        fill_zero(fill, blockIdx.x - a.tiles, gridDim.x - a.tiles);
+        return;
+    }
     const int part = a.tile / 8;
     const int i0 = blockIdx.x * a.tile + warp * part, i1 = min(a.n, i0 + part);
+#pragma unroll 4
     for (int i = i0 + lane; i < i1; i += 32) atomicAdd(&cnt[warp][(sort_key(a, i) >> a.shift) & 255], 1);
     int before = 0, total = 0;  // of digit d: in the CTAs before this one, and in all
-#pragma unroll 8
+#pragma unroll 16
     for (int b = 0; b < a.tiles; ++b) {
         const int c = __ldcg(a.hist + b * kDigits + d);
         total += c;
         before += b < (int)blockIdx.x ? c : 0;
     }
-    const int first = scan256(total, warp_sums) + before;  // its barriers also close the counting
-    int next = first;
+    int inc = total;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+        if (lane >= off) inc += o;
+    }
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();  // also closes the counting
+    int next = before + inc - total;
+    for (int w = 0; w < warp; ++w) next += sums[w];
     for (int w = 0; w < 8; ++w) {
         const int c = cnt[w][d];
         cnt[w][d] = next;
         next += c;
     }
     __syncthreads();
-    for (int i = i0; i < i1; i += 32) {
-        const unsigned active = __ballot_sync(0xFFFFFFFFu, i + lane < i1);
-        if (i + lane < i1) {
-            const uint32_t key = sort_key(a, i + lane);
-            const int digit = (key >> a.shift) & 255;
-            const unsigned peers = same_digit(active, digit);
+    for (int i = i0; i < i1; i += 32 * J) {
+        uint32_t key[J];
+        int idx[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int at = i + 32 * j + lane;
+            key[j] = at < i1 ? sort_key(a, at) : 0u;
+            idx[j] = at < i1 && a.idx_in ? __ldcg(a.idx_in + at) : at;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const bool in = i + 32 * j + lane < i1;
+            const unsigned active = __ballot_sync(0xFFFFFFFFu, in);
+            const int digit = (key[j] >> a.shift) & 255;
+            const unsigned peers = same_digit(digit, 8) & active;
             const int rank = __popc(peers & ((1u << lane) - 1));
             const int at = cnt[warp][digit] + rank;
-            __syncwarp(active);
-            if (rank == 0) cnt[warp][digit] += __popc(peers);
-            __syncwarp(active);
-            a.keys_out[at] = key;
-            a.idx_out[at] = a.idx_in ? a.idx_in[i + lane] : i + lane;
+            __syncwarp();
+            if (in && rank == 0) cnt[warp][digit] += __popc(peers);
+            __syncwarp();
+            if (in) {
+                a.keys_out[at] = key[j];
+                a.idx_out[at] = idx[j];
+            }
         }
     }
 }
 
-__global__ void __launch_bounds__(256) embed_plan_kernel(const uint32_t *keys, int n, int V, Piece *pieces, Run *runs,
-                                                         Counts *counts) {
+__global__ void __launch_bounds__(256) embed_plan_kernel(const uint32_t *keys, int n, int V, int groups,
+                                                         Piece *pieces, int *tickets, Counts *counts, int ctas,
+                                                         const Fill fill) {
     pdl_wait();
     pdl_trigger();
-    plan_place(keys, n, V, blockIdx.x * 256 + threadIdx.x, pieces, runs, counts);
+    if ((int)blockIdx.x >= ctas) {
+        fill_zero(fill, blockIdx.x - ctas, gridDim.x - ctas);
+        return;
+    }
+    plan_places(PlainKeys{keys}, n, V, (int)(blockIdx.x * 256 + (threadIdx.x & ~31u)), groups, pieces, tickets, counts);
 }
 
 // --------------------------------------------------------------------------
@@ -341,187 +453,210 @@ __global__ void __launch_bounds__(256) embed_plan_kernel(const uint32_t *keys, i
 // --------------------------------------------------------------------------
 struct SumArgs {
     const void *d_out;
-    const uint32_t *keys;
     const int *idx;
     const Piece *pieces;
-    const Run *runs;
     const Counts *counts;
+    int *tickets;    // [nodes][groups]
     float *partial;  // [slots][D]
     float *acc;      // [V][D] fp32, or
     uint16_t *bf16;  // [V][D]
     float scale;
-    int accumulate, n, V, D;
+    int accumulate, n, D;
 };
 
-// 8 channels of a lane
-__device__ __forceinline__ void load_row8(float (&v)[8], const uint16_t *p) {
-    const uint4 t = ldg16(p);
-    v[0] = bf16lo(t.x), v[1] = bf16hi(t.x), v[2] = bf16lo(t.y), v[3] = bf16hi(t.y);
-    v[4] = bf16lo(t.z), v[5] = bf16hi(t.z), v[6] = bf16lo(t.w), v[7] = bf16hi(t.w);
+// 8 columns of a row as they lie in memory, and added to a sum
+__device__ __forceinline__ void load8(uint4 &v, const uint16_t *p) { v = ldg16(p); }
+struct Floats8 {
+    float4 a, b;
+};
+__device__ __forceinline__ void load8(Floats8 &v, const float *p) {
+    v.a = __ldcg(reinterpret_cast<const float4 *>(p));
+    v.b = __ldcg(reinterpret_cast<const float4 *>(p + 4));
 }
-__device__ __forceinline__ void load_row8(float (&v)[8], const float *p) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ void add8(float (&s)[8], const uint4 &v) {
+    s[0] = __fadd_rn(s[0], bf16lo(v.x)), s[1] = __fadd_rn(s[1], bf16hi(v.x));
+    s[2] = __fadd_rn(s[2], bf16lo(v.y)), s[3] = __fadd_rn(s[3], bf16hi(v.y));
+    s[4] = __fadd_rn(s[4], bf16lo(v.z)), s[5] = __fadd_rn(s[5], bf16hi(v.z));
+    s[6] = __fadd_rn(s[6], bf16lo(v.w)), s[7] = __fadd_rn(s[7], bf16hi(v.w));
+}
+__device__ __forceinline__ void add8(float (&s)[8], const Floats8 &v) {
+    s[0] = __fadd_rn(s[0], v.a.x), s[1] = __fadd_rn(s[1], v.a.y);
+    s[2] = __fadd_rn(s[2], v.a.z), s[3] = __fadd_rn(s[3], v.a.w);
+    s[4] = __fadd_rn(s[4], v.b.x), s[5] = __fadd_rn(s[5], v.b.y);
+    s[6] = __fadd_rn(s[6], v.b.z), s[7] = __fadd_rn(s[7], v.b.w);
 }
 
-// N columns (4 or 8) of row v of the gradient
-template <int N>
-__device__ __forceinline__ void put_row(const SumArgs &a, int token, int col, const float (&s)[N]) {
+// 8 columns of row `token` of the gradient
+__device__ __forceinline__ void put_row(const SumArgs &a, int token, int col, const float (&s)[8]) {
     const long long at = (long long)token * a.D + col;
-    float r[N];
+    float r[8];
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = __fmul_rn(s[i], a.scale);
+    for (int i = 0; i < 8; ++i) r[i] = __fmul_rn(s[i], a.scale);
     if (a.bf16) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4)
-            *reinterpret_cast<uint2 *>(a.bf16 + at + i) =
-                make_uint2(pack_bf16x2(r[i], r[i + 1]), pack_bf16x2(r[i + 2], r[i + 3]));
+        stg16(a.bf16 + at, make_uint4(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]), pack_bf16x2(r[4], r[5]),
+                                      pack_bf16x2(r[6], r[7])));
         return;
     }
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        float4 *p = reinterpret_cast<float4 *>(a.acc + at + i);
-        float4 o = make_float4(r[i], r[i + 1], r[i + 2], r[i + 3]);
-        if (a.accumulate) {
-            const float4 c = *p;
-            o = make_float4(__fadd_rn(c.x, o.x), __fadd_rn(c.y, o.y), __fadd_rn(c.z, o.z), __fadd_rn(c.w, o.w));
-        }
-        *p = o;
+    float4 *p = reinterpret_cast<float4 *>(a.acc + at);
+    float4 lo = make_float4(r[0], r[1], r[2], r[3]), hi = make_float4(r[4], r[5], r[6], r[7]);
+    if (a.accumulate) {
+        const float4 x = p[0], y = p[1];
+        lo = make_float4(__fadd_rn(x.x, lo.x), __fadd_rn(x.y, lo.y), __fadd_rn(x.z, lo.z), __fadd_rn(x.w, lo.w));
+        hi = make_float4(__fadd_rn(y.x, hi.x), __fadd_rn(y.y, hi.y), __fadd_rn(y.z, hi.z), __fadd_rn(y.w, hi.w));
     }
+    p[0] = lo;
+    p[1] = hi;
 }
 
-// A warp per (piece, 256 columns); then, without accumulate, a warp per (32
-// rows of the table, 256 columns), which writes the rows without a token.
-template <typename T>
-__global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a) {
-    constexpr int U = 8;  // rows in flight
+// A piece of a longer run: leave its sum, and climb the run's tree while this
+// warp brings the last child of the node.  A call of its own: inlined, its
+// registers made the sums spill.
+__device__ __noinline__ void climb(const SumArgs &a, const int4 *tree, int token, int index, int col, float4 lo,
+                                   float4 hi) {
+    const int4 t = __ldcg(tree);
+    const int pieces = t.x;
+    int slot = t.y, node = t.z;
+    const bool live = col < a.D;
+    float s[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const int lane = threadIdx.x & 31, groups = gridDim.y, group = blockIdx.y;
+    int count = pieces;  // of the level
+    for (;;) {
+        float *q = a.partial + (long long)(slot + index) * a.D + col;
+        if (live) {
+            __stcg(reinterpret_cast<float4 *>(q), make_float4(s[0], s[1], s[2], s[3]));
+            __stcg(reinterpret_cast<float4 *>(q + 4), make_float4(s[4], s[5], s[6], s[7]));
+        }
+        const int parent = index / kFan, children = min(kFan, count - parent * kFan);
+        __threadfence();
+        __syncwarp();
+        int seen = 0;
+        if (lane == 0) seen = atomicAdd(a.tickets + (long long)(node + parent) * groups + group, 1);
+        if (__shfl_sync(0xFFFFFFFFu, seen, 0) + 1 < children) return;
+        __threadfence();
+        // the node's children in order, from +0
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = 0.0f;
+        if (live) {
+            const float *c = a.partial + (long long)(slot + parent * kFan) * a.D + col;
+            for (int k0 = 0; k0 < children; k0 += 4) {
+                Floats8 v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k] = Floats8();
+                    if (k0 + k < children) load8(v[k], c + (long long)(k0 + k) * a.D);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) add8(s, v[k]);
+            }
+        }
+        slot += count;
+        count = (count + kFan - 1) / kFan;
+        node += count;
+        index = parent;
+        if (count == 1) break;  // the root
+    }
+    if (live) put_row(a, token, col, s);
+}
+
+// A warp per (piece, 256 columns); blockIdx.y is the column group.
+template <typename T, typename Vec, int U>
+__global__ void __launch_bounds__(256, 4) embed_sum_kernel(const __grid_constant__ SumArgs a) {
     const int lane = threadIdx.x & 31;
-    const int groups = (a.D + 255) / 256;
-    const T *d_out = static_cast<const T *>(a.d_out);
+    const int col = blockIdx.y * 256 + lane * 8;
+    const bool live = col < a.D;
+    // lanes behind the last column read along with the first and write nothing
+    const T *d_out = static_cast<const T *>(a.d_out) + (live ? col : 0);
     pdl_wait();
     pdl_trigger();
-    const long long piece_tasks = (long long)__ldcg(&a.counts->pieces) * groups;
-    const long long total = piece_tasks + (a.accumulate ? 0 : (long long)((a.V + 31) / 32) * groups);
-    for (long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); task < total;
-         task += (long long)gridDim.x * 8) {
-        if (task < piece_tasks) {
-            const int4 pc = __ldcg(reinterpret_cast<const int4 *>(a.pieces + task / groups));
-            const Piece p{pc.x, pc.y, pc.z, pc.w};
-            const int col = (int)(task % groups) * 256 + lane * 8;
-            const bool live = col < a.D;
-            const int mine = lane < p.len ? __ldcg(a.idx + p.start + lane) : 0;
-            float s[8];
+    const int4 counts = __ldcg(reinterpret_cast<const int4 *>(a.counts));
+    const int longs = counts.y, total = counts.x + longs;
+    // the next piece's entry and places are loaded while this one's rows are
+    const auto entry = [&](int i) {
+        return reinterpret_cast<const int4 *>(a.pieces + (i < longs ? i : a.n - 1 - (i - longs)));
+    };
+    int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int step = gridDim.x * 8;
+    if (i >= total) return;
+    int4 p = __ldcg(entry(i));
+    int mine = lane < p.z ? __ldcg(a.idx + p.y + lane) : 0;
+#pragma unroll 1
+    for (; i < total; i += step) {
+        const int len = p.z;
+        int4 p_next = p;
+        if (i + step < total) p_next = __ldcg(entry(i + step));
+        float s[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] = 0.0f;
-            for (int r0 = 0; r0 < p.len; r0 += U) {
-                float v[U][8];
+        for (int k = 0; k < 8; ++k) s[k] = 0.0f;
+#pragma unroll 1
+        for (int r0 = 0; r0 < len; r0 += U) {
+            Vec v[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int row = __shfl_sync(0xFFFFFFFFu, mine, (r0 + u) & 31);
-                    if (live && r0 + u < p.len) load_row8(v[u], d_out + (long long)row * a.D + col);
-                }
+            for (int u = 0; u < U; ++u) {
+                const int row = __shfl_sync(0xFFFFFFFFu, mine, (r0 + u) & 31);
+                v[u] = Vec();  // +0 behind the end: adding it changes no sum begun from +0
+                if (r0 + u < len) load8(v[u], d_out + (long long)row * a.D);
+            }
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (r0 + u < p.len) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) s[i] = __fadd_rn(s[i], v[u][i]);
-                    }
-            }
-            if (live && p.slot < 0) {
-                put_row(a, p.token, col, s);
-            } else if (live) {
-                float *q = a.partial + (long long)p.slot * a.D + col;
-                *reinterpret_cast<float4 *>(q) = make_float4(s[0], s[1], s[2], s[3]);
-                *reinterpret_cast<float4 *>(q + 4) = make_float4(s[4], s[5], s[6], s[7]);
-            }
-        } else {
-            const long long zt = task - piece_tasks;
-            const int v0 = (int)(zt / groups) * 32, col = (int)(zt % groups) * 256 + lane * 8;
-            const int v = v0 + lane;
-            bool absent = false;
-            if (v < a.V) {
-                const int at = lower_bound(a.keys, a.n, (uint32_t)v);
-                absent = at == a.n || a.keys[at] != (uint32_t)v;
-            }
-            unsigned m = __ballot_sync(0xFFFFFFFFu, absent);
-            if (col >= a.D) m = 0;
-            for (; m; m &= m - 1) {
-                const long long o = (long long)(v0 + __ffs(m) - 1) * a.D + col;
-                if (a.bf16) {
-                    stg16(a.bf16 + o, make_uint4(0, 0, 0, 0));
-                } else {
-                    stg16(a.acc + o, make_uint4(0, 0, 0, 0));
-                    stg16(a.acc + o + 4, make_uint4(0, 0, 0, 0));
-                }
-            }
+            for (int u = 0; u < U; ++u) add8(s, v[u]);
         }
+        mine = lane < p_next.z ? __ldcg(a.idx + p_next.y + lane) : 0;
+        if (p.w >= 0)
+            climb(a, entry(i) + 1, p.x, p.w, col, make_float4(s[0], s[1], s[2], s[3]),
+                  make_float4(s[4], s[5], s[6], s[7]));
+        else if (live)
+            put_row(a, p.x, col, s);
+        p = p_next;
     }
 }
 
-// Runs of several pieces: a CTA per (run, 128 columns).  Warp w adds an eighth
-// of the partial sums in order, then the warps are added in order.
-__global__ void __launch_bounds__(256) embed_runs_kernel(const SumArgs a) {
-    __shared__ float red[8][128];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int groups = (a.D + 127) / 128;
-    pdl_wait();
-    pdl_trigger();
-    const long long total = (long long)__ldcg(&a.counts->runs) * groups;
-    for (long long task = blockIdx.x; task < total; task += gridDim.x) {
-        const int *rp = reinterpret_cast<const int *>(a.runs + task / groups);
-        const Run r{__ldcg(rp), __ldcg(rp + 1), __ldcg(rp + 2)};
-        const int col = (int)(task % groups) * 128 + lane * 4;
-        const int per = (r.pieces + 7) / 8, p0 = warp * per, p1 = min(r.pieces, p0 + per);
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (col < a.D) {
-            const float4 *q = reinterpret_cast<const float4 *>(a.partial + (long long)(r.slot + p0) * a.D + col);
-#pragma unroll 8
-            for (int p = p0; p < p1; ++p, q += a.D / 4) {
-                const float4 v = __ldcg(q);
-                s[0] = __fadd_rn(s[0], v.x), s[1] = __fadd_rn(s[1], v.y);
-                s[2] = __fadd_rn(s[2], v.z), s[3] = __fadd_rn(s[3], v.w);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red[warp][lane * 4 + i] = s[i];
-        __syncthreads();
-        if (warp == 0 && col < a.D) {
-#pragma unroll
-            for (int w = 1; w < 8; ++w) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = __fadd_rn(s[i], red[w][lane * 4 + i]);
-            }
-            put_row(a, r.token, col, s);
-        }
-        __syncthreads();
-    }
-}
-
-// Workspace: [counts | pieces n | runs | keys 2n | idx 2n | hist | partial].
+// Workspace.  A run of several pieces has at least 33 places, so all such runs
+// together have at most 2 n / 33 pieces; each run's partial sums are at most
+// 9/8 of its pieces, its nodes at most 1 + pieces / 8 (tree_size).
 struct Layout {
-    size_t counts, pieces, runs, keys, idx, hist, partial, bytes;
+    size_t counts, pieces, keys, idx, hist, tickets, partial, bytes;
 };
-size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 Layout layout(int n, int D) {
     Layout l;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
-        at += up256(bytes);
+        at += (bytes + 255) & ~(size_t)255;
         return here;
     };
+    const size_t groups = (size_t)(D + 255) / 256, N = (size_t)n;
     l.counts = take(sizeof(Counts));
-    l.pieces = take((size_t)n * sizeof(Piece));
-    l.runs = take(((size_t)n / kPiece + 1) * sizeof(Run));
-    l.keys = take((size_t)n * 2 * sizeof(uint32_t));
-    l.idx = take((size_t)n * 2 * sizeof(int));
+    l.pieces = take(N * sizeof(Piece));
+    l.keys = take(N * 2 * sizeof(uint32_t));
+    l.idx = take(N * 2 * sizeof(int));
     l.hist = take((size_t)kMaxTiles * kDigits * sizeof(int));
-    // a run of several pieces has at least 33 places and at most 2 pieces for
-    // every 33 of them
-    l.partial = take(((size_t)n / 16 + 1) * D * sizeof(float));
+    l.tickets = take((N / 16 + 1) * groups * sizeof(int));
+    l.partial = take((N * 9 / 128 + 2) * D * sizeof(float));
     l.bytes = at;
     return l;
+}
+
+int bit_length(unsigned v) {
+    int b = 0;
+    while (v >> b) ++b;
+    return b;
+}
+
+// CTAs that zero `vecs` 16-byte vectors: 32 KB each, at most two an SM
+int fill_ctas(long long vecs, int threads, const DeviceInfo &dev) {
+    const long long c = (vecs + 2047) / 2048, most = 2ll * dev.sm_count * (1024 / threads);
+    return (int)(c < most ? c : most);
+}
+
+template <int IPT>
+cudaError_t sort_cta(const void *tokens, int is64, int n, int V, int bits, int digit_bits, int passes, int groups,
+                     int *idx, Piece *pieces, int *tickets, Counts *counts, const Fill &fill, cudaStream_t stream,
+                     const DeviceInfo &dev) {
+    const size_t smem = sizeof(CtaShared) + (size_t)IPT * kCtaThreads * sizeof(uint32_t);
+    const cudaError_t e = ensure_smem_attr((const void *)embed_sort_cta_kernel<IPT>, smem, dev);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(embed_sort_cta_kernel<IPT>, dim3(1 + fill_ctas(fill.vecs, kCtaThreads, dev)), dim3(kCtaThreads),
+                      smem, stream, tokens, is64, n, V, bits, digit_bits, passes, groups, idx, pieces, tickets, counts,
+                      fill);
 }
 
 }  // namespace
@@ -548,19 +683,18 @@ cudaError_t launch_embed_bwd(const T *d_out, const void *tokens, int tokens_are_
     const Layout l = layout(n, D);
     Counts *counts = reinterpret_cast<Counts *>(base + l.counts);
     Piece *pieces = reinterpret_cast<Piece *>(base + l.pieces);
-    Run *runs = reinterpret_cast<Run *>(base + l.runs);
     uint32_t *keys = reinterpret_cast<uint32_t *>(base + l.keys);
     int *idx = reinterpret_cast<int *>(base + l.idx);
-    int passes = 1;  // keys are 0 .. V
-    while (passes < 4 && ((uint32_t)V >> (8 * passes)) != 0) ++passes;
+    int *tickets = reinterpret_cast<int *>(base + l.tickets);
+    const int groups = (D + 255) / 256;
+    const int key_bits = bit_length((unsigned)V), bits = n > 1 ? bit_length((unsigned)(n - 1)) : 1;  // keys are 0 .. V
+    Fill fill = {d_table ? reinterpret_cast<uint4 *>(d_table) : reinterpret_cast<uint4 *>(d_table_acc),
+                 accumulate ? 0 : (long long)V * D * (d_table ? 2 : 4) / 16};
     cudaError_t e = cudaSuccess;
-    if (n <= kSmall) {
-        // keys behind the end are all ones in the bytes sorted: with V also all
-        // ones they tie with padding, which comes first by its place
-        e = ensure_smem_attr((const void *)embed_sort_small_kernel, sizeof(SmallShared), dev);
-        if (e != cudaSuccess) return e;
-        e = launch_pdl(embed_sort_small_kernel, dim3(1), dim3(1024), sizeof(SmallShared), stream, tokens, tokens_are_64,
-                       n, V, passes, keys, idx, pieces, runs, counts);
+    if (n <= kCtaTokens && key_bits + bits <= 32) {
+        const int passes = (key_bits + 7) / 8, digit_bits = (key_bits + passes - 1) / passes;
+        e = sort_cta<kCtaTokens / kCtaThreads>(tokens, tokens_are_64, n, V, bits, digit_bits, passes, groups,
+                                               idx, pieces, tickets, counts, fill, stream, dev);
         if (e != cudaSuccess) return e;
     } else {
         SortArgs s = {};
@@ -574,6 +708,15 @@ cudaError_t launch_embed_bwd(const T *d_out, const void *tokens, int tokens_are_
         s.tile = (n + kMaxTiles - 1) / kMaxTiles;
         s.tile = s.tile <= kTileMin ? kTileMin : (s.tile + 255) / 256 * 256;
         s.tiles = (n + s.tile - 1) / s.tile;
+        // every launch zeroes an equal share
+        const int passes = (key_bits + 7) / 8, launches = 2 * passes + 1;
+        const long long share = (fill.vecs + launches - 1) / launches, end = fill.vecs;
+        long long from = 0;
+        auto next = [&]() {
+            const Fill f = {fill.p + from, end - from < share ? end - from : share};
+            from += f.vecs;
+            return f;
+        };
         for (int pass = 0; pass < passes; ++pass) {
             const int half = pass & 1;
             s.keys_in = pass == 0 ? nullptr : keys + (size_t)(1 - half) * n;
@@ -581,35 +724,39 @@ cudaError_t launch_embed_bwd(const T *d_out, const void *tokens, int tokens_are_
             s.keys_out = keys + (size_t)half * n;
             s.idx_out = idx + (size_t)half * n;
             s.shift = 8 * pass;
-            e = launch_pdl(embed_hist_kernel, dim3(s.tiles), dim3(256), 0, stream, s);
+            Fill f = next();
+            e = launch_pdl(embed_hist_kernel, dim3(s.tiles + fill_ctas(f.vecs, 256, dev)), dim3(256), 0, stream, s, f);
             if (e != cudaSuccess) return e;
-            e = launch_pdl(embed_scatter_kernel, dim3(s.tiles), dim3(256), 0, stream, s);
+            f = next();
+            e = launch_pdl(embed_scatter_kernel, dim3(s.tiles + fill_ctas(f.vecs, 256, dev)), dim3(256), 0, stream, s,
+                           f);
             if (e != cudaSuccess) return e;
         }
-        keys = s.keys_out;
         idx = s.idx_out;
-        e = launch_pdl(embed_plan_kernel, dim3((n + 255) / 256), dim3(256), 0, stream, (const uint32_t *)keys, n, V,
-                       pieces, runs, counts);
+        const Fill f = next();
+        const int ctas = (n + 255) / 256;
+        e = launch_pdl(embed_plan_kernel, dim3(ctas + fill_ctas(f.vecs, 256, dev)), dim3(256), 0, stream,
+                       (const uint32_t *)s.keys_out, n, V, groups, pieces, tickets, counts, ctas, f);
         if (e != cudaSuccess) return e;
     }
     SumArgs a = {};
     a.d_out = d_out;
-    a.keys = keys;
     a.idx = idx;
     a.pieces = pieces;
-    a.runs = runs;
     a.counts = counts;
+    a.tickets = tickets;
     a.partial = reinterpret_cast<float *>(base + l.partial);
     a.acc = d_table_acc;
     a.bf16 = d_table;
     a.scale = scale;
     a.accumulate = accumulate;
     a.n = n;
-    a.V = V;
     a.D = D;
-    e = launch_pdl(embed_sum_kernel<T>, dim3(dev.sm_count * 4), dim3(256), 0, stream, a);
-    if (e != cudaSuccess || n <= kPiece) return e;
-    return launch_pdl(embed_runs_kernel, dim3(dev.sm_count * 2), dim3(256), 0, stream, a);
+    // as many CTAs as the device holds, no more than pieces can be
+    const int most = (n + 7) / 8, want = (4 * dev.sm_count + groups - 1) / groups;
+    const dim3 grid(most < want ? most : want, groups);
+    if (sizeof(T) == 2) return launch_pdl(embed_sum_kernel<uint16_t, uint4, 8>, grid, dim3(256), 0, stream, a);
+    return launch_pdl(embed_sum_kernel<float, Floats8, 4>, grid, dim3(256), 0, stream, a);
 }
 
 template cudaError_t launch_embed_fwd<uint16_t>(const void *, int, const uint16_t *, float, uint16_t *, int, int, int,

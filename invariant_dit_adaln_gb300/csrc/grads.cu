@@ -8,7 +8,9 @@
 // flight per thread); the list travels in the kernel's parameters, so nothing
 // is copied to the device first and the launch can be captured.  A piece's
 // squares are summed in fp32 (16 or 8 terms in each of a thread's four chains,
-// then a fixed butterfly), the pieces' sums in fp64.  An element's thread and chain
+// then a fixed butterfly), the pieces' sums in compensated fp32 pairs (one SM
+// adds fp64 at a few values a cycle: in fp64 the join of 36,864 pieces took 20
+// us), and in fp64 where the range asks for it.  An element's thread and chain
 // depend on its index in the tensor alone, never on an address.
 #include "common.cuh"
 #include "ops.h"
@@ -30,7 +32,7 @@ struct GradList {
     unsigned char bf16[N];
     int count;
     long long base;  // pieces of the launches before this one
-    double *part;
+    float2 *part;  // a piece's sum is x * 2^y, y = 0 but for sums outside fp32's range
     const float *stats;
 };
 
@@ -144,26 +146,45 @@ __device__ __forceinline__ double warp_sum_f64(double v) {
 // 2^-112, which is 2^-32 of the smallest sum kept.
 constexpr float kLeastSum = 0x1p-80f;
 
+// A piece's sum in fp64, read again: rare, so it holds no registers elsewhere.
 template <int E>
-__device__ void piece_norm(const char *base, long long numel, int piece, double *part) {
+__device__ __noinline__ void piece_norm_f64(const char *p, int bytes, const char *base, const char *end,
+                                            float2 *part) {
+    __shared__ double red64[kThreads / 32];
+    double d = 0.0;
+    for (int i = 0; i < kVecs; ++i) d += squares_f64<E>(piece_vec<E>(p, i * kThreads + threadIdx.x, bytes, base, end));
+    d = warp_sum_f64(d);
+    if ((threadIdx.x & 31) == 0) red64[threadIdx.x >> 5] = d;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        d = red64[0];
+        for (int i = 1; i < kThreads / 32; ++i) d += red64[i];
+        int y = 0;
+        if (d > 0.0 && d <= 1.7e308) d = frexp(d, &y);
+        *part = make_float2((float)d, (float)y);
+    }
+}
+
+template <int E>
+__device__ __forceinline__ void piece_norm(const char *base, long long numel, int piece, float2 *part) {
     __shared__ float red[kThreads / 32];
     __shared__ uint32_t red_any[kThreads / 32];
-    __shared__ double red64[kThreads / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const char *p = base + (long long)piece * kGradPieceBytes, *end = base + numel * E;
     const int bytes = (int)min((long long)kGradPieceBytes, (long long)(end - p));
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     uint32_t any = 0;
-    uint4 v[kVecs];
     if (bytes == kGradPieceBytes && ((uintptr_t)p & 15u) == 0) {
+        uint4 v[kVecs];
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i] = *reinterpret_cast<const uint4 *>(p + 16 * (i * kThreads + threadIdx.x));
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) add_squares<E>(acc, any, v[i]);
     } else {
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) v[i] = piece_vec<E>(p, i * kThreads + threadIdx.x, bytes, base, end);
+#pragma unroll 2
+        for (int i = 0; i < kVecs; ++i)
+            add_squares<E>(acc, any, piece_vec<E>(p, i * kThreads + threadIdx.x, bytes, base, end));
     }
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) add_squares<E>(acc, any, v[i]);
     const float s = warp_sum(__fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3])));
     any = __reduce_or_sync(0xFFFFFFFFu, any);
     if (lane == 0) {
@@ -180,29 +201,17 @@ __device__ void piece_norm(const char *base, long long numel, int piece, double 
     }
     // the same for every thread: an overflow (or an infinity or NaN of the
     // input), or squares too small for fp32
-    if (!(sum <= 3.0e38f) || (any != 0 && sum < kLeastSum)) {
-        double d = 0.0;
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) d += squares_f64<E>(v[i]);
-        d = warp_sum_f64(d);
-        if (lane == 0) red64[warp] = d;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            d = red64[0];
-#pragma unroll
-            for (int i = 1; i < kThreads / 32; ++i) d += red64[i];
-            *part = d;
-        }
-    } else if (threadIdx.x == 0) {
-        *part = (double)sum;
-    }
+    if (!(sum <= 3.0e38f) || (any != 0 && sum < kLeastSum))
+        piece_norm_f64<E>(p, bytes, base, end, part);
+    else if (threadIdx.x == 0)
+        *part = make_float2(sum, 0.0f);
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_constant__ GradList<N> a) {
     const int t = find_tensor(a, (int)blockIdx.x);
     const int piece = (int)blockIdx.x - a.first[t];
-    double *part = a.part + a.base + blockIdx.x;
+    float2 *part = a.part + a.base + blockIdx.x;
     pdl_wait();
     pdl_trigger();
     if (a.bf16[t])
@@ -211,29 +220,63 @@ __global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_con
         piece_norm<4>(static_cast<const char *>(a.in[t]), a.numel[t], piece, part);
 }
 
-// The pieces' sums in a fixed order (thread i takes i, i + 1024, ...), the
-// norm and, with clip, the coefficient.
-__global__ void __launch_bounds__(1024) grad_norm_kernel(const double *part, long long n, float *stats, int clip,
-                                                         double max_norm) {
-    __shared__ double red[32];
+// the warp's pairs s + c, joined by a fixed butterfly; the same in every lane
+__device__ __forceinline__ void warp_twosum(float &s, float &c) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float so = __shfl_xor_sync(0xFFFFFFFFu, s, off);
+        c = __fadd_rn(c, __shfl_xor_sync(0xFFFFFFFFu, c, off));
+        float t = lane & off ? so : s;  // one order in both lanes
+        twosum(t, c, lane & off ? s : so);
+        s = t;
+    }
+}
+
+// The pieces' sums in a fixed order (thread i takes i, i + 1024, ..., then a
+// butterfly and the warps), the norm and, with clip, the coefficient.  A sum is
+// a pair s + c with the error of every addition in c.
+__global__ void __launch_bounds__(1024) grad_norm_kernel(const float2 *__restrict__ part, int n, float *stats,
+                                                         int clip, double max_norm) {
+    __shared__ float red_s[32], red_c[32];
+    __shared__ double red64[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    double s = 0.0;
-#pragma unroll 8
-    for (long long i = threadIdx.x; i < n; i += 1024) s += __ldcg(part + i);
-    s = warp_sum_f64(s);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        s = warp_sum_f64(red[threadIdx.x]);
-        if (threadIdx.x == 0) {
-            const double norm = sqrt(s);
-            stats[0] = (float)norm;
-            if (clip) {
-                // an infinite max_norm clips nothing; a NaN norm passes on
-                const double c = isinf(max_norm) && norm == norm ? 1.0 : max_norm / (norm + 1e-6);
-                stats[1] = c >= 1.0 ? 1.0f : (float)c;
-            }
+    float s = 0.0f, c = 0.0f;
+    bool scaled = false;
+    for (int i = threadIdx.x; i < n; i += 8 * 1024) {
+        float2 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = part[min(i + k * 1024, n - 1)];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const bool in = i + k * 1024 < n;
+            scaled |= in && v[k].y != 0.0f;
+            twosum(s, c, in ? v[k].x : 0.0f);
+        }
+    }
+    warp_twosum(s, c);
+    if (lane == 0) red_s[warp] = s, red_c[warp] = c;
+    scaled = __syncthreads_or(scaled);  // also publishes red_s, red_c
+    s = red_s[lane], c = red_c[lane];
+    warp_twosum(s, c);  // every warp: the same for all
+    double total = (double)s + (double)c;
+    if (scaled || !(s <= 3.0e38f)) {
+        total = 0.0;
+        for (int i = threadIdx.x; i < n; i += 1024) total += scalbn((double)part[i].x, (int)part[i].y);
+        total = warp_sum_f64(total);
+        if (lane == 0) red64[warp] = total;
+        __syncthreads();
+        total = warp_sum_f64(red64[lane]);
+    }
+    if (threadIdx.x == 0) {
+        const double norm = sqrt(total);
+        stats[0] = (float)norm;
+        if (clip) {
+            // an infinite max_norm clips nothing; a NaN norm passes on
+            const double f = isinf(max_norm) && norm == norm ? 1.0 : max_norm / (norm + 1e-6);
+            stats[1] = f >= 1.0 ? 1.0f : (float)f;
         }
     }
 }
@@ -325,7 +368,7 @@ int fill(GradList<N> &a, const adaln_tensor *in, const adaln_tensor *out, int fr
 // One launch per N tensors (at most 2^31 - 1 pieces): squares, or scaling when
 // outs is given.
 template <int N>
-cudaError_t run(const adaln_tensor *in, const adaln_tensor *out, int count, double *part, const float *stats,
+cudaError_t run(const adaln_tensor *in, const adaln_tensor *out, int count, float2 *part, const float *stats,
                 cudaStream_t stream) {
     GradList<N> a;
     a.base = 0;
@@ -344,7 +387,7 @@ cudaError_t run(const adaln_tensor *in, const adaln_tensor *out, int count, doub
 }
 
 // The parameter block is copied at every launch, so short lists take a short one.
-cudaError_t run_any(const adaln_tensor *in, const adaln_tensor *out, int count, double *part, const float *stats,
+cudaError_t run_any(const adaln_tensor *in, const adaln_tensor *out, int count, float2 *part, const float *stats,
                     cudaStream_t stream) {
     if (count <= 16) return run<16>(in, out, count, part, stats, stream);
     if (count <= 128) return run<128>(in, out, count, part, stats, stream);
@@ -355,12 +398,12 @@ cudaError_t run_any(const adaln_tensor *in, const adaln_tensor *out, int count, 
 
 cudaError_t launch_grad_norm(const adaln_tensor *grads, int count, float *stats, bool clip, double max_norm, void *ws,
                              cudaStream_t stream, const DeviceInfo &) {
-    double *part = static_cast<double *>(ws);
+    float2 *part = static_cast<float2 *>(ws);
     cudaError_t e = run_any(grads, nullptr, count, part, nullptr, stream);
     if (e != cudaSuccess) return e;
     long long pieces = 0;
     for (int i = 0; i < count; ++i) pieces += grad_pieces(grads[i]);
-    return launch_pdl(grad_norm_kernel, dim3(1), dim3(1024), 0, stream, (const double *)part, pieces, stats,
+    return launch_pdl(grad_norm_kernel, dim3(1), dim3(1024), 0, stream, (const float2 *)part, (int)pieces, stats,
                       clip ? 1 : 0, max_norm);
 }
 

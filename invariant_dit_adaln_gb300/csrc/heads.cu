@@ -21,7 +21,7 @@ namespace adaln {
 
 namespace {
 
-constexpr int kWarps = 8;  // warps of a CTA
+constexpr int kWarps = 4;  // warps of a CTA
 
 struct HeadsArgs {
     const void *x[2], *dy[2];
@@ -88,73 +88,108 @@ __device__ __forceinline__ Raw<float> load8(const float *p, const Slot &s) {
 }
 __device__ __forceinline__ void clear(Raw<uint16_t> &r) { r.a = r.b = make_uint2(0, 0); }
 __device__ __forceinline__ void clear(Raw<float> &r) { r.a = r.b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-__device__ __forceinline__ void values(float (&v)[8], const Raw<uint16_t> &r) {
-    v[0] = bf16lo(r.a.x), v[1] = bf16hi(r.a.x), v[2] = bf16lo(r.a.y), v[3] = bf16hi(r.a.y);
-    v[4] = bf16lo(r.b.x), v[5] = bf16hi(r.b.x), v[6] = bf16lo(r.b.y), v[7] = bf16hi(r.b.y);
-}
-__device__ __forceinline__ void values(float (&v)[8], const Raw<float> &r) {
-    v[0] = r.a.x, v[1] = r.a.y, v[2] = r.a.z, v[3] = r.a.w;
-    v[4] = r.b.x, v[5] = r.b.y, v[6] = r.b.z, v[7] = r.b.w;
-}
+
+// The values as four packed pairs: the first members of the lane's four channel
+// pairs in v[0], v[1], the second members in v[2], v[3].  Both rotations then
+// are the same arithmetic; an interleaved bf16 word is taken apart as it is
+// widened, which costs nothing.
 template <bool INTER>
-__device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8], const Slot &s) {
-    const uint2 a = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    const uint2 b = make_uint2(pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ void values(px2 (&v)[4], const Raw<uint16_t> &r) {
     if (INTER) {
-        *reinterpret_cast<uint4 *>(p + s.lo) = make_uint4(a.x, a.y, b.x, b.y);
+        v[0] = px_make(bf16lo(r.a.x), bf16lo(r.a.y)), v[1] = px_make(bf16lo(r.b.x), bf16lo(r.b.y));
+        v[2] = px_make(bf16hi(r.a.x), bf16hi(r.a.y)), v[3] = px_make(bf16hi(r.b.x), bf16hi(r.b.y));
     } else {
-        *reinterpret_cast<uint2 *>(p + s.lo) = a;
-        *reinterpret_cast<uint2 *>(p + s.hi) = b;
+        v[0] = px_bf16(r.a.x), v[1] = px_bf16(r.a.y), v[2] = px_bf16(r.b.x), v[3] = px_bf16(r.b.y);
     }
 }
 template <bool INTER>
-__device__ __forceinline__ void store8(float *p, const float (&v)[8], const Slot &s) {
-    *reinterpret_cast<float4 *>(p + s.lo) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p + s.hi) = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void values(px2 (&v)[4], const Raw<float> &r) {
+    if (INTER) {
+        v[0] = px_make(r.a.x, r.a.z), v[1] = px_make(r.b.x, r.b.z);
+        v[2] = px_make(r.a.y, r.a.w), v[3] = px_make(r.b.y, r.b.w);
+    } else {
+        v[0] = px_make(r.a.x, r.a.y), v[1] = px_make(r.a.z, r.a.w);
+        v[2] = px_make(r.b.x, r.b.y), v[3] = px_make(r.b.z, r.b.w);
+    }
+}
+// the column of value i (0 .. 7) of such four pairs
+template <bool INTER>
+__device__ __forceinline__ int column(int i, const Slot &s) {
+    if (INTER) return s.lo + 2 * (i & 3) + (i >> 2);
+    return i < 4 ? s.lo + i : s.hi + i - 4;
+}
+template <bool INTER>
+__device__ __forceinline__ void store8(uint16_t *p, const px2 (&v)[4], const Slot &s) {
+    if (INTER) {
+        *reinterpret_cast<uint4 *>(p + s.lo) =
+            make_uint4(pack_bf16x2(px_lo(v[0]), px_lo(v[2])), pack_bf16x2(px_hi(v[0]), px_hi(v[2])),
+                       pack_bf16x2(px_lo(v[1]), px_lo(v[3])), pack_bf16x2(px_hi(v[1]), px_hi(v[3])));
+    } else {
+        *reinterpret_cast<uint2 *>(p + s.lo) = make_uint2(px_to_bf16x2(v[0]), px_to_bf16x2(v[1]));
+        *reinterpret_cast<uint2 *>(p + s.hi) = make_uint2(px_to_bf16x2(v[2]), px_to_bf16x2(v[3]));
+    }
+}
+template <bool INTER>
+__device__ __forceinline__ void store8(float *p, const px2 (&v)[4], const Slot &s) {
+    float4 a, b;
+    if (INTER) {
+        a = make_float4(px_lo(v[0]), px_lo(v[2]), px_hi(v[0]), px_hi(v[2]));
+        b = make_float4(px_lo(v[1]), px_lo(v[3]), px_hi(v[1]), px_hi(v[3]));
+    } else {
+        a = make_float4(px_lo(v[0]), px_hi(v[0]), px_lo(v[1]), px_hi(v[1]));
+        b = make_float4(px_lo(v[2]), px_hi(v[2]), px_lo(v[3]), px_hi(v[3]));
+    }
+    *reinterpret_cast<float4 *>(p + s.lo) = a;
+    *reinterpret_cast<float4 *>(p + s.hi) = b;
+}
+template <bool INTER, typename T>
+__device__ __forceinline__ void store_zero(T *p, const Slot &s) {
+    const px2 zero[4] = {0, 0, 0, 0};
+    store8<INTER>(p, zero, s);
 }
 
 // the lane's weights (1 without weights, and in idle lanes)
 template <typename T, bool INTER>
-__device__ __forceinline__ void load_weights(float (&w)[8], const void *p, const Slot &s) {
+__device__ __forceinline__ void load_weights(px2 (&w)[4], const void *p, const Slot &s) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-    if (s.live && p != nullptr) values(w, load8<INTER>(static_cast<const T *>(p), s));
+    for (int i = 0; i < 4; ++i) w[i] = px_splat(1.0f);
+    if (s.live && p != nullptr) values<INTER>(w, load8<INTER>(static_cast<const T *>(p), s));
 }
 
-// the lane's angles at position p (0 <= p < P)
-__device__ __forceinline__ void load_angles(float (&c)[4], float (&s)[4], const HeadsArgs &a, long long p, int l) {
+// The lane's four angles at position p (0 <= p < P): cosines, sines, -sines.
+struct Angles {
+    px2 c[2], s[2], n[2];
+};
+__device__ __forceinline__ Angles load_angles(const HeadsArgs &a, long long p, int l) {
     const long long at = p * (a.Dr / 2) + 4 * l;
-    const float4 cv = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
-    const float4 sv = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
-    c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
-    s[0] = sv.x, s[1] = sv.y, s[2] = sv.z, s[3] = sv.w;
+    const float4 c = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
+    const float4 s = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
+    return {{px_make(c.x, c.y), px_make(c.z, c.w)},
+            {px_make(s.x, s.y), px_make(s.z, s.w)},
+            {px_make(-s.x, -s.y), px_make(-s.z, -s.w)}};
 }
-
-// Turn the lane's four pairs by its angles (BACK: by the negative angles).
-template <bool INTER, bool BACK>
-__device__ __forceinline__ void turn(float (&v)[8], const float (&c)[4], const float (&s)[4]) {
+// Turn the lane's pairs by its angles (BACK: by the negative angles).
+template <bool BACK>
+__device__ __forceinline__ void turn(px2 (&v)[4], const Angles &t) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + 4;
-        const float a = v[ia], b = v[ib];
-        const float sn = BACK ? -s[i] : s[i];
-        v[ia] = __fmaf_rn(a, c[i], -__fmul_rn(b, sn));
-        v[ib] = __fmaf_rn(a, sn, __fmul_rn(b, c[i]));
+    for (int i = 0; i < 2; ++i) {
+        const px2 a = v[i], b = v[2 + i];
+        v[i] = px_fma(b, BACK ? t.s[i] : t.n[i], px_mul(a, t.c[i]));
+        v[2 + i] = px_fma(a, BACK ? t.n[i] : t.s[i], px_mul(b, t.c[i]));
     }
 }
 
+// sum over the lane's 8 values of a b
+__device__ __forceinline__ float dot8(const px2 (&a)[4], const px2 (&b)[4]) {
+    const px2 t = px_fma(a[3], b[3], px_fma(a[2], b[2], px_fma(a[1], b[1], px_mul(a[0], b[0]))));
+    return __fadd_rn(px_lo(t), px_hi(t));
+}
+// sum over a row's lanes
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
     for (int off = LPR / 2; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
     return v;
-}
-
-__device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
-    float t = __fmul_rn(a[0], b[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) t = __fmaf_rn(a[i], b[i], t);
-    return t;
 }
 
 // --------------------------------------------------------------------------
@@ -176,6 +211,7 @@ __global__ void __launch_bounds__(32 * kWarps) heads_fwd_kernel(const __grid_con
     const long long b = (token >> 32) ? token / a.S : (unsigned)token / (unsigned)a.S;
     const int s = (int)(token - b * a.S);
     const int h0 = chunk * (U * RPW) + sub;
+    const long long xstep = RPW * a.xs[t][2], ostep = RPW * a.os[t][2];
     const T *x = static_cast<const T *>(a.x[t]) + b * a.xs[t][0] + s * a.xs[t][1] + h0 * a.xs[t][2];
     T *o = static_cast<T *>(a.out[t]) + b * a.os[t][0] + s * a.os[t][1] + h0 * a.os[t][2];
     const int rows = slot.live ? (a.H[t] - h0 + RPW - 1) / RPW : 0;  // the lane's heads: u < rows
@@ -187,40 +223,41 @@ __global__ void __launch_bounds__(32 * kWarps) heads_fwd_kernel(const __grid_con
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         clear(raw[u]);
-        if (u < rows) raw[u] = load8<INTER>(x + u * RPW * a.xs[t][2], slot);
+        if (u < rows) raw[u] = load8<INTER>(x + u * xstep, slot);
     }
-    float w[8];
+    px2 w[4];
     load_weights<T, INTER>(w, a.w[t], slot);
     if (p < 0 || p >= a.P) {  // padding
-        const float zero[8] = {};
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (u < rows) store8<INTER>(o + u * RPW * a.os[t][2], zero, slot);
+            if (u < rows) store_zero<INTER>(o + u * ostep, slot);
         return;
     }
-    float c[4], sn[4];
-    if (slot.turned) load_angles(c, sn, a, p, l);
+    Angles ang = {};
+    if (slot.turned) ang = load_angles(a, p, l);
     const float inv = __fdiv_rn(1.0f, (float)a.Dh);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float v[8];
-        values(v, raw[u]);
+        px2 v[4];
+        values<INTER>(v, raw[u]);
         const float ss = row_sum<LPR>(dot8(v, v));
-        const float r = __frsqrt_rn(__fmaf_rn(ss, inv, a.eps));
+        const px2 r = px_splat(rsqrtf(__fmaf_rn(ss, inv, a.eps)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], r), w[i]);
-        if (slot.turned) turn<INTER, false>(v, c, sn);
-        if (u < rows) store8<INTER>(o + u * RPW * a.os[t][2], v, slot);
+        for (int i = 0; i < 4; ++i) v[i] = px_mul(px_mul(v[i], r), w[i]);
+        if (slot.turned) turn<false>(v, ang);
+        if (u < rows) store8<INTER>(o + u * ostep, v, slot);
     }
 }
 
 // --------------------------------------------------------------------------
-// Backward: one CTA per (sample, tile of tokens, q or k).  Its warps take the
-// tile's (token, heads) tasks in turn; each lane keeps the dw sums of its 8
-// channels, joined over the CTA in a fixed order into the tile's partial.
+// Backward: one CTA per (sample, tile of tokens, q or k).  Each warp takes an
+// equal share of the tile's (token, heads) tasks, in order; each lane keeps
+// the dw sums of its 8 channels, joined over the CTA in a fixed order into the
+// tile's partial.
 // --------------------------------------------------------------------------
 template <typename T, int LPR, int U, bool INTER>
-__global__ void __launch_bounds__(32 * kWarps) heads_bwd_kernel(const __grid_constant__ HeadsArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
+heads_bwd_kernel(const __grid_constant__ HeadsArgs a) {
     constexpr int RPW = 32 / LPR;
     __shared__ float red[kWarps][LPR * 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
@@ -235,74 +272,79 @@ __global__ void __launch_bounds__(32 * kWarps) heads_bwd_kernel(const __grid_con
     const T *xb = static_cast<const T *>(a.x[t]) + b * a.xs[t][0];
     const T *gb = static_cast<const T *>(a.dy[t]) + b * a.dys[t][0];
     T *ob = static_cast<T *>(a.out[t]) + b * a.os[t][0];
-    float dw[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dw[i] = 0.0f;
+    // consecutive tasks: most share their token's position and angles
+    const int first = ntask * warp / kWarps, end = ntask * (warp + 1) / kWarps;
+    const long long xstep = RPW * a.xs[t][2], gstep = RPW * a.dys[t][2], ostep = RPW * a.os[t][2];
+    int s = s0 + first / nchunk, chunk = first % nchunk, at = -1;
+    bool real = false;
+    Angles ang = {};
+    px2 dw[4] = {0, 0, 0, 0}, w[4];
     pdl_wait();
     pdl_trigger();
-    float w[8];
     load_weights<T, INTER>(w, a.w[t], slot);
-    for (int task = warp; task < ntask; task += kWarps) {
-        const int s = s0 + task / nchunk;
-        const int h0 = (task % nchunk) * (U * RPW) + sub;
+#pragma unroll 1
+    for (int task = first; task < end; ++task) {
+        const int h0 = chunk * (U * RPW) + sub;
         const int rows = slot.live ? (a.H[t] - h0 + RPW - 1) / RPW : 0;  // the lane's heads: u < rows
         const T *x = xb + s * a.xs[t][1] + h0 * a.xs[t][2];
         const T *dy = gb + s * a.dys[t][1] + h0 * a.dys[t][2];
         T *o = ob + s * a.os[t][1] + h0 * a.os[t][2];
-        const long long p = position(a, b * a.S + s, s);
         Raw<T> rx[U], rg[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             clear(rx[u]);
             clear(rg[u]);
             if (u < rows) {
-                rx[u] = load8<INTER>(x + u * RPW * a.xs[t][2], slot);
-                rg[u] = load8<INTER>(dy + u * RPW * a.dys[t][2], slot);
+                rx[u] = load8<INTER>(x + u * xstep, slot);
+                rg[u] = load8<INTER>(dy + u * gstep, slot);
             }
         }
-        if (p < 0 || p >= a.P) {  // padding
-            const float zero[8] = {};
+        if (s != at) {
+            at = s;
+            const long long p = position(a, b * a.S + s, s);
+            real = p >= 0 && p < a.P;
+            if (slot.turned && real) ang = load_angles(a, p, l);
+        }
+        if (real) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                px2 v[4], g[4], gx[4];
+                values<INTER>(v, rx[u]);
+                values<INTER>(g, rg[u]);
+                if (slot.turned) turn<true>(g, ang);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gx[i] = px_mul(g[i], v[i]);
+                const float ss = row_sum<LPR>(dot8(v, v)), hx = row_sum<LPR>(dot8(gx, w));
+                // lanes without a row: 0, where r would be infinite at eps = 0
+                const float r = u < rows ? rsqrtf(__fmaf_rn(ss, inv, a.eps)) : 0.0f;
+                const px2 rr = px_splat(r), k = px_splat(-__fmul_rn(__fmul_rn(__fmul_rn(r, r), inv), hx));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dw[i] = px_fma(gx[i], rr, dw[i]);
+                    g[i] = px_mul(px_fma(v[i], k, px_mul(g[i], w[i])), rr);
+                }
+                if (u < rows) store8<INTER>(o + u * ostep, g, slot);
+            }
+        } else {  // padding
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (u < rows) store8<INTER>(o + u * RPW * a.os[t][2], zero, slot);
-            continue;
+                if (u < rows) store_zero<INTER>(o + u * ostep, slot);
         }
-        float c[4], sn[4];
-        if (slot.turned) load_angles(c, sn, a, p, l);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float v[8], g[8], h[8];
-            values(v, rx[u]);
-            values(g, rg[u]);
-            if (slot.turned) turn<INTER, true>(g, c, sn);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = __fmul_rn(g[i], w[i]);
-            const float ss = row_sum<LPR>(dot8(v, v));
-            const float hx = row_sum<LPR>(dot8(h, v));
-            // lanes without a row: 0, where r would be infinite at eps = 0
-            const float r = u < rows ? __frsqrt_rn(__fmaf_rn(ss, inv, a.eps)) : 0.0f;
-            const float k = __fmul_rn(__fmul_rn(__fmul_rn(r, r), inv), hx);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dw[i] = __fmaf_rn(g[i], __fmul_rn(v[i], r), dw[i]);
-                h[i] = __fmul_rn(r, __fmaf_rn(-v[i], k, h[i]));
-            }
-            if (u < rows) store8<INTER>(o + u * RPW * a.os[t][2], h, slot);
-        }
+        if (++chunk == nchunk) chunk = 0, ++s;
     }
     if (a.part == nullptr) return;
     // the warp's row groups, then the warps in ascending order
+    float sums[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[2 * i] = px_lo(dw[i]), sums[2 * i + 1] = px_hi(dw[i]);
 #pragma unroll
     for (int off = LPR; off < 32; off <<= 1) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dw[i] = __fadd_rn(dw[i], __shfl_xor_sync(0xFFFFFFFFu, dw[i], off));
+        for (int i = 0; i < 8; ++i) sums[i] = __fadd_rn(sums[i], __shfl_xor_sync(0xFFFFFFFFu, sums[i], off));
     }
     if (sub == 0 && slot.live) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            red[warp][slot.lo + i] = dw[i];
-            red[warp][slot.hi + i] = dw[4 + i];
-        }
+        for (int i = 0; i < 8; ++i) red[warp][column<INTER>(i, slot)] = sums[i];
     }
     __syncthreads();
     float *part = a.part + ((b * a.tiles + blockIdx.x) * 2 + t) * a.Dh;
@@ -315,13 +357,16 @@ __global__ void __launch_bounds__(32 * kWarps) heads_bwd_kernel(const __grid_con
 }
 
 // --------------------------------------------------------------------------
-// dw of a sample: its tiles' partials.  32 columns and 32 groups of tiles a
-// CTA: group g adds the tiles g, g + 32, ... in order, then the groups are
-// added in order.  Fixed by the number of tiles, that is by S, H, Dh.
-//   DIRECT: a CTA takes the samples one after the other and adds them onto the
-//   accumulator itself; otherwise blockIdx.z is the sample and its sum goes to
-//   sums [B][2][Dh].
+// dw of a sample: its tiles' partials.  A CTA takes 8 columns (one 32-byte
+// sector of a partial) and 128 groups of tiles: group g adds the tiles g, g +
+// 128, ... in order, then the groups are joined by a fixed tree.  The order
+// is fixed by the number of tiles, that is by S, H, Dh.
+//   DIRECT: a CTA takes all samples (at most kDirectSamples) and adds them onto
+//   the accumulator itself, which saves a launch; otherwise blockIdx.z is the
+//   sample and its sum goes to sums [B][2][Dh].
 // --------------------------------------------------------------------------
+constexpr int kDirectSamples = 6;
+
 struct FoldArgs {
     const float *part;
     float *sums;
@@ -331,37 +376,65 @@ struct FoldArgs {
 
 template <bool DIRECT>
 __global__ void __launch_bounds__(1024) heads_fold_kernel(const FoldArgs a) {
-    __shared__ float red[32][33];
-    const int col = threadIdx.x & 31, grp = threadIdx.x >> 5;
-    const int t = blockIdx.y, d = blockIdx.x * 32 + col;
+    constexpr int NB = DIRECT ? kDirectSamples : 1;
+    __shared__ float red[NB][32][8];
+    __shared__ float sums[NB][8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane & 7, grp = threadIdx.x >> 3;
+    const int t = blockIdx.y, d = blockIdx.x * 8 + col;
+    const long long b0 = DIRECT ? 0 : blockIdx.z;
+    const int nb = DIRECT ? a.B : 1;
+    float *dw = a.dw[t];
     pdl_wait();
     pdl_trigger();
-    float *dw = a.dw[t];
     if (dw == nullptr) return;
-    float acc = 0.0f;
-    if (DIRECT && grp == 0 && d < a.Dh && a.accumulate) acc = dw[d];
-    const long long b0 = DIRECT ? 0 : blockIdx.z, b1 = DIRECT ? a.B : b0 + 1;
-    for (long long b = b0; b < b1; ++b) {
-        const float *p = a.part + (b * a.tiles * 2 + t) * a.Dh + d;
-        float sum = 0.0f;
-        if (d < a.Dh) {
-#pragma unroll 8
-            for (int i = grp; i < a.tiles; i += 32) sum = __fadd_rn(sum, __ldcg(p + (long long)i * 2 * a.Dh));
-        }
-        red[grp][col] = sum;
-        __syncthreads();
-        if (grp == 0 && d < a.Dh) {
-            sum = red[0][col];
+    const long long sample = (long long)a.tiles * 2 * a.Dh;
+    const float *p = a.part + b0 * sample + t * a.Dh + d;
+    float sum[NB];
 #pragma unroll
-            for (int i = 1; i < 32; ++i) sum = __fadd_rn(sum, red[i][col]);
-            if (DIRECT)
-                acc = __fadd_rn(acc, sum);
-            else
-                a.sums[(b * 2 + t) * a.Dh + d] = sum;
+    for (int k = 0; k < NB; ++k) sum[k] = 0.0f;
+    for (int i0 = grp; i0 < a.tiles; i0 += 4 * 128) {
+        float v[NB][4];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + j * 128;
+                v[k][j] = 0.0f;  // +0 behind the end: adding it changes no sum begun from +0
+                if (k < nb && i < a.tiles) v[k][j] = __ldcg(p + k * sample + (long long)i * 2 * a.Dh);
+            }
         }
-        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int k = 0; k < NB; ++k) sum[k] = __fadd_rn(sum[k], v[k][j]);
+        }
     }
-    if (DIRECT && grp == 0 && d < a.Dh) dw[d] = acc;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+        sum[k] = __fadd_rn(sum[k], __shfl_xor_sync(0xFFFFFFFFu, sum[k], 8));
+        sum[k] = __fadd_rn(sum[k], __shfl_xor_sync(0xFFFFFFFFu, sum[k], 16));
+        if (lane < 8) red[k][warp][col] = sum[k];
+    }
+    __syncthreads();
+    if (warp < NB) {  // warp k joins the 32 warps' sums of sample k, 8 to a quarter
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v = __fadd_rn(v, red[warp][(lane >> 3) * 8 + i][col]);
+        v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+        v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+        if (lane < 8) sums[warp][col] = v;
+    }
+    if (DIRECT) __syncthreads();
+    if (threadIdx.x >= 8) return;
+    if (DIRECT) {
+        float acc = a.accumulate ? dw[d] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+            if (k < nb) acc = __fadd_rn(acc, sums[k][col]);
+        dw[d] = acc;
+    } else {
+        a.sums[(b0 * 2 + t) * a.Dh + d] = sums[0][col];
+    }
 }
 
 // the samples' sums onto the accumulators, in ascending order
@@ -475,9 +548,6 @@ int heads_tile_tokens(int Hq, int Hk, int Dh) {
     return chunks >= 24 ? 1 : 24 / chunks;
 }
 
-// Samples up to this many are added by the fold itself.
-constexpr int kDirectSamples = 4;
-
 size_t heads_bwd_ws_floats(int B, int S, int Hq, int Hk, int Dh) {
     const int tile = heads_tile_tokens(Hq, Hk, Dh);
     const size_t tiles = ((size_t)S + tile - 1) / tile;
@@ -514,7 +584,7 @@ cudaError_t launch_heads_bwd(const HeadsCall &c, cudaStream_t stream, const Devi
     const int tile = heads_tile_tokens(c.H[0], c.H[1], c.Dh);
     f.tiles = (c.S + tile - 1) / tile;
     f.sums = c.ws + (size_t)c.B * f.tiles * 2 * c.Dh;
-    const unsigned cols = (c.Dh + 31) / 32;
+    const unsigned cols = c.Dh / 8;
     if (c.B <= kDirectSamples) return launch_pdl(heads_fold_kernel<true>, dim3(cols, 2), dim3(1024), 0, stream, f);
     e = launch_pdl(heads_fold_kernel<false>, dim3(cols, 2, c.B), dim3(1024), 0, stream, f);
     if (e != cudaSuccess) return e;

@@ -474,7 +474,7 @@ size_t adaln_grad_norm_workspace_bytes(const adaln_tensor *grads, int count) {
     if (check_list(grads, count) != ADALN_OK) return 0;
     size_t pieces = 0;
     for (int i = 0; i < count; ++i) pieces += (size_t)grad_pieces(grads[i]);
-    return round256(pieces * sizeof(double));
+    return round256(pieces * sizeof(float2));
 }
 
 adaln_status adaln_grad_norm(const adaln_tensor *grads, int count, float *norm, void *workspace,

@@ -111,29 +111,24 @@ def embed_bwd(d_out, tokens, V, scale):
 
 def embed_bwd_order(d_out, tokens, V, scale):
     """The gradient by the documented order, in fp32 rounded step by step:
-    pieces of 32 occurrences from +0; with several pieces, eight contiguous
-    shares of them each from +0, then the shares in order."""
+    pieces of 32 occurrences from +0, and nodes of 32 children from +0 above
+    them."""
     t = tokens.cpu().long().reshape(-1)
     g = d_out.detach().cpu().float().reshape(t.numel(), -1)
     out = torch.zeros((V, g.shape[1]))
     for v in t[(t >= 0) & (t < V)].unique().tolist():
-        rows = g[t == v]
-
-        def chain(terms):
-            s = torch.zeros(g.shape[1])
-            for x in terms:
-                s = s + x
-            return s
-
-        sums = [chain(rows[i:i + 32]) for i in range(0, len(rows), 32)]
-        if len(sums) > 1:
-            per = (len(sums) + 7) // 8
-            shares = [chain(sums[per * w:per * (w + 1)]) for w in range(8)]
-            total = shares[0]
-            for x in shares[1:]:
-                total = total + x
-        else:
-            total = sums[0]
+        sums = list(g[t == v])
+        while True:
+            level = []
+            for i in range(0, len(sums), 32):
+                s = torch.zeros(g.shape[1])
+                for x in sums[i:i + 32]:
+                    s = s + x
+                level.append(s)
+            sums = level
+            if len(sums) == 1:
+                break
+        total = sums[0]
         out[v] = total * torch.tensor(scale, dtype=torch.float32)
     return out
 

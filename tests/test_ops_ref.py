@@ -56,5 +56,5 @@ def test_embed_order_is_the_sum():
     want, size, count = ops_ref.embed_bwd(d, tokens, 7, 0.5)
     got = ops_ref.embed_bwd_order(d, tokens, 7, 0.5)
     assert count.tolist() == [33, 0, 0, 301, 0, 1, 0]
-    # 32 in a piece, 2 in a share, 8 shares, the scale
+    # 32 in a piece, 10 pieces, the scale
     ops_ref.check(got, want, 43 * ops_ref.U * size, "order")
