@@ -12,9 +12,8 @@ no fallback path.  If the library is missing, every call raises.
 
 from __future__ import annotations
 
-import array
 import ctypes
-import functools
+import importlib.util
 import os
 import re
 
@@ -26,7 +25,6 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
-_ref = ctypes.byref
 
 _SIGNATURES = {
     "adaln_status_string": (ctypes.c_char_p, [_I]),
@@ -472,386 +470,158 @@ def adaln_proj_wgrad_rows(d_emb, u, n0, n1, dW_acc=None, db_acc=None, dW=None, d
 # include/adaln_ops.h: norm of queries and keys with rotation, embedding,
 # gradient norm
 #
-# A call given a `stream` runs as a whole on it: the copies and allocations made
-# here belong to that stream too.  Tensors must be on the current device.
+# These calls are marshalled by a compiled module (csrc/marshal.cpp): for small
+# sizes the host's time for a call is the call's time.  It does what this layer
+# does above: checks types, devices and shapes (tensors must be on the current
+# device), allocates missing outputs and workspaces, copies an input whose
+# layout the C ABI refuses, and raises on a non-zero status.  A call given a
+# `stream` runs as a whole on it: the copies and allocations belong to that
+# stream too.
 # ---------------------------------------------------------------------------
 
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", _P), ("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+_BOUND = ("adaln_qk_norm_rope_fwd", "adaln_f32_qk_norm_rope_fwd", "adaln_qk_norm_rope_bwd_workspace_bytes",
+          "adaln_qk_norm_rope_bwd", "adaln_f32_qk_norm_rope_bwd", "adaln_embed_fwd", "adaln_f32_embed_fwd",
+          "adaln_embed_bwd_workspace_bytes", "adaln_embed_bwd", "adaln_f32_embed_bwd",
+          "adaln_grad_norm_workspace_bytes", "adaln_grad_norm", "adaln_grad_clip")
+_marshal = None
 
 
-def _on_stream(call):
-    """Let the call's `stream` be the current stream while it runs."""
-    @functools.wraps(call)
-    def wrapped(*args, stream=None, **kwargs):
-        if stream is None:
-            return call(*args, **kwargs)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(stream):
-            return call(*args, **kwargs)
-    return wrapped
+def _raise_status(name, status):
+    raise AdaLNError(name, status)
 
 
-# The marshalling below is written for few Python operations: for small sizes
-# the host's time for a call is the call's time.
-
-_INDEX = {torch.int32: 0, torch.int64: 1}  # also: is it 64 bits wide
-_STEP = {torch.bfloat16: 7, torch.float32: 3}  # 16 bytes in elements, as a mask
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _device():
-    """The current device; without CUDA -2, which is no tensor's device, so that
-    the checks refuse the first tensor."""
-    try:
-        return torch.cuda.current_device()
-    except (AssertionError, RuntimeError):
-        return -2
+def _native():
+    """The marshalling module, bound to the loaded library.  Raises if missing."""
+    global _marshal
+    if _marshal is None:
+        L = load()
+        path = _build.marshal_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it first (invariant_dit_adaln_gb300.build.build())")
+        spec = importlib.util.spec_from_file_location("adaln_marshal", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*[ctypes.cast(getattr(L, n), _P).value for n in _BOUND], _raise_status)
+        _marshal = module
+    return _marshal
 
 
-def _refuse(t, dtypes, shape, name, dev):
-    """Raise for what is wrong with a tensor, if anything is."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name}: expected a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: on {t.device}, but the current device is {dev}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+def _on(stream):
+    """The context in which a torch stream, or a raw one, is the current stream."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
-def _good(t, dtypes, shape, dev):
-    return isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev and t.shape == shape
-
-
-def _flat(t, dtypes, shape, name, dev):
-    """A dense 16-byte aligned input: t, or a copy of it."""
-    if not _good(t, dtypes, shape, dev):
-        _refuse(t, dtypes, shape, name, dev)
-    if not t.is_contiguous():
-        return t.contiguous()
-    return t.clone() if t.data_ptr() & 15 else t
-
-
-def _result(t, dtype, shape, name, dev):
-    """A dense 16-byte aligned output: t, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    if not _good(t, (dtype,), shape, dev):
-        _refuse(t, (dtype,), shape, name, dev)
-    if not t.is_contiguous() or t.data_ptr() & 15:
-        raise ValueError(f"{name}: must be contiguous and 16-byte aligned")
-    return t
-
-
-def _scratch(ws, need, dev):
-    """A workspace of `need` bytes: ws, or a new one."""
-    if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("workspace: expected a contiguous CUDA tensor")
-    if ws.get_device() != dev:
-        raise ValueError(f"workspace: on {ws.device}, but the current device is {dev}")
-    if ws.numel() * ws.element_size() < need:
-        raise ValueError(f"workspace: {need} bytes needed")
-    return ws
-
-
-def _head_in(t, dtype, shape, name, dev, copy=True):
-    """(tensor, _Heads) of head rows [B, S, H, Dh]: t itself when its channels
-    are dense and its rows 16-byte aligned, else a copy (an input) or a refusal."""
-    if not _good(t, (dtype,), shape, dev):
-        _refuse(t, (dtype,), shape, name, dev)
-    b, s, h, c = t.stride()
-    p = t.data_ptr()
-    if (c != 1 or p & 15 or (b | s | h) & _STEP[dtype]) and t.numel():
-        used = (b if shape[0] > 1 else 0) | (s if shape[1] > 1 else 0) | (h if shape[2] > 1 else 0)
-        if c != 1 or p & 15 or used & _STEP[dtype]:
-            if not copy:
-                raise ValueError(f"{name}: channels must be dense and rows 16-byte aligned")
-            t = t.clone(memory_format=torch.contiguous_format)
-            b, s, h, _ = t.stride()
-            p = t.data_ptr()
-    return t, _Heads(p, b, s, h)
-
-
-def _head_out(t, dtype, shape, name, dev):
-    if t is not None:
-        return _head_in(t, dtype, shape, name, dev, False)
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    h = shape[3]
-    s = h * shape[2]
-    return t, _Heads(t.data_ptr(), s * shape[1], s, h)
-
-
-def _head_common(q, k, wq, wk, cos, sin, pos, dtype, dev):
-    """The shapes of q and k, the sizes, and what forward and backward share
-    (the tensors behind the pointers, to be kept for the call)."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q: expected a tensor [B, S, H, Dh]")
-    qshape = q.shape
-    B, S, Hq, Dh = qshape
-    Hk = 0
-    if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != 4:
-            raise ValueError("k: expected a tensor [B, S, H, Dh]")
-        Hk = k.shape[2]
-        if wk is not None:
-            wk = _flat(wk, (dtype,), (Dh,), "wk", dev)
-    else:
-        wk = None
-    if wq is not None:
-        wq = _flat(wq, (dtype,), (Dh,), "wq", dev)
-    P, Dr = (1 << 31) - 1, 0
-    if cos is not None and sin is not None:
-        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
-            raise ValueError("cos: expected a tensor [P, Dr / 2]")
-        P, Dr = cos.shape
-        cos = _flat(cos, (torch.float32,), (P, Dr), "cos", dev)
-        sin = _flat(sin, (torch.float32,), (P, Dr), "sin", dev)
-        Dr *= 2
-    elif cos is not None or sin is not None:
-        raise ValueError("cos, sin: give both or neither")
-    is64 = 0
-    if pos is not None:
-        pos = _flat(pos, _INDEX, (B, S), "pos", dev)
-        is64 = _INDEX[pos.dtype]
-    return qshape, (B, S, Hk, Dh), (B, S, Hq, Hk, Dh, Dr, P), (wq, wk, cos, sin, pos), is64
-
-
-def _qk_fwd(call, name, dtype, q, k, wq, wk, cos, sin, pos, q_out, k_out, eps, interleaved):
-    dev = _device()
-    qshape, kshape, sizes, flat, is64 = _head_common(q, k, wq, wk, cos, sin, pos, dtype, dev)
-    q, qs = _head_in(q, dtype, qshape, "q", dev)
-    q_out, qo = _head_out(q_out, dtype, qshape, "q_out", dev)
-    ks = ko = None
-    if k is not None:
-        k, ks = _head_in(k, dtype, kshape, "k", dev)
-        k_out, ko = _head_out(k_out, dtype, kshape, "k_out", dev)
-        ks, ko = _ref(ks), _ref(ko)
-    st = call(_ref(qs), ks, *[None if t is None else t.data_ptr() for t in flat], is64, _ref(qo), ko, *sizes,
-              1 if interleaved else 0, eps, _raw_stream(dev))
-    if st:
-        raise AdaLNError(name, st)
-    return q_out, k_out
-
-
-@_on_stream
-def adaln_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos=None, q_out=None, k_out=None, eps=1e-6, interleaved=True):
+def adaln_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos=None, q_out=None, k_out=None, eps=1e-6, interleaved=True,
+                           stream=None):
     """RMS norm of the head rows q [B,S,Hq,Dh] and k [B,S,Hk,Dh] (bf16, any
-    strides with dense channels; k may be None, wk is not used then) with weights wq, wk [Dh] (or
-    None), then the rotation of their first Dr channels by the rows pos [B,S]
-    (default: 0 .. S-1) of cos, sin [P,Dr/2] fp32.  A row whose position is
-    outside [0, P) is padding: zero.  q_out may be q and k_out k (in place), or
-    any rows of the same shape.  Returns (q_out, k_out)."""
-    return _qk_fwd(load().adaln_qk_norm_rope_fwd, "adaln_qk_norm_rope_fwd", torch.bfloat16, q, k, wq, wk,
-                   cos, sin, pos, q_out, k_out, eps, interleaved)
+    strides with dense channels; k may be None, wk is not used then) with
+    weights wq, wk [Dh] (or None), then the rotation of their first Dr channels
+    by the rows pos [B,S] (default: 0 .. S-1) of cos, sin [P,Dr/2] fp32.  A row
+    whose position is outside [0, P) is padding: zero.  q_out may be q and k_out
+    k (in place), or any rows of the same shape.  Returns (q_out, k_out)."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos, q_out, k_out, eps, interleaved)
+    return (_marshal or _native()).qk_fwd(False, q, k, wq, wk, cos, sin, pos, q_out, k_out, eps, interleaved)
 
 
-@_on_stream
-def adaln_f32_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos=None, q_out=None, k_out=None, eps=1e-6, interleaved=True):
+def adaln_f32_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos=None, q_out=None, k_out=None, eps=1e-6, interleaved=True,
+                               stream=None):
     """adaln_qk_norm_rope_fwd on fp32 head rows and weights."""
-    return _qk_fwd(load().adaln_f32_qk_norm_rope_fwd, "adaln_f32_qk_norm_rope_fwd", torch.float32, q, k, wq,
-                   wk, cos, sin, pos, q_out, k_out, eps, interleaved)
+    if stream is not None:
+        with _on(stream):
+            return adaln_f32_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos, q_out, k_out, eps, interleaved)
+    return (_marshal or _native()).qk_fwd(True, q, k, wq, wk, cos, sin, pos, q_out, k_out, eps, interleaved)
 
 
 def adaln_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hk, Dh):
     return load().adaln_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hk, Dh)
 
 
-def _qk_bwd(L, call, name, dtype, d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos, d_q, d_k, dwq_acc, dwk_acc, accumulate,
-            want_w, workspace, eps, interleaved):
-    dev = _device()
-    qshape, kshape, sizes, flat, is64 = _head_common(q, k, wq, wk, cos, sin, pos, dtype, dev)
-    q, qs = _head_in(q, dtype, qshape, "q", dev)
-    d_q_out, gq = _head_in(d_q_out, dtype, qshape, "d_q_out", dev)
-    d_q, oq = _head_out(d_q, dtype, qshape, "d_q", dev)
-    ks = gk = ok = None
-    if k is not None:
-        k, ks = _head_in(k, dtype, kshape, "k", dev)
-        d_k_out, gk = _head_in(d_k_out, dtype, kshape, "d_k_out", dev)
-        d_k, ok = _head_out(d_k, dtype, kshape, "d_k", dev)
-        ks, gk, ok = _ref(ks), _ref(gk), _ref(ok)
-    ws, nws, pq, pk = None, 0, None, None
-    if want_w:
-        if accumulate and (dwq_acc is None or (k is not None and dwk_acc is None)):
-            raise ValueError("accumulate: dwq_acc and dwk_acc must be given")
-        B, S, Hq, Hk, Dh = sizes[:5]
-        dwq_acc = _result(dwq_acc, torch.float32, (Dh,), "dwq_acc", dev)
-        pq = dwq_acc.data_ptr()
-        if Hk:
-            dwk_acc = _result(dwk_acc, torch.float32, (Dh,), "dwk_acc", dev)
-            pk = dwk_acc.data_ptr()
-        nws = L.adaln_qk_norm_rope_bwd_workspace_bytes(B, S, Hq, Hk, Dh)
-        ws = _scratch(workspace, nws, dev)
-    st = call(_ref(gq), gk, _ref(qs), ks, *[None if t is None else t.data_ptr() for t in flat], is64, _ref(oq), ok, pq,
-              pk, 1 if accumulate else 0, _ptr(ws), nws, *sizes, 1 if interleaved else 0, eps, _raw_stream(dev))
-    if st:
-        raise AdaLNError(name, st)
-    return d_q, d_k, dwq_acc, dwk_acc
-
-
-@_on_stream
 def adaln_qk_norm_rope_bwd(d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos=None, d_q=None, d_k=None, dwq_acc=None,
-                           dwk_acc=None, accumulate=False, want_w=True, workspace=None, eps=1e-6, interleaved=True):
+                           dwk_acc=None, accumulate=False, want_w=True, workspace=None, eps=1e-6, interleaved=True,
+                           stream=None):
     """Backward of adaln_qk_norm_rope_fwd from its inputs: (d_q, d_k, dwq_acc,
     dwk_acc).  d_q may be d_q_out and d_k d_k_out (in place).  The weight
     gradients are fp32 [Dh], allocated here when not given and want_w; accumulate
     adds to given ones."""
-    L = load()
-    return _qk_bwd(L, L.adaln_qk_norm_rope_bwd, "adaln_qk_norm_rope_bwd", torch.bfloat16, d_q_out, d_k_out, q, k, wq,
-                   wk, cos, sin, pos, d_q, d_k, dwq_acc, dwk_acc, accumulate, want_w, workspace, eps, interleaved)
+    if stream is not None:
+        with _on(stream):
+            return adaln_qk_norm_rope_bwd(d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos, d_q, d_k, dwq_acc, dwk_acc,
+                                          accumulate, want_w, workspace, eps, interleaved)
+    return (_marshal or _native()).qk_bwd(False, d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos, d_q, d_k, dwq_acc,
+                                          dwk_acc, accumulate, want_w, workspace, eps, interleaved)
 
 
-@_on_stream
 def adaln_f32_qk_norm_rope_bwd(d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos=None, d_q=None, d_k=None, dwq_acc=None,
                                dwk_acc=None, accumulate=False, want_w=True, workspace=None, eps=1e-6,
-                               interleaved=True):
+                               interleaved=True, stream=None):
     """adaln_qk_norm_rope_bwd on fp32 head rows, gradients and weights."""
-    L = load()
-    return _qk_bwd(L, L.adaln_f32_qk_norm_rope_bwd, "adaln_f32_qk_norm_rope_bwd", torch.float32, d_q_out, d_k_out, q,
-                   k, wq, wk, cos, sin, pos, d_q, d_k, dwq_acc, dwk_acc, accumulate, want_w, workspace, eps,
-                   interleaved)
+    if stream is not None:
+        with _on(stream):
+            return adaln_f32_qk_norm_rope_bwd(d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos, d_q, d_k, dwq_acc,
+                                              dwk_acc, accumulate, want_w, workspace, eps, interleaved)
+    return (_marshal or _native()).qk_bwd(True, d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos, d_q, d_k, dwq_acc,
+                                          dwk_acc, accumulate, want_w, workspace, eps, interleaved)
 
 
-def _embed_fwd(call, name, dtype, tokens, table, scale, out):
-    dev = _device()
-    if not _good(tokens, _INDEX, getattr(tokens, "shape", None), dev):
-        _refuse(tokens, _INDEX, None, "tokens", dev)
-    shape = tokens.shape
-    tokens = _flat(tokens, _INDEX, shape, "tokens", dev)
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table: expected a tensor [V, D]")
-    V, D = table.shape
-    table = _flat(table, (dtype,), (V, D), "table", dev)
-    out = _result(out, dtype, (*shape, D), "out", dev)
-    st = call(tokens.data_ptr(), _INDEX[tokens.dtype], table.data_ptr(), scale, out.data_ptr(), tokens.numel(), V, D,
-              _raw_stream(dev))
-    if st:
-        raise AdaLNError(name, st)
-    return out
-
-
-@_on_stream
-def adaln_embed_fwd(tokens, table, scale=1.0, out=None):
+def adaln_embed_fwd(tokens, table, scale=1.0, out=None, stream=None):
     """out[..., :] = bf16(scale * table[tokens, :]); tokens int32 or int64 of
     any shape, table [V,D] bf16.  A token outside [0, V) gives a zero row."""
-    return _embed_fwd(load().adaln_embed_fwd, "adaln_embed_fwd", torch.bfloat16, tokens, table, scale, out)
+    if stream is not None:
+        with _on(stream):
+            return adaln_embed_fwd(tokens, table, scale, out)
+    return (_marshal or _native()).embed_fwd(False, tokens, table, scale, out)
 
 
-@_on_stream
-def adaln_f32_embed_fwd(tokens, table, scale=1.0, out=None):
+def adaln_f32_embed_fwd(tokens, table, scale=1.0, out=None, stream=None):
     """adaln_embed_fwd on an fp32 table."""
-    return _embed_fwd(load().adaln_f32_embed_fwd, "adaln_f32_embed_fwd", torch.float32, tokens, table, scale, out)
+    if stream is not None:
+        with _on(stream):
+            return adaln_f32_embed_fwd(tokens, table, scale, out)
+    return (_marshal or _native()).embed_fwd(True, tokens, table, scale, out)
 
 
 def adaln_embed_bwd_workspace_bytes(n, V, D):
     return load().adaln_embed_bwd_workspace_bytes(n, V, D)
 
 
-def _embed_args(L, d_out, tokens, dtype, workspace, V, dev):
-    if not _good(tokens, _INDEX, getattr(tokens, "shape", None), dev):
-        _refuse(tokens, _INDEX, None, "tokens", dev)
-    shape = tokens.shape
-    tokens = _flat(tokens, _INDEX, shape, "tokens", dev)
-    if not isinstance(d_out, torch.Tensor) or d_out.dim() < 1:
-        raise ValueError("d_out: expected a tensor [..., D]")
-    D = d_out.shape[-1]
-    d_out = _flat(d_out, (dtype,), (*shape, D), "d_out", dev)
-    n = tokens.numel()
-    need = L.adaln_embed_bwd_workspace_bytes(n, V, D)
-    return tokens, d_out, n, D, _scratch(workspace, need, dev), need
-
-
-@_on_stream
-def adaln_embed_bwd(d_out, tokens, V, scale=1.0, d_table_acc=None, d_table=None, accumulate=False, workspace=None):
+def adaln_embed_bwd(d_out, tokens, V, scale=1.0, d_table_acc=None, d_table=None, accumulate=False, workspace=None,
+                    stream=None):
     """Gradient of a table [V,D] from d_out [..., D] bf16: scale times the sum of
     d_out over each token's occurrences, into d_table_acc (fp32, the default; +=
     with accumulate) or d_table (bf16).  Returns the one written."""
-    L, dev = load(), _device()
-    tokens, d_out, n, D, ws, need = _embed_args(L, d_out, tokens, torch.bfloat16, workspace, V, dev)
-    if d_table is None:
-        if accumulate and d_table_acc is None:
-            raise ValueError("accumulate: d_table_acc must be given")
-        d_table_acc = _result(d_table_acc, torch.float32, (V, D), "d_table_acc", dev)
-    else:
-        d_table = _result(d_table, torch.bfloat16, (V, D), "d_table", dev)
-    st = L.adaln_embed_bwd(d_out.data_ptr(), tokens.data_ptr(), _INDEX[tokens.dtype], scale, _ptr(d_table_acc),
-                           _ptr(d_table), 1 if accumulate else 0, _ptr(ws), need, n, V, D, _raw_stream(dev))
-    if st:
-        raise AdaLNError("adaln_embed_bwd", st)
-    return d_table_acc if d_table is None else d_table
+    if stream is not None:
+        with _on(stream):
+            return adaln_embed_bwd(d_out, tokens, V, scale, d_table_acc, d_table, accumulate, workspace)
+    return (_marshal or _native()).embed_bwd(False, d_out, tokens, V, scale, d_table_acc, d_table, accumulate,
+                                             workspace)
 
 
-@_on_stream
-def adaln_f32_embed_bwd(d_out, tokens, V, scale=1.0, d_table_acc=None, accumulate=False, workspace=None):
+def adaln_f32_embed_bwd(d_out, tokens, V, scale=1.0, d_table_acc=None, accumulate=False, workspace=None, stream=None):
     """adaln_embed_bwd on an fp32 d_out.  Returns d_table_acc."""
-    L, dev = load(), _device()
-    tokens, d_out, n, D, ws, need = _embed_args(L, d_out, tokens, torch.float32, workspace, V, dev)
-    if accumulate and d_table_acc is None:
-        raise ValueError("accumulate: d_table_acc must be given")
-    d_table_acc = _result(d_table_acc, torch.float32, (V, D), "d_table_acc", dev)
-    st = L.adaln_f32_embed_bwd(d_out.data_ptr(), tokens.data_ptr(), _INDEX[tokens.dtype], scale,
-                               d_table_acc.data_ptr(), 1 if accumulate else 0, _ptr(ws), need, n, V, D,
-                               _raw_stream(dev))
-    if st:
-        raise AdaLNError("adaln_f32_embed_bwd", st)
-    return d_table_acc
+    if stream is not None:
+        with _on(stream):
+            return adaln_f32_embed_bwd(d_out, tokens, V, scale, d_table_acc, accumulate, workspace)
+    return (_marshal or _native()).embed_bwd(True, d_out, tokens, V, scale, d_table_acc, None, accumulate, workspace)
 
 
-_GRAD_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+def adaln_grad_norm(grads, norm=None, workspace=None, stream=None):
+    """The global norm sqrt(sum x^2) over a list of contiguous fp32 and bf16
+    tensors, as a device tensor [1] fp32 (nothing is synchronized)."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_grad_norm(grads, norm, workspace)
+    return (_marshal or _native()).grad_norm(grads, norm, workspace)
 
 
-def _tensor_list(tensors, name, dev):
-    """A host array of adaln_tensor: three 64-bit words a tensor."""
-    words = []
-    for t in tensors:
-        if not isinstance(t, torch.Tensor) or t.dtype not in _GRAD_DTYPES or t.get_device() != dev:
-            _refuse(t, _GRAD_DTYPES, None, name, dev)
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: tensors must be contiguous")
-        words += (t.data_ptr(), t.numel(), _GRAD_DTYPES[t.dtype])
-    return array.array("q", words)
-
-
-@_on_stream
-def adaln_grad_norm(grads, norm=None, workspace=None):
-    """The global norm sqrt(sum x^2) over a list of fp32 and bf16 tensors, as a
-    device tensor [1] fp32 (nothing is synchronized)."""
-    L, dev, n = load(), _device(), len(grads)
-    arr = _tensor_list(grads, "grads", dev)
-    at = arr.buffer_info()[0]
-    norm = _result(norm, torch.float32, (1,), "norm", dev)
-    need = L.adaln_grad_norm_workspace_bytes(at, n)
-    ws = _scratch(workspace, need, dev)
-    st = L.adaln_grad_norm(at, n, norm.data_ptr(), _ptr(ws), need, _raw_stream(dev))
-    if st:
-        raise AdaLNError("adaln_grad_norm", st)
-    return norm
-
-
-@_on_stream
-def adaln_grad_clip(grads, max_norm, outs=None, stats=None, workspace=None):
+def adaln_grad_clip(grads, max_norm, outs=None, stats=None, workspace=None, stream=None):
     """outs[i] = coef * grads[i] with coef = min(1, max_norm / (norm + 1e-6)) of
     the list's global norm; outs=grads scales in place, None allocates.  Returns
     (outs, stats), stats = [norm, coef] on the device."""
-    L, dev, n = load(), _device(), len(grads)
-    arr = _tensor_list(grads, "grads", dev)
-    at = to = arr.buffer_info()[0]
-    if outs is None:
-        outs = [torch.empty_like(g) for g in grads]
-    if outs is not grads:
-        if len(outs) != n:
-            raise ValueError("outs: expected as many tensors as grads")
-        arr_out = _tensor_list(outs, "outs", dev)
-        to = arr_out.buffer_info()[0]
-    stats = _result(stats, torch.float32, (2,), "stats", dev)
-    need = L.adaln_grad_norm_workspace_bytes(at, n)
-    ws = _scratch(workspace, need, dev)
-    st = L.adaln_grad_clip(at, to, n, max_norm, stats.data_ptr(), _ptr(ws), need, _raw_stream(dev))
-    if st:
-        raise AdaLNError("adaln_grad_clip", st)
-    return outs, stats
+    if stream is not None:
+        with _on(stream):
+            return adaln_grad_clip(grads, max_norm, outs, stats, workspace)
+    return (_marshal or _native()).grad_clip(grads, max_norm, outs, stats, workspace)

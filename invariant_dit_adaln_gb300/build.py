@@ -4,14 +4,20 @@ The translation units are compiled in parallel and linked into
 ``invariant_dit_adaln_gb300/lib/libadaln.so`` (git-ignored).  Flags:
 ``-gencode arch=compute_103a,code=sm_103a -O3 -lineinfo --fmad=false``; no
 fast math, so every floating-point operation rounds as written.
+
+Beside it g++ builds ``lib/adaln_marshal_<torch version>.so``, the Python module
+that marshals PyTorch tensors for the calls of include/adaln_ops.h.  It is
+compiled against the installed PyTorch, hence the version in its name.
 """
 
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -26,6 +32,9 @@ SOURCES = ["api.cu", "out.cu", "proj.cu", "tc_proj.cu", "res.cu", "f32.cu", "noa
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "--fmad=false", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xptxas", "-warn-spills", f"-I{INCLUDE}", f"-I{CSRC}"]
+
+
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 
 
 def nvcc() -> str:
@@ -49,13 +58,52 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def marshal_path() -> str:
+    import torch
+    version = re.sub(r"[^0-9A-Za-z]+", "_", torch.__version__)
+    return os.path.join(LIBDIR, f"adaln_marshal_{version}.so")
+
+
+def _marshal_up_to_date() -> bool:
+    path = marshal_path()
+    if not os.path.exists(path):
+        return False
+    inputs = [MARSHAL_SOURCE] + [os.path.join(INCLUDE, f) for f in ("adaln.h", "adaln_ops.h")]
+    return all(os.path.getmtime(f) <= os.path.getmtime(path) for f in inputs)
+
+
+def build_marshal() -> str:
+    """Compile the marshalling module for the installed PyTorch; returns its path."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    path = marshal_path()
+    os.makedirs(LIBDIR, exist_ok=True)
+    tmp = path + f".tmp{os.getpid()}"
+    libs = os.path.join(base, "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
+           f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(base, 'include')}",
+           f"-I{os.path.join(base, 'include', 'torch', 'csrc', 'api', 'include')}", f"-I{os.path.join(cuda, 'include')}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", MARSHAL_SOURCE, "-o", tmp, f"-L{libs}",
+           f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
+    return path
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: str | None = None) -> str:
     """Compile and link the library; returns its path.  `variant` names a test
     build with extra flags, linked to lib/<variant>/libadaln.so with objects in
     _build/<variant>/ (the release library is lib/libadaln.so)."""
     lib = LIB if variant is None else os.path.join(LIBDIR, variant, "libadaln.so")
     objdir = BUILD if variant is None else os.path.join(BUILD, variant)
-    if not force and up_to_date(lib):
+    stale = force or not up_to_date(lib)
+    marshal = variant is None and (force or not _marshal_up_to_date())
+    if not stale:
+        if marshal:
+            build_marshal()
         return lib
     os.makedirs(objdir, exist_ok=True)
     os.makedirs(os.path.dirname(lib), exist_ok=True)
@@ -69,8 +117,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: s
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        module = ex.submit(build_marshal) if marshal else None
         results = list(ex.map(compile_one, SOURCES))
+        if module is not None:
+            module.result()
     logs = "".join(log for _, log in results)
     if verbose and logs.strip():
         print(logs, file=sys.stderr)

@@ -42,9 +42,14 @@ def test_exports(L):
 
 # --- head rows --------------------------------------------------------------
 
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("token", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
+
+
 def rows(i, B=2, S=5, H=4, Dh=64, off=0, strides=None):
     st = strides or (S * H * Dh, H * Dh, Dh)
-    return binding._Heads(i if i is None else at(i, off), *st)
+    return Heads(i if i is None else at(i, off), *st)
 
 
 BASE = dict(B=2, S=5, Hq=4, Hk=2, Dh=64, Dr=64, P=8, inter=1, eps=1e-6, is64=0)
