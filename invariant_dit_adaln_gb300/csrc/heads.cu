@@ -118,15 +118,16 @@ __device__ __forceinline__ int column(int i, const Slot &s) {
     if (INTER) return s.lo + 2 * (i & 3) + (i >> 2);
     return i < 4 ? s.lo + i : s.hi + i - 4;
 }
+// Streaming stores: the output of a large call does not fit L2 beside its inputs.
 template <bool INTER>
 __device__ __forceinline__ void store8(uint16_t *p, const px2 (&v)[4], const Slot &s) {
     if (INTER) {
-        *reinterpret_cast<uint4 *>(p + s.lo) =
-            make_uint4(pack_bf16x2(px_lo(v[0]), px_lo(v[2])), pack_bf16x2(px_hi(v[0]), px_hi(v[2])),
-                       pack_bf16x2(px_lo(v[1]), px_lo(v[3])), pack_bf16x2(px_hi(v[1]), px_hi(v[3])));
+        __stcs(reinterpret_cast<uint4 *>(p + s.lo),
+               make_uint4(pack_bf16x2(px_lo(v[0]), px_lo(v[2])), pack_bf16x2(px_hi(v[0]), px_hi(v[2])),
+                          pack_bf16x2(px_lo(v[1]), px_lo(v[3])), pack_bf16x2(px_hi(v[1]), px_hi(v[3]))));
     } else {
-        *reinterpret_cast<uint2 *>(p + s.lo) = make_uint2(px_to_bf16x2(v[0]), px_to_bf16x2(v[1]));
-        *reinterpret_cast<uint2 *>(p + s.hi) = make_uint2(px_to_bf16x2(v[2]), px_to_bf16x2(v[3]));
+        __stcs(reinterpret_cast<uint2 *>(p + s.lo), make_uint2(px_to_bf16x2(v[0]), px_to_bf16x2(v[1])));
+        __stcs(reinterpret_cast<uint2 *>(p + s.hi), make_uint2(px_to_bf16x2(v[2]), px_to_bf16x2(v[3])));
     }
 }
 template <bool INTER>
@@ -139,8 +140,8 @@ __device__ __forceinline__ void store8(float *p, const px2 (&v)[4], const Slot &
         a = make_float4(px_lo(v[0]), px_hi(v[0]), px_lo(v[1]), px_hi(v[1]));
         b = make_float4(px_lo(v[2]), px_hi(v[2]), px_lo(v[3]), px_hi(v[3]));
     }
-    *reinterpret_cast<float4 *>(p + s.lo) = a;
-    *reinterpret_cast<float4 *>(p + s.hi) = b;
+    __stcs(reinterpret_cast<float4 *>(p + s.lo), a);
+    __stcs(reinterpret_cast<float4 *>(p + s.hi), b);
 }
 template <bool INTER, typename T>
 __device__ __forceinline__ void store_zero(T *p, const Slot &s) {
@@ -156,17 +157,12 @@ __device__ __forceinline__ void load_weights(px2 (&w)[4], const void *p, const S
     if (s.live && p != nullptr) values<INTER>(w, load8<INTER>(static_cast<const T *>(p), s));
 }
 
-// The lane's four angles at position p (0 <= p < P): cosines, sines, -sines.
+// The lane's four angles: cosines and sines, from 16-byte aligned places.
 struct Angles {
-    px2 c[2], s[2], n[2];
+    px2 c[2], s[2];
 };
-__device__ __forceinline__ Angles load_angles(const HeadsArgs &a, long long p, int l) {
-    const long long at = p * (a.Dr / 2) + 4 * l;
-    const float4 c = __ldg(reinterpret_cast<const float4 *>(a.cos + at));
-    const float4 s = __ldg(reinterpret_cast<const float4 *>(a.sin + at));
-    return {{px_make(c.x, c.y), px_make(c.z, c.w)},
-            {px_make(s.x, s.y), px_make(s.z, s.w)},
-            {px_make(-s.x, -s.y), px_make(-s.z, -s.w)}};
+__device__ __forceinline__ Angles make_angles(const float4 &c, const float4 &s) {
+    return {{px_make(c.x, c.y), px_make(c.z, c.w)}, {px_make(s.x, s.y), px_make(s.z, s.w)}};
 }
 // Turn the lane's pairs by its angles (BACK: by the negative angles).
 template <bool BACK>
@@ -174,8 +170,9 @@ __device__ __forceinline__ void turn(px2 (&v)[4], const Angles &t) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const px2 a = v[i], b = v[2 + i];
-        v[i] = px_fma(b, BACK ? t.s[i] : t.n[i], px_mul(a, t.c[i]));
-        v[2 + i] = px_fma(a, BACK ? t.n[i] : t.s[i], px_mul(b, t.c[i]));
+        const px2 as = px_mul(a, t.s[i]), bs = px_mul(b, t.s[i]);
+        v[i] = BACK ? px_fma(a, t.c[i], bs) : px_sub(px_mul(a, t.c[i]), bs);
+        v[2 + i] = BACK ? px_sub(px_mul(b, t.c[i]), as) : px_fma(b, t.c[i], as);
     }
 }
 
@@ -234,7 +231,11 @@ __global__ void __launch_bounds__(32 * kWarps) heads_fwd_kernel(const __grid_con
         return;
     }
     Angles ang = {};
-    if (slot.turned) ang = load_angles(a, p, l);
+    if (slot.turned) {
+        const long long at = p * (a.Dr / 2) + 4 * l;
+        ang = make_angles(__ldg(reinterpret_cast<const float4 *>(a.cos + at)),
+                          __ldg(reinterpret_cast<const float4 *>(a.sin + at)));
+    }
     const float inv = __fdiv_rn(1.0f, (float)a.Dh);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -250,89 +251,186 @@ __global__ void __launch_bounds__(32 * kWarps) heads_fwd_kernel(const __grid_con
 }
 
 // --------------------------------------------------------------------------
-// Backward: one CTA per (sample, tile of tokens, q or k).  Each warp takes an
-// equal share of the tile's (token, heads) tasks, in order; each lane keeps
-// the dw sums of its 8 channels, joined over the CTA in a fixed order into the
-// tile's partial.
+// Tiles: one CTA per (tile of tokens, q or k, sample), for the backward and for
+// large forward calls.  Each warp takes an equal share of the tile's (token,
+// U * 32/LPR heads) tasks, in order, and copies their rows asynchronously into
+// a ring of kStages tasks of its own, so that the bytes in flight are not held
+// in registers.  (With the rows in registers the backward
+// was bound by load latency at 18 warps an SM: 70 us against NNN at B=2, S=4096,
+// 24 + 24 heads of 128 in bf16.)  A token's angles travel with its tasks; its
+// position is read one token ahead.
+//
+// Backward: each lane keeps the dw sums of its 8 channels, joined over the CTA
+// in a fixed order into the tile's partial.
 // --------------------------------------------------------------------------
-template <typename T, int LPR, int U, bool INTER>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
-heads_bwd_kernel(const __grid_constant__ HeadsArgs a) {
+constexpr int kStages = 4;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
+    // a size of 0 reads nothing and fills with zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The rows of one task of one tensor into dst (U * 32/LPR rows of LPR * 8
+// elements); lane l of a row copies its channels 8 l .. 8 l + 7.
+template <typename T, int LPR, int U>
+__device__ __forceinline__ void copy_rows(uint32_t dst, const T *src, long long step, int rows, int l, int sub) {
     constexpr int RPW = 32 / LPR;
-    __shared__ float red[kWarps][LPR * 8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+            cp_async16(dst + ((u * RPW + sub) * LPR * 8 + 8 * l + j * (16 / (int)sizeof(T))) * (int)sizeof(T),
+                       src + (u < rows ? u * step + 8 * l + j * (16 / (int)sizeof(T)) : 0), u < rows);
+    }
+}
+
+// A stage of the ring: the task's rows of x (and dy), then its token's cosines
+// and sines, 4 LPR floats each; in bytes.
+template <typename T, int LPR, int U, bool BWD>
+struct Stage {
+    static constexpr int kRows = U * 256 * (int)sizeof(T);
+    static constexpr int kAngles = (BWD ? 2 : 1) * kRows;
+    static constexpr int kBytes = kAngles + 32 * LPR;
+    static constexpr size_t kSmem = (size_t)kWarps * kStages * kBytes;
+};
+
+template <typename T, int LPR, int U, bool INTER, bool BWD>
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? (BWD ? 5 : 6) : 3)
+heads_tile_kernel(const __grid_constant__ HeadsArgs a) {
+    using St = Stage<T, LPR, U, BWD>;
+    constexpr int RPW = 32 / LPR;
+    extern __shared__ __align__(16) unsigned char ring_bytes[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
     const Slot slot = lane_slot<INTER>(l, a.Dh, a.Dr);
     const int t = blockIdx.y;
     const int nchunk = a.chunks[t];
     if (nchunk == 0) return;  // no keys
-    const float inv = __fdiv_rn(1.0f, (float)a.Dh);
+    unsigned char *ring = ring_bytes + warp * (kStages * St::kBytes);
+    const uint32_t ring_u32 = smem_u32(ring);
     const int s0 = blockIdx.x * a.tile;
     const int ntask = min(a.tile, a.S - s0) * nchunk;
     const long long b = blockIdx.z;
-    const T *xb = static_cast<const T *>(a.x[t]) + b * a.xs[t][0];
-    const T *gb = static_cast<const T *>(a.dy[t]) + b * a.dys[t][0];
-    T *ob = static_cast<T *>(a.out[t]) + b * a.os[t][0];
-    // consecutive tasks: most share their token's position and angles
     const int first = ntask * warp / kWarps, end = ntask * (warp + 1) / kWarps;
-    const long long xstep = RPW * a.xs[t][2], gstep = RPW * a.dys[t][2], ostep = RPW * a.os[t][2];
-    int s = s0 + first / nchunk, chunk = first % nchunk, at = -1;
-    bool real = false;
-    Angles ang = {};
-    px2 dw[4] = {0, 0, 0, 0}, w[4];
+    const int heads = slot.live ? (a.H[t] - sub + RPW - 1) / RPW : 0;  // the lane's heads of a token
+    px2 dw[4] = {0, 0, 0, 0};
     pdl_wait();
     pdl_trigger();
-    load_weights<T, INTER>(w, a.w[t], slot);
-#pragma unroll 1
-    for (int task = first; task < end; ++task) {
-        const int h0 = chunk * (U * RPW) + sub;
-        const int rows = slot.live ? (a.H[t] - h0 + RPW - 1) / RPW : 0;  // the lane's heads: u < rows
-        const T *x = xb + s * a.xs[t][1] + h0 * a.xs[t][2];
-        const T *dy = gb + s * a.dys[t][1] + h0 * a.dys[t][2];
-        T *o = ob + s * a.os[t][1] + h0 * a.os[t][2];
-        Raw<T> rx[U], rg[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            clear(rx[u]);
-            clear(rg[u]);
-            if (u < rows) {
-                rx[u] = load8<INTER>(x + u * xstep, slot);
-                rg[u] = load8<INTER>(dy + u * gstep, slot);
-            }
-        }
-        if (s != at) {
-            at = s;
+    if (first < end) {
+        const float inv = __fdiv_rn(1.0f, (float)a.Dh);
+        const int last = s0 + (end - 1) / nchunk;  // the warp's last token
+        // a token's position, or -1: padding
+        const auto where = [&](int s) {
             const long long p = position(a, b * a.S + s, s);
-            real = p >= 0 && p < a.P;
-            if (slot.turned && real) ang = load_angles(a, p, l);
-        }
-        if (real) {
+            return p >= 0 && p < a.P ? (int)p : -1;
+        };
+        // copies run kStages - 1 tasks ahead: the task with `left` tasks to the
+        // end, at token cs and chunk cc, its position known one token before
+        int cs = s0 + first / nchunk, cc = first % nchunk, left = end - first;
+        int s = cs, chunk = cc;
+        int p = where(cs), p_next = where(min(cs + 1, last));
+        unsigned real = 0;  // bit i: stage i holds a real token's task
+        const auto copy_next = [&](int stage) {
+            if (left > 0) {
+                --left;
+                const int rows = heads - cc * U;
+                const uint32_t dst = ring_u32 + stage * St::kBytes;
+                const long long xs = a.xs[t][2], gs = a.dys[t][2];
+                copy_rows<T, LPR, U>(dst,
+                                     static_cast<const T *>(a.x[t]) + b * a.xs[t][0] + cs * a.xs[t][1] +
+                                         (sub + cc * (U * RPW)) * xs,
+                                     RPW * xs, rows, l, sub);
+                if (BWD)
+                    copy_rows<T, LPR, U>(dst + St::kRows,
+                                         static_cast<const T *>(a.dy[t]) + b * a.dys[t][0] + cs * a.dys[t][1] +
+                                             (sub + cc * (U * RPW)) * gs,
+                                         RPW * gs, rows, l, sub);
+                if (sub == 0 && slot.turned && p >= 0) {
+                    const long long at = (long long)p * (a.Dr / 2) + 4 * l;
+                    cp_async16(dst + St::kAngles + 16 * l, a.cos + at, true);
+                    cp_async16(dst + St::kAngles + 16 * (LPR + l), a.sin + at, true);
+                }
+                real = p >= 0 ? real | 1u << stage : real & ~(1u << stage);
+                if (++cc == nchunk) {
+                    cc = 0, ++cs;
+                    p = p_next;
+                    if (cs < last) p_next = where(cs + 1);
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) copy_next(i);
+        px2 w[4];
+        load_weights<T, INTER>(w, a.w[t], slot);
+        int stage = 0;
+#pragma unroll 1
+        for (int task = first; task < end; ++task) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            Raw<T> rx[U], rg[U];
+            const unsigned char *at = ring + stage * St::kBytes;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                px2 v[4], g[4], gx[4];
-                values<INTER>(v, rx[u]);
-                values<INTER>(g, rg[u]);
-                if (slot.turned) turn<true>(g, ang);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) gx[i] = px_mul(g[i], v[i]);
-                const float ss = row_sum<LPR>(dot8(v, v)), hx = row_sum<LPR>(dot8(gx, w));
-                // lanes without a row: 0, where r would be infinite at eps = 0
-                const float r = u < rows ? rsqrtf(__fmaf_rn(ss, inv, a.eps)) : 0.0f;
-                const px2 rr = px_splat(r), k = px_splat(-__fmul_rn(__fmul_rn(__fmul_rn(r, r), inv), hx));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    dw[i] = px_fma(gx[i], rr, dw[i]);
-                    g[i] = px_mul(px_fma(v[i], k, px_mul(g[i], w[i])), rr);
-                }
-                if (u < rows) store8<INTER>(o + u * ostep, g, slot);
+                const T *row = reinterpret_cast<const T *>(at) + (u * RPW + sub) * LPR * 8;
+                rx[u] = load8<INTER>(row, slot);
+                if (BWD) rg[u] = load8<INTER>(row + St::kRows / (int)sizeof(T), slot);
             }
-        } else {  // padding
+            const Angles ang = make_angles(*reinterpret_cast<const float4 *>(at + St::kAngles + 16 * l),
+                                           *reinterpret_cast<const float4 *>(at + St::kAngles + 16 * (LPR + l)));
+            const bool known = real >> stage & 1u;
+            __syncwarp();  // every lane has read the stage that is copied into next time
+            copy_next(stage == 0 ? kStages - 1 : stage - 1);
+            if (++stage == kStages) stage = 0;
+            const int rows = heads - chunk * U;  // the lane's heads: u < rows
+            const long long os = a.os[t][2];
+            T *o = static_cast<T *>(a.out[t]) + b * a.os[t][0] + s * a.os[t][1] + (sub + chunk * (U * RPW)) * os;
+            if (known) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (u < rows) store_zero<INTER>(o + u * ostep, slot);
+                for (int u = 0; u < U; ++u) {
+                    px2 v[4];
+                    values<INTER>(v, rx[u]);
+                    const float ss = row_sum<LPR>(dot8(v, v));
+                    if (BWD) {
+                        px2 g[4], gx[4];
+                        values<INTER>(g, rg[u]);
+                        if (slot.turned) turn<true>(g, ang);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) gx[i] = px_mul(g[i], v[i]);
+                        const float hx = row_sum<LPR>(dot8(gx, w));
+                        // lanes without a row: 0, where r would be infinite at eps = 0
+                        const float r = u < rows ? rsqrtf(__fmaf_rn(ss, inv, a.eps)) : 0.0f;
+                        const px2 rr = px_splat(r);
+                        const px2 k = px_splat(-__fmul_rn(__fmul_rn(__fmul_rn(r, r), inv), hx));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            dw[i] = px_fma(gx[i], rr, dw[i]);
+                            v[i] = px_mul(px_fma(v[i], k, px_mul(g[i], w[i])), rr);
+                        }
+                    } else {
+                        const px2 r = px_splat(rsqrtf(__fmaf_rn(ss, inv, a.eps)));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = px_mul(px_mul(v[i], r), w[i]);
+                        if (slot.turned) turn<false>(v, ang);
+                    }
+                    if (u < rows) store8<INTER>(o + u * RPW * os, v, slot);
+                }
+            } else {  // padding
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u < rows) store_zero<INTER>(o + u * RPW * os, slot);
+            }
+            if (++chunk == nchunk) chunk = 0, ++s;
         }
-        if (++chunk == nchunk) chunk = 0, ++s;
+        cp_async_wait<0>();
     }
-    if (a.part == nullptr) return;
+    if (!BWD || a.part == nullptr) return;
+    __syncthreads();  // the rings are free
+    float(*red)[LPR * 8] = reinterpret_cast<float(*)[LPR * 8]>(ring_bytes);
     // the warp's row groups, then the warps in ascending order
     float sums[8];
 #pragma unroll
@@ -487,14 +585,35 @@ HeadsArgs make_args(const HeadsCall &c, int group) {
     return a;
 }
 
-// heads of a backward task: 4 rows a lane where a token has that many heads
-int bwd_rows(int Hq, int Hk, int Dh) {
-    const int rpw = 32 / lanes_per_row(Dh), h = Hq > Hk ? Hq : Hk;
-    return h > 2 * rpw ? 4 : h > rpw ? 2 : 1;
+// rows a lane in a tile's task: 2 where a token has heads for them
+int tile_rows(int Hq, int Hk, int Dh) {
+    const int h = Hq > Hk ? Hq : Hk;
+    return h > 32 / lanes_per_row(Dh) ? 2 : 1;
+}
+
+template <typename T, int LPR, int U, bool INTER, bool BWD>
+cudaError_t run_tile(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &dev) {
+    HeadsArgs a = make_args(c, U * (32 / LPR));
+    a.tile = heads_tile_tokens(c.S, c.H[0], c.H[1], c.Dh);
+    a.tiles = (c.S + a.tile - 1) / a.tile;
+    a.part = BWD && (c.dw[0] || c.dw[1]) ? c.ws : nullptr;
+    constexpr size_t smem = Stage<T, LPR, U, BWD>::kSmem;
+    const cudaError_t e = ensure_smem_attr((const void *)heads_tile_kernel<T, LPR, U, INTER, BWD>, smem, dev);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(heads_tile_kernel<T, LPR, U, INTER, BWD>, dim3(a.tiles, 2, c.B), dim3(32 * kWarps), smem, stream,
+                      a);
+}
+template <typename T, int LPR, bool BWD>
+cudaError_t pick_tile(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &dev) {
+    if (tile_rows(c.H[0], c.H[1], c.Dh) == 2)
+        return c.interleaved ? run_tile<T, LPR, 2, true, BWD>(c, stream, dev)
+                             : run_tile<T, LPR, 2, false, BWD>(c, stream, dev);
+    return c.interleaved ? run_tile<T, LPR, 1, true, BWD>(c, stream, dev)
+                         : run_tile<T, LPR, 1, false, BWD>(c, stream, dev);
 }
 
 template <typename T, int LPR, int U>
-cudaError_t run_fwd(const HeadsCall &c, cudaStream_t stream) {
+cudaError_t run_direct(const HeadsCall &c, cudaStream_t stream) {
     HeadsArgs a = make_args(c, U * (32 / LPR));
     // tasks of a launch are counted in 31 bits
     const long long tokens = (long long)c.B * c.S, nchunk = a.chunks[0] + a.chunks[1];
@@ -511,45 +630,29 @@ cudaError_t run_fwd(const HeadsCall &c, cudaStream_t stream) {
 
 template <typename T, int LPR>
 cudaError_t pick_fwd(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &dev) {
-    // 4 rows a lane where that still gives every SM 16 warps; few rows go one
-    // a lane, for the shortest path through the kernel
+    // Few rows go one a lane straight through registers, for the shortest path
+    // through the kernel; then 4 a lane, once that gives every SM 16 warps; and
+    // through the ring where a tile has 4 tasks or more for each warp.
     const long long rows = (long long)c.B * c.S * (c.H[0] + c.H[1]);
-    return rows / (4 * (32 / LPR)) >= 16ll * dev.sm_count ? run_fwd<T, LPR, 4>(c, stream)
-                                                          : run_fwd<T, LPR, 1>(c, stream);
-}
-
-template <typename T, int LPR, int U>
-cudaError_t run_bwd(const HeadsCall &c, cudaStream_t stream) {
-    HeadsArgs a = make_args(c, U * (32 / LPR));
-    a.tile = heads_tile_tokens(c.H[0], c.H[1], c.Dh);
-    a.tiles = (c.S + a.tile - 1) / a.tile;
-    a.part = (c.dw[0] || c.dw[1]) ? c.ws : nullptr;
-    const dim3 grid(a.tiles, 2, c.B);
-    return c.interleaved ? launch_pdl(heads_bwd_kernel<T, LPR, U, true>, grid, dim3(32 * kWarps), 0, stream, a)
-                         : launch_pdl(heads_bwd_kernel<T, LPR, U, false>, grid, dim3(32 * kWarps), 0, stream, a);
-}
-
-template <typename T, int LPR>
-cudaError_t pick_bwd(const HeadsCall &c, cudaStream_t stream) {
-    switch (bwd_rows(c.H[0], c.H[1], c.Dh)) {
-        case 4: return run_bwd<T, LPR, 4>(c, stream);
-        case 2: return run_bwd<T, LPR, 2>(c, stream);
-        default: return run_bwd<T, LPR, 1>(c, stream);
-    }
+    if (rows / (4 * (32 / LPR)) < 16ll * dev.sm_count) return run_direct<T, LPR, 1>(c, stream);
+    const int tile = heads_tile_tokens(c.S, c.H[0], c.H[1], c.Dh), group = tile_rows(c.H[0], c.H[1], c.Dh) * (32 / LPR);
+    if ((long long)tile * ((c.H[0] + group - 1) / group) < 4 * kWarps) return run_direct<T, LPR, 4>(c, stream);
+    return pick_tile<T, LPR, false>(c, stream, dev);
 }
 
 }  // namespace
 
-int heads_tile_tokens(int Hq, int Hk, int Dh) {
-    // about 24 tasks a CTA, 3 a warp: enough rows to pay for joining dw, and
-    // enough CTAs (1024 at B = 2, S = 4096, 24 + 24 heads of 128)
-    const int group = bwd_rows(Hq, Hk, Dh) * (32 / lanes_per_row(Dh)), h = Hq > Hk ? Hq : Hk;
+int heads_tile_tokens(int S, int Hq, int Hk, int Dh) {
+    // 48 tasks a CTA, 12 a warp: enough to fill the ring and to pay for joining
+    // dw; fewer tokens where a sample has few, so that it still spreads over the SMs
+    const int group = tile_rows(Hq, Hk, Dh) * (32 / lanes_per_row(Dh)), h = Hq > Hk ? Hq : Hk;
     const int chunks = (h + group - 1) / group;
-    return chunks >= 24 ? 1 : 24 / chunks;
+    const int most = chunks >= 48 ? 1 : 48 / chunks, spread = S < 128 ? 1 : S / 128;
+    return most < spread ? most : spread;
 }
 
 size_t heads_bwd_ws_floats(int B, int S, int Hq, int Hk, int Dh) {
-    const int tile = heads_tile_tokens(Hq, Hk, Dh);
+    const int tile = heads_tile_tokens(S, Hq, Hk, Dh);
     const size_t tiles = ((size_t)S + tile - 1) / tile;
     return (size_t)B * (tiles + 1) * 2 * Dh;
 }
@@ -565,13 +668,13 @@ cudaError_t launch_heads_fwd(const HeadsCall &c, cudaStream_t stream, const Devi
 }
 
 template <typename T>
-cudaError_t launch_heads_bwd(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &) {
+cudaError_t launch_heads_bwd(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &dev) {
     cudaError_t e;
     switch (lanes_per_row(c.Dh)) {
-        case 4: e = pick_bwd<T, 4>(c, stream); break;
-        case 8: e = pick_bwd<T, 8>(c, stream); break;
-        case 16: e = pick_bwd<T, 16>(c, stream); break;
-        default: e = pick_bwd<T, 32>(c, stream); break;
+        case 4: e = pick_tile<T, 4, true>(c, stream, dev); break;
+        case 8: e = pick_tile<T, 8, true>(c, stream, dev); break;
+        case 16: e = pick_tile<T, 16, true>(c, stream, dev); break;
+        default: e = pick_tile<T, 32, true>(c, stream, dev); break;
     }
     if (e != cudaSuccess || (!c.dw[0] && !c.dw[1])) return e;
     FoldArgs f = {};
@@ -581,7 +684,7 @@ cudaError_t launch_heads_bwd(const HeadsCall &c, cudaStream_t stream, const Devi
     f.B = c.B;
     f.Dh = c.Dh;
     f.accumulate = c.accumulate;
-    const int tile = heads_tile_tokens(c.H[0], c.H[1], c.Dh);
+    const int tile = heads_tile_tokens(c.S, c.H[0], c.H[1], c.Dh);
     f.tiles = (c.S + tile - 1) / tile;
     f.sums = c.ws + (size_t)c.B * f.tiles * 2 * c.Dh;
     const unsigned cols = c.Dh / 8;
