@@ -7,15 +7,17 @@
 // tokens first, so that every row of d_out is read once, every row of dT has
 // one owner, and no floating-point atomic decides an order:
 //   1. a stable radix sort of (token, place), at most 8 bits a pass: in the
-//      shared memory of one CTA where a token and a place fit 32 bits together
-//      and n <= kCtaTokens, otherwise by a histogram and a scatter kernel a pass;
-//   2. the runs of equal tokens cut into pieces of 32 places.  Which list entry
-//      a piece gets is left to an integer atomic: it decides who computes
-//      the piece, not what;
-//   3. a warp per (piece, 256 columns) adds the piece's rows in ascending order.
-//      A token with one piece is written at once.  The pieces of longer runs
-//      are the leaves of a 32-way tree: whoever brings the last child of a node
-//      adds the children in order (a ticket per node; nobody waits).
+//      shared memory of one CTA or of a cluster where a token and a place fit 32
+//      bits together, otherwise by a histogram and a scatter kernel a pass;
+//   2. runs of more than 32 equal tokens are listed in pieces of 32 places.
+//      Which list entry a piece gets is left to an integer atomic: it decides
+//      who computes the piece, not what;
+//   3. a warp takes a piece, or the shorter runs that begin among some
+//      consecutive places, at 256 columns, and adds each run's rows in ascending
+//      order, 8 rows in flight whatever the runs' lengths.  A short run's row is
+//      written at once.  The pieces of a long run are the leaves of a 32-way
+//      tree: whoever brings the last child of a node adds the children in order
+//      (a ticket per node; nobody waits).
 // Sorting is a chain of latencies that leaves the memory idle, so the table is
 // zeroed meanwhile, by the other CTAs of the sorting launches; step 3 then
 // writes the rows of tokens that occur.
@@ -26,26 +28,22 @@ namespace adaln {
 
 namespace {
 
-constexpr int kCtaThreads = 1024;
-// Tokens that one CTA sorts, four a thread (11 us at 4096, most of it latency).
-// With 32 a thread one CTA took 67 us for 32768 tokens; the kernels that share
-// them among CTAs take about 25 us at any such size.
-constexpr int kCtaTokens = 4 * kCtaThreads;
+constexpr int kTeamThreads = 1024;
 constexpr int kPiece = 32;        // places of a piece
 constexpr int kFan = 32;          // children of a node
 constexpr int kDigits = 256;      // at most 8 bits a pass
-constexpr int kTileMin = 1024;    // tokens of a sorting CTA
+constexpr int kTileMin = 1024;    // tokens of a CTA in the sort by kernels
 constexpr int kMaxTiles = 256;    // ... and the number of such CTAs
 
-// One piece of a token's run.  A run of several pieces has a partial sum for
-// every piece and every node below the root, level by level from `slot`, and a
-// ticket (per column group) for every node, level by level from `node`.
+// One piece of a long run.  The run has a partial sum for every piece and every
+// node below the root, level by level from `slot`, and a ticket (per column
+// group) for every node, level by level from `node`.
 struct __align__(16) Piece {
-    int token, start, len, index;  // index: which piece of the run; -1: the only one
+    int token, start, len, index;  // index: which piece of the run
     int pieces, slot, node, unused;
 };
 struct Counts {
-    int singles, pieces, slots, nodes;  // runs of one piece; pieces, partial sums and nodes of the longer runs
+    int pieces, slots, nodes;
 };
 
 // partial sums and nodes of a run of np > 1 pieces
@@ -134,12 +132,32 @@ __device__ void fill_zero(const Fill &f, int cta, int ctas) {
 }
 
 // --------------------------------------------------------------------------
-// pieces of the sorted tokens
+// long runs of the sorted tokens
 // --------------------------------------------------------------------------
-struct PackedKeys {  // token << bits | place
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t smem, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ uint32_t cluster_load(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Items token << bits | place in the shared memory of the C CTAs of a team,
+// 1 << shift in each.
+template <int C>
+struct TeamKeys {
     const uint32_t *items;
-    int bits;
-    __device__ uint32_t operator()(int i) const { return items[i] >> bits; }
+    int bits, shift;
+    __device__ uint32_t operator()(int i) const {
+        if (C == 1) return items[i] >> bits;
+        return cluster_load(cluster_addr(smem_u32(items + (i & ((1 << shift) - 1))), i >> shift)) >> bits;
+    }
 };
 struct PlainKeys {
     const uint32_t *keys;
@@ -166,107 +184,92 @@ __device__ int run_end(const Keys &keys, int n, int from, uint32_t key) {
     return lo + __popc(__ballot_sync(0xFFFFFFFFu, lo + lane < hi && keys(lo + lane) == key));
 }
 
-// The pieces of the runs that begin at the warp's 32 places base + lane.
+// The pieces of the long run that begins among the warp's 32 places base +
+// lane, if one does (it covers every place behind its first, so there is one at
+// most).
 template <typename Keys>
 __device__ void plan_places(const Keys &keys, int n, int V, int base, int groups, Piece *pieces, int *tickets,
                             Counts *counts) {
-    if (base >= n) return;
     const int lane = threadIdx.x & 31, i = base + lane;
     const uint32_t key = i < n ? keys(i) : 0xFFFFFFFFu;
+    const uint32_t ahead = i + kPiece < n ? keys(i + kPiece) : 0xFFFFFFFFu;
     uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, key, 1);
-    if (lane == 0 && i > 0) prev = keys(i - 1);
-    const bool edge = i >= n || i == 0 || key != prev;
-    const bool head = edge && i < n && key < (uint32_t)V;
-    const unsigned edges = __ballot_sync(0xFFFFFFFFu, edge);
-    int len = 0;
-    if (edges != 0) {
-        // the last run may go on behind the warp's places
-        const int last = 31 - __clz(edges);
-        const int last_head = __shfl_sync(0xFFFFFFFFu, (int)head, last);
-        int behind = base + 32;
-        if (last_head) behind = run_end(keys, n, base + 32, __shfl_sync(0xFFFFFFFFu, key, last));
-        const unsigned next = lane < 31 ? edges & (0xFFFFFFFEu << lane) : 0u;
-        if (head) len = (next ? base + __ffs(next) - 1 : behind) - i;
-    }
-    const int np = (len + kPiece - 1) / kPiece;
-    int slots = 0, nodes = 0;
-    if (np > 1) tree_size(np, slots, nodes);
-    // one atomic per warp and counter.  Long runs fill the list from the front,
-    // so that their trees are begun first; the others from the back.
-    const unsigned longs = __ballot_sync(0xFFFFFFFFu, np > 1), ones = __ballot_sync(0xFFFFFFFFu, np == 1);
-    int4 *out = reinterpret_cast<int4 *>(pieces);
-    if (ones) {
-        int at = 0;
-        if (lane == 0) at = atomicAdd(&counts->singles, __popc(ones));
-        at = n - 1 - __shfl_sync(0xFFFFFFFFu, at, 0) - __popc(ones & ((1u << lane) - 1));
-        if (np == 1) out[2 * at] = make_int4((int)key, i, len, -1);
-    }
+    if (lane == 0 && i > 0 && i < n) prev = keys(i - 1);
+    const bool head = i < n && key < (uint32_t)V && (i == 0 || prev != key);
+    const unsigned longs = __ballot_sync(0xFFFFFFFFu, head && ahead == key);
     if (longs == 0) return;
-    const int mine = np > 1 ? np : 0;
-    int at = mine, slot = slots, node = nodes;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, at, off), y = __shfl_up_sync(0xFFFFFFFFu, slot, off),
-                  z = __shfl_up_sync(0xFFFFFFFFu, node, off);
-        if (lane >= off) at += x, slot += y, node += z;
+    const int src = __ffs(longs) - 1, start = base + src;
+    const int token = __shfl_sync(0xFFFFFFFFu, (int)key, src);
+    const int len = run_end(keys, n, start + kPiece + 1, (uint32_t)token) - start, np = (len + kPiece - 1) / kPiece;
+    int slots, nodes, at = 0, slot = 0, node = 0;
+    tree_size(np, slots, nodes);
+    if (lane == 0) {
+        at = atomicAdd(&counts->pieces, np);
+        slot = atomicAdd(&counts->slots, slots);
+        node = atomicAdd(&counts->nodes, nodes);
     }
-    int at0 = 0, slot0 = 0, node0 = 0;
-    if (lane == 31) {
-        at0 = atomicAdd(&counts->pieces, at);
-        slot0 = atomicAdd(&counts->slots, slot);
-        node0 = atomicAdd(&counts->nodes, node);
+    at = __shfl_sync(0xFFFFFFFFu, at, 0);
+    slot = __shfl_sync(0xFFFFFFFFu, slot, 0);
+    node = __shfl_sync(0xFFFFFFFFu, node, 0);
+    int4 *out = reinterpret_cast<int4 *>(pieces);
+    for (int p = lane; p < np; p += 32) {
+        out[2 * (at + p)] = make_int4(token, start + p * kPiece, min(kPiece, len - p * kPiece), p);
+        out[2 * (at + p) + 1] = make_int4(np, slot, node, 0);
     }
-    at += __shfl_sync(0xFFFFFFFFu, at0, 31) - mine;
-    slot += __shfl_sync(0xFFFFFFFFu, slot0, 31) - slots;
-    node += __shfl_sync(0xFFFFFFFFu, node0, 31) - nodes;
-    for (unsigned m = longs; m; m &= m - 1) {  // long runs: by all lanes
-        const int src = __ffs(m) - 1;
-        const int l_token = __shfl_sync(0xFFFFFFFFu, (int)key, src), l_start = __shfl_sync(0xFFFFFFFFu, i, src);
-        const int l_len = __shfl_sync(0xFFFFFFFFu, len, src), l_np = __shfl_sync(0xFFFFFFFFu, np, src);
-        const int l_at = __shfl_sync(0xFFFFFFFFu, at, src), l_slot = __shfl_sync(0xFFFFFFFFu, slot, src);
-        const int l_node = __shfl_sync(0xFFFFFFFFu, node, src), l_nodes = __shfl_sync(0xFFFFFFFFu, nodes, src);
-        for (int p = lane; p < l_np; p += 32) {
-            out[2 * (l_at + p)] = make_int4(l_token, l_start + p * kPiece, min(kPiece, l_len - p * kPiece), p);
-            out[2 * (l_at + p) + 1] = make_int4(l_np, l_slot, l_node, 0);
-        }
-        for (long long k = lane; k < (long long)l_nodes * groups; k += 32) tickets[(long long)l_node * groups + k] = 0;
-    }
+    for (long long k = lane; k < (long long)nodes * groups; k += 32) tickets[(long long)node * groups + k] = 0;
 }
 
 // --------------------------------------------------------------------------
-// sorting in one CTA: 32 warps, IPT items a thread; warp w holds the places
-// [32 IPT w, 32 IPT (w + 1)) of every pass.  An item is token << bits | place.
+// sorting in shared memory: a team of one CTA, or of a cluster of 8, with IPT
+// items a thread.  CTA r of the team holds the places [r PER, (r + 1) PER) of
+// every pass, PER = 1024 IPT, and its warp w 32 IPT of them.  Each pass counts
+// the digits, shares the counts over the team, and sends every item to its
+// place in the team's memory.  The other CTAs of the grid zero the table.
 // --------------------------------------------------------------------------
 constexpr int kCntStride = kDigits + 1;  // keeps the scan's reads in different banks
-struct CtaShared {
+struct TeamShared {
     int cnt[32][kCntStride];  // per warp and digit: the count, then the next place
+    int hist[kDigits];        // the CTA's counts, read by the team
     int sums[32];
     Counts counts;
     uint32_t items[1];  // [IPT * 1024]
 };
 
-template <int IPT>
-__global__ void __launch_bounds__(kCtaThreads)
-embed_sort_cta_kernel(const void *tokens, int is64, int n, int V, int bits, int digit_bits, int passes, int groups,
-                      int *idx_out, Piece *pieces, int *tickets, Counts *counts, Fill fill) {
+template <int C>
+__device__ __forceinline__ void team_sync() {
+    if (C == 1) {
+        __syncthreads();
+    } else {
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+}
+
+template <int C, int IPT>
+__device__ __forceinline__ void
+team_sort(const void *tokens, int is64, int n, int V, int bits, int digit_bits, int passes, int groups, uint32_t *keys_out,
+          int *idx_out, Piece *pieces, int *tickets, Counts *counts, const Fill &fill) {
     extern __shared__ __align__(16) unsigned char raw[];
-    CtaShared &sh = *reinterpret_cast<CtaShared *>(raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    TeamShared &sh = *reinterpret_cast<TeamShared *>(raw);
+    constexpr int PER = kTeamThreads * IPT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = C == 1 ? 0 : (int)blockIdx.x % C;
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x > 0) {
-        fill_zero(fill, blockIdx.x - 1, gridDim.x - 1);
+    if (blockIdx.x >= C) {
+        fill_zero(fill, blockIdx.x - C, gridDim.x - C);
         return;
     }
-    const int base = warp * (32 * IPT) + lane;
+    const int local = warp * (32 * IPT) + lane;  // the thread's places: local + 32 j of the CTA's
     const int nd = 1 << digit_bits;
     uint32_t item[IPT];
 #pragma unroll
     for (int j = 0; j < IPT; ++j) {
-        const int i = base + 32 * j;
+        const int i = team * PER + local + 32 * j;
         item[j] = i < n ? token_key(tokens, is64, i, V) << bits | i : 0xFFFFFFFFu;  // behind the end: last
     }
-    if (threadIdx.x == 0) sh.counts = Counts{0, 0, 0, 0};
+    if (threadIdx.x == 0) {
+        sh.counts = Counts{0, 0, 0};
+        if (C > 1 && team == 0) *counts = Counts{0, 0, 0};
+    }
     for (int pass = 0; pass < passes; ++pass) {
         const int shift = bits + pass * digit_bits;
         for (int d = lane; d < nd; d += 32) sh.cnt[warp][d] = 0;
@@ -274,16 +277,42 @@ embed_sort_cta_kernel(const void *tokens, int is64, int n, int V, int bits, int 
 #pragma unroll
         for (int j = 0; j < IPT; ++j) atomicAdd(&sh.cnt[warp][(item[j] >> shift) & (nd - 1)], 1);
         __syncthreads();
-        // exclusive scan over (digit, warp): thread 4 d + q has the warps 8 q ..
+        // thread 4 d + q: the counts of digit d in the warps 8 q .. 8 q + 7
         const int d = threadIdx.x >> 2, q = threadIdx.x & 3;
         int c[8], sum = 0;
-        if (d < nd) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) c[k] = sh.cnt[8 * q + k][d];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum += c[k];
+        for (int k = 0; k < 8; ++k) {
+            c[k] = d < nd ? sh.cnt[8 * q + k][d] : 0;
+            sum += c[k];
         }
-        int inc = sum;
+        int upto = sum;  // inclusive over the quad
+#pragma unroll
+        for (int off = 1; off < 4; off <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+            if (q >= off) upto += o;
+        }
+        int total = __shfl_sync(0xFFFFFFFFu, upto, lane | 3), before = 0;  // of the digit: all, and before this CTA
+        if (C > 1) {
+            if (q == 0 && d < nd) sh.hist[d] = total;
+            team_sync<C>();
+            total = 0;
+            if (d < nd) {
+#pragma unroll
+                for (int k = 0; k < C / 4; ++k) {
+                    const int r = q * (C / 4) + k;
+                    const int h = (int)cluster_load(cluster_addr(smem_u32(&sh.hist[d]), r));
+                    total += h;
+                    before += r < team ? h : 0;
+                }
+            }
+#pragma unroll
+            for (int off = 1; off < 4; off <<= 1) {
+                total += __shfl_xor_sync(0xFFFFFFFFu, total, off);
+                before += __shfl_xor_sync(0xFFFFFFFFu, before, off);
+            }
+        }
+        // exclusive scan over the digits, one value a quad
+        int inc = q == 0 ? total : 0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int o = __shfl_up_sync(0xFFFFFFFFu, inc, off);
@@ -291,13 +320,13 @@ embed_sort_cta_kernel(const void *tokens, int is64, int n, int V, int bits, int 
         }
         if (lane == 31) sh.sums[warp] = inc;
         __syncthreads();
-        int before = lane < warp ? sh.sums[lane] : 0;
-        before = __reduce_add_sync(0xFFFFFFFFu, before) + inc - sum;
+        int first = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sh.sums[lane] : 0) + inc - total;
+        first = __shfl_sync(0xFFFFFFFFu, first, lane & ~3) + before + upto - sum;
         if (d < nd) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                sh.cnt[8 * q + k][d] = before;
-                before += c[k];
+                sh.cnt[8 * q + k][d] = first;
+                first += c[k];
             }
         }
         __syncthreads();
@@ -306,26 +335,52 @@ embed_sort_cta_kernel(const void *tokens, int is64, int n, int V, int bits, int 
             const int digit = (item[j] >> shift) & (nd - 1);
             const unsigned peers = same_digit(digit, digit_bits);
             const int rank = __popc(peers & ((1u << lane) - 1));
-            const int at = sh.cnt[warp][digit];
+            const int at = sh.cnt[warp][digit] + rank;
             __syncwarp();
             if (rank == 0) sh.cnt[warp][digit] = at + __popc(peers);
             __syncwarp();
-            sh.items[at + rank] = item[j];
+            if (C == 1)
+                sh.items[at] = item[j];
+            else
+                cluster_store(cluster_addr(smem_u32(&sh.items[at % PER]), at / PER), item[j]);
         }
-        __syncthreads();
+        team_sync<C>();
         if (pass + 1 < passes) {
+            // with C > 1 the next pass's first barrier keeps others from writing here before this is read
 #pragma unroll
-            for (int j = 0; j < IPT; ++j) item[j] = sh.items[base + 32 * j];
-            __syncthreads();
+            for (int j = 0; j < IPT; ++j) item[j] = sh.items[local + 32 * j];
+            if (C == 1) __syncthreads();
         }
     }
     const uint32_t mask = (1u << bits) - 1u;
-    for (int i = threadIdx.x; i < n; i += kCtaThreads) idx_out[i] = (int)(sh.items[i] & mask);
-    const PackedKeys keys{sh.items, bits};
-    for (int i0 = warp * 32; i0 < n; i0 += kCtaThreads)
-        plan_places(keys, n, V, i0, groups, pieces, tickets, &sh.counts);
-    __syncthreads();
-    if (threadIdx.x == 0) *counts = sh.counts;
+    const int mine = min(PER, n - team * PER);  // may be negative
+    for (int i = threadIdx.x; i < mine; i += kTeamThreads) {
+        keys_out[team * PER + i] = sh.items[i] >> bits;
+        idx_out[team * PER + i] = (int)(sh.items[i] & mask);
+    }
+    __syncwarp();
+    const TeamKeys<C> keys{sh.items, bits, 31 - __clz(PER)};
+    for (int i0 = warp * 32; i0 < mine; i0 += kTeamThreads)
+        plan_places(keys, n, V, team * PER + i0, groups, pieces, tickets, C == 1 ? &sh.counts : counts);
+    __syncwarp();
+    team_sync<C>();  // nobody leaves while its memory is read
+    if (C == 1 && threadIdx.x == 0) *counts = sh.counts;
+}
+
+template <int IPT>
+__global__ void __launch_bounds__(kTeamThreads)
+embed_sort_cta_kernel(const void *tokens, int is64, int n, int V, int bits, int digit_bits, int passes, int groups,
+                      uint32_t *keys_out, int *idx_out, Piece *pieces, int *tickets, Counts *counts, const Fill fill) {
+    team_sort<1, IPT>(tokens, is64, n, V, bits, digit_bits, passes, groups, keys_out, idx_out, pieces, tickets, counts,
+                      fill);
+}
+template <int IPT>
+__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kTeamThreads)
+embed_sort_cluster_kernel(const void *tokens, int is64, int n, int V, int bits, int digit_bits, int passes, int groups,
+                          uint32_t *keys_out, int *idx_out, Piece *pieces, int *tickets, Counts *counts,
+                          const Fill fill) {
+    team_sort<8, IPT>(tokens, is64, n, V, bits, digit_bits, passes, groups, keys_out, idx_out, pieces, tickets, counts,
+                      fill);
 }
 
 // --------------------------------------------------------------------------
@@ -359,7 +414,7 @@ __global__ void __launch_bounds__(256) embed_hist_kernel(const SortArgs a, const
         fill_zero(fill, blockIdx.x - a.tiles, gridDim.x - a.tiles);
         return;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.counts = Counts{0, 0, 0, 0};
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.counts = Counts{0, 0, 0};
     const int i1 = min(a.n, (int)(blockIdx.x + 1) * a.tile);
 #pragma unroll 4
     for (int i = blockIdx.x * a.tile + threadIdx.x; i < i1; i += 256)
@@ -453,6 +508,7 @@ __global__ void __launch_bounds__(256) embed_plan_kernel(const uint32_t *keys, i
 // --------------------------------------------------------------------------
 struct SumArgs {
     const void *d_out;
+    const uint32_t *keys;
     const int *idx;
     const Piece *pieces;
     const Counts *counts;
@@ -461,29 +517,28 @@ struct SumArgs {
     float *acc;      // [V][D] fp32, or
     uint16_t *bf16;  // [V][D]
     float scale;
-    int accumulate, n, D;
+    int accumulate, n, V, D;
+    int places;  // of a task: 8, 16 or 32
 };
 
-// 8 columns of a row as they lie in memory, and added to a sum
-__device__ __forceinline__ void load8(uint4 &v, const uint16_t *p) { v = ldg16(p); }
+// 8 columns, added to a sum
 struct Floats8 {
     float4 a, b;
 };
-__device__ __forceinline__ void load8(Floats8 &v, const float *p) {
-    v.a = __ldcg(reinterpret_cast<const float4 *>(p));
-    v.b = __ldcg(reinterpret_cast<const float4 *>(p + 4));
-}
-__device__ __forceinline__ void add8(float (&s)[8], const uint4 &v) {
-    s[0] = __fadd_rn(s[0], bf16lo(v.x)), s[1] = __fadd_rn(s[1], bf16hi(v.x));
-    s[2] = __fadd_rn(s[2], bf16lo(v.y)), s[3] = __fadd_rn(s[3], bf16hi(v.y));
-    s[4] = __fadd_rn(s[4], bf16lo(v.z)), s[5] = __fadd_rn(s[5], bf16hi(v.z));
-    s[6] = __fadd_rn(s[6], bf16lo(v.w)), s[7] = __fadd_rn(s[7], bf16hi(v.w));
-}
 __device__ __forceinline__ void add8(float (&s)[8], const Floats8 &v) {
     s[0] = __fadd_rn(s[0], v.a.x), s[1] = __fadd_rn(s[1], v.a.y);
     s[2] = __fadd_rn(s[2], v.a.z), s[3] = __fadd_rn(s[3], v.a.w);
     s[4] = __fadd_rn(s[4], v.b.x), s[5] = __fadd_rn(s[5], v.b.y);
     s[6] = __fadd_rn(s[6], v.b.z), s[7] = __fadd_rn(s[7], v.b.w);
+}
+// ... of a ring's row: one 16-byte word of bf16, or two of fp32, 512 bytes apart
+__device__ __forceinline__ Floats8 ring_row(const uint16_t *p) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    return {make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y)),
+            make_float4(bf16lo(v.z), bf16hi(v.z), bf16lo(v.w), bf16hi(v.w))};
+}
+__device__ __forceinline__ Floats8 ring_row(const float *p) {
+    return {*reinterpret_cast<const float4 *>(p), *reinterpret_cast<const float4 *>(p + 128)};
 }
 
 // 8 columns of row `token` of the gradient
@@ -508,18 +563,15 @@ __device__ __forceinline__ void put_row(const SumArgs &a, int token, int col, co
     p[1] = hi;
 }
 
-// A piece of a longer run: leave its sum, and climb the run's tree while this
-// warp brings the last child of the node.  A call of its own: inlined, its
-// registers made the sums spill.
-__device__ __noinline__ void climb(const SumArgs &a, const int4 *tree, int token, int index, int col, float4 lo,
-                                   float4 hi) {
+// A piece of a long run: leave its sum, and climb the run's tree while this
+// warp brings the last child of the node.
+__device__ __forceinline__ void climb(const SumArgs &a, const int4 *tree, int token, int index, int col,
+                                      float (&s)[8]) {
     const int4 t = __ldcg(tree);
-    const int pieces = t.x;
-    int slot = t.y, node = t.z;
+    int count = t.x, slot = t.y, node = t.z;  // of the level
     const bool live = col < a.D;
-    float s[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     const int lane = threadIdx.x & 31, groups = gridDim.y, group = blockIdx.y;
-    int count = pieces;  // of the level
+#pragma unroll 1
     for (;;) {
         float *q = a.partial + (long long)(slot + index) * a.D + col;
         if (live) {
@@ -538,12 +590,16 @@ __device__ __noinline__ void climb(const SumArgs &a, const int4 *tree, int token
         for (int i = 0; i < 8; ++i) s[i] = 0.0f;
         if (live) {
             const float *c = a.partial + (long long)(slot + parent * kFan) * a.D + col;
+#pragma unroll 1
             for (int k0 = 0; k0 < children; k0 += 4) {
                 Floats8 v[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    v[k] = Floats8();
-                    if (k0 + k < children) load8(v[k], c + (long long)(k0 + k) * a.D);
+                    v[k] = Floats8();  // +0 behind the end: adding it changes no sum begun from +0
+                    if (k0 + k < children) {
+                        const float4 *f = reinterpret_cast<const float4 *>(c + (long long)(k0 + k) * a.D);
+                        v[k] = {__ldcg(f), __ldcg(f + 1)};
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) add8(s, v[k]);
@@ -558,60 +614,114 @@ __device__ __noinline__ void climb(const SumArgs &a, const int4 *tree, int token
     if (live) put_row(a, token, col, s);
 }
 
-// A warp per (piece, 256 columns); blockIdx.y is the column group.
-template <typename T, typename Vec, int U>
-__global__ void __launch_bounds__(256, 4) embed_sum_kernel(const __grid_constant__ SumArgs a) {
-    const int lane = threadIdx.x & 31;
+// A warp per (piece of a long run | short runs that begin at a.places places,
+// 256 columns); blockIdx.y is the column group.  A lane copies its 8 columns of
+// the task's rows asynchronously into a ring of its own, 8 KB a warp: all that
+// the SM can have in flight, whatever the lengths of the runs.  (One run at a
+// time, its rows in registers, took 40 us for 32768 rows of 1024 in runs of
+// mostly one or two.)
+constexpr int kSumWarps = 8;
+constexpr int kRingBytes = 8192;  // of a warp
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kSumWarps, 3) embed_sum_kernel(const __grid_constant__ SumArgs a) {
+    constexpr int R = kRingBytes / (256 * (int)sizeof(T));  // rows of the ring
+    extern __shared__ __align__(16) unsigned char ring_bytes[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // row r at mine + r * 256: the lane's 8 columns, in 16-byte words 512 bytes
+    // apart (fp32: two words)
+    T *ring = reinterpret_cast<T *>(ring_bytes + warp * kRingBytes);
     const int col = blockIdx.y * 256 + lane * 8;
     const bool live = col < a.D;
     // lanes behind the last column read along with the first and write nothing
     const T *d_out = static_cast<const T *>(a.d_out) + (live ? col : 0);
     pdl_wait();
     pdl_trigger();
-    const int4 counts = __ldcg(reinterpret_cast<const int4 *>(a.counts));
-    const int longs = counts.y, total = counts.x + longs;
-    // the next piece's entry and places are loaded while this one's rows are
-    const auto entry = [&](int i) {
-        return reinterpret_cast<const int4 *>(a.pieces + (i < longs ? i : a.n - 1 - (i - longs)));
-    };
-    int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int step = gridDim.x * 8;
-    if (i >= total) return;
-    int4 p = __ldcg(entry(i));
-    int mine = lane < p.z ? __ldcg(a.idx + p.y + lane) : 0;
+    const int longs = __ldcg(&a.counts->pieces), total = longs + (a.n + a.places - 1) / a.places;
 #pragma unroll 1
-    for (; i < total; i += step) {
-        const int len = p.z;
-        int4 p_next = p;
-        if (i + step < total) p_next = __ldcg(entry(i + step));
-        float s[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s[k] = 0.0f;
-#pragma unroll 1
-        for (int r0 = 0; r0 < len; r0 += U) {
-            Vec v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int row = __shfl_sync(0xFFFFFFFFu, mine, (r0 + u) & 31);
-                v[u] = Vec();  // +0 behind the end: adding it changes no sum begun from +0
-                if (r0 + u < len) load8(v[u], d_out + (long long)row * a.D);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) add8(s, v[u]);
+    for (int task = blockIdx.x * kSumWarps + warp; task < total; task += gridDim.x * kSumWarps) {
+        // the task's places: [begin, end) of the 64 from `base`, two a lane;
+        // bit i of `heads`: a run begins at place base + i
+        int base, begin = 0, end;
+        unsigned long long heads = 1;
+        int4 piece = make_int4(0, 0, 0, 0);
+        uint32_t key = 0, key2 = 0;
+        if (task < longs) {
+            piece = __ldcg(reinterpret_cast<const int4 *>(a.pieces + task));
+            base = piece.y;
+            end = piece.z;
+        } else {
+            base = (task - longs) * a.places;
+            key = base + lane < a.n ? __ldcg(a.keys + base + lane) : 0xFFFFFFFFu;
+            key2 = base + 32 + lane < a.n ? __ldcg(a.keys + base + 32 + lane) : 0xFFFFFFFFu;
         }
-        mine = lane < p_next.z ? __ldcg(a.idx + p_next.y + lane) : 0;
-        if (p.w >= 0)
-            climb(a, entry(i) + 1, p.x, p.w, col, make_float4(s[0], s[1], s[2], s[3]),
-                  make_float4(s[4], s[5], s[6], s[7]));
-        else if (live)
-            put_row(a, p.x, col, s);
-        p = p_next;
+        const int at = base + lane < a.n ? __ldcg(a.idx + base + lane) : 0;
+        const int at2 = base + 32 + lane < a.n ? __ldcg(a.idx + base + 32 + lane) : 0;
+        if (task >= longs) {
+            uint32_t prev = __shfl_up_sync(0xFFFFFFFFu, key, 1), prev2 = __shfl_up_sync(0xFFFFFFFFu, key2, 1);
+            const uint32_t key31 = __shfl_sync(0xFFFFFFFFu, key, 31);
+            if (lane == 0) prev = base > 0 ? __ldcg(a.keys + base - 1) : 0xFFFFFFFFu, prev2 = key31;
+            heads = __ballot_sync(0xFFFFFFFFu, key != prev) |
+                    (unsigned long long)__ballot_sync(0xFFFFFFFFu, key2 != prev2) << 32;
+            const unsigned long long mine = heads & ((1ull << a.places) - 1);
+            if (mine == 0) continue;
+            begin = __ffsll((long long)mine) - 1;
+            const int last = 63 - __clzll((long long)mine);  // the last run begins here
+            const unsigned long long behind = heads >> (last + 1);  // last < 32
+            end = behind ? last + __ffsll((long long)behind) : 64;
+            // a long last run, and padding (which sorts last), are left out
+            if (end - last > kPiece) end = last;
+            const int tokens = __popc(__ballot_sync(0xFFFFFFFFu, key < (uint32_t)a.V)) +
+                               __popc(__ballot_sync(0xFFFFFFFFu, key2 < (uint32_t)a.V));
+            end = min(end, tokens);
+        }
+        const auto copy = [&](int r) {  // place r of the task
+            if (r < end) {
+                const int row = __shfl_sync(0xFFFFFFFFu, r < 32 ? at : at2, r & 31);
+                const T *src = d_out + (long long)row * a.D;
+                T *dst = ring + (r % R) * 256 + lane * (16 / (int)sizeof(T));
+#pragma unroll
+                for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+                    cp_async16(dst + j * 128, src + j * (16 / (int)sizeof(T)));
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll 1
+        for (int r = begin; r < begin + R - 1; ++r) copy(r);
+        float s[8];
+        int first = begin;  // of the current run
+#pragma unroll 1
+        for (int r = begin; begin < end; ++r) {
+            if (r == end || ((heads >> r) & 1)) {
+                if (r > begin) {
+                    if (task < longs) {
+                        climb(a, reinterpret_cast<const int4 *>(a.pieces + task) + 1, piece.x, piece.w, col, s);
+                    } else {
+                        const int token = (int)__shfl_sync(0xFFFFFFFFu, first < 32 ? key : key2, first & 31);
+                        if (live) put_row(a, token, col, s);
+                    }
+                }
+                if (r == end) break;
+                first = r;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) s[k] = 0.0f;
+            }
+            asm volatile("cp.async.wait_group %0;" ::"n"(R - 2) : "memory");
+            const T *p = ring + (r % R) * 256 + lane * (16 / (int)sizeof(T));
+            add8(s, ring_row(p));
+            copy(r + R - 1);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
 }
 
-// Workspace.  A run of several pieces has at least 33 places, so all such runs
-// together have at most 2 n / 33 pieces; each run's partial sums are at most
-// 9/8 of its pieces, its nodes at most 1 + pieces / 8 (tree_size).
+// Workspace.  A long run has at least 33 places, so all long runs together have
+// at most 2 n / 33 pieces; each run's partial sums are at most 9/8 of its pieces,
+// its nodes at most 1 + pieces / 8 (tree_size).
 struct Layout {
     size_t counts, pieces, keys, idx, hist, tickets, partial, bytes;
 };
@@ -625,7 +735,7 @@ Layout layout(int n, int D) {
     };
     const size_t groups = (size_t)(D + 255) / 256, N = (size_t)n;
     l.counts = take(sizeof(Counts));
-    l.pieces = take(N * sizeof(Piece));
+    l.pieces = take((N * 2 / 33 + 1) * sizeof(Piece));
     l.keys = take(N * 2 * sizeof(uint32_t));
     l.idx = take(N * 2 * sizeof(int));
     l.hist = take((size_t)kMaxTiles * kDigits * sizeof(int));
@@ -647,16 +757,23 @@ int fill_ctas(long long vecs, int threads, const DeviceInfo &dev) {
     return (int)(c < most ? c : most);
 }
 
-template <int IPT>
-cudaError_t sort_cta(const void *tokens, int is64, int n, int V, int bits, int digit_bits, int passes, int groups,
-                     int *idx, Piece *pieces, int *tickets, Counts *counts, const Fill &fill, cudaStream_t stream,
-                     const DeviceInfo &dev) {
-    const size_t smem = sizeof(CtaShared) + (size_t)IPT * kCtaThreads * sizeof(uint32_t);
-    const cudaError_t e = ensure_smem_attr((const void *)embed_sort_cta_kernel<IPT>, smem, dev);
+// C CTAs sort (C = 1 or 8), the others zero
+template <int C, int IPT>
+cudaError_t sort_team(const void *tokens, int is64, int n, int V, int bits, int digit_bits, int passes, int groups,
+                      uint32_t *keys, int *idx, Piece *pieces, int *tickets, Counts *counts, const Fill &fill, cudaStream_t stream,
+                      const DeviceInfo &dev) {
+    const auto kernel = []() {
+        if constexpr (C == 1)
+            return embed_sort_cta_kernel<IPT>;
+        else
+            return embed_sort_cluster_kernel<IPT>;
+    }();
+    const size_t smem = sizeof(TeamShared) + (size_t)IPT * kTeamThreads * sizeof(uint32_t);
+    const cudaError_t e = ensure_smem_attr((const void *)kernel, smem, dev);
     if (e != cudaSuccess) return e;
-    return launch_pdl(embed_sort_cta_kernel<IPT>, dim3(1 + fill_ctas(fill.vecs, kCtaThreads, dev)), dim3(kCtaThreads),
-                      smem, stream, tokens, is64, n, V, bits, digit_bits, passes, groups, idx, pieces, tickets, counts,
-                      fill);
+    const int zeroing = (fill_ctas(fill.vecs, kTeamThreads, dev) + C - 1) / C * C;
+    return launch_pdl(kernel, dim3(C + zeroing), dim3(kTeamThreads), smem, stream, tokens, is64, n, V, bits,
+                      digit_bits, passes, groups, keys, idx, pieces, tickets, counts, fill);
 }
 
 }  // namespace
@@ -691,10 +808,15 @@ cudaError_t launch_embed_bwd(const T *d_out, const void *tokens, int tokens_are_
     Fill fill = {d_table ? reinterpret_cast<uint4 *>(d_table) : reinterpret_cast<uint4 *>(d_table_acc),
                  accumulate ? 0 : (long long)V * D * (d_table ? 2 : 4) / 16};
     cudaError_t e = cudaSuccess;
-    if (n <= kCtaTokens && key_bits + bits <= 32) {
+    // In shared memory where a token and a place fit 32 bits: by one CTA up to
+    // 4 tokens a thread, then by a cluster of 8, up to 16 a thread.
+    if (n <= 8 * 16 * kTeamThreads && key_bits + bits <= 32) {
         const int passes = (key_bits + 7) / 8, digit_bits = (key_bits + passes - 1) / passes;
-        e = sort_cta<kCtaTokens / kCtaThreads>(tokens, tokens_are_64, n, V, bits, digit_bits, passes, groups,
-                                               idx, pieces, tickets, counts, fill, stream, dev);
+        auto sort = n <= 4 * kTeamThreads       ? sort_team<1, 4>
+                    : n <= 8 * 4 * kTeamThreads ? sort_team<8, 4>
+                                                : sort_team<8, 16>;
+        e = sort(tokens, tokens_are_64, n, V, bits, digit_bits, passes, groups, keys, idx, pieces, tickets, counts,
+                 fill, stream, dev);
         if (e != cudaSuccess) return e;
     } else {
         SortArgs s = {};
@@ -732,15 +854,17 @@ cudaError_t launch_embed_bwd(const T *d_out, const void *tokens, int tokens_are_
                            f);
             if (e != cudaSuccess) return e;
         }
+        keys = s.keys_out;
         idx = s.idx_out;
         const Fill f = next();
         const int ctas = (n + 255) / 256;
         e = launch_pdl(embed_plan_kernel, dim3(ctas + fill_ctas(f.vecs, 256, dev)), dim3(256), 0, stream,
-                       (const uint32_t *)s.keys_out, n, V, groups, pieces, tickets, counts, ctas, f);
+                       (const uint32_t *)keys, n, V, groups, pieces, tickets, counts, ctas, f);
         if (e != cudaSuccess) return e;
     }
     SumArgs a = {};
     a.d_out = d_out;
+    a.keys = keys;
     a.idx = idx;
     a.pieces = pieces;
     a.counts = counts;
@@ -751,12 +875,19 @@ cudaError_t launch_embed_bwd(const T *d_out, const void *tokens, int tokens_are_
     a.scale = scale;
     a.accumulate = accumulate;
     a.n = n;
+    a.V = V;
     a.D = D;
-    // as many CTAs as the device holds, no more than pieces can be
-    const int most = (n + 7) / 8, want = (4 * dev.sm_count + groups - 1) / groups;
-    const dim3 grid(most < want ? most : want, groups);
-    if (sizeof(T) == 2) return launch_pdl(embed_sum_kernel<uint16_t, uint4, 8>, grid, dim3(256), 0, stream, a);
-    return launch_pdl(embed_sum_kernel<float, Floats8, 4>, grid, dim3(256), 0, stream, a);
+    // as many CTAs as the device holds; as many places a task as still give
+    // every warp of them two
+    const int want = (3 * dev.sm_count + groups - 1) / groups;
+    a.places = 8;
+    while (a.places < 32 && (long long)n >= 4ll * a.places * want * kSumWarps) a.places *= 2;
+    const long long most = (long long)n / (a.places * kSumWarps) + n / (kPiece * kSumWarps) + 1;
+    const dim3 grid((unsigned)(most < want ? most : want), groups);
+    const size_t smem = kSumWarps * kRingBytes;
+    e = ensure_smem_attr((const void *)embed_sum_kernel<T>, smem, dev);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(embed_sum_kernel<T>, grid, dim3(32 * kSumWarps), smem, stream, a);
 }
 
 template cudaError_t launch_embed_fwd<uint16_t>(const void *, int, const uint16_t *, float, uint16_t *, int, int, int,

@@ -256,14 +256,15 @@ __global__ void __launch_bounds__(32 * kWarps) heads_fwd_kernel(const __grid_con
 // U * 32/LPR heads) tasks, in order, and copies their rows asynchronously into
 // a ring of kStages tasks of its own, so that the bytes in flight are not held
 // in registers.  (With the rows in registers the backward
-// was bound by load latency at 18 warps an SM: 70 us against NNN at B=2, S=4096,
-// 24 + 24 heads of 128 in bf16.)  A token's angles travel with its tasks; its
+// was bound by load latency at 18 warps an SM: 70 us against 60 at B=2, S=4096,
+// 24 + 24 heads of 128 in bf16; 2, 3 and 4 rows a lane and 3 or 4 stages differ
+// by 2 %.)  A token's angles travel with its tasks; its
 // position is read one token ahead.
 //
 // Backward: each lane keeps the dw sums of its 8 channels, joined over the CTA
 // in a fixed order into the tile's partial.
 // --------------------------------------------------------------------------
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
     // a size of 0 reads nothing and fills with zeros
@@ -300,7 +301,7 @@ struct Stage {
 };
 
 template <typename T, int LPR, int U, bool INTER, bool BWD>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? (BWD ? 5 : 6) : 3)
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? (BWD ? 5 : 7) : 3)
 heads_tile_kernel(const __grid_constant__ HeadsArgs a) {
     using St = Stage<T, LPR, U, BWD>;
     constexpr int RPW = 32 / LPR;
@@ -490,19 +491,19 @@ __global__ void __launch_bounds__(1024) heads_fold_kernel(const FoldArgs a) {
     float sum[NB];
 #pragma unroll
     for (int k = 0; k < NB; ++k) sum[k] = 0.0f;
-    for (int i0 = grp; i0 < a.tiles; i0 += 4 * 128) {
-        float v[NB][4];
+    for (int i0 = grp; i0 < a.tiles; i0 += 2 * 128) {
+        float v[NB][2];
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const int i = i0 + j * 128;
                 v[k][j] = 0.0f;  // +0 behind the end: adding it changes no sum begun from +0
                 if (k < nb && i < a.tiles) v[k][j] = __ldcg(p + k * sample + (long long)i * 2 * a.Dh);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
             for (int k = 0; k < NB; ++k) sum[k] = __fadd_rn(sum[k], v[k][j]);
         }
@@ -591,10 +592,26 @@ int tile_rows(int Hq, int Hk, int Dh) {
     return h > 32 / lanes_per_row(Dh) ? 2 : 1;
 }
 
+// Tokens of a tile with about `tasks` tasks; fewer where a sample has few, so
+// that it still spreads over the SMs.
+int tile_tokens(int tasks, int S, int Hq, int Hk, int Dh) {
+    const int group = tile_rows(Hq, Hk, Dh) * (32 / lanes_per_row(Dh)), h = Hq > Hk ? Hq : Hk;
+    const int chunks = (h + group - 1) / group;
+    const int most = chunks >= tasks ? 1 : tasks / chunks, spread = S < 64 ? 1 : S / 64;
+    return most < spread ? most : spread;
+}
+// Backward: 48 tasks a CTA, 12 a warp, fill the ring and pay for joining dw (24:
+// 64 us, 96: 66 us against 60 at the size above).  It is fixed by S, the head
+// counts and the head size, and with it the order of dw.
+int bwd_tile(int S, int Hq, int Hk, int Dh) { return tile_tokens(48, S, Hq, Hk, Dh); }
+// Forward: 24, for a finer tail (fp32, 4593 tokens of 20 + 4 heads of 96: 15.8 us
+// against 17.4 with 48).
+int fwd_tile(int S, int Hq, int Hk, int Dh) { return tile_tokens(24, S, Hq, Hk, Dh); }
+
 template <typename T, int LPR, int U, bool INTER, bool BWD>
 cudaError_t run_tile(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &dev) {
     HeadsArgs a = make_args(c, U * (32 / LPR));
-    a.tile = heads_tile_tokens(c.S, c.H[0], c.H[1], c.Dh);
+    a.tile = (BWD ? bwd_tile : fwd_tile)(c.S, c.H[0], c.H[1], c.Dh);
     a.tiles = (c.S + a.tile - 1) / a.tile;
     a.part = BWD && (c.dw[0] || c.dw[1]) ? c.ws : nullptr;
     constexpr size_t smem = Stage<T, LPR, U, BWD>::kSmem;
@@ -631,28 +648,20 @@ cudaError_t run_direct(const HeadsCall &c, cudaStream_t stream) {
 template <typename T, int LPR>
 cudaError_t pick_fwd(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &dev) {
     // Few rows go one a lane straight through registers, for the shortest path
-    // through the kernel; then 4 a lane, once that gives every SM 16 warps; and
-    // through the ring where a tile has 4 tasks or more for each warp.
+    // through the kernel (8 tokens of 24 + 24 heads: 3.6 us of kernel); from 16
+    // warps an SM on 4 a lane, or through the ring where a tile has 4 tasks or
+    // more for each warp (at the size above 35.7 us against 41).
     const long long rows = (long long)c.B * c.S * (c.H[0] + c.H[1]);
     if (rows / (4 * (32 / LPR)) < 16ll * dev.sm_count) return run_direct<T, LPR, 1>(c, stream);
-    const int tile = heads_tile_tokens(c.S, c.H[0], c.H[1], c.Dh), group = tile_rows(c.H[0], c.H[1], c.Dh) * (32 / LPR);
+    const int tile = fwd_tile(c.S, c.H[0], c.H[1], c.Dh), group = tile_rows(c.H[0], c.H[1], c.Dh) * (32 / LPR);
     if ((long long)tile * ((c.H[0] + group - 1) / group) < 4 * kWarps) return run_direct<T, LPR, 4>(c, stream);
     return pick_tile<T, LPR, false>(c, stream, dev);
 }
 
 }  // namespace
 
-int heads_tile_tokens(int S, int Hq, int Hk, int Dh) {
-    // 48 tasks a CTA, 12 a warp: enough to fill the ring and to pay for joining
-    // dw; fewer tokens where a sample has few, so that it still spreads over the SMs
-    const int group = tile_rows(Hq, Hk, Dh) * (32 / lanes_per_row(Dh)), h = Hq > Hk ? Hq : Hk;
-    const int chunks = (h + group - 1) / group;
-    const int most = chunks >= 48 ? 1 : 48 / chunks, spread = S < 128 ? 1 : S / 128;
-    return most < spread ? most : spread;
-}
-
 size_t heads_bwd_ws_floats(int B, int S, int Hq, int Hk, int Dh) {
-    const int tile = heads_tile_tokens(S, Hq, Hk, Dh);
+    const int tile = bwd_tile(S, Hq, Hk, Dh);
     const size_t tiles = ((size_t)S + tile - 1) / tile;
     return (size_t)B * (tiles + 1) * 2 * Dh;
 }
@@ -684,7 +693,7 @@ cudaError_t launch_heads_bwd(const HeadsCall &c, cudaStream_t stream, const Devi
     f.B = c.B;
     f.Dh = c.Dh;
     f.accumulate = c.accumulate;
-    const int tile = heads_tile_tokens(c.S, c.H[0], c.H[1], c.Dh);
+    const int tile = bwd_tile(c.S, c.H[0], c.H[1], c.Dh);
     f.tiles = (c.S + tile - 1) / tile;
     f.sums = c.ws + (size_t)c.B * f.tiles * 2 * c.Dh;
     const unsigned cols = c.Dh / 8;

@@ -27,8 +27,6 @@ struct HeadsCall {
     int accumulate;
     float *ws;
 };
-// tokens of a tile: fixed by S, the head counts and the head size only
-int heads_tile_tokens(int S, int Hq, int Hk, int Dh);
 size_t heads_bwd_ws_floats(int B, int S, int Hq, int Hk, int Dh);
 template <typename T>
 cudaError_t launch_heads_fwd(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &dev);

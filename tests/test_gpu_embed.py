@@ -49,13 +49,17 @@ def test_lookup(n, V, D, dtype):
         assert torch.equal(FWD[dtype](t.to(torch.int32), table, scale=scale), want)
 
 
-# around the sizes of the one-CTA sort (4, 16 and 32 tokens a thread; token and
-# place in 32 bits) and the larger one (tiles of 1024), one to three digits, one
-# occurrence to all, trees of one to three levels
+# around the sizes of the sorts (one CTA to 4096, a cluster to 32768 and 131072 if
+# token and place fit 32 bits, kernels over tiles of 1024), one to three digits,
+# one occurrence to all, trees of one to three levels
 BACK = [(1, 1, 8, "even"), (31, 4, 16, "even"), (32, 3, 8, "one"), (33, 3, 8, "one"), (500, 40, 264, "even"),
         (1000, 255, 8, "skew"), (1000, 256, 8, "skew"), (4096, 257, 40, "skew"), (4097, 65535, 24, "skew"),
         (9000, 65536, 16, "skew"), (20000, 200, 8, "even"), (6000, 300000, 8, "even"), (4096, 1001, 16, "one"),
-        (8192, 2, 8, "one"), (300, 65535, 8, "none"), (5000, 10, 8, "none"), (700, 1 << 24, 8, "even")]
+        (8192, 2, 8, "one"), (16384, 500, 8, "skew"), (16385, 70000, 8, "skew"),
+        (32768, 130000, 8, "skew"), (32769, 3, 8, "skew"), (32768, 131071, 8, "even"), (32768, 131072, 8, "even"),
+        (40000, 1, 8, "one"), (2000, (1 << 21) - 1, 8, "even"), (2000, 1 << 21, 8, "even"),
+        (131072, 32767, 8, "skew"), (131072, 32768, 8, "skew"), (131073, 500, 8, "skew"), (100000, 20000, 8, "even"),
+        (300, 65535, 8, "none"), (5000, 10, 8, "none"), (700, 1 << 24, 8, "even")]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
