@@ -205,13 +205,13 @@ typedef struct adaln_tensor {
 } adaln_tensor;
 
 /* Workspace bytes adaln_grad_norm and adaln_grad_clip need: 8 bytes for each
- * 32 KB of each tensor.  0 for a list that the calls refuse. */
+ * 16 KB of each tensor.  0 for a list that the calls refuse. */
 size_t adaln_grad_norm_workspace_bytes(const adaln_tensor *grads, int count);
 
 /*
  * adaln_grad_norm — norm[0] = sqrt(sum over all elements of all tensors of x^2).
  *
- * Squares are summed in fp32 within 32 KB of a tensor (in fp64 where fp32 would
+ * Squares are summed in fp32 within 16 KB of a tensor (in fp64 where fp32 would
  * overflow or lose them), then in pairs of fp32 with the additions' errors (or in
  * fp64).  The order is fixed by the list's sizes
  * and types alone, not by addresses.  The result is infinite or NaN exactly as

@@ -518,7 +518,7 @@ struct SumArgs {
     uint16_t *bf16;  // [V][D]
     float scale;
     int accumulate, n, V, D;
-    int places;  // of a task: 8, 16 or 32
+    int places;  // of a task: 16 or 32
 };
 
 // 8 columns, added to a sum
@@ -877,11 +877,11 @@ cudaError_t launch_embed_bwd(const T *d_out, const void *tokens, int tokens_are_
     a.n = n;
     a.V = V;
     a.D = D;
-    // as many CTAs as the device holds; as many places a task as still give
-    // every warp of them two
+    // as many CTAs as the device holds; 16 places a task (4096 labels of 3072
+    // columns: 21.2 us against 24.5 with 8 and 27 with 4), or 32 where that still
+    // gives every warp two tasks
     const int want = (3 * dev.sm_count + groups - 1) / groups;
-    a.places = 8;
-    while (a.places < 32 && (long long)n >= 4ll * a.places * want * kSumWarps) a.places *= 2;
+    a.places = (long long)n >= 2ll * 32 * want * kSumWarps ? 32 : 16;
     const long long most = (long long)n / (a.places * kSumWarps) + n / (kPiece * kSumWarps) + 1;
     const dim3 grid((unsigned)(most < want ? most : want), groups);
     const size_t smem = kSumWarps * kRingBytes;

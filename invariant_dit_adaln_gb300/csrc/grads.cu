@@ -4,12 +4,13 @@
 //   norm = sqrt(sum x^2),  coef = min(1, max_norm / (norm + 1e-6)),  out = coef x
 //
 // Bound by HBM: the norm reads every byte once, clipping reads it again and
-// writes it.  One CTA takes one 32 KB piece of one tensor (8 16-byte loads in
-// flight per thread); the list travels in the kernel's parameters, so nothing
+// writes it.  One CTA takes one 16 KB piece of one tensor (4 16-byte loads in
+// flight per thread; with 32 KB 60 ragged tensors of 120 MB take 76 us instead of
+// 72, and 1.2 GB 607 instead of 611); the list travels in the kernel's parameters, so nothing
 // is copied to the device first and the launch can be captured.  A piece's
-// squares are summed in fp32 (16 or 8 terms in each of a thread's four chains,
+// squares are summed in fp32 (8 or 4 terms in each of a thread's four chains,
 // then a fixed butterfly), the pieces' sums in compensated fp32 pairs (one SM
-// adds fp64 at a few values a cycle: in fp64 the join of 36,864 pieces took 20
+// adds fp64 at a few values a cycle: in fp64 the join of 36,864 sums took 20
 // us), and in fp64 where the range asks for it.  An element's thread and chain
 // depend on its index in the tensor alone, never on an address.
 #include "common.cuh"
@@ -20,7 +21,7 @@ namespace adaln {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVecs = kGradPieceBytes / 16 / kThreads;  // 16-byte vectors of a thread: 8
+constexpr int kVecs = kGradPieceBytes / 16 / kThreads;  // 16-byte vectors of a thread: 4
 
 // Tensors of one launch; first[i] is the index of tensor i's first piece.
 template <int N>
@@ -142,8 +143,8 @@ __device__ __forceinline__ double warp_sum_f64(double v) {
 }
 
 // Below this a piece's fp32 sum may have lost squares to underflow: a square
-// that fp32 rounds or flushes is off by at most 2^-126, 2^14 of them by
-// 2^-112, which is 2^-32 of the smallest sum kept.
+// that fp32 rounds or flushes is off by at most 2^-126, 2^13 of them by
+// 2^-113, which is 2^-33 of the smallest sum kept.
 constexpr float kLeastSum = 0x1p-80f;
 
 // A piece's sum in fp64, read again: rare, so it holds no registers elsewhere.

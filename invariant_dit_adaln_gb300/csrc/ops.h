@@ -44,8 +44,8 @@ cudaError_t launch_embed_bwd(const T *d_out, const void *tokens, int tokens_are_
                              const DeviceInfo &dev);
 
 // grads.cu --------------------------------------------------------------------
-// 32 KB pieces of a tensor of `numel` elements
-constexpr int64_t kGradPieceBytes = 32768;
+// 16 KB pieces of a tensor of `numel` elements
+constexpr int64_t kGradPieceBytes = 16384;
 inline int64_t grad_pieces(const adaln_tensor &t) {
     const int64_t per = kGradPieceBytes / (t.dtype == ADALN_BF16 ? 2 : 4);
     return (t.numel + per - 1) / per;

@@ -58,7 +58,7 @@ BACK = [(1, 1, 8, "even"), (31, 4, 16, "even"), (32, 3, 8, "one"), (33, 3, 8, "o
         (8192, 2, 8, "one"), (16384, 500, 8, "skew"), (16385, 70000, 8, "skew"),
         (32768, 130000, 8, "skew"), (32769, 3, 8, "skew"), (32768, 131071, 8, "even"), (32768, 131072, 8, "even"),
         (40000, 1, 8, "one"), (2000, (1 << 21) - 1, 8, "even"), (2000, 1 << 21, 8, "even"),
-        (131072, 32767, 8, "skew"), (131072, 32768, 8, "skew"), (131073, 500, 8, "skew"), (100000, 20000, 8, "even"),
+        (131072, 32767, 8, "one"), (131072, 32768, 8, "one"), (131072, 1500, 8, "skew"), (131073, 500, 8, "skew"), (100000, 2000, 8, "even"),
         (300, 65535, 8, "none"), (5000, 10, 8, "none"), (700, 1 << 24, 8, "even")]
 
 

@@ -75,3 +75,35 @@ def test_training_step():
     graph.replay()
     assert torch.equal(got["stats"], r["stats"])
     assert all(torch.equal(a, c) for a, c in zip(got["clipped"], r["clipped"]))
+
+
+def test_calls_at_once():
+    """Calls on two streams, each with its own workspace and outputs, give the bits of the calls one by one."""
+    lib()
+    g = torch.Generator().manual_seed(3)
+    sets = []
+    for seed in range(2):
+        n, V, D = (3000, 200, 512) if seed else (9000, 5000, 256)
+        t = torch.randint(-1, V, (n,), generator=g).cuda()
+        d = torch.randn((n, D), generator=g).to(torch.bfloat16).cuda()
+        q = torch.randn((2, 300, 8, 64), generator=g).to(torch.bfloat16).cuda()
+        cos, sin = torch.rand((300, 32), generator=g).cuda(), torch.rand((300, 32), generator=g).cuda()
+        sets.append((t, d, V, q, cos, sin))
+
+    def run(t, d, V, q, cos, sin):
+        table = b.adaln_embed_bwd(d, t, V)
+        dq, _, dw, _ = b.adaln_qk_norm_rope_bwd(q, None, q, None, None, None, cos, sin)
+        outs, stats = b.adaln_grad_clip([table, dw], 0.1)
+        return [table, dq, dw, *outs, stats]
+
+    want = [run(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for k in range(20):
+        with torch.cuda.stream(streams[k % 2]):
+            got.append(run(*sets[k % 2]))
+    torch.cuda.synchronize()
+    for k, r in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(r, want[k % 2]))
