@@ -32,6 +32,7 @@ struct GradList {
     int first[N + 1];
     unsigned char bf16[N];
     int count;
+    int in_place;    // out is in, for every tensor
     long long base;  // pieces of the launches before this one
     float2 *part;  // a piece's sum is x * 2^y, y = 0 but for sums outside fp32's range
     const float *stats;
@@ -329,15 +330,18 @@ __device__ void piece_scale(const char *base, char *out, long long numel, int pi
     if (tail + at < bytes) scale_one<E>(src + tail + at, dst + tail + at, c);
 }
 
+// One CTA a piece here too: as many CTAs as the device holds, each over several
+// pieces, took 660 us instead of 607 for 1.2 GB.
 template <int N>
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ GradList<N> a) {
+    pdl_wait();
+    pdl_trigger();
+    const float c = __ldcg(a.stats + 1);
+    if (c == 1.0f && a.in_place) return;
     // last pieces first: the norm read them last, so L2 still holds them
     const int at = (int)(gridDim.x - 1 - blockIdx.x);
     const int t = find_tensor(a, at);
     const int piece = at - a.first[t];
-    pdl_wait();
-    pdl_trigger();
-    const float c = __ldcg(a.stats + 1);
     if (c == 1.0f && a.in[t] == a.out[t]) return;
     if (a.bf16[t])
         piece_scale<2>(static_cast<const char *>(a.in[t]), static_cast<char *>(a.out[t]), a.numel[t], piece, c);
@@ -350,6 +354,7 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
 template <int N>
 int fill(GradList<N> &a, const adaln_tensor *in, const adaln_tensor *out, int from, int count) {
     a.count = 0;
+    a.in_place = 1;
     a.first[0] = 0;
     int i = from;
     for (; i < count && a.count < N; ++i) {
@@ -358,6 +363,7 @@ int fill(GradList<N> &a, const adaln_tensor *in, const adaln_tensor *out, int fr
         if ((int64_t)a.first[a.count] + pieces > 0x7FFFFFFF) break;
         a.in[a.count] = in[i].data;
         a.out[a.count] = out ? out[i].data : nullptr;
+        if (a.out[a.count] != a.in[a.count]) a.in_place = 0;
         a.numel[a.count] = in[i].numel;
         a.bf16[a.count] = in[i].dtype == ADALN_BF16;
         a.first[a.count + 1] = a.first[a.count] + (int)pieces;
