@@ -266,8 +266,11 @@ __global__ void __launch_bounds__(32 * kWarps) heads_fwd_kernel(const __grid_con
 // --------------------------------------------------------------------------
 constexpr int kStages = 3;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
-    // a size of 0 reads nothing and fills with zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes, or zeros without reading
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -276,17 +279,27 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The rows of one task of one tensor into dst (U * 32/LPR rows of LPR * 8
-// elements); lane l of a row copies its channels 8 l .. 8 l + 7.
-template <typename T, int LPR, int U>
-__device__ __forceinline__ void copy_rows(uint32_t dst, const T *src, long long step, int rows, int l, int sub) {
-    constexpr int RPW = 32 / LPR;
+// The rows of one task of one tensor: the lane's 8 channels of rows src, src +
+// step, ... to dst, dst + (a warp's rows), ...; `all`: every lane has all U of them,
+// otherwise u < rows.
+template <typename T, int U>
+__device__ __forceinline__ void copy_rows(uint32_t dst, const T *src, long long step, bool all, int rows) {
+    constexpr int E = 16 / (int)sizeof(T);
+    if (all) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int j = 0; j < (int)sizeof(T) / 2; ++j)
-            cp_async16(dst + ((u * RPW + sub) * LPR * 8 + 8 * l + j * (16 / (int)sizeof(T))) * (int)sizeof(T),
-                       src + (u < rows ? u * step + 8 * l + j * (16 / (int)sizeof(T)) : 0), u < rows);
+            for (int j = 0; j < 8 / E; ++j)
+                cp_async16(dst + u * 256 * (int)sizeof(T) + 16 * j, src + u * step + E * j);
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int j = 0; j < 8 / E; ++j)
+                cp_async16_if(dst + u * 256 * (int)sizeof(T) + 16 * j, src + (u < rows ? u * step + E * j : 0),
+                              u < rows);
+        }
     }
 }
 
@@ -301,7 +314,7 @@ struct Stage {
 };
 
 template <typename T, int LPR, int U, bool INTER, bool BWD>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? (BWD ? 5 : 7) : 3)
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? (BWD ? (LPR == 32 ? 4 : 5) : 7) : 4)
 heads_tile_kernel(const __grid_constant__ HeadsArgs a) {
     using St = Stage<T, LPR, U, BWD>;
     constexpr int RPW = 32 / LPR;
@@ -312,7 +325,6 @@ heads_tile_kernel(const __grid_constant__ HeadsArgs a) {
     const int nchunk = a.chunks[t];
     if (nchunk == 0) return;  // no keys
     unsigned char *ring = ring_bytes + warp * (kStages * St::kBytes);
-    const uint32_t ring_u32 = smem_u32(ring);
     const int s0 = blockIdx.x * a.tile;
     const int ntask = min(a.tile, a.S - s0) * nchunk;
     const long long b = blockIdx.z;
@@ -329,35 +341,44 @@ heads_tile_kernel(const __grid_constant__ HeadsArgs a) {
             const long long p = position(a, b * a.S + s, s);
             return p >= 0 && p < a.P ? (int)p : -1;
         };
-        // copies run kStages - 1 tasks ahead: the task with `left` tasks to the
-        // end, at token cs and chunk cc, its position known one token before
-        int cs = s0 + first / nchunk, cc = first % nchunk, left = end - first;
-        int s = cs, chunk = cc;
+        // Copies run kStages - 1 tasks ahead, at chunk cc of token cs; its position
+        // is known one token before.  Pointers advance by a chunk, and by what is
+        // left of the token's stride behind its last chunk.
+        int cs = s0 + first / nchunk, cc = first % nchunk, chunk = cc, todo = end - first;
+        const int whole = (8 * LPR == a.Dh) ? a.H[t] / (U * RPW) : 0;  // chunks with a row for every lane
+        const long long xrow = RPW * a.xs[t][2], grow = RPW * a.dys[t][2], orow = RPW * a.os[t][2];
+        const long long xwrap = a.xs[t][1] - nchunk * U * xrow, gwrap = a.dys[t][1] - nchunk * U * grow,
+                        owrap = a.os[t][1] - nchunk * U * orow;
+        const T *xsrc = static_cast<const T *>(a.x[t]) + b * a.xs[t][0] + cs * a.xs[t][1] + cc * U * xrow +
+                        sub * a.xs[t][2] + 8 * l;
+        const T *gsrc = nullptr;
+        if (BWD)
+            gsrc = static_cast<const T *>(a.dy[t]) + b * a.dys[t][0] + cs * a.dys[t][1] + cc * U * grow +
+                   sub * a.dys[t][2] + 8 * l;
+        T *o = static_cast<T *>(a.out[t]) + b * a.os[t][0] + cs * a.os[t][1] + cc * U * orow + sub * a.os[t][2];
         int p = where(cs), p_next = where(min(cs + 1, last));
         unsigned real = 0;  // bit i: stage i holds a real token's task
-        const auto copy_next = [&](int stage) {
-            if (left > 0) {
-                --left;
-                const int rows = heads - cc * U;
-                const uint32_t dst = ring_u32 + stage * St::kBytes;
-                const long long xs = a.xs[t][2], gs = a.dys[t][2];
-                copy_rows<T, LPR, U>(dst,
-                                     static_cast<const T *>(a.x[t]) + b * a.xs[t][0] + cs * a.xs[t][1] +
-                                         (sub + cc * (U * RPW)) * xs,
-                                     RPW * xs, rows, l, sub);
-                if (BWD)
-                    copy_rows<T, LPR, U>(dst + St::kRows,
-                                         static_cast<const T *>(a.dy[t]) + b * a.dys[t][0] + cs * a.dys[t][1] +
-                                             (sub + cc * (U * RPW)) * gs,
-                                         RPW * gs, rows, l, sub);
+        const uint32_t lane_dst = smem_u32(ring) + lane * 8 * (int)sizeof(T);
+        const uint32_t angle_dst = smem_u32(ring) + St::kAngles + 16 * l;
+        const auto copy_next = [&](int stage, bool more) {
+            if (more) {
+                const int rows = heads - cc * U;  // the lane's heads: u < rows
+                const uint32_t dst = lane_dst + stage * St::kBytes;
+                const bool all = cc < whole;
+                copy_rows<T, U>(dst, xsrc, xrow, all, rows);
+                if (BWD) copy_rows<T, U>(dst + St::kRows, gsrc, grow, all, rows);
                 if (sub == 0 && slot.turned && p >= 0) {
                     const long long at = (long long)p * (a.Dr / 2) + 4 * l;
-                    cp_async16(dst + St::kAngles + 16 * l, a.cos + at, true);
-                    cp_async16(dst + St::kAngles + 16 * (LPR + l), a.sin + at, true);
+                    cp_async16(angle_dst + stage * St::kBytes, a.cos + at);
+                    cp_async16(angle_dst + stage * St::kBytes + 16 * LPR, a.sin + at);
                 }
                 real = p >= 0 ? real | 1u << stage : real & ~(1u << stage);
+                xsrc += U * xrow;
+                if (BWD) gsrc += U * grow;
                 if (++cc == nchunk) {
                     cc = 0, ++cs;
+                    xsrc += xwrap;
+                    if (BWD) gsrc += gwrap;
                     p = p_next;
                     if (cs < last) p_next = where(cs + 1);
                 }
@@ -365,40 +386,31 @@ heads_tile_kernel(const __grid_constant__ HeadsArgs a) {
             cp_async_commit();
         };
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) copy_next(i);
+        for (int i = 0; i < kStages - 1; ++i) copy_next(i, i < todo);
         px2 w[4];
         load_weights<T, INTER>(w, a.w[t], slot);
         int stage = 0;
 #pragma unroll 1
-        for (int task = first; task < end; ++task) {
+        for (; todo > 0; --todo) {
             cp_async_wait<kStages - 2>();
-            __syncwarp();
-            Raw<T> rx[U], rg[U];
+            __syncwarp();  // the stage is whole, and every lane has read the one before it
+            copy_next(stage == 0 ? kStages - 1 : stage - 1, todo > kStages - 1);
             const unsigned char *at = ring + stage * St::kBytes;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const T *row = reinterpret_cast<const T *>(at) + (u * RPW + sub) * LPR * 8;
-                rx[u] = load8<INTER>(row, slot);
-                if (BWD) rg[u] = load8<INTER>(row + St::kRows / (int)sizeof(T), slot);
-            }
-            const Angles ang = make_angles(*reinterpret_cast<const float4 *>(at + St::kAngles + 16 * l),
-                                           *reinterpret_cast<const float4 *>(at + St::kAngles + 16 * (LPR + l)));
             const bool known = real >> stage & 1u;
-            __syncwarp();  // every lane has read the stage that is copied into next time
-            copy_next(stage == 0 ? kStages - 1 : stage - 1);
             if (++stage == kStages) stage = 0;
-            const int rows = heads - chunk * U;  // the lane's heads: u < rows
-            const long long os = a.os[t][2];
-            T *o = static_cast<T *>(a.out[t]) + b * a.os[t][0] + s * a.os[t][1] + (sub + chunk * (U * RPW)) * os;
+            const int rows = heads - chunk * U;
             if (known) {
+                const Angles ang = make_angles(*reinterpret_cast<const float4 *>(at + St::kAngles + 16 * l),
+                                               *reinterpret_cast<const float4 *>(at + St::kAngles + 16 * (LPR + l)));
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
+                    const T *row = reinterpret_cast<const T *>(at) + (u * RPW + sub) * LPR * 8;
                     px2 v[4];
-                    values<INTER>(v, rx[u]);
+                    values<INTER>(v, load8<INTER>(row, slot));
                     const float ss = row_sum<LPR>(dot8(v, v));
                     if (BWD) {
                         px2 g[4], gx[4];
-                        values<INTER>(g, rg[u]);
+                        values<INTER>(g, load8<INTER>(row + St::kRows / (int)sizeof(T), slot));
                         if (slot.turned) turn<true>(g, ang);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) gx[i] = px_mul(g[i], v[i]);
@@ -418,14 +430,15 @@ heads_tile_kernel(const __grid_constant__ HeadsArgs a) {
                         for (int i = 0; i < 4; ++i) v[i] = px_mul(px_mul(v[i], r), w[i]);
                         if (slot.turned) turn<false>(v, ang);
                     }
-                    if (u < rows) store8<INTER>(o + u * RPW * os, v, slot);
+                    if (u < rows) store8<INTER>(o + u * orow, v, slot);
                 }
             } else {  // padding
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (u < rows) store_zero<INTER>(o + u * RPW * os, slot);
+                    if (u < rows) store_zero<INTER>(o + u * orow, slot);
             }
-            if (++chunk == nchunk) chunk = 0, ++s;
+            o += U * orow;
+            if (++chunk == nchunk) chunk = 0, o += owrap;
         }
         cp_async_wait<0>();
     }
