@@ -247,12 +247,12 @@ __global__ void __launch_bounds__(1024) grad_norm_kernel(const float2 *__restric
     pdl_trigger();
     float s = 0.0f, c = 0.0f;
     bool scaled = false;
-    for (int i = threadIdx.x; i < n; i += 8 * 1024) {
-        float2 v[8];
+    for (int i = threadIdx.x; i < n; i += 16 * 1024) {
+        float2 v[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = part[min(i + k * 1024, n - 1)];
+        for (int k = 0; k < 16; ++k) v[k] = part[min(i + k * 1024, n - 1)];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 16; ++k) {
             const bool in = i + k * 1024 < n;
             scaled |= in && v[k].y != 0.0f;
             twosum(s, c, in ? v[k].x : 0.0f);
