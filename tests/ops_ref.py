@@ -52,10 +52,10 @@ def angles(cos, sin, pos, B, S):
 def heads_fwd(x, w, cos, sin, pos, eps, interleaved):
     """(y, bound) of head rows x [B,S,H,Dh].
 
-    r: the chain of 8 fused adds in a lane and at most 5 across lanes, 1/Dh and
-    the fused eps give 15 U on the argument, half of that on r, 1 U for the
-    root: 9 U.  n = x r w: 2 more.  A turned channel: 2 more on its two terms.
-    12 are used as 16.
+    r: the chain of 5 adds in a lane and at most 5 across lanes, 1/Dh and the
+    fused eps give 13 U on the argument, half of that on r, and 4 U for the
+    reciprocal root (CUDA bounds rsqrtf by 2 ulp): 11 U.  n = x r w: 2 more.  A
+    turned channel: 3 more on its two terms.  16 in all.
     """
     B, S = x.shape[:2]
     c, s, real = angles(cos, sin, pos, B, S)
@@ -68,15 +68,15 @@ def heads_fwd(x, w, cos, sin, pos, eps, interleaved):
     return y, err * (1 + half) + (half if x.dtype != torch.float32 else 0.0) * y.abs()
 
 
-def heads_bwd(dy, x, w, cos, sin, pos, eps, interleaved, samples=1, tiles=1):
+def heads_bwd(dy, x, w, cos, sin, pos, eps, interleaved):
     """(dx, bound, dw, bound) of head rows.
 
     With G the size of g's terms, M = sum G |w| |x|: g is within 3 U of G, h
-    within 4 U, hx within 18 U of M (13 adds, h, the product), r^2/Dh within 22
-    U, r within 9 U.  So dx is within r U (16 G |w| + 64 |x| r^2/Dh M).
-    dw: 3 U on g, 10 U on x r and the sum's depth: 12 rows a lane, 3 shuffles, 8
-    warps, 32 + tiles / 32 in the fold, the samples; each addition onto a given
-    accumulator is one of them.
+    within 4 U, hx within 16 U of M (10 adds, g x, the product), r^2/Dh within 25
+    U, r within 11 U.  So dx is within r U (16 G |w| + 64 |x| r^2/Dh M).
+    dw: 15 U on g x r and the sum's depth: at most 24 rows a lane or 2 H (a tile
+    holds 48 tasks of 2 rows over 4 warps, or one token), 3 shuffles, 4 warps, a
+    128th of the tiles (at most S) and 14 in the fold, the samples.
     """
     B, S = x.shape[:2]
     c, s, real = angles(cos, sin, pos, B, S)
@@ -92,7 +92,7 @@ def heads_bwd(dy, x, w, cos, sin, pos, eps, interleaved, samples=1, tiles=1):
     half = HALF[x.dtype]
     err = err * (1 + half) + (half if x.dtype != torch.float32 else 0.0) * dx.abs()
     dw = torch.where(real, g * xf * r, 0.0).sum((0, 1, 2))
-    depth = 13 + 12 + 3 + 8 + 32 + (tiles + 31) // 32 + samples
+    depth = 15 + max(24, 2 * x.shape[2]) + 3 + 4 + (S + 127) // 128 + 14 + B
     dw_err = depth * U * torch.where(real, G * xf.abs() * r, 0.0).sum((0, 1, 2))
     return dx, err, dw, dw_err
 

@@ -142,6 +142,18 @@ def test_empty_and_far():
     assert (table[V - 1] == 3).all() and (table[1] == 2).all() and not table[2:V - 1].any() and not table[0].any()
 
 
+@pytest.mark.parametrize("n", [1 << 24, 3000001])
+def test_most_tokens(n):
+    """Sums of small whole numbers are exact in any order."""
+    g = torch.Generator("cuda").manual_seed(n)
+    t = torch.randint(-1, 1000, (n,), generator=g, device="cuda", dtype=torch.int32)
+    t[: n // 8] = 7  # a tree of four levels
+    d = torch.randint(-1, 2, (n, 8), generator=g, device="cuda").to(BF16)
+    want = torch.zeros((1001, 8), device="cuda", dtype=torch.float64)
+    want.index_add_(0, torch.where(t < 0, 1000, t).long(), d.double())
+    assert torch.equal(BWD[BF16](d, t, 1000).double(), want[:1000])
+
+
 def test_graph_and_stream():
     for n, V in ((1000, 77), (7000, 777)):
         t, g = make("skew", n, V, 128, BF16)

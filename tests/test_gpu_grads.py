@@ -38,7 +38,7 @@ def make(sizes, seed=0, mixed=True):
             for i, n in enumerate(sizes)]
 
 
-LISTS = [[], [0], [1], [0, 1, 0, 3], [4095, 4096, 4097, 8191, 8192, 8193, 16383, 16384, 16385], [1] * 17, [5] * 129, [3] * 1500,
+LISTS = [[], [0], [1], [0, 1, 0, 3], [4095, 4096, 4097, 8191, 8192, 8193, 16383, 16384, 16385], [1] * 17, [5] * 129, [3] * 1500, [1, 0, 2] * 2000,
          [1000000, 7, 333333], [40000] * 70]
 
 

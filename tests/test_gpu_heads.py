@@ -48,11 +48,6 @@ def make(dtype, B, S, Hq, Hk, Dh, Dr, seed=0, P=None, pads=True):
     return d
 
 
-def tiles_of(S, Hq, Hk, Dh):
-    """An upper bound of the backward's tiles: one token each."""
-    return S
-
-
 def check_both(d, dtype, interleaved, eps=1e-6):
     q, k, pos = d["q"], d["k"], d["pos"]
     yq, yk = FWD[dtype](q, k, d["wq"], d["wk"], d["cos"], d["sin"], pos=pos, eps=eps, interleaved=interleaved)
@@ -62,8 +57,7 @@ def check_both(d, dtype, interleaved, eps=1e-6):
         B, S, H, Dh = x.shape
         want, err = ops_ref.heads_fwd(x, w, d["cos"], d["sin"], pos, eps, interleaved)
         ops_ref.check(y, want, err, n)
-        want, err, want_w, err_w = ops_ref.heads_bwd(gy, x, w, d["cos"], d["sin"], pos, eps, interleaved, B,
-                                                     tiles_of(S, H, H, Dh))
+        want, err, want_w, err_w = ops_ref.heads_bwd(gy, x, w, d["cos"], d["sin"], pos, eps, interleaved)
         ops_ref.check(dx, want, err, "d" + n)
         ops_ref.check(dw, want_w, err_w, "dw" + n)
     return yq, yk, dq, dk, dwq, dwk
@@ -97,7 +91,7 @@ def test_no_weights_no_keys_no_positions():
     want, err = ops_ref.heads_fwd(d["q"], None, d["cos"], d["sin"], None, 1e-6, True)
     ops_ref.check(y, want, err, "q")
     dq, dk, dwq, dwk = BWD[BF16](d["gq"], None, d["q"], None, None, None, d["cos"], d["sin"])
-    want, err, want_w, err_w = ops_ref.heads_bwd(d["gq"], d["q"], None, d["cos"], d["sin"], None, 1e-6, True, 2, 10)
+    want, err, want_w, err_w = ops_ref.heads_bwd(d["gq"], d["q"], None, d["cos"], d["sin"], None, 1e-6, True)
     ops_ref.check(dq, want, err, "dq")
     ops_ref.check(dwq, want_w, err_w, "dwq")
     assert dk is None and dwk is None
@@ -245,6 +239,13 @@ def test_far_offsets():
     cos[-8:], sin[-8:] = d["cos"], d["sin"]
     got = FWD[BF16](d["q"], d["k"], d["wq"], d["wk"], cos, sin, pos=d["pos"] + (P - 8))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("shape", [(65535, 1, 1, 1, 8, 8), (1, 262144, 1, 2, 8, 0), (1, 2, 1024, 1, 256, 64),
+                                   (2, 1, 1, 1024, 16, 16), (300, 2, 2, 2, 128, 128)])
+def test_largest(shape):
+    """The most samples, tokens and heads."""
+    check_both(make(BF16, *shape, P=40, pads=False), BF16, True)
 
 
 def test_graph_and_stream():
