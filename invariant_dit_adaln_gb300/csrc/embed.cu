@@ -517,7 +517,7 @@ struct SumArgs {
     float *acc;      // [V][D] fp32, or
     uint16_t *bf16;  // [V][D]
     float scale;
-    int accumulate, n, V, D;
+    int accumulate, n, V, D, groups;
     int places;  // of a task: 16 or 32
 };
 
@@ -565,12 +565,12 @@ __device__ __forceinline__ void put_row(const SumArgs &a, int token, int col, co
 
 // A piece of a long run: leave its sum, and climb the run's tree while this
 // warp brings the last child of the node.
-__device__ __forceinline__ void climb(const SumArgs &a, const int4 *tree, int token, int index, int col,
-                                      float (&s)[8]) {
+__device__ __forceinline__ void climb(const SumArgs &a, const int4 *tree, int token, int index, int group,
+                                      int col, float (&s)[8]) {
     const int4 t = __ldcg(tree);
     int count = t.x, slot = t.y, node = t.z;  // of the level
     const bool live = col < a.D;
-    const int lane = threadIdx.x & 31, groups = gridDim.y, group = blockIdx.y;
+    const int lane = threadIdx.x & 31;
 #pragma unroll 1
     for (;;) {
         float *q = a.partial + (long long)(slot + index) * a.D + col;
@@ -582,7 +582,7 @@ __device__ __forceinline__ void climb(const SumArgs &a, const int4 *tree, int to
         __threadfence();
         __syncwarp();
         int seen = 0;
-        if (lane == 0) seen = atomicAdd(a.tickets + (long long)(node + parent) * groups + group, 1);
+        if (lane == 0) seen = atomicAdd(a.tickets + (long long)(node + parent) * a.groups + group, 1);
         if (__shfl_sync(0xFFFFFFFFu, seen, 0) + 1 < children) return;
         __threadfence();
         // the node's children in order, from +0
@@ -615,7 +615,7 @@ __device__ __forceinline__ void climb(const SumArgs &a, const int4 *tree, int to
 }
 
 // A warp per (piece of a long run | short runs that begin at a.places places,
-// 256 columns); blockIdx.y is the column group.  A lane copies its 8 columns of
+// 256 columns), the column groups of a task side by side.  A lane copies its 8 columns of
 // the task's rows asynchronously into a ring of its own, 8 KB a warp: all that
 // the SM can have in flight, whatever the lengths of the runs.  (One run at a
 // time, its rows in registers, took 40 us for 32768 rows of 1024 in runs of
@@ -635,15 +635,16 @@ __global__ void __launch_bounds__(32 * kSumWarps, 3) embed_sum_kernel(const __gr
     // row r at mine + r * 256: the lane's 8 columns, in 16-byte words 512 bytes
     // apart (fp32: two words)
     T *ring = reinterpret_cast<T *>(ring_bytes + warp * kRingBytes);
-    const int col = blockIdx.y * 256 + lane * 8;
-    const bool live = col < a.D;
-    // lanes behind the last column read along with the first and write nothing
-    const T *d_out = static_cast<const T *>(a.d_out) + (live ? col : 0);
     pdl_wait();
     pdl_trigger();
     const int longs = __ldcg(&a.counts->pieces), total = longs + (a.n + a.places - 1) / a.places;
 #pragma unroll 1
-    for (int task = blockIdx.x * kSumWarps + warp; task < total; task += gridDim.x * kSumWarps) {
+    for (int id = blockIdx.x * kSumWarps + warp; id < total * a.groups; id += gridDim.x * kSumWarps) {
+        const int task = id / a.groups, group = id - task * a.groups;
+        const int col = group * 256 + lane * 8;
+        const bool live = col < a.D;
+        // lanes behind the last column read along with the first and write nothing
+        const T *d_out = static_cast<const T *>(a.d_out) + (live ? col : 0);
         // the task's places: [begin, end) of the 64 from `base`, two a lane;
         // bit i of `heads`: a run begins at place base + i
         int base, begin = 0, end;
@@ -699,7 +700,7 @@ __global__ void __launch_bounds__(32 * kSumWarps, 3) embed_sum_kernel(const __gr
             if (r == end || ((heads >> r) & 1)) {
                 if (r > begin) {
                     if (task < longs) {
-                        climb(a, reinterpret_cast<const int4 *>(a.pieces + task) + 1, piece.x, piece.w, col, s);
+                        climb(a, reinterpret_cast<const int4 *>(a.pieces + task) + 1, piece.x, piece.w, group, col, s);
                     } else {
                         const int token = (int)__shfl_sync(0xFFFFFFFFu, first < 32 ? key : key2, first & 31);
                         if (live) put_row(a, token, col, s);
@@ -879,13 +880,14 @@ cudaError_t launch_embed_bwd(const T *d_out, const void *tokens, int tokens_are_
     a.n = n;
     a.V = V;
     a.D = D;
+    a.groups = groups;
     // as many CTAs as the device holds; 16 places a task (4096 labels of 3072
-    // columns: 21.2 us against 24.5 with 8 and 27 with 4), or 32 where that still
-    // gives every warp two tasks
-    const int want = (3 * dev.sm_count + groups - 1) / groups;
-    a.places = (long long)n >= 2ll * 32 * want * kSumWarps ? 32 : 16;
-    const long long most = (long long)n / (a.places * kSumWarps) + n / (kPiece * kSumWarps) + 1;
-    const dim3 grid((unsigned)(most < want ? most : want), groups);
+    // columns: 20 us against 23 with 8), or 32 where that still gives every warp
+    // two tasks
+    const long long want = 3 * dev.sm_count;
+    a.places = (long long)n * groups >= 2 * 32 * want * kSumWarps ? 32 : 16;
+    const long long most = (((long long)n / a.places + n / kPiece + 2) * groups + kSumWarps - 1) / kSumWarps;
+    const dim3 grid((unsigned)(most < want ? most : want));
     const size_t smem = kSumWarps * kRingBytes;
     e = ensure_smem_attr((const void *)embed_sum_kernel<T>, smem, dev);
     if (e != cudaSuccess) return e;

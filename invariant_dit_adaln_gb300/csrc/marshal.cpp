@@ -421,22 +421,20 @@ PyObject *grad_clip(PyObject *const *a) {
     const int dev = current_device();
     const List grads(a[0], "grads", dev);
     const double max_norm = number(a[1]);
-    PyObject *outs = a[2];
-    std::vector<Tensor> fresh;
-    if (!given(outs)) {
-        const Py_ssize_t n = PySequence_Fast_GET_SIZE(grads.seq);
-        outs = PyList_New(n);
-        if (!outs) throw Refused();
-        for (Py_ssize_t i = 0; i < n; ++i)
-            PyList_SET_ITEM(outs, i,
-                            THPVariable_Wrap(at::empty_like(THPVariable_Unpack(PySequence_Fast_GET_ITEM(grads.seq, i)))));
-    } else {
-        Py_INCREF(outs);
-    }
     struct Keep {
         PyObject *o;
         ~Keep() { Py_XDECREF(o); }
-    } keep{outs};
+    } keep{given(a[2]) ? Py_NewRef(a[2]) : PyList_New(0)};
+    PyObject *outs = keep.o;
+    if (!outs) throw Refused();
+    if (!given(a[2])) {
+        for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(grads.seq); ++i) {
+            PyObject *t = THPVariable_Wrap(at::empty_like(THPVariable_Unpack(PySequence_Fast_GET_ITEM(grads.seq, i))));
+            const int bad = t ? PyList_Append(outs, t) : -1;
+            Py_XDECREF(t);
+            if (bad) throw Refused();
+        }
+    }
     const List to(outs, "outs", dev);
     if (to.t.size() != grads.t.size()) refuse(PyExc_ValueError, "outs: expected as many tensors as grads");
     const Tensor stats = result(a[3], "stats", dev, at::kFloat, {2});
