@@ -809,15 +809,14 @@ cudaError_t launch_embed_bwd(const T *d_out, const void *tokens, int tokens_are_
     Fill fill = {d_table ? reinterpret_cast<uint4 *>(d_table) : reinterpret_cast<uint4 *>(d_table_acc),
                  accumulate ? 0 : (long long)V * D * (d_table ? 2 : 4) / 16};
     cudaError_t e = cudaSuccess;
-    // In shared memory where a token and a place fit 32 bits: by one CTA up to
-    // 4 tokens a thread (9.5 us at 4096; with 32 a thread 67 us at 32768), then by a
-    // cluster of 8, up to 16 a thread (21 us at 32768, zeroing 102 MB meanwhile;
-    // the kernels 36 us, and three more launches).
-    if (n <= 8 * 16 * kTeamThreads && key_bits + bits <= 32) {
+    // In shared memory where a token and a place fit 32 bits: 4 tokens a thread, by
+    // one CTA (9.5 us at 4096; with 32 a thread 67 us at 32768) or by a cluster of 8
+    // (the whole call at 20000 tokens x 64: 29.7 us against 31.8 with the kernels,
+    // and three launches fewer).  Beyond, the kernels: with 16 a thread the
+    // cluster's call takes 49 us at 33000 and 64 at 75351, theirs 32 and 46.
+    if (n <= 8 * 4 * kTeamThreads && key_bits + bits <= 32) {
         const int passes = (key_bits + 7) / 8, digit_bits = (key_bits + passes - 1) / passes;
-        auto sort = n <= 4 * kTeamThreads       ? sort_team<1, 4>
-                    : n <= 8 * 4 * kTeamThreads ? sort_team<8, 4>
-                                                : sort_team<8, 16>;
+        auto sort = n <= 4 * kTeamThreads ? sort_team<1, 4> : sort_team<8, 4>;
         e = sort(tokens, tokens_are_64, n, V, bits, digit_bits, passes, groups, keys, idx, pieces, tickets, counts,
                  fill, stream, dev);
         if (e != cudaSuccess) return e;

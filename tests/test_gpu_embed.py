@@ -49,9 +49,9 @@ def test_lookup(n, V, D, dtype):
         assert torch.equal(FWD[dtype](t.to(torch.int32), table, scale=scale), want)
 
 
-# around the sizes of the sorts (one CTA to 4096, a cluster to 32768 and 131072 if
-# token and place fit 32 bits, kernels over tiles of 1024), one to three digits,
-# one occurrence to all, trees of one to three levels
+# around the sizes of the sorts (one CTA to 4096 and a cluster to 32768 if token
+# and place fit 32 bits, kernels over tiles of 1024 otherwise), one to three
+# digits, one occurrence to all, trees of one to three levels
 BACK = [(1, 1, 8, "even"), (31, 4, 16, "even"), (32, 3, 8, "one"), (33, 3, 8, "one"), (500, 40, 264, "even"),
         (1000, 255, 8, "skew"), (1000, 256, 8, "skew"), (4096, 257, 40, "skew"), (4097, 65535, 24, "skew"),
         (9000, 65536, 16, "skew"), (20000, 200, 8, "even"), (6000, 300000, 8, "even"), (4096, 1001, 16, "one"),
