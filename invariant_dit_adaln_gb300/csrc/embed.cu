@@ -426,6 +426,7 @@ __global__ void __launch_bounds__(256) embed_hist_kernel(const SortArgs a, const
 __global__ void __launch_bounds__(256) embed_scatter_kernel(const SortArgs a, const Fill fill) {
     constexpr int J = 4;             // places of a lane in flight
     __shared__ int cnt[8][kDigits];  // per warp and digit: the count, then the next place
+    __shared__ int joined[16][kDigits];
     __shared__ int sums[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = threadIdx.x;
     for (int w = 0; w < 8; ++w) cnt[w][d] = 0;
@@ -440,12 +441,30 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(const SortArgs a, co
     const int i0 = blockIdx.x * a.tile + warp * part, i1 = min(a.n, i0 + part);
 #pragma unroll 4
     for (int i = i0 + lane; i < i1; i += 32) atomicAdd(&cnt[warp][(sort_key(a, i) >> a.shift) & 255], 1);
-    int before = 0, total = 0;  // of digit d: in the CTAs before this one, and in all
-#pragma unroll 16
-    for (int b = 0; b < a.tiles; ++b) {
-        const int c = __ldcg(a.hist + b * kDigits + d);
-        total += c;
-        before += b < (int)blockIdx.x ? c : 0;
+    // Digits 8 lane .. 8 lane + 7 in all CTAs and in those before this one: warp w
+    // adds the CTAs w, w + 8, ..., then the warps are joined.
+    int all[8] = {}, ahead[8] = {};
+#pragma unroll 4
+    for (int b = warp; b < a.tiles; b += 8) {
+        const int4 *h = reinterpret_cast<const int4 *>(a.hist + b * kDigits + 8 * lane);
+        const int4 x = __ldcg(h), y = __ldcg(h + 1);
+        const int v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            all[k] += v[k];
+            ahead[k] += b < (int)blockIdx.x ? v[k] : 0;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        joined[warp][8 * lane + k] = all[k];
+        joined[8 + warp][8 * lane + k] = ahead[k];
+    }
+    __syncthreads();
+    int total = 0, before = 0;  // of digit d
+    for (int w = 0; w < 8; ++w) {
+        total += joined[w][d];
+        before += joined[8 + w][d];
     }
     int inc = total;
 #pragma unroll
