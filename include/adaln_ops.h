@@ -13,8 +13,9 @@
  * with the differences stated at each call.  No call allocates or
  * synchronizes, and every call can be captured into a CUDA graph.  Two calls
  * (or two replayed graphs) that can run at the same time must not share a
- * workspace or an output.  No kernel of this part waits on another thread
- * block, so none can set the words adaln_device_error() reads.
+ * workspace or an output.  Thread blocks of this part wait on one another only
+ * at the hardware barriers of a cluster, whose blocks run together, so no call
+ * sets the words adaln_device_error() reads.
  */
 #ifndef ADALN_OPS_H
 #define ADALN_OPS_H

@@ -634,11 +634,11 @@ __device__ __forceinline__ void climb(const SumArgs &a, const int4 *tree, int to
 }
 
 // A warp per (piece of a long run | short runs that begin at a.places places,
-// 256 columns), the column groups of a task side by side.  A lane copies its 8 columns of
-// the task's rows asynchronously into a ring of its own, 8 KB a warp: all that
-// the SM can have in flight, whatever the lengths of the runs.  (One run at a
-// time, its rows in registers, took 40 us for 32768 rows of 1024 in runs of
-// mostly one or two.)
+// 256 columns), the column groups of a task side by side.  A lane copies its 8
+// columns of the task's rows asynchronously into a ring of its own, 8 KB a warp:
+// all that the SM can have in flight, whatever the lengths of the runs.  (One
+// run at a time, its rows in registers, took 40 us instead of 28 for 32768 rows
+// of 1024 in runs of mostly one or two.)
 constexpr int kSumWarps = 8;
 constexpr int kRingBytes = 8192;  // of a warp
 
@@ -651,8 +651,8 @@ __global__ void __launch_bounds__(32 * kSumWarps, 3) embed_sum_kernel(const __gr
     constexpr int R = kRingBytes / (256 * (int)sizeof(T));  // rows of the ring
     extern __shared__ __align__(16) unsigned char ring_bytes[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // row r at mine + r * 256: the lane's 8 columns, in 16-byte words 512 bytes
-    // apart (fp32: two words)
+    // row r at ring + (r % R) * 256: the lane's 8 columns in 16-byte words, fp32
+    // two of them, 512 bytes apart
     T *ring = reinterpret_cast<T *>(ring_bytes + warp * kRingBytes);
     pdl_wait();
     pdl_trigger();
