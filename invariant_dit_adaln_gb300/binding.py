@@ -509,7 +509,9 @@ def _native():
 def _on(stream):
     """The context in which a torch stream, or a raw one, is the current stream."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        # 0 and 1 are the default stream's handles; ExternalStream takes 0 for
+        # "none given" and returns one of PyTorch's pool, ordered with nothing
+        stream = torch.cuda.default_stream() if int(stream) in (0, 1) else torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
 
 
