@@ -285,9 +285,11 @@ __device__ __forceinline__ void cp_async_wait() {
 
 // The rows of one task of one tensor: the lane's 8 channels of rows src, src +
 // step, ... to dst, dst + (a warp's rows), ...; `all`: every lane has all U of them,
-// otherwise u < rows.
+// otherwise u < rows.  A row that a lane does not have lies behind the heads: its
+// zeros name `base`, an address of the tensor, as their source.
 template <typename T, int U>
-__device__ __forceinline__ void copy_rows(uint32_t dst, const T *src, long long step, bool all, int rows) {
+__device__ __forceinline__ void copy_rows(uint32_t dst, const T *src, const T *base, long long step, bool all,
+                                          int rows) {
     constexpr int E = 16 / (int)sizeof(T);
     if (all) {
 #pragma unroll
@@ -301,7 +303,7 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, const T *src, long long 
         for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int j = 0; j < 8 / E; ++j)
-                cp_async16_if(dst + u * 256 * (int)sizeof(T) + 16 * j, src + (u < rows ? u * step + E * j : 0),
+                cp_async16_if(dst + u * 256 * (int)sizeof(T) + 16 * j, u < rows ? src + u * step + E * j : base,
                               u < rows);
         }
     }
@@ -369,8 +371,8 @@ heads_tile_kernel(const __grid_constant__ HeadsArgs a) {
                 const int rows = heads - cc * U;  // the lane's heads: u < rows
                 const uint32_t dst = lane_dst + stage * St::kBytes;
                 const bool all = cc < whole;
-                copy_rows<T, U>(dst, xsrc, xrow, all, rows);
-                if (BWD) copy_rows<T, U>(dst + St::kRows, gsrc, grow, all, rows);
+                copy_rows<T, U>(dst, xsrc, static_cast<const T *>(a.x[t]), xrow, all, rows);
+                if (BWD) copy_rows<T, U>(dst + St::kRows, gsrc, static_cast<const T *>(a.dy[t]), grow, all, rows);
                 if (sub == 0 && slot.turned && p >= 0) {
                     const long long at = (long long)p * (a.Dr / 2) + 4 * l;
                     cp_async16(angle_dst + stage * St::kBytes, a.cos + at);

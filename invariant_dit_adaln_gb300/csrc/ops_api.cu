@@ -24,6 +24,12 @@ bool valid_eps(float eps) { return eps >= 0.0f && eps <= 3.0e38f; }
 
 // ---- head rows -------------------------------------------------------------
 
+// The stride of a dimension of size 1 is not used, so it may hold anything: 0 from
+// here on, also for the kernels, whose lanes without a row form addresses with it.
+adaln_heads used(const adaln_heads &t, int B, int S, int H) {
+    return {t.data, B > 1 ? t.batch : 0, S > 1 ? t.token : 0, H > 1 ? t.head : 0};
+}
+
 // Head rows as a lattice of dense byte runs: the dimensions of more than one
 // index, innermost first, those that continue the run below them merged into it.
 struct Lattice {
@@ -35,7 +41,8 @@ struct Lattice {
     bool nested;                 // no two runs share a byte: each stride covers what lies inside it
 };
 
-Lattice lattice(const adaln_heads &t, int B, int S, int H, int Dh, int es) {
+Lattice lattice(const adaln_heads &rows, int B, int S, int H, int Dh, int es) {
+    const adaln_heads t = used(rows, B, S, H);
     Lattice l = {};
     l.base = (uintptr_t)t.data;
     l.run = (int64_t)Dh * es;
@@ -209,7 +216,7 @@ adaln_status heads_fwd(const adaln_heads *q, const adaln_heads *k, const T *wq, 
     if (st != ADALN_OK) return st;
     if (B == 0 || S == 0) return ADALN_OK;
     for (int t = 0; t < 2; ++t)
-        if (c.H[t] > 0) c.x[t] = *ins[t], c.out[t] = *outs[t];
+        if (c.H[t] > 0) c.x[t] = used(*ins[t], B, S, c.H[t]), c.out[t] = used(*outs[t], B, S, c.H[t]);
     return from_cuda(launch_heads_fwd<T>(c, (cudaStream_t)stream, dev));
 }
 
@@ -243,7 +250,11 @@ adaln_status heads_bwd(const adaln_heads *d_q_out, const adaln_heads *d_k_out, c
         return from_cuda(e);
     }
     for (int t = 0; t < 2; ++t)
-        if (c.H[t] > 0) c.dy[t] = *ins[t], c.x[t] = *ins[2 + t], c.out[t] = *outs[t];
+        if (c.H[t] > 0) {
+            c.dy[t] = used(*ins[t], B, S, c.H[t]);
+            c.x[t] = used(*ins[2 + t], B, S, c.H[t]);
+            c.out[t] = used(*outs[t], B, S, c.H[t]);
+        }
     return from_cuda(launch_heads_bwd<T>(c, (cudaStream_t)stream, dev));
 }
 
