@@ -91,7 +91,8 @@ adaln_status adaln_f32_qk_norm_rope_fwd(const adaln_heads *q, const adaln_heads 
                                         int Hk, int Dh, int Dr, int P, int interleaved, float eps, void *stream);
 
 /* Workspace bytes adaln_qk_norm_rope_bwd and adaln_f32_qk_norm_rope_bwd need
- * when dwq_acc or dwk_acc is given (0 otherwise): fp32 partial sums. */
+ * when dwq_acc or dwk_acc is given (0 otherwise): fp32 partial sums.  0 for
+ * sizes that the calls refuse. */
 size_t adaln_qk_norm_rope_bwd_workspace_bytes(int B, int S, int Hq, int Hk, int Dh);
 
 /*
@@ -156,7 +157,8 @@ adaln_status adaln_f32_embed_fwd(const void *tokens, int tokens_are_64, const fl
                                  int n, int V, int D, void *stream);
 
 /* Workspace bytes adaln_embed_bwd and adaln_f32_embed_bwd need: the sorted
- * tokens, the list of pieces, and fp32 partial sums of long runs. */
+ * tokens, the list of pieces, and fp32 partial sums of long runs.  0 for sizes
+ * that the calls refuse. */
 size_t adaln_embed_bwd_workspace_bytes(int n, int V, int D);
 
 /*

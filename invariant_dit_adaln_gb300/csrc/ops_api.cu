@@ -128,15 +128,18 @@ bool aligned_rows(const adaln_heads &t, int B, int S, int H, int es) {
     return aligned16(t.data);
 }
 
+bool valid_heads(int B, int S, int Hq, int Hk, int Dh) {
+    return Dh >= 8 && Dh <= 256 && Dh % 8 == 0 && Hq >= 1 && Hq <= kMaxHeads && Hk >= 0 && Hk <= kMaxHeads && B >= 0 &&
+           B <= 65535 && S >= 0 && S <= kMaxS && (double)B * S * (Hq + Hk) * Dh < kMaxElements;
+}
+
 // The checks that forward and backward share; `ins` are the head rows read (q,
 // k and, backward, the output gradients at the same index), `outs` those
 // written.  In place: outs[t] may be exactly ins[place + t].
 adaln_status check_heads(HeadsCall &c, const adaln_heads *const *ins, int nin, const adaln_heads *const *outs,
                          int place, int es) {
     const int Hq = c.H[0], Hk = c.H[1];
-    if (c.Dh < 8 || c.Dh > 256 || c.Dh % 8 != 0 || c.Dr < 0 || c.Dr > c.Dh || c.Dr % 8 != 0 || Hq < 1 ||
-        Hq > kMaxHeads || Hk < 0 || Hk > kMaxHeads || c.P < 0 || c.B < 0 || c.B > 65535 || c.S < 0 || c.S > kMaxS ||
-        (double)c.B * c.S * (Hq + Hk) * c.Dh >= kMaxElements)
+    if (!valid_heads(c.B, c.S, Hq, Hk, c.Dh) || c.Dr < 0 || c.Dr > c.Dh || c.Dr % 8 != 0 || c.P < 0)
         return ADALN_ERR_SHAPE;
     if (c.pos == nullptr && c.Dr > 0 && c.S > c.P) return ADALN_ERR_SHAPE;
     const bool empty = c.B == 0 || c.S == 0;
@@ -413,7 +416,7 @@ adaln_status grad_call(const adaln_tensor *grads, const adaln_tensor *outs, int 
 extern "C" {
 
 size_t adaln_qk_norm_rope_bwd_workspace_bytes(int B, int S, int Hq, int Hk, int Dh) {
-    if (B <= 0 || S <= 0 || Hq <= 0 || Hk < 0 || Dh <= 0 || Dh > 256) return 0;
+    if (B == 0 || S == 0 || !valid_heads(B, S, Hq, Hk, Dh)) return 0;
     return round256(heads_bwd_ws_floats(B, S, Hq, Hk, Dh) * sizeof(float));
 }
 
