@@ -547,8 +547,8 @@ def adaln_qk_norm_rope_bwd(d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos=None, d
                            stream=None):
     """Backward of adaln_qk_norm_rope_fwd from its inputs: (d_q, d_k, dwq_acc,
     dwk_acc).  d_q may be d_q_out and d_k d_k_out (in place).  The weight
-    gradients are fp32 [Dh], allocated here when not given and want_w; accumulate
-    adds to given ones."""
+    gradients are fp32 [Dh]: given ones are filled, or added to with accumulate;
+    want_w allocates those not given (None without it)."""
     if stream is not None:
         with _on(stream):
             return adaln_qk_norm_rope_bwd(d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos, d_q, d_k, dwq_acc, dwk_acc,

@@ -17,6 +17,7 @@
 
 #include <array>
 #include <initializer_list>
+#include <string>
 #include <vector>
 
 #include "adaln_ops.h"
@@ -286,13 +287,14 @@ PyObject *qk_bwd(PyObject *const *a) {
         k = rows_in(a[4], "k", z.dev, t, z.k);
         dk = rows_out(a[11], "d_k", z.dev, t, z.k);
     }
+    // given accumulators are filled; want_w allocates the missing ones
     Tensor dwq, dwk, ws;
     size_t need = 0;
-    if (want_w) {
-        if (accumulate && (!given(a[12]) || (z.keys && !given(a[13]))))
-            refuse(PyExc_ValueError, "accumulate: dwq_acc and dwk_acc must be given");
-        dwq = result(a[12], "dwq_acc", z.dev, at::kFloat, {z.q[3]});
-        if (z.Hk) dwk = result(a[13], "dwk_acc", z.dev, at::kFloat, {z.q[3]});
+    if (want_w && accumulate && (!given(a[12]) || (z.keys && !given(a[13]))))
+        refuse(PyExc_ValueError, "accumulate: dwq_acc and dwk_acc must be given");
+    if (want_w || given(a[12])) dwq = result(a[12], "dwq_acc", z.dev, at::kFloat, {z.q[3]});
+    if (z.Hk && (want_w || given(a[13]))) dwk = result(a[13], "dwk_acc", z.dev, at::kFloat, {z.q[3]});
+    if (dwq.defined() || dwk.defined()) {
         need = lib.qk_bwd_bytes(z.B, z.S, z.Hq, z.Hk, z.Dh);
         ws = scratch(a[16], need, z.dev);
     }

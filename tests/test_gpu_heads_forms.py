@@ -67,3 +67,36 @@ def test_strides_of_one_sample_or_token_are_not_used(dtype):
         want = calls(dtype, d, *(d[n] for n in names))
         got = calls(dtype, d, *(odd(d[n]) for n in names))
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_given_accumulators_are_filled(dtype):
+    """Whatever want_w says: it allocates those not given."""
+    d = make(dtype, 3, 20, 4, 2, 64, 32)
+
+    def back(k=True, **kw):
+        keys = (d["gk"], d["k"]) if k else (None, None)
+        return BWD[dtype](d["gq"], keys[0], d["q"], keys[1], d["wq"], d["wk"], d["cos"], d["sin"], pos=d["pos"], **kw)
+
+    want = back()
+    full = [torch.full((64,), 7.0, device="cuda") for _ in range(2)]
+    added = back(dwq_acc=full[0].clone(), dwk_acc=full[1].clone(), accumulate=True)[2:]
+    for want_w in (True, False):
+        for give in ((0,), (1,), (0, 1)):
+            acc = [full[i].clone() if i in give else None for i in range(2)]
+            got = back(dwq_acc=acc[0], dwk_acc=acc[1], want_w=want_w)
+            for i in range(2):
+                if i in give:
+                    assert got[2 + i] is acc[i] or got[2 + i].data_ptr() == acc[i].data_ptr()
+                if i in give or want_w:
+                    assert torch.equal(got[2 + i], want[2 + i])
+                else:
+                    assert got[2 + i] is None
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            if len(give) == 2 or not want_w:
+                acc = [full[i].clone() if i in give else None for i in range(2)]
+                got = back(dwq_acc=acc[0], dwk_acc=acc[1], want_w=want_w, accumulate=True)
+                for i in range(2):
+                    assert torch.equal(acc[i], added[i]) if i in give else got[2 + i] is None
+    alone = back(k=False, want_w=False, dwq_acc=full[0].clone())
+    assert torch.equal(alone[2], back(k=False)[2]) and alone[1] is None and alone[3] is None
