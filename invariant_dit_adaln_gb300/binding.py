@@ -522,7 +522,8 @@ def adaln_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos=None, q_out=None, k_out=N
     weights wq, wk [Dh] (or None), then the rotation of their first Dr channels
     by the rows pos [B,S] (default: 0 .. S-1) of cos, sin [P,Dr/2] fp32.  A row
     whose position is outside [0, P) is padding: zero.  q_out may be q and k_out
-    k (in place), or any rows of the same shape.  Returns (q_out, k_out)."""
+    k (in place), or any rows of the same shape; k_out is refused without k.
+    Returns (q_out, k_out)."""
     if stream is not None:
         with _on(stream):
             return adaln_qk_norm_rope_fwd(q, k, wq, wk, cos, sin, pos, q_out, k_out, eps, interleaved)
@@ -548,7 +549,8 @@ def adaln_qk_norm_rope_bwd(d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos=None, d
     """Backward of adaln_qk_norm_rope_fwd from its inputs: (d_q, d_k, dwq_acc,
     dwk_acc).  d_q may be d_q_out and d_k d_k_out (in place).  The weight
     gradients are fp32 [Dh]: given ones are filled, or added to with accumulate;
-    want_w allocates those not given (None without it)."""
+    want_w allocates those not given (None without it).  Without k nothing for
+    it may be given but wk."""
     if stream is not None:
         with _on(stream):
             return adaln_qk_norm_rope_bwd(d_q_out, d_k_out, q, k, wq, wk, cos, sin, pos, d_q, d_k, dwq_acc, dwk_acc,

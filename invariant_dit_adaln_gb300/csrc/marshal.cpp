@@ -18,6 +18,7 @@
 #include <array>
 #include <initializer_list>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "adaln_ops.h"
@@ -244,6 +245,12 @@ struct HeadSizes {
     }
 };
 
+// without k there is nothing to write to the outputs for it, or to read
+void no_keys(std::initializer_list<std::pair<PyObject *, const char *>> args) {
+    for (const auto &a : args)
+        if (given(a.first)) refuse(PyExc_ValueError, "%s: given without k", a.second);
+}
+
 ScalarType float_type(PyObject *o) { return truth(o) ? at::kFloat : at::kBFloat16; }
 
 // qk_fwd(f32, q, k, wq, wk, cos, sin, pos, q_out, k_out, eps, interleaved)
@@ -257,6 +264,8 @@ PyObject *qk_fwd(PyObject *const *a) {
     if (z.keys) {
         k = rows_in(a[2], "k", z.dev, t, z.k);
         ko = rows_out(a[9], "k_out", z.dev, t, z.k);
+    } else {
+        no_keys({{a[9], "k_out"}});
     }
     const adaln_heads *kh = z.keys ? &k.h : nullptr, *koh = z.keys ? &ko.h : nullptr;
     const float *c = (const float *)ptr(z.cos), *s = (const float *)ptr(z.sin);
@@ -286,6 +295,8 @@ PyObject *qk_bwd(PyObject *const *a) {
         gk = rows_in(a[2], "d_k_out", z.dev, t, z.k);
         k = rows_in(a[4], "k", z.dev, t, z.k);
         dk = rows_out(a[11], "d_k", z.dev, t, z.k);
+    } else {
+        no_keys({{a[2], "d_k_out"}, {a[11], "d_k"}, {a[13], "dwk_acc"}});
     }
     // given accumulators are filled; want_w allocates the missing ones
     Tensor dwq, dwk, ws;
@@ -293,7 +304,7 @@ PyObject *qk_bwd(PyObject *const *a) {
     if (want_w && accumulate && (!given(a[12]) || (z.keys && !given(a[13]))))
         refuse(PyExc_ValueError, "accumulate: dwq_acc and dwk_acc must be given");
     if (want_w || given(a[12])) dwq = result(a[12], "dwq_acc", z.dev, at::kFloat, {z.q[3]});
-    if (z.Hk && (want_w || given(a[13]))) dwk = result(a[13], "dwk_acc", z.dev, at::kFloat, {z.q[3]});
+    if ((want_w && z.Hk) || given(a[13])) dwk = result(a[13], "dwk_acc", z.dev, at::kFloat, {z.q[3]});
     if (dwq.defined() || dwk.defined()) {
         need = lib.qk_bwd_bytes(z.B, z.S, z.Hq, z.Hk, z.Dh);
         ws = scratch(a[16], need, z.dev);

@@ -100,3 +100,18 @@ def test_given_accumulators_are_filled(dtype):
                     assert torch.equal(acc[i], added[i]) if i in give else got[2 + i] is None
     alone = back(k=False, want_w=False, dwq_acc=full[0].clone())
     assert torch.equal(alone[2], back(k=False)[2]) and alone[1] is None and alone[3] is None
+
+
+def test_nothing_for_keys_without_keys():
+    d = make(BF16, 1, 5, 4, 2, 64, 32)
+    args = (None, d["wq"], d["wk"], d["cos"], d["sin"])
+    with pytest.raises(ValueError, match="k_out"):
+        FWD[BF16](d["q"], *args, k_out=torch.empty_like(d["k"]))
+    w = torch.zeros(64, device="cuda")
+    for name, value in (("d_k", torch.empty_like(d["k"])), ("dwk_acc", w)):
+        for want_w in (True, False):
+            with pytest.raises(ValueError, match=name):
+                BWD[BF16](d["gq"], None, d["q"], *args, want_w=want_w, **{name: value})
+    with pytest.raises(ValueError, match="d_k_out"):
+        BWD[BF16](d["gq"], d["gk"], d["q"], *args)
+    assert FWD[BF16](d["q"], *args)[1] is None
