@@ -10,8 +10,8 @@
  *
  * The conventions of adaln.h hold (device pointers, 16-byte alignment, caller-
  * owned buffers, asynchronous on `stream`, order of the checks, status codes),
- * with the differences stated at each call.  No call allocates or
- * synchronizes, and every call can be captured into a CUDA graph.  Two calls
+ * with the differences stated at each call.  No call allocates (device or host
+ * memory) or synchronizes, and every call can be captured into a CUDA graph.  Two calls
  * (or two replayed graphs) that can run at the same time must not share a
  * workspace or an output.  Thread blocks of this part wait on one another only
  * at the hardware barriers of a cluster, whose blocks run together, so no call

@@ -3,7 +3,6 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include <algorithm>
 
@@ -341,42 +340,72 @@ bool list_aligned(const adaln_tensor *t, int count) {
     return true;
 }
 
-struct Span {
-    uintptr_t begin, end;
-    bool out;
+// The ranges of a call: the gradients not scaled in place (read), the outputs
+// and more[] (written).  A gradient scaled in place counts once, as written.
+struct Ranges {
+    const adaln_tensor *grads, *outs;
+    int count;
+    const Buf *more;
+    int nmore;
+
+    int size() const { return 2 * count + nmore; }
+    // range i, if there is one
+    bool get(int i, uintptr_t &begin, uintptr_t &end, bool &out) const {
+        if (i >= 2 * count) {
+            const Buf &b = more[i - 2 * count];
+            begin = (uintptr_t)b.p, end = begin + b.bytes, out = true;
+            return b.p && b.bytes > 0;
+        }
+        const int k = i >> 1;
+        out = i & 1;
+        if (grads[k].numel == 0 || (out ? !outs : outs && outs[k].data == grads[k].data)) return false;
+        begin = (uintptr_t)(out ? outs : grads)[k].data;
+        end = begin + (uintptr_t)grads[k].numel * elem_bytes(grads[k]);
+        return true;
+    }
 };
 
-// Does a written range overlap another range?  A gradient scaled in place
-// counts once, as written.  Sorted sweep: the lists can hold thousands.
-adaln_status spans_overlap(const adaln_tensor *grads, const adaln_tensor *outs, int count, const Buf *more,
-                           int nmore) {
-    Span local[160], *s = local;
-    const size_t most = 2 * (size_t)count + nmore;
-    if (most > 160) {
-        s = static_cast<Span *>(malloc(most * sizeof(Span)));
-        if (!s) return ADALN_ERR_CUDA;
+struct Place {
+    uintptr_t begin;
+    int i;
+    bool operator<(const Place &o) const { return begin < o.begin || (begin == o.begin && i < o.i); }
+};
+
+// Does a written range overlap another range?  A sweep in ascending order.  The
+// lists can hold thousands and no call allocates, so the order comes in blocks
+// of N places on the stack: each pass over the list keeps the N / 2 least ranges
+// behind the block before it, or all that are left where they fit.
+template <int N>
+__attribute__((noinline)) bool written_overlap(const Ranges &r) {
+    Place block[N], last = {0, -1};
+    uintptr_t any_end = 0, out_end = 0, begin, end;
+    bool out;
+    for (bool more = true; more;) {
+        int n = 0;
+        Place most = {UINTPTR_MAX, 0x7FFFFFFF};  // the least place left out
+        more = false;
+        for (int i = 0; i < r.size(); ++i) {
+            if (!r.get(i, begin, end, out)) continue;
+            const Place p = {begin, i};
+            if (!(last < p) || !(p < most)) continue;
+            block[n++] = p;
+            if (n == N) {
+                std::nth_element(block, block + N / 2, block + N);
+                n = N / 2;
+                most = block[n];
+                more = true;
+            }
+        }
+        std::sort(block, block + n);
+        for (int k = 0; k < n; ++k) {
+            r.get(block[k].i, begin, end, out);
+            if (begin < (out ? any_end : out_end)) return true;
+            any_end = std::max(any_end, end);
+            if (out) out_end = std::max(out_end, end);
+        }
+        if (n > 0) last = block[n - 1];
     }
-    size_t n = 0;
-    for (int i = 0; i < count; ++i) {
-        if (grads[i].numel == 0) continue;
-        const uintptr_t bytes = (uintptr_t)grads[i].numel * elem_bytes(grads[i]);
-        const uintptr_t g = (uintptr_t)grads[i].data, o = outs ? (uintptr_t)outs[i].data : 0;
-        if (!outs || o != g) s[n++] = Span{g, g + bytes, false};
-        if (outs) s[n++] = Span{o, o + bytes, true};
-    }
-    for (int i = 0; i < nmore; ++i)
-        if (more[i].p && more[i].bytes > 0)
-            s[n++] = Span{(uintptr_t)more[i].p, (uintptr_t)more[i].p + more[i].bytes, true};
-    std::sort(s, s + n, [](const Span &a, const Span &b) { return a.begin < b.begin; });
-    uintptr_t any_end = 0, out_end = 0;
-    bool bad = false;
-    for (size_t i = 0; i < n && !bad; ++i) {
-        bad = s[i].begin < (s[i].out ? any_end : out_end);
-        any_end = std::max(any_end, s[i].end);
-        if (s[i].out) out_end = std::max(out_end, s[i].end);
-    }
-    if (s != local) free(s);
-    return bad ? ADALN_ERR_ALIAS : ADALN_OK;
+    return false;
 }
 
 adaln_status grad_call(const adaln_tensor *grads, const adaln_tensor *outs, int count, bool clip, double max_norm,
@@ -400,8 +429,9 @@ adaln_status grad_call(const adaln_tensor *grads, const adaln_tensor *outs, int 
         return ADALN_ERR_ALIGN;
     const size_t need = adaln_grad_norm_workspace_bytes(grads, count);
     const Buf more[] = {{stats, clip ? 8u : 4u}, {workspace, need}};
-    st = spans_overlap(grads, clip ? outs : nullptr, count, more, 2);
-    if (st != ADALN_OK) return st;
+    // 60 tensors with outputs, out of order: 4 us on the host; 2000: 0.24 ms; 65536: 29 ms
+    const Ranges ranges = {grads, clip ? outs : nullptr, count, more, 2};
+    if (ranges.size() < 512 ? written_overlap<512>(ranges) : written_overlap<8192>(ranges)) return ADALN_ERR_ALIAS;
     if (need > 0 && (!workspace || workspace_bytes < need)) return ADALN_ERR_WORKSPACE;
     DeviceInfo dev;
     st = check_current_device(&dev);
