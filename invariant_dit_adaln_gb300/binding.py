@@ -497,7 +497,7 @@ def _native():
         L = load()
         path = _build.marshal_path()
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it first (invariant_dit_adaln_gb300.build.build())")
+            raise RuntimeError(f"{path} is missing: build it first (invariant_dit_adaln_gb300.build.build_marshal())")
         spec = importlib.util.spec_from_file_location("adaln_marshal", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

@@ -5,9 +5,12 @@ The translation units are compiled in parallel and linked into
 ``-gencode arch=compute_103a,code=sm_103a -O3 -lineinfo --fmad=false``; no
 fast math, so every floating-point operation rounds as written.
 
-Beside it g++ builds ``lib/adaln_marshal_<torch version>.so``, the Python module
-that marshals PyTorch tensors for the calls of include/adaln_ops.h.  It is
-compiled against the installed PyTorch, hence the version in its name.
+Beside it g++ builds ``lib/adaln_marshal_<Python>_<torch version>.so``, the
+Python module that marshals PyTorch tensors for the calls of
+include/adaln_ops.h.  It is compiled against the running Python and the
+installed PyTorch, hence its name.  The library does not need it: where it
+cannot be built, build() warns, and only those calls from Python are missing
+(they raise).
 """
 
 from __future__ import annotations
@@ -18,6 +21,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -61,7 +65,7 @@ def up_to_date(lib: str = LIB) -> bool:
 def marshal_path() -> str:
     import torch
     version = re.sub(r"[^0-9A-Za-z]+", "_", torch.__version__)
-    return os.path.join(LIBDIR, f"adaln_marshal_{version}.so")
+    return os.path.join(LIBDIR, f"adaln_marshal_{sys.implementation.cache_tag}_{version}.so")
 
 
 def _marshal_up_to_date() -> bool:
@@ -73,7 +77,8 @@ def _marshal_up_to_date() -> bool:
 
 
 def build_marshal() -> str:
-    """Compile the marshalling module for the installed PyTorch; returns its path."""
+    """Compile the marshalling module for the installed PyTorch; returns its path.
+    Raises where there is no PyTorch with its headers, or no C++ compiler."""
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
@@ -93,18 +98,38 @@ def build_marshal() -> str:
     return path
 
 
+def _try_marshal(force: bool):
+    """Build the module if it is out of date; the exception if that fails, for
+    any reason: no PyTorch, none with CUDA headers, no compiler."""
+    try:
+        if force or not _marshal_up_to_date():
+            if os.path.exists(marshal_path()):
+                os.remove(marshal_path())  # never called with headers other than its own
+            build_marshal()
+    except Exception as e:
+        return e
+    return None
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: str | None = None) -> str:
     """Compile and link the library; returns its path.  `variant` names a test
     build with extra flags, linked to lib/<variant>/libadaln.so with objects in
-    _build/<variant>/ (the release library is lib/libadaln.so)."""
+    _build/<variant>/ (the release library is lib/libadaln.so).  Warns if the
+    marshalling module cannot be built."""
     lib = LIB if variant is None else os.path.join(LIBDIR, variant, "libadaln.so")
     objdir = BUILD if variant is None else os.path.join(BUILD, variant)
-    stale = force or not up_to_date(lib)
-    marshal = variant is None and (force or not _marshal_up_to_date())
-    if not stale:
-        if marshal:
-            build_marshal()
-        return lib
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        module = ex.submit(_try_marshal, force) if variant is None else None
+        if force or not up_to_date(lib):
+            _build_library(lib, objdir, extra_flags, verbose)
+        failure = module.result() if module is not None else None
+    if failure is not None:
+        warnings.warn("libadaln.so is built, but not the module behind the Python calls of adaln_ops.h: "
+                      f"{type(failure).__name__}: {failure}", RuntimeWarning, stacklevel=2)
+    return lib
+
+
+def _build_library(lib, objdir, extra_flags, verbose) -> None:
     os.makedirs(objdir, exist_ok=True)
     os.makedirs(os.path.dirname(lib), exist_ok=True)
     cc = nvcc()
@@ -117,11 +142,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: s
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stdout + r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        module = ex.submit(build_marshal) if marshal else None
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        if module is not None:
-            module.result()
     logs = "".join(log for _, log in results)
     if verbose and logs.strip():
         print(logs, file=sys.stderr)
@@ -131,7 +153,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: s
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
-    return lib
 
 
 # Test build: the first wait of every waiting kernel goes to an mbarrier that
