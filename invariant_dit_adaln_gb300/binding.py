@@ -612,6 +612,11 @@ def adaln_f32_embed_bwd(d_out, tokens, V, scale=1.0, d_table_acc=None, accumulat
     return (_marshal or _native()).embed_bwd(True, d_out, tokens, V, scale, d_table_acc, None, accumulate, workspace)
 
 
+def adaln_grad_norm_workspace_bytes(grads):
+    """Workspace bytes of adaln_grad_norm and adaln_grad_clip for a list of tensors."""
+    return (_marshal or _native()).grad_workspace_bytes(grads)
+
+
 def adaln_grad_norm(grads, norm=None, workspace=None, stream=None):
     """The global norm sqrt(sum x^2) over a list of contiguous fp32 and bf16
     tensors, as a device tensor [1] fp32 (nothing is synchronized)."""

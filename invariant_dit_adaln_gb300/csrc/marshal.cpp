@@ -417,6 +417,12 @@ struct List {
     int count() const { return size_of((long long)t.size()); }
 };
 
+// grad_workspace_bytes(grads)
+PyObject *grad_workspace_bytes(PyObject *const *a) {
+    const List grads(a[0], "grads", current_device());
+    return PyLong_FromSize_t(lib.grad_bytes(grads.t.data(), grads.count()));
+}
+
 // grad_norm(grads, norm, workspace)
 PyObject *grad_norm(PyObject *const *a) {
     const int dev = current_device();
@@ -502,6 +508,7 @@ PyMethodDef methods[] = {CALL(qk_fwd, 12),
                          CALL(qk_bwd, 19),
                          CALL(embed_fwd, 5),
                          CALL(embed_bwd, 9),
+                         CALL(grad_workspace_bytes, 1),
                          CALL(grad_norm, 3),
                          CALL(grad_clip, 5),
                          {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, nullptr},

@@ -1,0 +1,40 @@
+"""adaln_grad_norm and adaln_grad_clip: what may be handed over as a list, and
+the workspace a caller keeps."""
+
+from __future__ import annotations
+
+import pytest
+import torch
+
+from gpu_util import lib
+from invariant_dit_adaln_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def L():
+    return lib()
+
+
+def make(sizes):
+    g = torch.Generator().manual_seed(len(sizes))
+    return [torch.randn(n, generator=g).to(BF16 if i % 2 else F32).cuda() for i, n in enumerate(sizes)]
+
+
+@pytest.mark.parametrize("sizes", [[], [0], [1], [4096, 4097], [8192 * 7 + 1, 3, 100000, 0, 8193]])
+def test_workspace_of_the_size_asked_for(sizes):
+    """8 bytes for each 16 KB of each tensor, rounded up to 256; smaller ones are refused."""
+    grads = make(sizes)
+    need = binding.adaln_grad_norm_workspace_bytes(grads)
+    pieces = sum(-(-t.numel() * t.element_size() // 16384) for t in grads)
+    assert need == -(-8 * pieces // 256) * 256
+    want = binding.adaln_grad_norm(grads)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert torch.equal(binding.adaln_grad_norm(grads, workspace=ws), want)
+    assert torch.equal(binding.adaln_grad_clip(grads, 1.0, workspace=ws)[1][:1], want)
+    if need:
+        with pytest.raises(ValueError):
+            binding.adaln_grad_norm(grads, workspace=ws[:-1])

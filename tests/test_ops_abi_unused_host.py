@@ -4,12 +4,13 @@ dereferenced."""
 
 from __future__ import annotations
 
+import os
 import random
 import subprocess
 
 import pytest
 
-from invariant_dit_adaln_gb300 import build
+from invariant_dit_adaln_gb300 import binding, build
 from test_ops_abi_host import (ALIAS, DEVICE, L, at, clip, heads_bwd, heads_fwd, no_gpu, norm, rows,  # noqa: F401
                                tensors)
 
@@ -152,3 +153,11 @@ def test_checks_allocate_nothing(L, tmp_path):  # noqa: F811
     subprocess.run(["gcc", "-O1", "-rdynamic", f"-I{build.INCLUDE}", str(src), "-o", str(exe), "-ldl"], check=True)
     out = subprocess.run([str(exe), build.LIB], capture_output=True, text=True, check=True).stdout
     assert [tuple(map(int, line.split())) for line in out.splitlines()] == [(n, 5, 0) for n in (1, 79, 80, 500, 65536)]
+
+
+def test_every_function_is_exported_and_bound(L):  # noqa: F811
+    names = binding.declared_symbols(os.path.join(build.INCLUDE, "adaln_ops.h"))
+    assert len(names) == 13
+    for n in names:
+        assert hasattr(L, n), n
+        assert callable(getattr(binding, n, None)), n
