@@ -461,7 +461,8 @@ PyObject *grad_clip(PyObject *const *a) {
     const Tensor ws = scratch(a[4], need, dev);
     status("adaln_grad_clip", lib.grad_clip(grads.t.data(), to.t.data(), grads.count(), max_norm, (float *)ptr(stats),
                                             ptr(ws), need, stream_of(dev)));
-    return Py_BuildValue("(ON)", outs, THPVariable_Wrap(stats));
+    // the caller's own object, but for an iterator, which is used up by now
+    return Py_BuildValue("(ON)", PyIter_Check(outs) ? to.seq : outs, THPVariable_Wrap(stats));
 }
 
 // ---- module --------------------------------------------------------------------------

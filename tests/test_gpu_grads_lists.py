@@ -38,3 +38,17 @@ def test_workspace_of_the_size_asked_for(sizes):
     if need:
         with pytest.raises(ValueError):
             binding.adaln_grad_norm(grads, workspace=ws[:-1])
+
+
+def test_lists_of_any_kind():
+    """Lists, tuples and iterators; the outputs come back as they were given, an iterator as a list."""
+    grads = make([5000, 7, 300])
+    want, stats = binding.adaln_grad_clip(grads, 0.5)
+    assert torch.equal(binding.adaln_grad_norm(iter(grads)), stats[:1])
+    for kind in (list, tuple, iter, lambda x: (t for t in x)):
+        outs = [torch.empty_like(t) for t in grads]
+        given = kind(outs)
+        back, s2 = binding.adaln_grad_clip(kind(grads), 0.5, outs=given)
+        assert torch.equal(s2, stats) and len(list(back)) == 3
+        assert back is given or isinstance(back, list)
+        assert all(torch.equal(a, w) for a, w in zip(outs, want)) and all(a is b for a, b in zip(back, outs))
