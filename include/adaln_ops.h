@@ -11,11 +11,11 @@
  * The conventions of adaln.h hold (device pointers, 16-byte alignment, caller-
  * owned buffers, asynchronous on `stream`, order of the checks, status codes),
  * with the differences stated at each call.  No call allocates (device or host
- * memory) or synchronizes, and every call can be captured into a CUDA graph.  Two calls
- * (or two replayed graphs) that can run at the same time must not share a
- * workspace or an output.  Thread blocks of this part wait on one another only
- * at the hardware barriers of a cluster, whose blocks run together, so no call
- * sets the words adaln_device_error() reads.
+ * memory) or synchronizes, and every call can be captured into a CUDA graph.
+ * Two calls (or two replayed graphs) that can run at the same time must not
+ * share a workspace or an output.  Thread blocks of this part wait on one
+ * another only at the hardware barriers of a cluster, whose blocks run together,
+ * so no call sets the words adaln_device_error() reads.
  */
 #ifndef ADALN_OPS_H
 #define ADALN_OPS_H
@@ -216,9 +216,9 @@ size_t adaln_grad_norm_workspace_bytes(const adaln_tensor *grads, int count);
  *
  * Squares are summed in fp32 within 16 KB of a tensor (in fp64 where fp32 would
  * overflow or lose them), then in pairs of fp32 with the additions' errors (or in
- * fp64).  The order is fixed by the list's sizes
- * and types alone, not by addresses.  The result is infinite or NaN exactly as
- * the exact norm (rounded to fp32) is.
+ * fp64).  The order is fixed by the list's sizes and types alone, not by
+ * addresses.  The result is infinite or NaN exactly as the exact norm (rounded
+ * to fp32) is.
  *
  *   grads  host array of `count` tensors (0 <= count <= 65536; read before the
  *          call returns), mixed types; numel >= 0, fewer than 2^40 in all.  A
@@ -235,7 +235,9 @@ adaln_status adaln_grad_norm(const adaln_tensor *grads, int count, float *norm, 
  *   out[i] = round(coef * grad[i])                fp32 product, one rounding
  *   stats  = [norm, coef]                         [2] fp32 output (device)
  *
- * A norm that is infinite gives coef 0, one that is NaN gives NaN everywhere.
+ * coef is formed from the norm before it is rounded to fp32.  An infinity among
+ * the elements gives coef 0 (and NaN where it stands), a NaN gives NaN everywhere;
+ * with an infinite max_norm coef is 1 unless the norm is NaN.
  * outs[i] has the numel and dtype of grads[i]; its data may be exactly
  * grads[i]'s (in place: with coef 1 nothing is written then) and must not
  * overlap any other tensor of the two lists, stats or the workspace.  max_norm

@@ -52,3 +52,21 @@ def test_lists_of_any_kind():
         assert torch.equal(s2, stats) and len(list(back)) == 3
         assert back is given or isinstance(back, list)
         assert all(torch.equal(a, w) for a, w in zip(outs, want)) and all(a is b for a, b in zip(back, outs))
+
+
+def test_coefficient_of_norms_beyond_fp32():
+    """coef comes from the norm before its rounding: elements that fp32 holds with
+    a norm that it does not are scaled, not lost; only infinite elements give 0."""
+    g = [torch.full((20000,), 3e38, device="cuda")]
+    norm = float(g[0].double().square().sum().sqrt())
+    outs, stats = binding.adaln_grad_clip(g, 1e38)
+    assert stats[0] == float("inf")
+    # one rounding of coef, as the sums of squares are within 12 U of the norm: 14 U; a product's rounding more
+    assert abs(float(stats[1]) - 1e38 / norm) <= 14 * 2.0 ** -24 * (1e38 / norm)
+    want = g[0].double() * (1e38 / norm)
+    assert ((outs[0].double() - want).abs() <= 15 * 2.0 ** -24 * want).all()
+    outs, stats = binding.adaln_grad_clip(g, float("inf"))
+    assert stats.tolist() == [float("inf"), 1.0] and torch.equal(outs[0], g[0])
+    g[0][5] = float("-inf")
+    outs, stats = binding.adaln_grad_clip(g, 1e38)
+    assert stats.tolist() == [float("inf"), 0.0] and outs[0][5].isnan() and int(outs[0].count_nonzero()) == 1
