@@ -96,3 +96,23 @@ def test_captured_with_a_kept_workspace():
         ws.fill_(255)
         graph.replay()
         assert torch.equal(got.cpu(), ops_ref.embed_bwd_order(g, t, V, 1.0))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradients_of_padding_are_not_read(dtype):
+    """NaN and infinities at padding tokens change nothing; a NaN at a token stays in its row and column."""
+    for n, V, D in ((700, 50, 264), (9000, 40, 264), (33000, 3000, 8)):
+        t, _ = make("skew", n, V, 8, dtype, seed=n)
+        g = rows(n, D, dtype, n)
+        want = BWD[dtype](g, t, V)
+        bad = (t < 0) | (t >= V)
+        assert bad.sum() > 32
+        g[bad] = float("nan")
+        g[bad.nonzero()[::2, 0]] = float("-inf")
+        assert torch.equal(BWD[dtype](g, t, V), want)
+        token = int(t[t >= 0].mode().values)
+        g[(t == token).nonzero()[-1, 0], D - 3] = float("nan")
+        got = BWD[dtype](g, t, V)
+        assert got[token, D - 3].isnan()
+        got[token, D - 3] = want[token, D - 3]
+        assert torch.equal(got, want)
