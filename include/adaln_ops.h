@@ -10,8 +10,9 @@
  *
  * The conventions of adaln.h hold (device pointers, 16-byte alignment, caller-
  * owned buffers, asynchronous on `stream`, order of the checks, status codes),
- * with the differences stated at each call.  No call allocates (device or host
- * memory) or synchronizes, and every call can be captured into a CUDA graph.
+ * with the differences stated at each call.  No call allocates or synchronizes
+ * (the first one of a kernel on a device keeps a small record on the host), and
+ * every call can be captured into a CUDA graph.
  * Two calls (or two replayed graphs) that can run at the same time must not
  * share a workspace or an output.  Thread blocks of this part wait on one
  * another only at the hardware barriers of a cluster, whose blocks run together,

@@ -14,8 +14,8 @@
 //      who computes the piece, not what;
 //   3. a warp takes a piece, or the shorter runs that begin among some
 //      consecutive places, at 256 columns, and adds each run's rows in ascending
-//      order, up to 15 rows in flight whatever the runs' lengths.  A short run's row is
-//      written at once.  The pieces of a long run are the leaves of a 32-way
+//      order, up to 15 rows (bf16; 7 of fp32) in flight whatever the runs' lengths.
+//      A short run's row is written at once.  The pieces of a long run are the leaves of a 32-way
 //      tree: whoever brings the last child of a node adds the children in order
 //      (a ticket per node; nobody waits).
 // Sorting is a chain of latencies that leaves the memory idle, so the table is
@@ -831,10 +831,14 @@ cudaError_t launch_embed_bwd(const T *d_out, const void *tokens, int tokens_are_
                  accumulate ? 0 : (long long)V * D * (d_table ? 2 : 4) / 16};
     cudaError_t e = cudaSuccess;
     // In shared memory where a token and a place fit 32 bits: 4 tokens a thread, by
-    // one CTA (9.5 us at 4096; with 32 a thread 67 us at 32768) or by a cluster of 8
-    // (the whole call at 20000 tokens x 64: 29.7 us against 31.8 with the kernels,
-    // and three launches fewer).  Beyond, the kernels: with 16 a thread the
-    // cluster's call takes 49 us at 33000 and 64 at 75351, theirs 32 and 46.
+    // one CTA (9.5 us at 4096; with 32 a thread 67 us at 32768) or by a cluster of 8.
+    // Beyond, the kernels: with 16 a thread the cluster's call takes 49 us at 33000
+    // and 64 at 75351, theirs 32 and 46.  Between, the cluster's call against theirs
+    // in us from graphs, text of 1001 tokens x 64 columns: 20.6 / 22.7 at 4097, 23.8
+    // / 25.5 at 8192, 27.6 / 30.2 at 20000, 30.0 / 30.9 at 32768; of 50021 tokens x
+    // 1024: 30.0 / 37.6, 29.8 / 39.9, 40.8 / 50.7, 47.5 / 58.1.  Of 50021 x 64 they
+    // are within 1.2 us of one another from 8192 to 24576.  A cluster's CTA holds 4096
+    // places whatever n is, so at 5000 tokens two of its eight sort.
     if (n <= 8 * 4 * kTeamThreads && key_bits + bits <= 32) {
         const int passes = (key_bits + 7) / 8, digit_bits = (key_bits + passes - 1) / passes;
         auto sort = n <= 4 * kTeamThreads ? sort_team<1, 4> : sort_team<8, 4>;

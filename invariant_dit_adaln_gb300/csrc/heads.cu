@@ -256,11 +256,11 @@ __global__ void __launch_bounds__(32 * kWarps) heads_fwd_kernel(const __grid_con
 // large forward calls.  Each warp takes an equal share of the tile's (token,
 // U * 32/LPR heads) tasks, in order, and copies their rows asynchronously into
 // a ring of kStages tasks of its own, so that the bytes in flight are not held
-// in registers.  A token's angles travel with its tasks; its position is read
+// in registers.  Padded rows are copied too.  A token's angles travel with its tasks; its position is read
 // one token ahead.
 //
 // Measured at B=2, S=4096, 24 + 24 heads of 128 in bf16, back to back: forward
-// 34.2 us (203 MB, 5.9 TB/s), backward 58.4 us with the join of dw (304 MB, 5.2
+// 34.1 us (203 MB, 6.0 TB/s), backward 57.1 us with the join of dw (304 MB, 5.3
 // TB/s).  With the rows in registers the backward was bound by load latency at
 // 18 warps an SM: 70 us.  2 and 4 rows a lane and 3 or 4 stages differ by 2 %;
 // any register spilled in the loop costs 10 us, hence the launch bounds.
@@ -623,8 +623,8 @@ int tile_tokens(int tasks, int S, int Hq, int Hk, int Dh) {
 // 4 us more, 96: 5 us more at the size above).  It is fixed by S, the head
 // counts and the head size, and with it the order of dw.
 int bwd_tile(int S, int Hq, int Hk, int Dh) { return tile_tokens(48, S, Hq, Hk, Dh); }
-// Forward: 24, for a finer tail (fp32, 4593 tokens of 20 + 4 heads of 96: 15.8 us
-// against 17.4 with 48).
+// Forward: 24, for a finer tail (fp32, 4593 tokens of 20 + 4 heads of 96: 14.6 us
+// from a graph against 15.8 with 48).
 int fwd_tile(int S, int Hq, int Hk, int Dh) { return tile_tokens(24, S, Hq, Hk, Dh); }
 
 template <typename T, int LPR, int U, bool INTER, bool BWD>
@@ -669,7 +669,7 @@ cudaError_t pick_fwd(const HeadsCall &c, cudaStream_t stream, const DeviceInfo &
     // Few rows go one a lane straight through registers, for the shortest path
     // through the kernel (8 tokens of 24 + 24 heads: 3.6 us of kernel); from 16
     // warps an SM on 4 a lane, or through the ring where a tile has 4 tasks or
-    // more for each warp (at the size above 34.2 us against 41).
+    // more for each warp (at the size above 34.1 us against 41).
     const long long rows = (long long)c.B * c.S * (c.H[0] + c.H[1]);
     if (rows / (4 * (32 / LPR)) < 16ll * dev.sm_count) return run_direct<T, LPR, 1>(c, stream);
     const int tile = fwd_tile(c.S, c.H[0], c.H[1], c.Dh), group = tile_rows(c.H[0], c.H[1], c.Dh) * (32 / LPR);
