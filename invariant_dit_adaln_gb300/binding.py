@@ -1,5 +1,5 @@
-"""ctypes binding of libadaln.so: the C ABI of include/adaln.h and
-include/adaln_ops.h with the same entry-point names, taking PyTorch CUDA
+"""Binding of libadaln.so: the C ABI of include/adaln.h, adaln_ops.h and
+adaln_tune.h with the same entry-point names, taking PyTorch CUDA
 tensors.
 
 This layer only marshals arguments: it checks dtypes, devices and shapes,
@@ -71,6 +71,36 @@ _SIGNATURES.update({
     "adaln_grad_norm_workspace_bytes": (_SZ, [_P, _I]),
     "adaln_grad_norm": (_I, [_P, _I, _P, _P, _SZ, _P]),
     "adaln_grad_clip": (_I, [_P, _P, _I, ctypes.c_double, _P, _P, _SZ, _P]),
+})
+
+# include/adaln_tune.h
+_L = ctypes.c_int64
+_PACK = (_I, [_P, _P, _L, _I, _P])
+_FWD8 = (_I, [_P] * 6 + [_I] * 3 + [_F, _P])
+_BWD8 = (_I, [_P] * 8 + [_SZ] + [_I] * 3 + [_P])
+_AGAIN8 = (_I, [_P] * 5 + [_I] * 3 + [_P])
+_LORA_FWD = (_I, [_P] * 5 + [_I] + [_P] * 4 + [_SZ] + [_I] * 6 + [_P])
+_LORA_BWD = (_I, [_P] * 7 + [_I] + [_P] * 5 + [_I, _P, _SZ] + [_I] * 6 + [_P])
+_SIGNATURES.update({
+    "adaln_ckpt8_row_bytes": (_SZ, [_I]),
+    "adaln_ckpt8_pack": _PACK,
+    "adaln_f32_ckpt8_pack": _PACK,
+    "adaln_ckpt8_unpack": _PACK,
+    "adaln_f32_ckpt8_unpack": _PACK,
+    "adaln_out_fwd_ckpt8": _FWD8,
+    "adaln_f32_out_fwd_ckpt8": _FWD8,
+    "adaln_out_bwd_ckpt8_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "adaln_out_bwd_ckpt8": _BWD8,
+    "adaln_f32_out_bwd_ckpt8": _BWD8,
+    "adaln_out_again_ckpt8": _AGAIN8,
+    "adaln_f32_out_again_ckpt8": _AGAIN8,
+    "adaln_lora_state_bytes": (_SZ, [_I] * 3),
+    "adaln_lora_fwd": _LORA_FWD,
+    "adaln_f32_lora_fwd": _LORA_FWD,
+    "adaln_lora_bwd_workspace_bytes": (_SZ, [_I] * 5),
+    "adaln_f32_lora_bwd_workspace_bytes": (_SZ, [_I] * 5),
+    "adaln_lora_bwd": _LORA_BWD,
+    "adaln_f32_lora_bwd": _LORA_BWD,
 })
 
 _lib = None
@@ -482,7 +512,13 @@ def adaln_proj_wgrad_rows(d_emb, u, n0, n1, dW_acc=None, db_acc=None, dW=None, d
 _BOUND = ("adaln_qk_norm_rope_fwd", "adaln_f32_qk_norm_rope_fwd", "adaln_qk_norm_rope_bwd_workspace_bytes",
           "adaln_qk_norm_rope_bwd", "adaln_f32_qk_norm_rope_bwd", "adaln_embed_fwd", "adaln_f32_embed_fwd",
           "adaln_embed_bwd_workspace_bytes", "adaln_embed_bwd", "adaln_f32_embed_bwd",
-          "adaln_grad_norm_workspace_bytes", "adaln_grad_norm", "adaln_grad_clip")
+          "adaln_grad_norm_workspace_bytes", "adaln_grad_norm", "adaln_grad_clip",
+          "adaln_ckpt8_row_bytes", "adaln_ckpt8_pack", "adaln_f32_ckpt8_pack", "adaln_ckpt8_unpack",
+          "adaln_f32_ckpt8_unpack", "adaln_out_fwd_ckpt8", "adaln_f32_out_fwd_ckpt8",
+          "adaln_out_bwd_ckpt8_workspace_bytes", "adaln_out_bwd_ckpt8", "adaln_f32_out_bwd_ckpt8",
+          "adaln_out_again_ckpt8", "adaln_f32_out_again_ckpt8", "adaln_lora_state_bytes", "adaln_lora_fwd",
+          "adaln_f32_lora_fwd", "adaln_lora_bwd_workspace_bytes", "adaln_f32_lora_bwd_workspace_bytes",
+          "adaln_lora_bwd", "adaln_f32_lora_bwd")
 _marshal = None
 
 
@@ -634,3 +670,163 @@ def adaln_grad_clip(grads, max_norm, outs=None, stats=None, workspace=None, stre
         with _on(stream):
             return adaln_grad_clip(grads, max_norm, outs, stats, workspace)
     return (_marshal or _native()).grad_clip(grads, max_norm, outs, stats, workspace)
+
+
+# ---------------------------------------------------------------------------
+# include/adaln_tune.h: activations in 8 bits, low-rank adapters (marshalled as
+# the calls above)
+# ---------------------------------------------------------------------------
+
+def adaln_ckpt8_row_bytes(D):
+    """Bytes of the 8-bit record of a row of D channels."""
+    return load().adaln_ckpt8_row_bytes(D)
+
+
+def adaln_ckpt8_pack(x, ckpt=None, stream=None):
+    """The 8-bit records [..., adaln_ckpt8_row_bytes(D)] uint8 of x [..., D] bf16:
+    int8 codes and a power-of-two scale for each group of 32 channels."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_ckpt8_pack(x, ckpt)
+    return (_marshal or _native()).ckpt8_pack(False, x, ckpt)
+
+
+def adaln_f32_ckpt8_pack(x, ckpt=None, stream=None):
+    """adaln_ckpt8_pack of an fp32 x."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_f32_ckpt8_pack(x, ckpt)
+    return (_marshal or _native()).ckpt8_pack(True, x, ckpt)
+
+
+def adaln_ckpt8_unpack(ckpt, D, out=None, stream=None):
+    """The values [..., D] that records stand for, in bf16 (exact)."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_ckpt8_unpack(ckpt, D, out)
+    return (_marshal or _native()).ckpt8_unpack(False, ckpt, D, out)
+
+
+def adaln_f32_ckpt8_unpack(ckpt, D, out=None, stream=None):
+    """adaln_ckpt8_unpack in fp32 (the same values)."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_f32_ckpt8_unpack(ckpt, D, out)
+    return (_marshal or _native()).ckpt8_unpack(True, ckpt, D, out)
+
+
+def adaln_out_fwd_ckpt8(x, emb, out=None, mean=None, rstd=None, ckpt=None, eps=1e-6, stream=None):
+    """adaln_out_fwd that also writes the 8-bit records of x, which its backward
+    then reads instead of x.  Returns (out, mean, rstd, ckpt)."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_out_fwd_ckpt8(x, emb, out, mean, rstd, ckpt, eps)
+    return (_marshal or _native()).out_fwd_ckpt8(False, x, emb, out, mean, rstd, ckpt, eps)
+
+
+def adaln_f32_out_fwd_ckpt8(x, emb, out=None, mean=None, rstd=None, ckpt=None, eps=1e-6, stream=None):
+    """adaln_out_fwd_ckpt8 in fp32 (adaln_f32_out_fwd and the records)."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_f32_out_fwd_ckpt8(x, emb, out, mean, rstd, ckpt, eps)
+    return (_marshal or _native()).out_fwd_ckpt8(True, x, emb, out, mean, rstd, ckpt, eps)
+
+
+def adaln_out_bwd_ckpt8_workspace_bytes(B, S, D):
+    return load().adaln_out_bwd_ckpt8_workspace_bytes(B, S, D)
+
+
+def adaln_out_bwd_ckpt8(dy, ckpt, emb, mean, rstd, dx=None, d_emb=None, workspace=None, stream=None):
+    """adaln_out_bwd at the values that the records stand for (the same bytes).
+    Returns (dx [B,S,D] bf16, d_emb [B,2D] fp32)."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_out_bwd_ckpt8(dy, ckpt, emb, mean, rstd, dx, d_emb, workspace)
+    return (_marshal or _native()).out_bwd_ckpt8(False, dy, ckpt, emb, mean, rstd, dx, d_emb, workspace)
+
+
+def adaln_f32_out_bwd_ckpt8(dy, ckpt, emb, mean, rstd, dx=None, d_emb=None, workspace=None, stream=None):
+    """adaln_f32_out_bwd at the values that the records stand for."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_f32_out_bwd_ckpt8(dy, ckpt, emb, mean, rstd, dx, d_emb, workspace)
+    return (_marshal or _native()).out_bwd_ckpt8(True, dy, ckpt, emb, mean, rstd, dx, d_emb, workspace)
+
+
+def adaln_out_again_ckpt8(ckpt, emb, mean, rstd, out=None, stream=None):
+    """The norm's output [B,S,D] bf16 taken again from the records and the
+    forward's statistics: the input of the next projection, for its weight
+    gradient."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_out_again_ckpt8(ckpt, emb, mean, rstd, out)
+    return (_marshal or _native()).out_again_ckpt8(False, ckpt, emb, mean, rstd, out)
+
+
+def adaln_f32_out_again_ckpt8(ckpt, emb, mean, rstd, out=None, stream=None):
+    """adaln_out_again_ckpt8 in fp32."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_f32_out_again_ckpt8(ckpt, emb, mean, rstd, out)
+    return (_marshal or _native()).out_again_ckpt8(True, ckpt, emb, mean, rstd, out)
+
+
+def adaln_lora_state_bytes(B, S, R):
+    return load().adaln_lora_state_bytes(B, S, R)
+
+
+def adaln_lora_fwd(x, A, U, scale, ids, y=None, lens=None, out=None, state=None, stream=None):
+    """out = y + scale[a] (x A[a]^T) U[a] with the adapter a = ids[b] of each
+    sample: x [B,S,K], y [B,S,N] bf16 (any strides with dense channels; y None:
+    zero), A [NA,R,K], U [NA,R,N] bf16, scale [NA] fp32, ids [B] int32 or int64
+    (outside [0, NA): no adapter), lens [B] int32 the rows of each sample (None:
+    all).  out may be y (in place); rows past a sample's end are not written (zero
+    in an out allocated here).  Returns (out, state), the state for
+    adaln_lora_bwd."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_lora_fwd(x, A, U, scale, ids, y, lens, out, state)
+    return (_marshal or _native()).lora_fwd(False, x, A, U, scale, ids, y, lens, out, state)
+
+
+def adaln_f32_lora_fwd(x, A, U, scale, ids, y=None, lens=None, out=None, state=None, stream=None):
+    """adaln_lora_fwd on fp32 rows and adapters."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_f32_lora_fwd(x, A, U, scale, ids, y, lens, out, state)
+    return (_marshal or _native()).lora_fwd(True, x, A, U, scale, ids, y, lens, out, state)
+
+
+def adaln_lora_bwd_workspace_bytes(B, S, K, N, R):
+    return load().adaln_lora_bwd_workspace_bytes(B, S, K, N, R)
+
+
+def adaln_f32_lora_bwd_workspace_bytes(B, S, K, N, R):
+    return load().adaln_f32_lora_bwd_workspace_bytes(B, S, K, N, R)
+
+
+def adaln_lora_bwd(d_out, x, state, A, U, scale, ids, lens=None, dx_base=None, dx=None, dA_acc=None, dU_acc=None,
+                   accumulate=False, want_x=True, want_w=True, workspace=None, stream=None):
+    """Backward of adaln_lora_fwd from its inputs and state: (dx, dA_acc, dU_acc).
+    dx [B,S,K] bf16 = dx_base (what else flows into x; None: zero) plus the
+    adapter's part, and may be dx_base; it is computed where given or want_x.  The
+    adapters' gradients are fp32 [NA,R,K] and [NA,R,N]: given ones are filled, or
+    added to with accumulate; want_w allocates those not given (None without
+    it)."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_lora_bwd(d_out, x, state, A, U, scale, ids, lens, dx_base, dx, dA_acc, dU_acc, accumulate,
+                                  want_x, want_w, workspace)
+    return (_marshal or _native()).lora_bwd(False, d_out, x, state, A, U, scale, ids, lens, dx_base, dx, dA_acc, dU_acc,
+                                            accumulate, want_x, want_w, workspace)
+
+
+def adaln_f32_lora_bwd(d_out, x, state, A, U, scale, ids, lens=None, dx_base=None, dx=None, dA_acc=None, dU_acc=None,
+                       accumulate=False, want_x=True, want_w=True, workspace=None, stream=None):
+    """adaln_lora_bwd on fp32 rows, gradients and adapters."""
+    if stream is not None:
+        with _on(stream):
+            return adaln_f32_lora_bwd(d_out, x, state, A, U, scale, ids, lens, dx_base, dx, dA_acc, dU_acc, accumulate,
+                                      want_x, want_w, workspace)
+    return (_marshal or _native()).lora_bwd(True, d_out, x, state, A, U, scale, ids, lens, dx_base, dx, dA_acc, dU_acc,
+                                            accumulate, want_x, want_w, workspace)

@@ -7,7 +7,7 @@ fast math, so every floating-point operation rounds as written.
 
 Beside it g++ builds ``lib/adaln_marshal_<Python>_<torch version>.so``, the
 Python module that marshals PyTorch tensors for the calls of
-include/adaln_ops.h.  It is compiled against the running Python and the
+include/adaln_ops.h and include/adaln_tune.h.  It is compiled against the running Python and the
 installed PyTorch, hence its name.  The library does not need it: where it
 cannot be built, build() warns, and only those calls from Python are missing
 (they raise).
@@ -31,8 +31,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libadaln.so")
+HEADERS = ("adaln.h", "adaln_ops.h", "adaln_tune.h")
 SOURCES = ["api.cu", "out.cu", "proj.cu", "tc_proj.cu", "res.cu", "f32.cu", "noalloc.cu",
-           "ops_api.cu", "heads.cu", "embed.cu", "grads.cu"]
+           "ops_api.cu", "heads.cu", "embed.cu", "grads.cu", "tune_api.cu", "ckpt.cu", "lora.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "--fmad=false", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xptxas", "-warn-spills", f"-I{INCLUDE}", f"-I{CSRC}"]
@@ -51,7 +52,7 @@ def nvcc() -> str:
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    files += [os.path.join(INCLUDE, f) for f in ("adaln.h", "adaln_ops.h")]
+    files += [os.path.join(INCLUDE, f) for f in HEADERS]
     return files
 
 
@@ -72,7 +73,7 @@ def _marshal_up_to_date() -> bool:
     path = marshal_path()
     if not os.path.exists(path):
         return False
-    inputs = [MARSHAL_SOURCE] + [os.path.join(INCLUDE, f) for f in ("adaln.h", "adaln_ops.h")]
+    inputs = [MARSHAL_SOURCE] + [os.path.join(INCLUDE, f) for f in HEADERS]
     return all(os.path.getmtime(f) <= os.path.getmtime(path) for f in inputs)
 
 

@@ -1,0 +1,96 @@
+// The 8-bit record of a row (include/adaln_tune.h): codes, scale bytes.
+#pragma once
+
+#include "common.cuh"
+
+namespace adaln {
+
+constexpr int kCkptGroup = 32;  // channels a scale byte covers
+
+__host__ __device__ constexpr int ckpt8_code_bytes(int D) { return (D + 15) / 16 * 16; }
+__host__ __device__ constexpr int ckpt8_groups(int D) { return (D + kCkptGroup - 1) / kCkptGroup; }
+__host__ __device__ constexpr int ckpt8_row_bytes(int D) { return ckpt8_code_bytes(D) + (ckpt8_groups(D) + 15) / 16 * 16; }
+
+// The scale byte of a group from the fp32 bits of its largest magnitude m 2^e,
+// 1 <= m < 2: k = e - 6 brings it to 64 m < 128, and from m = 127.5 / 64 (mantissa
+// bits 0x7F0000) on it is one more, which is a carry into the exponent.  k ends at
+// 121: with 122 the code 64 would stand for 2^128.
+constexpr uint32_t kCkptLastScale = 121 + 127;
+__device__ __forceinline__ uint32_t ckpt8_scale(uint32_t max_bits) {
+    if (max_bits >= 0x7F800000u) return 255u;
+    const int s = (int)((max_bits + 0x10000u) >> 23) - 6;
+    return s < 1 ? 1u : min((uint32_t)s, kCkptLastScale);
+}
+// 2^k of a scale byte k + 127 (255: infinity, which makes every value 0 * inf = NaN)
+__device__ __forceinline__ float ckpt8_step(uint32_t scale) { return __uint_as_float(scale << 23); }
+// 2^-k (scale bytes 1 .. 253)
+__device__ __forceinline__ float ckpt8_inverse(uint32_t scale) { return __uint_as_float((254u - scale) << 23); }
+
+// Four codes, low byte first: x 2^-k rounded to an integer by adding 1.5 * 2^23
+// (the product with a power of two is exact, and the fused form rounds once, to
+// even); the integer stands in the low bits, in two's complement.
+__device__ __forceinline__ uint32_t ckpt8_codes(px2 lo, px2 hi, px2 inv) {
+    const px2 magic = px_splat(12582912.0f);
+    const px2 a = px_fma(lo, inv, magic), b = px_fma(hi, inv, magic);
+    const uint32_t p = __byte_perm(__float_as_uint(px_lo(a)), __float_as_uint(px_hi(a)), 0x0040);
+    const uint32_t q = __byte_perm(__float_as_uint(px_lo(b)), __float_as_uint(px_hi(b)), 0x0040);
+    return __byte_perm(p, q, 0x5410);
+}
+
+// Four codes as exact fp32 pairs: byte + 128 in the low bits of 2^23, less 2^23 + 128
+__device__ __forceinline__ void ckpt8_floats(uint32_t w, px2 &lo, px2 &hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const px2 less = px_splat(-8388736.0f);
+    lo = px_add(px_make(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540)),
+                        __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7541))), less);
+    hi = px_add(px_make(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7542)),
+                        __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7543))), less);
+}
+
+// the largest magnitude's bits among 8 channels, bf16 (as 16-bit halves) or fp32
+__device__ __forceinline__ uint32_t ckpt8_max(const uint4 &v) {
+    const uint32_t m = 0x7FFF7FFFu;
+    const uint32_t a = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+    return max(a & 0xFFFFu, a >> 16) << 16;
+}
+__device__ __forceinline__ uint32_t ckpt8_max(const float4 &a, const float4 &b) {
+    const uint32_t m = 0x7FFFFFFFu;
+    const uint32_t x = max(max(__float_as_uint(a.x) & m, __float_as_uint(a.y) & m),
+                           max(__float_as_uint(a.z) & m, __float_as_uint(a.w) & m));
+    const uint32_t y = max(max(__float_as_uint(b.x) & m, __float_as_uint(b.y) & m),
+                           max(__float_as_uint(b.z) & m, __float_as_uint(b.w) & m));
+    return max(x, y);
+}
+
+// Vector v (8 channels) of a record, by the lane that holds it; four neighbouring
+// lanes, the first with v a multiple of 4, hold a group (lanes past the row's V
+// vectors give zeros, max_bits 0).  All four run this.  Fills the record's
+// padding as well.
+__device__ __forceinline__ void ckpt8_put(unsigned char *rec, int D, int V, int v, uint32_t max_bits,
+                                          px2 (&x)[4]) {
+    max_bits = max(max_bits, __shfl_xor_sync(0xFFFFFFFFu, max_bits, 1));
+    max_bits = max(max_bits, __shfl_xor_sync(0xFFFFFFFFu, max_bits, 2));
+    const uint32_t scale = ckpt8_scale(max_bits);
+    const int code_bytes = ckpt8_code_bytes(D);
+    if (v * 8 < code_bytes) {
+        uint2 c = make_uint2(0u, 0u);
+        if (v < V && scale != 255u) {
+            const px2 inv = px_splat(ckpt8_inverse(scale));
+            if (scale == kCkptLastScale) {  // values from 127.5 2^121 on would round to 128: 127
+                const float most = 127.0f * 0x1p121f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    x[q] = px_make(fminf(fmaxf(px_lo(x[q]), -most), most), fminf(fmaxf(px_hi(x[q]), -most), most));
+            }
+            c = make_uint2(ckpt8_codes(x[0], x[1], inv), ckpt8_codes(x[2], x[3], inv));
+        }
+        *reinterpret_cast<uint2 *>(rec + (size_t)v * 8) = c;
+    }
+    if ((v & 3) == 0 && v < V) {
+        rec[code_bytes + (v >> 2)] = (unsigned char)scale;
+        if (v + 4 >= V)
+            for (int i = (v >> 2) + 1; i & 15; ++i) rec[code_bytes + i] = 0;
+    }
+}
+
+}  // namespace adaln

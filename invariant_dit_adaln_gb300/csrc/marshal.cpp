@@ -1,4 +1,4 @@
-// Marshalling of the calls of include/adaln_ops.h for Python: checks PyTorch
+// Marshalling of the calls of include/adaln_ops.h and adaln_tune.h for Python: checks PyTorch
 // tensors, copies inputs whose layout the C ABI refuses, allocates missing
 // outputs and workspaces, and calls the C ABI on the current stream.  No
 // computation.  In Python these steps took 10 to 35 us a call, several times
@@ -22,6 +22,7 @@
 #include <vector>
 
 #include "adaln_ops.h"
+#include "adaln_tune.h"
 
 namespace {
 
@@ -41,6 +42,25 @@ struct Library {
     decltype(&adaln_grad_norm_workspace_bytes) grad_bytes;
     decltype(&adaln_grad_norm) grad_norm;
     decltype(&adaln_grad_clip) grad_clip;
+    decltype(&adaln_ckpt8_row_bytes) ckpt8_bytes;
+    decltype(&adaln_ckpt8_pack) ckpt8_pack;
+    decltype(&adaln_f32_ckpt8_pack) f32_ckpt8_pack;
+    decltype(&adaln_ckpt8_unpack) ckpt8_unpack;
+    decltype(&adaln_f32_ckpt8_unpack) f32_ckpt8_unpack;
+    decltype(&adaln_out_fwd_ckpt8) fwd_ckpt8;
+    decltype(&adaln_f32_out_fwd_ckpt8) f32_fwd_ckpt8;
+    decltype(&adaln_out_bwd_ckpt8_workspace_bytes) bwd_ckpt8_bytes;
+    decltype(&adaln_out_bwd_ckpt8) bwd_ckpt8;
+    decltype(&adaln_f32_out_bwd_ckpt8) f32_bwd_ckpt8;
+    decltype(&adaln_out_again_ckpt8) again_ckpt8;
+    decltype(&adaln_f32_out_again_ckpt8) f32_again_ckpt8;
+    decltype(&adaln_lora_state_bytes) lora_state_bytes;
+    decltype(&adaln_lora_fwd) lora_fwd;
+    decltype(&adaln_f32_lora_fwd) f32_lora_fwd;
+    decltype(&adaln_lora_bwd_workspace_bytes) lora_bwd_bytes;
+    decltype(&adaln_f32_lora_bwd_workspace_bytes) f32_lora_bwd_bytes;
+    decltype(&adaln_lora_bwd) lora_bwd;
+    decltype(&adaln_f32_lora_bwd) f32_lora_bwd;
 } lib;
 PyObject *raise_status;  // called with (name, status); raises
 
@@ -70,7 +90,8 @@ using Shape = std::initializer_list<int64_t>;
 
 const char *type_name(ScalarType t) {
     return t == at::kBFloat16 ? "torch.bfloat16" : t == at::kFloat ? "torch.float32" : t == at::kInt ? "torch.int32"
-                                                                                                  : "torch.int64";
+           : t == at::kByte                                                                    ? "torch.uint8"
+                                                                                               : "torch.int64";
 }
 
 bool given(PyObject *o) { return o != Py_None; }
@@ -465,6 +486,286 @@ PyObject *grad_clip(PyObject *const *a) {
     return Py_BuildValue("(ON)", PyIter_Check(outs) ? to.seq : outs, THPVariable_Wrap(stats));
 }
 
+// ---- activations in 8 bits ----------------------------------------------------------
+
+// the sizes of a dense [..., D] tensor without its last dimension
+std::vector<int64_t> leading(const Tensor &x) {
+    return std::vector<int64_t>(x.sizes().begin(), x.sizes().end() - 1);
+}
+std::vector<int64_t> with(std::vector<int64_t> shape, int64_t last) {
+    shape.push_back(last);
+    return shape;
+}
+
+int64_t rows_before(const std::vector<int64_t> &lead) {
+    int64_t rows = 1;
+    for (int64_t n : lead) rows *= n;
+    return rows;
+}
+
+const Tensor &of_dim(PyObject *o, const char *name, int64_t least, int64_t most, const char *shape) {
+    if (!THPVariable_Check(o)) refuse(PyExc_TypeError, "%s: expected a CUDA tensor", name);
+    const Tensor &x = THPVariable_Unpack(o);
+    if (x.dim() < least || x.dim() > most) refuse(PyExc_ValueError, "%s: expected a tensor %s", name, shape);
+    return x;
+}
+
+// bytes of a record of D channels; refuses a D without records
+int64_t record(int64_t D) {
+    const size_t n = lib.ckpt8_bytes(size_of(D));
+    if (n == 0) refuse(PyExc_ValueError, "ckpt: no records of %lld channels", (long long)D);
+    return (int64_t)n;
+}
+
+// ckpt8_pack(f32, x, ckpt)
+PyObject *ckpt8_pack(PyObject *const *a) {
+    const ScalarType t = float_type(a[0]);
+    const int dev = device_of(a[1], "x");
+    of_dim(a[1], "x", 1, 64, "[..., D]");
+    const Tensor x = flat(tensor(a[1], "x", dev, t, t));
+    const auto lead = leading(x);
+    const int64_t D = x.size(-1), rows = rows_before(lead);
+    const Tensor ckpt = result(a[2], "ckpt", dev, at::kByte, with(lead, record(D)));
+    if (t == at::kFloat)
+        status("adaln_f32_ckpt8_pack", lib.f32_ckpt8_pack((const float *)ptr(x), (uint8_t *)ptr(ckpt), rows,
+                                                          size_of(D), stream_of(dev)));
+    else
+        status("adaln_ckpt8_pack", lib.ckpt8_pack((const adaln_bf16 *)ptr(x), (uint8_t *)ptr(ckpt), rows, size_of(D),
+                                                  stream_of(dev)));
+    return THPVariable_Wrap(ckpt);
+}
+
+// ckpt8_unpack(f32, ckpt, D, out)
+PyObject *ckpt8_unpack(PyObject *const *a) {
+    const ScalarType t = float_type(a[0]);
+    const int dev = device_of(a[1], "ckpt");
+    const int64_t D = integer(a[2]);
+    const auto lead = leading(of_dim(a[1], "ckpt", 1, 64, "[..., row_bytes]"));
+    const Tensor ckpt = flat(a[1], "ckpt", dev, at::kByte, at::kByte, with(lead, record(D)));
+    const Tensor out = result(a[3], "out", dev, t, with(lead, D));
+    if (t == at::kFloat)
+        status("adaln_f32_ckpt8_unpack", lib.f32_ckpt8_unpack((const uint8_t *)ptr(ckpt), (float *)ptr(out),
+                                                              rows_before(lead), size_of(D), stream_of(dev)));
+    else
+        status("adaln_ckpt8_unpack", lib.ckpt8_unpack((const uint8_t *)ptr(ckpt), (adaln_bf16 *)ptr(out),
+                                                      rows_before(lead), size_of(D), stream_of(dev)));
+    return THPVariable_Wrap(out);
+}
+
+// out_fwd_ckpt8(f32, x, emb, out, mean, rstd, ckpt, eps)
+PyObject *out_fwd_ckpt8(PyObject *const *a) {
+    const ScalarType t = float_type(a[0]);
+    const int dev = device_of(a[1], "x");
+    of_dim(a[1], "x", 3, 3, "[B, S, D]");
+    const Tensor x = flat(tensor(a[1], "x", dev, t, t));
+    const int64_t B = x.size(0), S = x.size(1), D = x.size(2);
+    const Tensor emb = flat(a[2], "emb", dev, t, t, {B, 2 * D});
+    const Tensor ckpt = result(a[6], "ckpt", dev, at::kByte, {B, S, record(D)});
+    const Tensor out = result(a[3], "out", dev, t, {B, S, D}), mean = result(a[4], "mean", dev, at::kFloat, {B, S}),
+                 rstd = result(a[5], "rstd", dev, at::kFloat, {B, S});
+    const float eps = (float)number(a[7]);
+    if (t == at::kFloat)
+        status("adaln_f32_out_fwd_ckpt8",
+               lib.f32_fwd_ckpt8((const float *)ptr(x), (const float *)ptr(emb), (float *)ptr(out), (float *)ptr(mean),
+                                 (float *)ptr(rstd), (uint8_t *)ptr(ckpt), size_of(B), size_of(S), size_of(D), eps,
+                                 stream_of(dev)));
+    else
+        status("adaln_out_fwd_ckpt8",
+               lib.fwd_ckpt8((const adaln_bf16 *)ptr(x), (const adaln_bf16 *)ptr(emb), (adaln_bf16 *)ptr(out),
+                             (float *)ptr(mean), (float *)ptr(rstd), (uint8_t *)ptr(ckpt), size_of(B), size_of(S),
+                             size_of(D), eps, stream_of(dev)));
+    return Py_BuildValue("(NNNN)", THPVariable_Wrap(out), THPVariable_Wrap(mean), THPVariable_Wrap(rstd),
+                         THPVariable_Wrap(ckpt));
+}
+
+// out_bwd_ckpt8(f32, dy, ckpt, emb, mean, rstd, dx, d_emb, workspace)
+PyObject *out_bwd_ckpt8(PyObject *const *a) {
+    const ScalarType t = float_type(a[0]);
+    const int dev = device_of(a[1], "dy");
+    of_dim(a[1], "dy", 3, 3, "[B, S, D]");
+    const Tensor dy = flat(tensor(a[1], "dy", dev, t, t));
+    const int64_t B = dy.size(0), S = dy.size(1), D = dy.size(2);
+    const Tensor ckpt = flat(a[2], "ckpt", dev, at::kByte, at::kByte, {B, S, record(D)});
+    const Tensor emb = flat(a[3], "emb", dev, t, t, {B, 2 * D});
+    const Tensor mean = flat(a[4], "mean", dev, at::kFloat, at::kFloat, {B, S}),
+                 rstd = flat(a[5], "rstd", dev, at::kFloat, at::kFloat, {B, S});
+    const Tensor dx = result(a[6], "dx", dev, t, {B, S, D}), d_emb = result(a[7], "d_emb", dev, at::kFloat, {B, 2 * D});
+    const int b = size_of(B), s = size_of(S), d = size_of(D);
+    const size_t need = lib.bwd_ckpt8_bytes(b, s, d);
+    const Tensor ws = scratch(a[8], need, dev);
+    if (t == at::kFloat)
+        status("adaln_f32_out_bwd_ckpt8",
+               lib.f32_bwd_ckpt8((const float *)ptr(dy), (const uint8_t *)ptr(ckpt), (const float *)ptr(emb),
+                                 (const float *)ptr(mean), (const float *)ptr(rstd), (float *)ptr(dx),
+                                 (float *)ptr(d_emb), ptr(ws), need, b, s, d, stream_of(dev)));
+    else
+        status("adaln_out_bwd_ckpt8",
+               lib.bwd_ckpt8((const adaln_bf16 *)ptr(dy), (const uint8_t *)ptr(ckpt), (const adaln_bf16 *)ptr(emb),
+                             (const float *)ptr(mean), (const float *)ptr(rstd), (adaln_bf16 *)ptr(dx),
+                             (float *)ptr(d_emb), ptr(ws), need, b, s, d, stream_of(dev)));
+    return Py_BuildValue("(NN)", THPVariable_Wrap(dx), THPVariable_Wrap(d_emb));
+}
+
+// out_again_ckpt8(f32, ckpt, emb, mean, rstd, out)
+PyObject *out_again_ckpt8(PyObject *const *a) {
+    const ScalarType t = float_type(a[0]);
+    const int dev = device_of(a[1], "ckpt");
+    const Tensor &c = of_dim(a[1], "ckpt", 3, 3, "[B, S, row_bytes]");
+    const int64_t B = c.size(0), S = c.size(1), D = of_dim(a[2], "emb", 2, 2, "[B, 2D]").size(1) / 2;
+    const Tensor ckpt = flat(a[1], "ckpt", dev, at::kByte, at::kByte, {B, S, record(D)});
+    const Tensor emb = flat(a[2], "emb", dev, t, t, {B, 2 * D});
+    const Tensor mean = flat(a[3], "mean", dev, at::kFloat, at::kFloat, {B, S}),
+                 rstd = flat(a[4], "rstd", dev, at::kFloat, at::kFloat, {B, S});
+    const Tensor out = result(a[5], "out", dev, t, {B, S, D});
+    if (t == at::kFloat)
+        status("adaln_f32_out_again_ckpt8",
+               lib.f32_again_ckpt8((const uint8_t *)ptr(ckpt), (const float *)ptr(emb), (const float *)ptr(mean),
+                                   (const float *)ptr(rstd), (float *)ptr(out), size_of(B), size_of(S), size_of(D),
+                                   stream_of(dev)));
+    else
+        status("adaln_out_again_ckpt8",
+               lib.again_ckpt8((const uint8_t *)ptr(ckpt), (const adaln_bf16 *)ptr(emb), (const float *)ptr(mean),
+                               (const float *)ptr(rstd), (adaln_bf16 *)ptr(out), size_of(B), size_of(S), size_of(D),
+                               stream_of(dev)));
+    return THPVariable_Wrap(out);
+}
+
+// ---- low-rank adapters -----------------------------------------------------------------
+
+// Rows [B, S, C]: x itself where the C ABI takes its strides, else a copy (an
+// input) or a refusal (an output).
+struct TokenRows {
+    Tensor x;
+    adaln_rows r = {nullptr, 0, 0};
+    TokenRows() = default;
+    TokenRows(Tensor t, const char *name, bool copy, bool positive) : x(std::move(t)) {
+        if (!usable(positive)) {
+            if (!copy) refuse(PyExc_ValueError, "%s: channels must be dense and rows 16-byte aligned", name);
+            x = x.clone(at::MemoryFormat::Contiguous);
+        }
+        r = adaln_rows{x.data_ptr(), x.stride(0), x.stride(1)};
+    }
+    bool usable(bool positive) const {
+        if (x.numel() == 0) return true;
+        const int64_t step = 16 / x.element_size();
+        if ((x.stride(2) != 1 && x.size(2) > 1) || !aligned(x)) return false;
+        for (int i = 0; i < 2; ++i)
+            if (x.size(i) > 1 && (x.stride(i) % step != 0 || (positive && x.stride(i) == 0))) return false;
+        return true;
+    }
+};
+TokenRows token_rows(PyObject *o, const char *name, int dev, ScalarType t, at::IntArrayRef shape, bool input,
+                     bool positive) {
+    const Tensor &x = tensor(o, name, dev, t, t);
+    shape_is(x, shape, name);
+    return TokenRows(x, name, input, positive);
+}
+
+// what forward and backward share
+struct Adapters {
+    ScalarType t;
+    int dev;
+    int64_t b, s, k, n, r, na;
+    int B, S, K, N, R, NA, is64;
+    Tensor A, U, scale, ids, lens;
+
+    Adapters(PyObject *of32, PyObject *ox, PyObject *oA, PyObject *oU, PyObject *oscale, PyObject *oids,
+             PyObject *olens)
+        : t(float_type(of32)), dev(device_of(ox, "x")) {
+        const Tensor &x = of_dim(ox, "x", 3, 3, "[B, S, K]");
+        b = x.size(0), s = x.size(1), k = x.size(2);
+        const Tensor &a = of_dim(oA, "A", 3, 3, "[NA, R, K]"), &u = of_dim(oU, "U", 3, 3, "[NA, R, N]");
+        na = a.size(0), r = a.size(1), n = u.size(2);
+        A = flat(oA, "A", dev, t, t, {na, r, k});
+        U = flat(oU, "U", dev, t, t, {na, r, n});
+        scale = flat(oscale, "scale", dev, at::kFloat, at::kFloat, {na});
+        ids = flat(oids, "ids", dev, at::kInt, at::kLong, {b});
+        is64 = ids.scalar_type() == at::kLong;
+        if (given(olens)) lens = flat(olens, "lens", dev, at::kInt, at::kInt, {b});
+        B = size_of(b), S = size_of(s), K = size_of(k), N = size_of(n), R = size_of(r), NA = size_of(na);
+    }
+    // a new tensor of rows: those past the end of a sample are zero
+    Tensor fresh(at::IntArrayRef shape) const {
+        Tensor x = make(shape, t, dev);
+        if (lens.defined()) x.zero_();
+        return x;
+    }
+};
+
+// lora_fwd(f32, x, A, U, scale, ids, y, lens, out, state)
+PyObject *lora_fwd(PyObject *const *a) {
+    const Adapters z(a[0], a[1], a[2], a[3], a[4], a[5], a[7]);
+    const TokenRows x = token_rows(a[1], "x", z.dev, z.t, {z.b, z.s, z.k}, true, true);
+    TokenRows y, out;
+    if (given(a[6])) y = token_rows(a[6], "y", z.dev, z.t, {z.b, z.s, z.n}, a[6] != a[8], false);
+    out = given(a[8]) ? token_rows(a[8], "out", z.dev, z.t, {z.b, z.s, z.n}, false, true)
+                      : TokenRows(z.fresh({z.b, z.s, z.n}), "out", false, true);
+    const size_t need = lib.lora_state_bytes(z.B, z.S, z.R);
+    Tensor state;
+    if (given(a[9])) {
+        state = tensor(a[9], "state", z.dev, at::kByte, at::kByte);
+        if (!state.is_contiguous() || !aligned(state) || state.nbytes() < need)
+            refuse(PyExc_ValueError, "state: %zu contiguous, 16-byte aligned bytes needed", need);
+    } else {
+        state = make({(int64_t)need}, at::kByte, z.dev);
+    }
+    const adaln_rows *yr = given(a[6]) ? &y.r : nullptr;
+    const int32_t *lens = (const int32_t *)ptr(z.lens);
+    const float *scale = (const float *)ptr(z.scale);
+    if (z.t == at::kFloat)
+        status("adaln_f32_lora_fwd",
+               lib.f32_lora_fwd(&x.r, (const float *)ptr(z.A), (const float *)ptr(z.U), scale, ptr(z.ids), z.is64, lens,
+                                yr, &out.r, ptr(state), need, z.B, z.S, z.K, z.N, z.R, z.NA, stream_of(z.dev)));
+    else
+        status("adaln_lora_fwd",
+               lib.lora_fwd(&x.r, (const adaln_bf16 *)ptr(z.A), (const adaln_bf16 *)ptr(z.U), scale, ptr(z.ids), z.is64,
+                            lens, yr, &out.r, ptr(state), need, z.B, z.S, z.K, z.N, z.R, z.NA, stream_of(z.dev)));
+    return Py_BuildValue("(NN)", THPVariable_Wrap(out.x), THPVariable_Wrap(state));
+}
+
+// lora_bwd(f32, d_out, x, state, A, U, scale, ids, lens, dx_base, dx, dA_acc, dU_acc, accumulate, want_x, want_w,
+//          workspace)
+PyObject *lora_bwd(PyObject *const *a) {
+    const Adapters z(a[0], a[2], a[4], a[5], a[6], a[7], a[8]);
+    const bool accumulate = truth(a[13]), want_x = truth(a[14]), want_w = truth(a[15]);
+    const TokenRows g = token_rows(a[1], "d_out", z.dev, z.t, {z.b, z.s, z.n}, true, true),
+                    x = token_rows(a[2], "x", z.dev, z.t, {z.b, z.s, z.k}, true, true);
+    const Tensor &state = tensor(a[3], "state", z.dev, at::kByte, at::kByte);
+    if (!state.is_contiguous() || !aligned(state) || state.nbytes() < lib.lora_state_bytes(z.B, z.S, z.R))
+        refuse(PyExc_ValueError, "state: not that of a forward of these sizes");
+    TokenRows base, dx;
+    if (given(a[9])) base = token_rows(a[9], "dx_base", z.dev, z.t, {z.b, z.s, z.k}, a[9] != a[10], false);
+    if (given(a[10]))
+        dx = token_rows(a[10], "dx", z.dev, z.t, {z.b, z.s, z.k}, false, true);
+    else if (want_x)
+        dx = TokenRows(z.fresh({z.b, z.s, z.k}), "dx", false, true);
+    // given accumulators are filled; want_w allocates the missing ones
+    Tensor dA, dU;
+    if (want_w && accumulate && (!given(a[11]) || !given(a[12])))
+        refuse(PyExc_ValueError, "accumulate: dA_acc and dU_acc must be given");
+    if (want_w || given(a[11])) dA = result(a[11], "dA_acc", z.dev, at::kFloat, {z.na, z.r, z.k});
+    if (want_w || given(a[12])) dU = result(a[12], "dU_acc", z.dev, at::kFloat, {z.na, z.r, z.n});
+    const size_t need = z.t == at::kFloat ? lib.f32_lora_bwd_bytes(z.B, z.S, z.K, z.N, z.R)
+                                          : lib.lora_bwd_bytes(z.B, z.S, z.K, z.N, z.R);
+    const Tensor ws = scratch(a[16], need, z.dev);
+    const adaln_rows *br = given(a[9]) ? &base.r : nullptr, *dr = dx.x.defined() ? &dx.r : nullptr;
+    const int32_t *lens = (const int32_t *)ptr(z.lens);
+    const float *scale = (const float *)ptr(z.scale);
+    if (z.t == at::kFloat)
+        status("adaln_f32_lora_bwd",
+               lib.f32_lora_bwd(&g.r, &x.r, ptr(state), (const float *)ptr(z.A), (const float *)ptr(z.U), scale,
+                                ptr(z.ids), z.is64, lens, br, dr, (float *)ptr(dA), (float *)ptr(dU), accumulate,
+                                ptr(ws), need, z.B, z.S, z.K, z.N, z.R, z.NA, stream_of(z.dev)));
+    else
+        status("adaln_lora_bwd",
+               lib.lora_bwd(&g.r, &x.r, ptr(state), (const adaln_bf16 *)ptr(z.A), (const adaln_bf16 *)ptr(z.U), scale,
+                            ptr(z.ids), z.is64, lens, br, dr, (float *)ptr(dA), (float *)ptr(dU), accumulate, ptr(ws),
+                            need, z.B, z.S, z.K, z.N, z.R, z.NA, stream_of(z.dev)));
+    return Py_BuildValue("(NNN)", dx.x.defined() ? THPVariable_Wrap(dx.x) : Py_NewRef(Py_None),
+                         dA.defined() ? THPVariable_Wrap(dA) : Py_NewRef(Py_None),
+                         dU.defined() ? THPVariable_Wrap(dU) : Py_NewRef(Py_None));
+}
+
 // ---- module --------------------------------------------------------------------------
 
 template <PyObject *(*F)(PyObject *const *), Py_ssize_t N>
@@ -482,14 +783,15 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// bind(addresses of the 13 functions in the header's order, raise_status)
+// bind(addresses of the 32 functions in the headers' order, raise_status)
+constexpr int kBound = 32;
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    if (n != 14) {
-        PyErr_SetString(PyExc_TypeError, "expected 14 arguments");
+    if (n != kBound + 1) {
+        PyErr_Format(PyExc_TypeError, "expected %d arguments", kBound + 1);
         return nullptr;
     }
-    void *f[13];
-    for (int i = 0; i < 13; ++i) {
+    void *f[kBound];
+    for (int i = 0; i < kBound; ++i) {
         f[i] = PyLong_AsVoidPtr(args[i]);
         if (!f[i]) return nullptr;
     }
@@ -499,8 +801,18 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
                   (decltype(lib.f32_embed_fwd))f[6],  (decltype(lib.embed_bwd_bytes))f[7],
                   (decltype(lib.embed_bwd))f[8],      (decltype(lib.f32_embed_bwd))f[9],
                   (decltype(lib.grad_bytes))f[10],    (decltype(lib.grad_norm))f[11],
-                  (decltype(lib.grad_clip))f[12]};
-    Py_XSETREF(raise_status, Py_NewRef(args[13]));
+                  (decltype(lib.grad_clip))f[12],
+                  (decltype(lib.ckpt8_bytes))f[13],     (decltype(lib.ckpt8_pack))f[14],
+                  (decltype(lib.f32_ckpt8_pack))f[15],  (decltype(lib.ckpt8_unpack))f[16],
+                  (decltype(lib.f32_ckpt8_unpack))f[17], (decltype(lib.fwd_ckpt8))f[18],
+                  (decltype(lib.f32_fwd_ckpt8))f[19],   (decltype(lib.bwd_ckpt8_bytes))f[20],
+                  (decltype(lib.bwd_ckpt8))f[21],       (decltype(lib.f32_bwd_ckpt8))f[22],
+                  (decltype(lib.again_ckpt8))f[23],     (decltype(lib.f32_again_ckpt8))f[24],
+                  (decltype(lib.lora_state_bytes))f[25], (decltype(lib.lora_fwd))f[26],
+                  (decltype(lib.f32_lora_fwd))f[27],    (decltype(lib.lora_bwd_bytes))f[28],
+                  (decltype(lib.f32_lora_bwd_bytes))f[29], (decltype(lib.lora_bwd))f[30],
+                  (decltype(lib.f32_lora_bwd))f[31]};
+    Py_XSETREF(raise_status, Py_NewRef(args[kBound]));
     Py_RETURN_NONE;
 }
 
@@ -512,6 +824,13 @@ PyMethodDef methods[] = {CALL(qk_fwd, 12),
                          CALL(grad_workspace_bytes, 1),
                          CALL(grad_norm, 3),
                          CALL(grad_clip, 5),
+                         CALL(ckpt8_pack, 3),
+                         CALL(ckpt8_unpack, 4),
+                         CALL(out_fwd_ckpt8, 8),
+                         CALL(out_bwd_ckpt8, 9),
+                         CALL(out_again_ckpt8, 6),
+                         CALL(lora_fwd, 10),
+                         CALL(lora_bwd, 17),
                          {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "adaln_marshal", nullptr, -1, methods};
