@@ -152,9 +152,9 @@ size_t adaln_lora_state_bytes(int B, int S, int R);
  *   out   [B, S, N]   bf16 rows    may describe exactly y's rows (in place)
  *   state             written: what adaln_lora_bwd needs, adaln_lora_state_bytes
  *
- * h is held in fp32, or where S > 16 (bf16) as the sum of two bf16 parts, which
- * differs from it by at most 2^-17 relative.  A row's result does not depend on
- * the other samples; its order depends on K, R and S only.
+ * h is held in fp32; where S > 16 (bf16) the product with U takes it to 16
+ * significant bits (2^-17 relative).  A row's result does not depend on the other
+ * samples; its order depends on K, R and S only.
  *
  * Sizes: K, N multiples of 8 in [8, 65536]; R a multiple of 8 in [8, 128] (fill
  * up smaller adapters with zeros); 0 <= NA <= 65535; B, S as in adaln.h; B * S *
@@ -184,7 +184,7 @@ size_t adaln_f32_lora_bwd_workspace_bytes(int B, int S, int K, int N, int R);
  * adaln_lora_bwd — backward of adaln_lora_fwd, with the state that it left:
  *
  *   e[b,s,r]  = scale[a] * sum_n d_out[b,s,n] U[a,r,n]          fp32
- *   dx[b,s,k] = dx_base[b,s,k] + sum_r e[b,s,r] A[a,r,k]        fp32, one rounding
+ *   dx[b,s,k] = dx_base[b,s,k] + sum_r e[b,s,r] A[a,r,k]        as out
  *   dA[a,r,k] = sum over the rows (b,s) with ids[b] == a of e[b,s,r] x[b,s,k]
  *   dU[a,r,n] = the same of h[b,s,r] d_out[b,s,n]               fp32
  *
@@ -196,7 +196,7 @@ size_t adaln_f32_lora_bwd_workspace_bytes(int B, int S, int K, int N, int R);
  *   dA_acc  [NA, R, K] fp32 in/out, or NULL (not computed)
  *   dU_acc  [NA, R, N] fp32 in/out, or NULL (not computed)
  *
- * dA and dU sum a sample's rows in an order fixed by S and the type, in pieces of
+ * dA and dU sum a sample's rows in an order fixed by S, R and the type, in pieces of
  * consecutive rows that each start from +0, and add the pieces, ascending, sample
  * by sample, onto the accumulator (accumulate ? its value : +0): bitwise
  * independent of how samples are split into accumulating calls.  With accumulate

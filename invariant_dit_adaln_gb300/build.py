@@ -33,7 +33,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libadaln.so")
 HEADERS = ("adaln.h", "adaln_ops.h", "adaln_tune.h")
 SOURCES = ["api.cu", "out.cu", "proj.cu", "tc_proj.cu", "res.cu", "f32.cu", "noalloc.cu",
-           "ops_api.cu", "heads.cu", "embed.cu", "grads.cu", "tune_api.cu", "ckpt.cu", "lora.cu"]
+           "ops_api.cu", "heads.cu", "embed.cu", "grads.cu", "tune_api.cu", "ckpt.cu", "lora.cu", "lora_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "--fmad=false", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xptxas", "-warn-spills", f"-I{INCLUDE}", f"-I{CSRC}"]

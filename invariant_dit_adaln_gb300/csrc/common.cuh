@@ -30,6 +30,8 @@ enum DeviceError : unsigned {
     kErrProjFwdWait = 0x301,
     kErrProjTcWait = 0x302,
     kErrProjOutWait = 0x303,
+    kErrLoraShrinkWait = 0x401,
+    kErrLoraGradWait = 0x402,
     kErrDrainFailed = 0x8000,  // or-ed in: an issued copy did not land while leaving
 };
 

@@ -113,6 +113,7 @@ int proj_fwd_tc_ksplit(int D);
 cudaError_t launch_proj_fwd_tc(const uint16_t *u, const uint16_t *W, const uint16_t *bias, uint16_t *emb, int B,
                                int D, cudaStream_t stream, const DeviceInfo &dev);
 int read_and_clear_tc_error();
+int read_and_clear_lora_error();  // lora_tc.cu
 // the LayerNorm forward, then y = out Wp^T + bp on the tensor cores (J = 64,
 // D a multiple of 64)
 bool proj_out_tc_supported(int D, int J);

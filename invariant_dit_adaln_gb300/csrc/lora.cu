@@ -8,8 +8,7 @@
 // 2 R flop for each channel read or written: bound by memory for bf16 on the
 // tensor cores; on the CUDA cores (fp32, and samples of a few tokens) by issue
 // from R = 16 or so on.
-#include "common.cuh"
-#include "tune.h"
+#include "lora.cuh"
 
 namespace adaln {
 
@@ -49,13 +48,6 @@ struct Vec<float> {
     }
 };
 
-// the adapter of sample b, -1 for none
-__device__ __forceinline__ int adapter_of(const void *ids, int is64, int b, int NA) {
-    const long long i = is64 ? static_cast<const long long *>(ids)[b] : static_cast<const int *>(ids)[b];
-    return i >= 0 && i < NA ? (int)i : -1;
-}
-__device__ __forceinline__ int rows_of(const int *lens, int b, int S) { return lens ? min(max(lens[b], 0), S) : S; }
-
 // NV values of every lane summed over the warp by a transposed butterfly: lane l
 // ends with value l mod NV.  The order of a sum does not depend on NV.
 template <int NV>
@@ -81,10 +73,11 @@ __device__ __forceinline__ float scatter_sum(float (&a)[NV], int lane) {
 // --------------------------------------------------------------------------
 // shrink: a warp (KS == 1) or the CTA's four warps (KS == 4, the channels split
 // among them) form kRB ranks of TOK tokens of a sample.  A lane takes the 16-byte
-// vectors of its share in ascending order, even and odd channels in the halves of
-// a packed accumulator; halves, butterfly, warps ascending.  State fp32 [B,S,R].
+// vectors of its share in ascending order (NV of them requested at once), even and
+// odd channels in the halves of a packed accumulator; halves, butterfly, warps
+// ascending.  State fp32 [B,S,R].
 // --------------------------------------------------------------------------
-template <typename T, int TOK, int KS>
+template <typename T, int TOK, int KS, int NV>
 __global__ void __launch_bounds__(128)
 lora_shrink_kernel(const T *__restrict__ src, long long batch, long long token, const T *__restrict__ W,
                    const float *__restrict__ scale, const void *ids, int is64, const int *lens,
@@ -105,26 +98,38 @@ lora_shrink_kernel(const T *__restrict__ src, long long batch, long long token, 
         for (int r = 0; r < kRB; ++r) acc[i][r] = 0ull;
     if (n > 0) {
         const T *w = W + ((long long)a * R + r0) * C, *x = src + b * batch + s0 * token;
-        for (int v = KS == 4 ? (int)threadIdx.x : lane; v < C / E; v += KS == 4 ? 128 : 32) {
-            Vec<T> xv[TOK];
+        constexpr int kStep = KS * 32;
+        for (int v0 = KS == 4 ? (int)threadIdx.x : lane; v0 < C / E; v0 += NV * kStep) {
+            Vec<T> xv[NV][TOK], wv[NV][kRB];
 #pragma unroll
-            for (int i = 0; i < TOK; ++i) {
-                xv[i].zero();
-                if (i < n) xv[i].load(x + i * token + (long long)v * E);
+            for (int u = 0; u < NV; ++u) {
+                const long long at = (long long)(v0 + u * kStep) * E;
+                const bool in = v0 + u * kStep < C / E;
+#pragma unroll
+                for (int i = 0; i < TOK; ++i) {
+                    xv[u][i].zero();
+                    if (in && i < n) xv[u][i].load(x + i * token + at);
+                }
+#pragma unroll
+                for (int r = 0; r < kRB; ++r) {
+                    wv[u][r].zero();
+                    if (in) wv[u][r].load(w + (long long)r * C + at);
+                }
             }
-            px2 xp[TOK][E / 2];
 #pragma unroll
-            for (int i = 0; i < TOK; ++i) xv[i].pairs(xp[i]);
+            for (int u = 0; u < NV; ++u) {
+                px2 xp[TOK][E / 2];
 #pragma unroll
-            for (int r = 0; r < kRB; ++r) {
-                Vec<T> wv;
-                wv.load(w + (long long)r * C + (long long)v * E);
-                px2 wp[E / 2];
-                wv.pairs(wp);
+                for (int i = 0; i < TOK; ++i) xv[u][i].pairs(xp[i]);
 #pragma unroll
-                for (int i = 0; i < TOK; ++i)
+                for (int r = 0; r < kRB; ++r) {
+                    px2 wp[E / 2];
+                    wv[u][r].pairs(wp);
 #pragma unroll
-                    for (int q = 0; q < E / 2; ++q) acc[i][r] = px_fma(xp[i][q], wp[q], acc[i][r]);
+                    for (int i = 0; i < TOK; ++i)
+#pragma unroll
+                        for (int q = 0; q < E / 2; ++q) acc[i][r] = px_fma(xp[i][q], wp[q], acc[i][r]);
+                }
             }
         }
     }
@@ -167,8 +172,17 @@ lora_expand_kernel(const float *__restrict__ h, const T *__restrict__ W, const v
     if (n <= 0) return;
     const int a = adapter_of(ids, is64, b, NA);
     if (a < 0 && base == out) return;
-    for (int i = threadIdx.x; i < TOK * R; i += 128)
-        hs[i / R][i % R] = i / R < n ? h[((long long)b * S + s0) * R + i] : 0.0f;
+    Vec<T> y[TOK];
+#pragma unroll
+    for (int i = 0; i < TOK; ++i) {
+        y[i].zero();
+        // not the read-only path: base may be out
+        if (base && i < n && c0 < C)
+            y[i].v = *reinterpret_cast<const uint4 *>(base + b * base_batch + (s0 + i) * base_token + c0);
+    }
+    if (a >= 0)
+        for (int i = threadIdx.x; i < TOK * R; i += 128)
+            hs[i / R][i % R] = i / R < n ? h[((long long)b * S + s0) * R + i] : 0.0f;
     __syncthreads();
     if (c0 >= C) return;
     px2 acc[TOK][E / 2];
@@ -178,168 +192,243 @@ lora_expand_kernel(const float *__restrict__ h, const T *__restrict__ W, const v
         for (int q = 0; q < E / 2; ++q) acc[i][q] = 0ull;
     if (a >= 0) {
         const T *w = W + (long long)a * R * C + c0;
-#pragma unroll 4
-        for (int r = 0; r < R; ++r) {
-            Vec<T> wv;
-            wv.load(w + (long long)r * C);
-            px2 wp[E / 2];
-            wv.pairs(wp);
+        for (int r0 = 0; r0 < R; r0 += kRB) {
+            Vec<T> wv[kRB];
 #pragma unroll
-            for (int i = 0; i < TOK; ++i) {
-                const px2 hr = px_splat(hs[i][r]);
+            for (int r = 0; r < kRB; ++r) wv[r].load(w + (long long)(r0 + r) * C);
 #pragma unroll
-                for (int q = 0; q < E / 2; ++q) acc[i][q] = px_fma(hr, wp[q], acc[i][q]);
+            for (int r = 0; r < kRB; ++r) {
+                px2 wp[E / 2];
+                wv[r].pairs(wp);
+#pragma unroll
+                for (int i = 0; i < TOK; ++i) {
+                    const px2 hr = px_splat(hs[i][r0 + r]);
+#pragma unroll
+                    for (int q = 0; q < E / 2; ++q) acc[i][q] = px_fma(hr, wp[q], acc[i][q]);
+                }
             }
         }
     }
 #pragma unroll
     for (int i = 0; i < TOK; ++i) {
         if (i >= n) break;
-        if (base) {
-            Vec<T> y;
-            // not the read-only path: base may be out
-            y.v = *reinterpret_cast<const uint4 *>(base + b * base_batch + (s0 + i) * base_token + c0);
-            px2 yp[E / 2];
-            y.pairs(yp);
+        px2 yp[E / 2];
+        y[i].pairs(yp);
 #pragma unroll
-            for (int q = 0; q < E / 2; ++q) acc[i][q] = px_add(yp[q], acc[i][q]);
-        }
+        for (int q = 0; q < E / 2; ++q) acc[i][q] = px_add(yp[q], acc[i][q]);
         stg16(out + b * batch + (s0 + i) * token + c0, Vec<T>::pack(acc[i]));
     }
 }
 
 // --------------------------------------------------------------------------
-// grad: a thread holds 4 channels of kRB ranks.  A piece is kGradPiece
-// consecutive rows of a sample, summed from +0 by fused multiply-adds in
-// ascending order; the pieces are added in ascending order, sample by sample.
+// grad: a lane holds 4 channels of kRB ranks.  A piece is kGradPiece consecutive
+// rows of a sample, summed by fused multiply-adds, ascending, from +0; the pieces
+// are added in ascending order, sample by sample.
 //
-// Two schedules of the same sums.  OWNER: the CTA takes every piece of an
-// adapter and writes the accumulator.  Otherwise each CTA takes one piece, writes
-// its sum to the workspace, and lora_join_kernel adds them.  The second has as
-// many CTAs as there are pieces, and moves R fp32 for each channel of a piece
-// twice.
+// Two schedules, chosen by S, R and the type.  lora_grad_parts_kernel: a CTA takes
+// one piece (a warp its rows s mod 4 == w, kFlight of them requested at once; the
+// four sums are added in order of w) and writes its sum to the workspace, and
+// lora_join_kernel adds them: as many CTAs as there are pieces, and R fp32 for each
+// channel of a piece moved twice.  lora_grad_owner_kernel: a thread takes every
+// piece of an adapter and writes the accumulator.
 // --------------------------------------------------------------------------
-struct GradOperand {
-    const void *src;
-    long long batch, token;
-    const float *h;  // [B, S, R]
-    float *acc;      // [NA, R, C], NULL: not asked for
-    float *part;     // [B][pieces][R][C]
-    int C;
-    int blocks;      // CTAs along the channels
+constexpr int kFlight = 8;
+
+template <typename T>
+struct Four;  // 4 channels of a row
+template <>
+struct Four<uint16_t> {
+    uint2 v;
+    __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
+    __device__ __forceinline__ void load(const uint16_t *p) { v = __ldg(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ void pairs(px2 (&x)[2]) const { x[0] = px_bf16(v.x), x[1] = px_bf16(v.y); }
+};
+template <>
+struct Four<float> {
+    float4 v;
+    __device__ __forceinline__ void zero() { v = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    __device__ __forceinline__ void load(const float *p) { v = __ldg(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void pairs(px2 (&x)[2]) const { x[0] = px_make(v.x, v.y), x[1] = px_make(v.z, v.w); }
 };
 
-template <typename T>
-__device__ __forceinline__ void load4(const T *p, px2 (&x)[2]);
-template <>
-__device__ __forceinline__ void load4<uint16_t>(const uint16_t *p, px2 (&x)[2]) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-    x[0] = px_bf16(v.x), x[1] = px_bf16(v.y);
-}
-template <>
-__device__ __forceinline__ void load4<float>(const float *p, px2 (&x)[2]) {
-    const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
-    x[0] = px_make(v.x, v.y), x[1] = px_make(v.z, v.w);
-}
-
-// rows [s0, s1) of a sample into acc, from what it holds
-template <typename T>
-__device__ __forceinline__ void grad_rows(const GradOperand &o, int b, int s0, int s1, int S, int R, int r0, int c0,
-                                          px2 (&acc)[kRB][2]) {
-    const T *x = static_cast<const T *>(o.src) + b * o.batch + s0 * o.token + c0;
-    const float *h = o.h + ((long long)b * S + s0) * R + r0;
-#pragma unroll 4
-    for (int s = s0; s < s1; ++s, x += o.token, h += R) {
-        px2 xp[2];
-        load4<T>(x, xp);
-        const float4 ha = __ldg(reinterpret_cast<const float4 *>(h)), hb = __ldg(reinterpret_cast<const float4 *>(h) + 1);
-        const float hr[kRB] = {ha.x, ha.y, ha.z, ha.w, hb.x, hb.y, hb.z, hb.w};
+typedef px2 RankAcc[kRB][2];
+__device__ __forceinline__ void zero_acc(RankAcc &a) {
 #pragma unroll
-        for (int r = 0; r < kRB; ++r) {
-            const px2 e = px_splat(hr[r]);
-            acc[r][0] = px_fma(e, xp[0], acc[r][0]);
-            acc[r][1] = px_fma(e, xp[1], acc[r][1]);
-        }
+    for (int r = 0; r < kRB; ++r) a[r][0] = a[r][1] = 0ull;
+}
+__device__ __forceinline__ void add_acc(RankAcc &a, const RankAcc &b) {
+#pragma unroll
+    for (int r = 0; r < kRB; ++r) a[r][0] = px_add(a[r][0], b[r][0]), a[r][1] = px_add(a[r][1], b[r][1]);
+}
+// a row's products: x of 4 channels, h of kRB ranks in shared memory
+template <typename T>
+__device__ __forceinline__ void add_row(RankAcc &a, const Four<T> &x, const float *h) {
+    px2 xp[2];
+    x.pairs(xp);
+    const float4 ha = *reinterpret_cast<const float4 *>(h), hb = *reinterpret_cast<const float4 *>(h + 4);
+    const float hr[kRB] = {ha.x, ha.y, ha.z, ha.w, hb.x, hb.y, hb.z, hb.w};
+#pragma unroll
+    for (int r = 0; r < kRB; ++r) {
+        const px2 e = px_splat(hr[r]);
+        a[r][0] = px_fma(e, xp[0], a[r][0]);
+        a[r][1] = px_fma(e, xp[1], a[r][1]);
     }
 }
+__device__ __forceinline__ float4 of_acc(const RankAcc &a, int r) {
+    return make_float4(px_lo(a[r][0]), px_hi(a[r][0]), px_lo(a[r][1]), px_hi(a[r][1]));
+}
 
-template <typename T, bool OWNER>
-__global__ void __launch_bounds__(128)
-lora_grad_kernel(const GradOperand o0, const GradOperand o1, const void *ids, int is64, const int *lens, int accumulate,
-                 int B, int S, int R, int NA, int pieces) {
-    const int rb = R / kRB;
+// the operand, rank block and first channel of a CTA; blocks of `width` channels
+__device__ __forceinline__ const GradOperand &grad_place(const GradOperand &o0, const GradOperand &o1, int rb, int width,
+                                                         int &r0, int &c0) {
     const bool first = (int)blockIdx.x < o0.blocks * rb;
     const GradOperand &o = first ? o0 : o1;
     const int at = first ? blockIdx.x : blockIdx.x - o0.blocks * rb;
-    const int r0 = at / o.blocks * kRB, c0 = (at % o.blocks * 128 + threadIdx.x) * 4;
+    r0 = at / o.blocks * kRB, c0 = at % o.blocks * width;
+    return o;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(128)
+lora_grad_parts_kernel(const GradOperand o0, const GradOperand o1, const void *ids, int is64, const int *lens, int S,
+                       int R, int NA, int pieces) {
+    __shared__ __align__(16) float hs[kGradPiece][kRB];
+    __shared__ float4 sums[3][kRB][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int r0, c0;
+    const GradOperand &o = grad_place(o0, o1, R / kRB, 128, r0, c0);
+    c0 += lane * 4;
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.z, s0 = blockIdx.y * kGradPiece;
+    const int n = min(rows_of(lens, b, S) - s0, kGradPiece);
+    if (n <= 0 || adapter_of(ids, is64, b, NA) < 0) return;
+    const float *h = o.h + ((long long)b * S + s0) * R + r0;
+    for (int i = threadIdx.x; i < n * 2; i += 128)
+        *reinterpret_cast<float4 *>(&hs[i >> 1][(i & 1) * 4]) =
+            *reinterpret_cast<const float4 *>(h + (long long)(i >> 1) * R + (i & 1) * 4);
+    __syncthreads();
+    RankAcc acc;
+    zero_acc(acc);
+    if (c0 < o.C) {
+        const T *x = static_cast<const T *>(o.src) + b * o.batch + s0 * o.token + c0;
+        for (int s = warp; s < n; s += 4 * kFlight) {
+            Four<T> v[kFlight];
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k)
+                if (s + 4 * k < n) v[k].load(x + (s + 4 * k) * o.token);
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k)
+                if (s + 4 * k < n) add_row(acc, v[k], hs[s + 4 * k]);
+        }
+    }
+    if (warp > 0)
+#pragma unroll
+        for (int r = 0; r < kRB; ++r) sums[warp - 1][r][lane] = of_acc(acc, r);
+    __syncthreads();
+    if (warp > 0 || c0 >= o.C) return;
+    float *p = o.part + (((long long)b * pieces + blockIdx.y) * R + r0) * o.C + c0;
+#pragma unroll
+    for (int r = 0; r < kRB; ++r) {
+        float4 v = of_acc(acc, r);
+#pragma unroll
+        for (int w = 0; w < 3; ++w) {
+            const float4 u = sums[w][r][lane];
+            v = make_float4(__fadd_rn(v.x, u.x), __fadd_rn(v.y, u.y), __fadd_rn(v.z, u.z), __fadd_rn(v.w, u.w));
+        }
+        stg16f(p + (long long)r * o.C, v);
+    }
+}
+
+// The rows of the adapter's samples, S for each, as one sequence, 64 at a time: h
+// of these goes through shared memory, and kFlight rows of x are requested at
+// once, of one sample or of several.  (With one row requested after the other, 257
+// samples of one token, 4 adapters of rank 16, 3072 to 6144 channels took 54 us.)
+constexpr int kWindow = 64;
+template <typename T>
+__global__ void __launch_bounds__(128)
+lora_grad_owner_kernel(const GradOperand o0, const GradOperand o1, const void *ids, int is64, const int *lens,
+                       int accumulate, int B, int S, int R, int NA) {
+    __shared__ __align__(16) float hs[kWindow][kRB];
+    __shared__ int place_b[kWindow], place_s[kWindow];  // sample and row, -1 past its end
+    __shared__ int found[128], count[4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int r0, c0;
+    const GradOperand &o = grad_place(o0, o1, R / kRB, 512, r0, c0);
+    c0 += threadIdx.x * 4;
     const bool live = c0 < o.C;
     pdl_wait();
     pdl_trigger();
-    px2 sum[kRB][2], acc[kRB][2];
-    if (!OWNER) {
-        const int b = blockIdx.z, s0 = blockIdx.y * kGradPiece;
-        const int s1 = min(rows_of(lens, b, S), s0 + kGradPiece);
-        if (s0 >= s1 || adapter_of(ids, is64, b, NA) < 0 || !live) return;
-#pragma unroll
-        for (int r = 0; r < kRB; ++r) acc[r][0] = acc[r][1] = 0ull;
-        grad_rows<T>(o, b, s0, s1, S, R, r0, c0, acc);
-        float *p = o.part + (((long long)b * pieces + blockIdx.y) * R + r0) * o.C + c0;
-#pragma unroll
-        for (int r = 0; r < kRB; ++r)
-            stg16f(p + (long long)r * o.C,
-                   make_float4(px_lo(acc[r][0]), px_hi(acc[r][0]), px_lo(acc[r][1]), px_hi(acc[r][1])));
-        return;
-    }
     const int a = blockIdx.y;
     float *p = o.acc + ((long long)a * R + r0) * o.C + c0;
-    bool any = false;
-#pragma unroll
-    for (int r = 0; r < kRB; ++r) sum[r][0] = sum[r][1] = 0ull;
-    __shared__ int found[128];
-    __shared__ int count[4];
+    const T *src = static_cast<const T *>(o.src) + c0;
+    RankAcc total, acc;
+    zero_acc(total);
+    bool any = false, open = false;
     for (int b0 = 0; b0 < B; b0 += 128) {
         // the samples of adapter a among the next 128, in order
         const int b = b0 + threadIdx.x;
         const bool mine = b < B && adapter_of(ids, is64, b, NA) == a;
         const unsigned vote = __ballot_sync(0xFFFFFFFFu, mine);
-        if ((threadIdx.x & 31) == 0) count[threadIdx.x >> 5] = __popc(vote);
+        if (lane == 0) count[warp] = __popc(vote);
         __syncthreads();
-        int before = 0, total = 0;
+        int before = 0, samples = 0;
         for (int w = 0; w < 4; ++w) {
-            if (w < (int)(threadIdx.x >> 5)) before += count[w];
-            total += count[w];
+            if (w < warp) before += count[w];
+            samples += count[w];
         }
-        if (mine) found[before + __popc(vote & ((1u << (threadIdx.x & 31)) - 1u))] = b;
+        if (mine) found[before + __popc(vote & ((1u << lane) - 1u))] = b;
         __syncthreads();
-        if (live) {
-            if (total > 0 && !any) {
-                any = true;
-                if (accumulate)
+        if (samples > 0 && !any) {
+            any = true;
+            if (accumulate && live)
 #pragma unroll
-                    for (int r = 0; r < kRB; ++r) {
-                        const float4 v = *reinterpret_cast<const float4 *>(p + (long long)r * o.C);
-                        sum[r][0] = px_make(v.x, v.y), sum[r][1] = px_make(v.z, v.w);
-                    }
-            }
-            for (int i = 0; i < total; ++i) {
-                const int bb = found[i], n = rows_of(lens, bb, S);
-                for (int s0 = 0; s0 < n; s0 += kGradPiece) {
-#pragma unroll
-                    for (int r = 0; r < kRB; ++r) acc[r][0] = acc[r][1] = 0ull;
-                    grad_rows<T>(o, bb, s0, min(n, s0 + kGradPiece), S, R, r0, c0, acc);
-#pragma unroll
-                    for (int r = 0; r < kRB; ++r)
-                        sum[r][0] = px_add(sum[r][0], acc[r][0]), sum[r][1] = px_add(sum[r][1], acc[r][1]);
+                for (int r = 0; r < kRB; ++r) {
+                    const float4 v = *reinterpret_cast<const float4 *>(p + (long long)r * o.C);
+                    total[r][0] = px_make(v.x, v.y), total[r][1] = px_make(v.z, v.w);
+                }
+        }
+        for (long long i0 = 0; i0 < (long long)samples * S; i0 += kWindow) {
+            const int rows = (int)min((long long)kWindow, (long long)samples * S - i0);
+            {
+                const int i = threadIdx.x >> 1, q = (threadIdx.x & 1) * 4;
+                if (i < rows) {
+                    const int bb = found[(i0 + i) / S], s = (int)((i0 + i) % S);
+                    const bool real = s < rows_of(lens, bb, S);
+                    if (q == 0) place_b[i] = bb, place_s[i] = real ? s : -1;
+                    if (real)
+                        *reinterpret_cast<float4 *>(&hs[i][q]) =
+                            *reinterpret_cast<const float4 *>(o.h + ((long long)bb * S + s) * R + r0 + q);
                 }
             }
+            __syncthreads();
+            if (live)
+                for (int i = 0; i < rows; i += kFlight) {
+                    Four<T> v[kFlight];
+                    int s[kFlight];
+#pragma unroll
+                    for (int k = 0; k < kFlight; ++k) {
+                        s[k] = i + k < rows ? place_s[i + k] : -1;
+                        if (s[k] >= 0) v[k].load(src + place_b[i + k] * o.batch + s[k] * o.token);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kFlight; ++k) {
+                        if (s[k] < 0) continue;
+                        if (s[k] % kGradPiece == 0) {  // a new piece
+                            if (open) add_acc(total, acc);
+                            open = true;
+                            zero_acc(acc);
+                        }
+                        add_row(acc, v[k], hs[i + k]);
+                    }
+                }
+            __syncthreads();
         }
-        __syncthreads();
     }
+    if (open) add_acc(total, acc);
     if (live && (any || !accumulate))
 #pragma unroll
-        for (int r = 0; r < kRB; ++r)
-            stg16f(p + (long long)r * o.C,
-                   make_float4(px_lo(sum[r][0]), px_hi(sum[r][0]), px_lo(sum[r][1]), px_hi(sum[r][1])));
+        for (int r = 0; r < kRB; ++r) stg16f(p + (long long)r * o.C, of_acc(total, r));
 }
 
 // The pieces' sums onto the accumulators: a thread holds 4 channels of a rank.
@@ -384,10 +473,8 @@ cudaError_t shrink(const adaln_rows &src, const T *W, const LoraCall &c, int C, 
         return launch_pdl(kern, dim3(ctas, grid.y, grid.z), dim3(128), 0, stream, p, (long long)src.batch,
                           (long long)src.token, W, c.scale, c.ids, c.ids_are_64, c.lens, h, c.S, C, c.R, c.NA);
     };
-    // few tokens a sample: the channels over four warps
-    if (c.S == 1) return go(lora_shrink_kernel<T, 1, 4>, 1);
-    if (c.S <= 16) return go(lora_shrink_kernel<T, 4, 4>, (c.S + 3) / 4);
-    return go(lora_shrink_kernel<T, 4, 1>, (c.S + 15) / 16);
+    if (c.S == 1) return go(lora_shrink_kernel<T, 1, 4, 3>, 1);
+    return go(lora_shrink_kernel<T, 4, 4, 1>, (c.S + 3) / 4);
 }
 
 template <typename T>
@@ -404,56 +491,83 @@ cudaError_t expand(const float *h, const T *W, const LoraCall &c, int C, cudaStr
     return go(lora_expand_kernel<T, 8>, 8);
 }
 
+template <typename T>
+bool on_tensor_cores(int S) { return sizeof(T) == 2 && S >= kLoraTcMinTokens; }
+
 // Pieces in parallel, where their sums are no more than what is read anyway
 bool grad_in_parts(int S, int R, int es, int piece) {
     return (long long)((S + piece - 1) / piece) * R * 4 <= (long long)S * es;
 }
 
+// rows of a piece
 template <typename T>
-cudaError_t grads(const float *h, const float *e, float *part, const LoraCall &c, cudaStream_t stream) {
-    const int pieces = (c.S + kGradPiece - 1) / kGradPiece, rb = c.R / kRB;
-    GradOperand o0 = {c.x.data, c.x.batch, c.x.token, e, c.dA, part, c.K, c.dA ? (c.K + 511) / 512 : 0};
+int piece_rows(int S) { return on_tensor_cores<T>(S) ? kLoraTcPiece : kGradPiece; }
+
+template <typename T>
+cudaError_t grads(const float *h, const float *e, float *part, const LoraCall &c, cudaStream_t stream,
+                  const DeviceInfo &dev) {
+    const int rows = piece_rows<T>(c.S), pieces = (c.S + rows - 1) / rows, rb = c.R / kRB;
+    const bool in_parts = grad_in_parts(c.S, c.R, sizeof(T), rows);
+    const int width = in_parts ? 128 : 512;  // channels of a CTA
+    GradOperand o0 = {c.x.data, c.x.batch, c.x.token, e, c.dA, part, c.K, c.dA ? (c.K + width - 1) / width : 0};
     GradOperand o1 = {c.d_out.data, c.d_out.batch, c.d_out.token, h, c.dU,
-                      part + (long long)c.B * pieces * c.R * c.K, c.N, c.dU ? (c.N + 511) / 512 : 0};
+                      part + (long long)c.B * pieces * c.R * c.K, c.N, c.dU ? (c.N + width - 1) / width : 0};
     const unsigned x = (unsigned)((o0.blocks + o1.blocks) * rb);
-    if (!grad_in_parts(c.S, c.R, sizeof(T), kGradPiece))
-        return launch_pdl(lora_grad_kernel<T, true>, dim3(x, c.NA), dim3(128), 0, stream, o0, o1, c.ids, c.ids_are_64,
-                          c.lens, c.accumulate, c.B, c.S, c.R, c.NA, pieces);
-    cudaError_t err = launch_pdl(lora_grad_kernel<T, false>, dim3(x, pieces, c.B), dim3(128), 0, stream, o0, o1, c.ids,
-                                 c.ids_are_64, c.lens, c.accumulate, c.B, c.S, c.R, c.NA, pieces);
-    if (err != cudaSuccess) return err;
+    cudaError_t err;
+    if (on_tensor_cores<T>(c.S))
+        err = lora_tc_grads(o0, o1, c, in_parts, stream, dev);
+    else if (in_parts)
+        err = launch_pdl(lora_grad_parts_kernel<T>, dim3(x, pieces, c.B), dim3(128), 0, stream, o0, o1, c.ids,
+                         c.ids_are_64, c.lens, c.S, c.R, c.NA, pieces);
+    else
+        err = launch_pdl(lora_grad_owner_kernel<T>, dim3(x, c.NA), dim3(128), 0, stream, o0, o1, c.ids, c.ids_are_64, c.lens,
+                         c.accumulate, c.B, c.S, c.R, c.NA);
+    if (err != cudaSuccess || !in_parts) return err;
     const long long n = (long long)c.R * ((c.dA ? c.K : 0) + (c.dU ? c.N : 0)) / 4;
     return launch_pdl(lora_join_kernel, dim3((unsigned)((n + 127) / 128), c.NA), dim3(128), 0, stream, o0, o1, c.ids,
-                      c.ids_are_64, c.lens, c.accumulate, c.B, c.S, c.R, c.NA, pieces, kGradPiece);
+                      c.ids_are_64, c.lens, c.accumulate, c.B, c.S, c.R, c.NA, pieces, rows);
 }
 
 }  // namespace
 
-size_t lora_state_bytes(int B, int S, int R) { return (size_t)B * R * ((S + 7) / 8 * 8) * 4; }
+// fp32, or three bf16 parts (lora.cuh)
+size_t lora_state_bytes(int B, int S, int R) { return (size_t)B * R * ((S + 7) / 8 * 8) * 6; }
 
 template <typename T>
 size_t lora_bwd_ws_bytes(int B, int S, int K, int N, int R) {
-    const size_t pieces = grad_in_parts(S, R, sizeof(T), kGradPiece) ? (S + kGradPiece - 1) / kGradPiece : 0;
+    const int rows = piece_rows<T>(S);
+    const size_t pieces = grad_in_parts(S, R, sizeof(T), rows) ? (S + rows - 1) / rows : 0;
     return lora_state_bytes(B, S, R) + (size_t)B * pieces * R * ((size_t)K + N) * 4;
 }
 
 template <typename T>
-cudaError_t launch_lora_fwd(const LoraCall &c, cudaStream_t stream, const DeviceInfo &) {
-    float *h = static_cast<float *>(c.state);
-    const cudaError_t err = shrink<T>(c.x, static_cast<const T *>(c.A), c, c.K, h, stream);
-    if (err != cudaSuccess) return err;
-    return expand<T>(h, static_cast<const T *>(c.U), c, c.N, stream);
+static cudaError_t down(const adaln_rows &src, const void *W, const LoraCall &c, int C, void *h, cudaStream_t stream,
+                 const DeviceInfo &dev) {
+    if (c.NA == 0) return cudaSuccess;  // nothing reads h
+    if (on_tensor_cores<T>(c.S)) return lora_tc_shrink(src, W, c, C, h, stream, dev);
+    return shrink<T>(src, static_cast<const T *>(W), c, C, static_cast<float *>(h), stream);
+}
+template <typename T>
+static cudaError_t up(const void *h, const void *W, const LoraCall &c, int C, cudaStream_t stream, const DeviceInfo &dev) {
+    if (on_tensor_cores<T>(c.S)) return lora_tc_expand(h, W, c, C, stream, dev);
+    return expand<T>(static_cast<const float *>(h), static_cast<const T *>(W), c, C, stream);
 }
 
 template <typename T>
-cudaError_t launch_lora_bwd(const LoraCall &c, cudaStream_t stream, const DeviceInfo &) {
+cudaError_t launch_lora_fwd(const LoraCall &c, cudaStream_t stream, const DeviceInfo &dev) {
+    const cudaError_t err = down<T>(c.x, c.A, c, c.K, c.state, stream, dev);
+    return err != cudaSuccess ? err : up<T>(c.state, c.U, c, c.N, stream, dev);
+}
+
+template <typename T>
+cudaError_t launch_lora_bwd(const LoraCall &c, cudaStream_t stream, const DeviceInfo &dev) {
     const float *h = static_cast<const float *>(c.state);
     float *e = static_cast<float *>(c.ws);
     cudaError_t err = cudaSuccess;
-    if (c.dA || c.out.data) err = shrink<T>(c.d_out, static_cast<const T *>(c.U), c, c.N, e, stream);
-    if (err == cudaSuccess && c.out.data) err = expand<T>(e, static_cast<const T *>(c.A), c, c.K, stream);
+    if (c.dA || c.out.data) err = down<T>(c.d_out, c.U, c, c.N, e, stream, dev);
+    if (err == cudaSuccess && c.out.data) err = up<T>(e, c.A, c, c.K, stream, dev);
     if (err == cudaSuccess && (c.dA || c.dU) && c.NA > 0)
-        err = grads<T>(h, e, e + lora_state_bytes(c.B, c.S, c.R) / 4, c, stream);
+        err = grads<T>(h, e, e + lora_state_bytes(c.B, c.S, c.R) / 4, c, stream, dev);
     return err;
 }
 

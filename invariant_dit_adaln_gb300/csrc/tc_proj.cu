@@ -28,10 +28,9 @@
 // its tensor memory and returns without writing emb.
 #include <cuda.h>
 
-#include <mutex>
-
 #include "common.cuh"
 #include "internal.h"
+#include "tc.cuh"
 
 namespace adaln {
 
@@ -109,45 +108,6 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t sbo = 1024)
 constexpr uint32_t kTcIdesc =
     (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTcN >> 3) << 17) | ((uint32_t)(kTcM >> 4) << 24);
 
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_hint(void *dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar,
-                                                 uint64_t pol) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
-        "%3}], [%4], %5;" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "l"(pol)
-        : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// address of the same shared-memory location in CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t map_to_rank(const void *p, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z),
-                 "f"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
-    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
 // the kTcN accumulator columns [col, col + kTcN) of this warp's 32 lanes
 static_assert(kTcN == 16 || kTcN == 32, "accumulator tile width");
 __device__ __forceinline__ void tmem_ld_tile(uint32_t taddr, uint32_t (&v)[kTcN]) {
@@ -171,9 +131,6 @@ __device__ __forceinline__ void tmem_ld_tile(uint32_t taddr, uint32_t (&v)[kTcN]
     }
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-
-// k blocks [kb_begin(r), kb_begin(r + 1)) belong to range r of ksplit
-__device__ __forceinline__ int kb_begin(int KB, int ksplit, int r) { return (int)((long long)KB * r / ksplit); }
 
 struct TcArgs {
     const uint16_t *bias;
@@ -650,27 +607,6 @@ proj_out_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
 // --------------------------------------------------------------------------
 // host side
 // --------------------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// the driver's tensor-map encoder, looked up once through the runtime
-static EncodeTiledFn encode_fn() {
-    static std::once_flag once;
-    static EncodeTiledFn fn = nullptr;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-        else
-            cudaGetLastError();
-    });
-    return fn;
-}
-
 // A [rows, cols] bf16 row-major tensor as a TMA map whose boxes are
 // box_rows x 64 columns, 128-byte swizzled; elements outside read as zeros.
 static bool make_map(CUtensorMap *m, const void *ptr, int rows, int cols, int box_rows) {

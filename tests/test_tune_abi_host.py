@@ -250,7 +250,7 @@ def test_lora_overlaps(L, f32):
 
 def test_lora_sizes(L):
     s = L.adaln_lora_state_bytes
-    assert s(2, 20, 16) == 2 * 24 * 16 * 4 and s(0, 5, 8) == s(5, 0, 8) == 0
+    assert s(2, 20, 16) == 2 * 24 * 16 * 6 and s(0, 5, 8) == s(5, 0, 8) == 0
     for bad in ((-1, 5, 8), (65536, 5, 8), (1, 262145, 8), (1, 5, 4), (1, 5, 136)):
         assert s(*bad) == 0
     for f in (L.adaln_lora_bwd_workspace_bytes, L.adaln_f32_lora_bwd_workspace_bytes):
