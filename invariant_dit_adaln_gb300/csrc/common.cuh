@@ -32,6 +32,7 @@ enum DeviceError : unsigned {
     kErrProjOutWait = 0x303,
     kErrLoraShrinkWait = 0x401,
     kErrLoraGradWait = 0x402,
+    kErrLoraExpandWait = 0x403,
     kErrDrainFailed = 0x8000,  // or-ed in: an issued copy did not land while leaving
 };
 

@@ -439,7 +439,7 @@ lora_join_kernel(const GradOperand o0, const GradOperand o1, const void *ids, in
     int i = blockIdx.x * 128 + threadIdx.x;
     pdl_wait();
     pdl_trigger();
-    if (i >= n0 + n1) return;
+    const bool live = i < n0 + n1;
     const GradOperand &o = i < n0 ? o0 : o1;
     if (i >= n0) i -= n0;
     const int a = blockIdx.y;
@@ -447,18 +447,27 @@ lora_join_kernel(const GradOperand o0, const GradOperand o1, const void *ids, in
     float4 *p = reinterpret_cast<float4 *>(o.acc + a * size) + i;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     bool any = false;
-    for (int b = 0; b < B; ++b) {
-        if (adapter_of(ids, is64, b, NA) != a) continue;
-        if (!any && accumulate) s = *p;
-        any = true;
-        const int k = (rows_of(lens, b, S) + piece_rows - 1) / piece_rows;
-        const float4 *q = reinterpret_cast<const float4 *>(o.part + (long long)b * pieces * size) + i;
-#pragma unroll 4
-        for (int j = 0; j < k; ++j) {
-            const float4 v = __ldcs(q + j * (size / 4));
-            s = make_float4(__fadd_rn(s.x, v.x), __fadd_rn(s.y, v.y), __fadd_rn(s.z, v.z), __fadd_rn(s.w, v.w));
+    const int lane = threadIdx.x & 31;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        // the samples of adapter a among the next 32, and their rows, by a lane each
+        const int mine = b0 + lane;
+        unsigned left = __ballot_sync(0xFFFFFFFFu, mine < B && adapter_of(ids, is64, mine, NA) == a);
+        const int n = mine < B ? rows_of(lens, mine, S) : 0;
+        for (; left; left &= left - 1) {
+            const int b = b0 + __ffs(left) - 1;
+            const int k = (__shfl_sync(0xFFFFFFFFu, n, b - b0) + piece_rows - 1) / piece_rows;
+            if (!live) continue;
+            if (!any && accumulate) s = *p;
+            any = true;
+            const float4 *q = reinterpret_cast<const float4 *>(o.part + (long long)b * pieces * size) + i;
+#pragma unroll 8
+            for (int j = 0; j < k; ++j) {
+                const float4 v = __ldcs(q + j * (size / 4));
+                s = make_float4(__fadd_rn(s.x, v.x), __fadd_rn(s.y, v.y), __fadd_rn(s.z, v.z), __fadd_rn(s.w, v.w));
+            }
         }
     }
+    if (!live) return;
     if (any || !accumulate) *p = s;
 }
 

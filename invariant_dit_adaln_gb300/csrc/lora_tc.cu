@@ -5,10 +5,9 @@
 // bound by memory; what matters is that the bytes flow without passing through
 // registers where they need not.  shrink and grad read their rows by TMA into
 // shared memory, from where tcgen05.mma takes them; only their small results
-// leave tensor memory.  expand adds a product of depth 2 R to rows that every
-// element of must be touched anyway: its rows go through registers, as the
-// accumulators of mma.sync in an order that makes each thread's eight columns
-// contiguous.
+// leave tensor memory.  expand's rows come and leave by TMA as well; a thread adds
+// to 64 bytes of a row at a time.  (With mma.sync, rows in registers: 37 instead of
+// XX us for 4222 rows of 9216 channels at rank 32, bound by issue.)
 //
 // h and e are held as three bf16 parts, whose sum is the fp32 number itself.  The
 // gradients, which are fp32, take all three (two would leave 2.5e-6 of error, more
@@ -76,6 +75,10 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 }
 __device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Waits until the SM has the columns.  A kernel lets the next one start
+// (pdl_trigger) only after all its CTAs have theirs: a CTA of the next kernel holds
+// its columns while it waits for this kernel's end, so one that came first could
+// keep this kernel from ever getting them.
 __device__ __forceinline__ void tmem_alloc(uint32_t *at, int cols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(at)), "r"(cols)
                  : "memory");
@@ -95,6 +98,16 @@ __device__ __forceinline__ void tmem_ld4(uint32_t addr, uint32_t (&v)[4]) {
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                  : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
 __device__ __forceinline__ void tmem_ld_done() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
@@ -104,10 +117,28 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void bars_init(TcBars &sm, int acc_arrivals) {
+// barrier `id` of `count` threads; is `flag` set in all of them?
+__device__ __forceinline__ bool named_bar_and(int id, int count, bool flag) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+        "selp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((int)flag), "r"(id), "r"(count)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+__device__ __forceinline__ void bars_init(TcBars &sm, int acc_arrivals, int empty_arrivals = 1) {
     for (int s = 0; s < kMaxStages; ++s) {
         mbar_init(&sm.full[s], 1);
-        mbar_init(&sm.empty[s], 1);
+        mbar_init(&sm.empty[s], empty_arrivals);
     }
     for (int p = 0; p < 2; ++p) {
         mbar_init(&sm.acc_full[p], 1);
@@ -177,38 +208,52 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
     volatile int *abort_flag = &sm.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.y * kM, b = blockIdx.z;
-    pdl_wait();
-    pdl_trigger();
-    const int a = adapter_of(g.ids, g.is64, b, g.NA);
-    const int n = rows_of(g.lens, b, g.S);
-    // no adapter, or no row of this tile: nothing reads its state (the whole cluster leaves)
-    if (a < 0 || t0 >= n) return;
-    const float scale = g.scale[a];
     const uint32_t rank = g.ks > 1 ? cluster_rank() : 0u;
     const int KB = (g.C + kBlk - 1) / kBlk;
     const int kb0 = kb_begin(KB, g.ks, (int)rank), nkb = kb_begin(KB, g.ks, (int)rank + 1) - kb0;
-    if (threadIdx.x == 0) bars_init(sm, 1);
+    if (threadIdx.x == 0) {
+        prefetch_map(&map_x), prefetch_map(&map_w);
+        bars_init(sm, 1);
+    }
     if (warp == 1) tmem_alloc(&sm.tmem, g.tmem_cols);
+    pdl_wait();
+    const int a = adapter_of(g.ids, g.is64, b, g.NA);
+    const int n = rows_of(g.lens, b, g.S);
+    // no adapter, or no row of this tile: nothing reads its state (the whole cluster leaves)
+    const bool idle = a < 0 || t0 >= n;
+    const float scale = idle ? 0.0f : g.scale[a];
+    auto copy = [&](int i) {  // block i of this range
+        const int s = i % g.stages;
+        unsigned char *st = ring + (size_t)s * stage_bytes;
+        mbar_arrive_expect_tx(&sm.full[s], (uint32_t)stage_bytes);
+        tma_load_3d(st, &map_x, (kb0 + i) * kBlk, t0, b, &sm.full[s]);
+        tma_load_3d(st + kRowTile, &map_w, (kb0 + i) * kBlk, 0, a, &sm.full[s]);
+    };
+    // the first copies before the CTAs of the cluster meet
+    const int early = idle ? 0 : min(nkb, g.stages);
+    if (threadIdx.x == 0)
+        for (int i = 0; i < early; ++i) copy(i);
     tc_before_sync();
-    if (g.ks > 1)
+    if (g.ks > 1 && !idle)
         cluster_sync();  // also: the cluster's CTAs run, so their shared memory may be written
     else
         __syncthreads();
+    pdl_trigger();  // not before every CTA holds its tensor memory (tmem_alloc)
     tc_after_sync();
     const uint32_t tmem = sm.tmem;
+    if (idle) {
+        if (warp == 1) tmem_free(tmem, g.tmem_cols);
+        return;
+    }
 
     if (warp == 0 && lane == 0) {
-        int issued = 0;
-        for (int i = 0; i < nkb; ++i) {
-            const int s = i % g.stages;
-            if (i >= g.stages && !mbar_wait_or_abort(&sm.empty[s], (uint32_t)(i / g.stages - 1) & 1u, abort_flag)) {
+        int issued = early;
+        for (int i = early; i < nkb; ++i) {
+            if (!mbar_wait_or_abort(&sm.empty[i % g.stages], (uint32_t)(i / g.stages - 1) & 1u, abort_flag)) {
                 *abort_flag = 1;
                 break;
             }
-            unsigned char *st = ring + (size_t)s * stage_bytes;
-            mbar_arrive_expect_tx(&sm.full[s], (uint32_t)stage_bytes);
-            tma_load_3d(st, &map_x, (kb0 + i) * kBlk, t0, b, &sm.full[s]);
-            tma_load_3d(st + kRowTile, &map_w, (kb0 + i) * kBlk, 0, a, &sm.full[s]);
+            copy(i);
             issued = i + 1;
         }
         // every copy issued has landed before the CTA may leave
@@ -289,133 +334,303 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
 }
 
 // --------------------------------------------------------------------------
-// expand.  A CTA takes 256 channels of a run of tokens, 32 at a time; a warp 32
-// channels.  With A the state [k][token] and B the adapter [k][channel], both
-// transposed by ldmatrix; k runs over the 2 R rows of the state's first two parts,
-// each part against the same R rows of the adapter.  Column n = 2 c + i of the MMA's tile j
-// stands for channel 8 c + 2 j + i of the warp's 32, so that the accumulators of
-// a thread are 8 consecutive channels of a token: one 16-byte load and store.
-// The adapter's tile is permuted accordingly on its way into shared memory.
+// expand.  A tile is 128 tokens (MMA M) by 64 channels (MMA N).  The state
+// [k][token] is A, M-major, the adapter [k][channel] B, N-major, both as they lie
+// in memory; k runs over the 2 R rows of the state's first two parts, each part
+// against the same R rows of the adapter.  (Where R is an odd multiple of 8, an
+// instruction of k = 16 would wrap around them: they are copied twice.)
+//
+// As many CTAs as the device holds take every gridDim.x-th of the tiles that have
+// rows, in the order of the channels, then the tokens: all end at the same time,
+// whatever the samples' lengths, and those that run side by side move along the
+// same rows.  A tile's base, state and adapter come by TMA into a stage of a ring;
+// two accumulators; a thread adds row t's accumulators to the base in shared memory,
+// from where the tile leaves by TMA.  A tile that the sample's end crosses leaves by
+// row.  (One tile a CTA, of 128 channels, four CTAs an SM, each waiting for its own
+// copies: 36 us instead of XX for 4222 rows of 9216 channels at rank 32.  Each CTA a
+// run of one row of tiles: 45, the last CTAs alone on the device.)
+//
+// Roles (192 threads): warp 0 finds the tiles and lane 0 copies, warp 1 lane 0 the
+// MMAs, warps 2 to 5 a token a thread.
 // --------------------------------------------------------------------------
-constexpr int kExTok = 32;                 // tokens a warp multiplies at once, the next 32 requested before
-constexpr int kExC = 256;                  // channels of a CTA
-constexpr int kExWPitch = kExC * 2 + 16;   // bytes; 16 more, so that 8 rows lie in distinct banks
-// tokens of a CTA, whose state stays in shared memory beside the adapter's tile:
-// the more, the fewer times the tile is read, the fewer CTAs share an SM
-__host__ __device__ constexpr int ex_run(int R) { return R <= 32 ? 256 : R <= 64 ? 128 : 64; }
-__host__ __device__ constexpr int ex_h_pitch(int run) { return run * 2 + 16; }
+constexpr int kExThreads = 192;
+constexpr int kExTile = kM * kBlk * 2;  // 16 KB: 64 channels of the base
+constexpr int kExStages = 4;
+static_assert(kExStages <= kMaxStages, "barriers");
 
-__device__ __forceinline__ void ldsm_trans(uint32_t addr, uint32_t (&v)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "r"(addr)
+enum BaseKind { kNoBase, kBaseByTma, kBaseByRow };
+
+struct ExpandArgs {
+    const void *ids;
+    int is64;
+    const int *lens;
+    const uint16_t *base;
+    long long base_batch, base_token;
+    uint16_t *out;
+    long long batch, token;
+    int S, C, R, NA;
+    int B;
+    int copies;  // of the adapter's rows
+    int kind;    // of the base
+    int stages;
+};
+
+struct ExpandTile {  // what a stage holds
+    int b, t0, c0;
+    int n;  // rows of the sample from t0 on; 0: there are no more tiles
+    int a;  // adapter, -1: none
+};
+
+// The tiles x, x + step, ... of a call, for a warp.  Without lens every sample has
+// the same number of token tiles; with them the warp goes through the samples, 32 at
+// a time.
+struct ExpandTiles {
+    const ExpandArgs &g;
+    long long u, step;  // tile number
+    int ct;             // channel tiles
+    int w0;             // first sample of the window
+    long long before;   // token tiles of the samples before it
+    int rows, upto;     // this lane's sample: its rows, and the token tiles up to its end
+    __device__ __forceinline__ ExpandTiles(const ExpandArgs &args, int lane)
+        : g(args), u(blockIdx.x), step(gridDim.x), ct((args.C + kBlk - 1) / kBlk), w0(0), before(0) {
+        if (g.lens) window(lane);
+    }
+    __device__ __forceinline__ void window(int lane) {
+        rows = w0 + lane < g.B ? rows_of(g.lens, w0 + lane, g.S) : 0;
+        upto = (rows + kM - 1) / kM;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d) upto += v;
+        }
+    }
+    // the next tile, n == 0 after the last; the same in every lane
+    __device__ __forceinline__ ExpandTile next(int lane) {
+        ExpandTile t = {0, 0, 0, 0, -1};
+        for (;; u += step) {
+            const long long tt = u / ct;  // token tile
+            t.c0 = (int)(u - tt * ct) * kBlk;
+            if (!g.lens) {
+                const int per = (g.S + kM - 1) / kM;
+                if (tt >= (long long)g.B * per) return t;
+                t.b = (int)(tt / per), t.t0 = (int)(tt - (long long)t.b * per) * kM, t.n = g.S - t.t0;
+            } else {
+                unsigned past;
+                for (;;) {  // the first sample whose end lies beyond tt
+                    past = __ballot_sync(0xFFFFFFFFu, before + upto > tt);
+                    if (past) break;
+                    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+                    w0 += 32;
+                    if (w0 >= g.B) return t;
+                    window(lane);
+                }
+                const int i = __ffs(past) - 1, n = __shfl_sync(0xFFFFFFFFu, rows, i);
+                const int end = __shfl_sync(0xFFFFFFFFu, upto, i);
+                t.b = w0 + i, t.t0 = (int)(tt - before - (end - (n + kM - 1) / kM)) * kM, t.n = n - t.t0;
+            }
+            t.a = adapter_of(g.ids, g.is64, t.b, g.NA);
+            if (t.a >= 0 || g.base != g.out) break;
+            t.n = 0;  // in place without an adapter: nothing to do
+        }
+        u += step;
+        return t;
+    }
+};
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
-        "%2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// all but the last N stores have read their shared memory
+template <int N>
+__device__ __forceinline__ void tma_store_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-__global__ void __launch_bounds__(256, 2)
-lora_expand_tc_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict__ W, const void *ids, int is64,
-                      const int *lens, const uint16_t *base, long long base_batch, long long base_token, uint16_t *out,
-                      long long batch, long long token, int S, int Sp, int C, int R, int NA, int run) {
-    extern __shared__ __align__(16) unsigned char ex_smem[];
-    unsigned char *w_s = ex_smem, *h_s = ex_smem + (size_t)R * kExWPitch;
+__global__ void __launch_bounds__(kExThreads)
+lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_w,
+                      const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_o,
+                      const ExpandArgs g) {
+    extern __shared__ unsigned char tc_smem_raw[];
+    __shared__ ExpandTile info[kExStages];
+    const uint32_t raw = smem_u32(tc_smem_raw);
+    unsigned char *ring = tc_smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const int R = g.R, h_box = 2 * R * 128, w_rows = R * 128, w_tile = g.copies * w_rows;
+    const int stage_bytes = kExTile + 2 * h_box + w_tile;  // base, state, adapter
+    TcBars &sm = *reinterpret_cast<TcBars *>(ring + (size_t)g.stages * stage_bytes);
+    volatile int *abort_flag = &sm.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.z, s0 = blockIdx.y * run, c0 = blockIdx.x * kExC;
-    const int h_pitch = ex_h_pitch(run);
-    pdl_wait();
-    pdl_trigger();
-    const int n = min(rows_of(lens, b, S), s0 + run) - s0;
-    if (n <= 0) return;
-    const int a = adapter_of(ids, is64, b, NA);
-    if (a < 0 && base == out) return;
-    const int ch = c0 + warp * 32 + (lane & 3) * 8;  // this thread's channels
-    const bool live = ch < C;
-    const uint16_t *y_at = base + b * base_batch + (s0 + (lane >> 2)) * base_token + ch;
-    uint16_t *o_at = out + b * batch + (s0 + (lane >> 2)) * token + ch;
-    auto request = [&](int s, uint4 (&y)[2][2]) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                y[m][k] = make_uint4(0u, 0u, 0u, 0u);
-                // not the read-only path: base may be out
-                if (base && live && s + m * 16 + k * 8 + (lane >> 2) < n)
-                    y[m][k] = *reinterpret_cast<const uint4 *>(y_at + (s + m * 16 + k * 8) * base_token);
-            }
-    };
-    uint4 y[2][2], next[2][2];
-    request(0, y);
-    if (a >= 0) {
-        const uint16_t *w = W + (long long)a * R * C;
-        for (int i = threadIdx.x; i < R * (kExC / 8); i += 256) {
-            const int r = i / (kExC / 8), v = i % (kExC / 8);  // 8 channels: c = v % 4 of strip v / 4
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (c0 + v * 8 < C) x = ldg16(w + (long long)r * C + c0 + v * 8);
-            unsigned char *p = w_s + r * kExWPitch + (v >> 2) * 64 + (v & 3) * 4;
-            *reinterpret_cast<uint32_t *>(p) = x.x;
-            *reinterpret_cast<uint32_t *>(p + 16) = x.y;
-            *reinterpret_cast<uint32_t *>(p + 32) = x.z;
-            *reinterpret_cast<uint32_t *>(p + 48) = x.w;
-        }
-        const uint16_t *hp = h + (size_t)b * 3 * R * Sp + s0;
-        const int vecs = (min(n, run) + 31) / 32 * 4;  // 8 tokens each, whole steps of 32
-        for (int i = threadIdx.x; i < 2 * R * vecs; i += 256) {
-            const int k = i / vecs, v = i - k * vecs;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (s0 + v * 8 < Sp) x = *reinterpret_cast<const uint4 *>(hp + (size_t)k * Sp + v * 8);
-            *reinterpret_cast<uint4 *>(h_s + k * h_pitch + v * 16) = x;
-        }
-        __syncthreads();
+    if (threadIdx.x == 0) {
+        prefetch_map(&map_h), prefetch_map(&map_w), prefetch_map(&map_y), prefetch_map(&map_o);
+        bars_init(sm, 128, 2);
     }
-    if (c0 + warp * 32 >= C) return;
-    const int blocks = R >> 3;
-    const uint32_t ws = smem_u32(w_s) + (lane & 7) * kExWPitch + warp * 64 + (lane >> 3) * 16;
-    const uint32_t hs = smem_u32(h_s) + ((lane >> 4) * 8 + (lane & 7)) * h_pitch + ((lane >> 3) & 1) * 16;
-    for (int s = 0; s < n; s += kExTok) {
-        request(s + kExTok, next);
-        float acc[2][4][4];
+    if (warp == 1) tmem_alloc(&sm.tmem, 2 * kBlk);
+    pdl_wait();
+    const bool by_tma = g.kind == kBaseByTma;
+    tc_before_sync();
+    __syncthreads();
+    pdl_trigger();
+    tc_after_sync();
+    const uint32_t tmem = sm.tmem;
+    bool ok = true;
+    if (warp == 0) {
+        ExpandTiles tiles(g, lane);
+        int issued = 0;
+        for (int i = 0;; ++i) {
+            const ExpandTile t = tiles.next(lane);
+            const int s = i % g.stages;
+            // free: the tile's MMAs are done, and its store has read it
+            if (i >= g.stages) ok = mbar_wait_or_abort(&sm.empty[s], (uint32_t)(i / g.stages - 1) & 1u, abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                *abort_flag = 1;
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                unsigned char *p = ring + (size_t)s * stage_bytes;
+                info[s] = t;
+                const int bytes = t.n == 0 ? 0 : (by_tma ? kExTile : 0) + (t.a >= 0 ? 2 * h_box + w_tile : 0);
+                mbar_arrive_expect_tx(&sm.full[s], (uint32_t)bytes);
+                if (t.n > 0 && by_tma) tma_load_3d(p, &map_y, t.c0, t.t0, t.b, &sm.full[s]);
+                if (t.n > 0 && t.a >= 0) {
+                    for (int k = 0; k < 2; ++k)
+                        tma_load_3d(p + kExTile + k * h_box, &map_h, t.t0 + k * kBlk, 0, t.b, &sm.full[s]);
+                    for (int k = 0; k < g.copies; ++k)
+                        tma_load_3d(p + kExTile + 2 * h_box + k * w_rows, &map_w, t.c0, 0, t.a, &sm.full[s]);
+                }
+            }
+            issued = i + 1;
+            if (t.n == 0) break;
+        }
+        // every copy issued lands before the CTA leaves
+        if (lane == 0)
+            for (int s = 0; s < g.stages && s < issued; ++s) {
+                const int last = s + g.stages * ((issued - 1 - s) / g.stages);
+                if (!mbar_wait_bounded(&sm.full[s], (uint32_t)(last / g.stages) & 1u, kDrainNs))
+                    report_error_lora(kErrDrainFailed);
+            }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = f16_idesc(kBlk, true) | (1u << 16);  // B N-major
+            bool go = first_wait(sm);
+            for (int i = 0, m = 0; go; ++i) {
+                const int s = i % g.stages, p = m & 1;
+                go = mbar_wait_or_abort(&sm.full[s], (uint32_t)(i / g.stages) & 1u, abort_flag);
+                if (!go || info[s].n == 0) break;
+                const bool add = info[s].a >= 0;
+                mbar_arrive(&sm.empty[s]);  // one of two; the other comes after the tile's accumulators were taken
+                if (!add) continue;
+                if (m >= 2) go = mbar_wait_or_abort(&sm.acc_empty[p], (uint32_t)(m / 2 - 1) & 1u, abort_flag);
+                if (!go) break;
+                tc_after_sync();
+                const uint32_t at = smem_u32(ring + (size_t)s * stage_bytes + kExTile);
+                const uint64_t hd = sw128_desc(at, (uint32_t)h_box, 1024),
+                               wd = sw128_desc(at + 2 * (uint32_t)h_box, 0, 1024);
+                for (int k = 0, r = 0; k < R / 8; ++k) {  // rows 16 k .. of the state, r .. of the adapter
+                    mma_f16(tmem + (uint32_t)(p * kBlk), hd + (2048u >> 4) * k, wd + (uint32_t)(r * 128 >> 4), idesc,
+                            k > 0);
+                    r += 16;
+                    if (r >= g.copies * R) r -= g.copies * R;
+                }
+                mma_commit(&sm.acc_full[p]);
+                ++m;
+            }
+            if (!go) {
+                *abort_flag = 1;
+                // MMAs issued before may still be writing the accumulators
+                mma_commit(&sm.done);
+                if (!mbar_wait_bounded(&sm.done, 0u, kDrainNs)) report_error_lora(kErrDrainFailed);
+            }
+        }
+    } else {
+        const int t = (warp & 3) * 32 + lane;  // a warp reads the tensor memory of lanes 32 (warp mod 4) ..
+        const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        int held = -1;  // thread 64: the stage that the last store may still be reading
+        for (int i = 0, m = 0;; ++i) {
+            const int s = i % g.stages, p = m & 1;
+            ok = mbar_wait_or_abort(&sm.full[s], (uint32_t)(i / g.stages) & 1u, abort_flag);
+            const ExpandTile e = info[s];
+            if (ok && e.n > 0 && e.a >= 0)
+                ok = mbar_wait_or_abort(&sm.acc_full[p], (uint32_t)(m / 2) & 1u, abort_flag);
+            // the four warps go on, or give up, together
+            if (!named_bar_and(1, 128, ok)) {
+                ok = false;
+                *abort_flag = 1;
+                break;
+            }
+            if (e.n == 0) break;
+            const bool whole = e.n >= kM || e.t0 + e.n == g.S;  // no row of the tile is to be left alone
+            unsigned char *tile = ring + (size_t)s * stage_bytes;
+            const long long row = e.t0 + t;
+            const uint16_t *y_row = g.base + e.b * g.base_batch + row * g.base_token + e.c0;
+            uint16_t *o_row = g.out + e.b * g.batch + row * g.token + e.c0;
+            tc_after_sync();
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+            for (int c = 0; c < kBlk; c += 32) {
+                uint32_t v[32];
+                if (e.a >= 0) {
+                    tmem_ld32(trow + (uint32_t)(p * kBlk + c), v);
+                    tmem_ld_done();
+                }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                for (int q = 0; q < 4; ++q) {
+                    unsigned char *at = tile + t * 128 + (((c / 8 + q) ^ (t & 7)) << 4);  // the row's 128 bytes, swizzled
+                    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+                    if (by_tma)
+                        y = *reinterpret_cast<const uint4 *>(at);
+                    else if (g.kind == kBaseByRow && t < e.n && e.c0 + c + q * 8 < g.C)
+                        y = *reinterpret_cast<const uint4 *>(y_row + c + q * 8);
+                    if (e.a >= 0) {
+                        uint32_t yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[m][j][k] = 0.0f;
-        if (a >= 0) {
-            for (int k = 0, w0 = 0; k < blocks; ++k) {  // rows 16 k .. of the state, 8 w0 .. and 8 w1 .. of W
-                const int w1 = w0 + 1 == blocks ? 0 : w0 + 1;
-                uint32_t wa[4], wb[4];
-                ldsm_trans(ws + w0 * 8 * kExWPitch, wa);
-                ldsm_trans(ws + w1 * 8 * kExWPitch, wb);
-                w0 = w1 + 1 == blocks ? 0 : w1 + 1;
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    uint32_t ha[4];
-                    ldsm_trans(hs + k * 16 * h_pitch + (s + m * 16) * 2, ha);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mma_bf16(acc[m][j], ha, wa[j], wb[j]);
+                        for (int j = 0; j < 4; ++j)
+                            yw[j] = px_to_bf16x2(px_add(px_bf16(yw[j]), px_make(__uint_as_float(v[q * 8 + 2 * j]),
+                                                                               __uint_as_float(v[q * 8 + 2 * j + 1]))));
+                        y = make_uint4(yw[0], yw[1], yw[2], yw[3]);
+                    }
+                    if (whole)
+                        *reinterpret_cast<uint4 *>(at) = y;
+                    else if (t < e.n && e.c0 + c + q * 8 < g.C)
+                        stg16(o_row + c + q * 8, y);
+                }
+            }
+            if (e.a >= 0) {
+                tc_before_sync();
+                mbar_arrive(&sm.acc_empty[p]);
+                ++m;
+            }
+            if (whole) fence_proxy_async_smem();
+            named_bar(1, 128);
+            if (threadIdx.x == 64) {
+                if (whole) {
+                    tma_store_3d(&map_o, tile, e.c0, e.t0, e.b);
+                    tma_store_commit();
+                    if (held >= 0) {
+                        tma_store_read<1>();
+                        mbar_arrive(&sm.empty[held]);
+                    }
+                    held = s;
+                } else {
+                    if (held >= 0) {
+                        tma_store_read<0>();
+                        mbar_arrive(&sm.empty[held]);
+                    }
+                    held = -1;
+                    mbar_arrive(&sm.empty[s]);
                 }
             }
         }
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (live && s + m * 16 + k * 8 + (lane >> 2) < n) {
-                    const uint32_t yw[4] = {y[m][k].x, y[m][k].y, y[m][k].z, y[m][k].w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        o[j] = px_to_bf16x2(px_add(px_bf16(yw[j]), px_make(acc[m][j][2 * k], acc[m][j][2 * k + 1])));
-                    stg16(o_at + (s + m * 16 + k * 8) * token, make_uint4(o[0], o[1], o[2], o[3]));
-                }
-                y[m][k] = next[m][k];
-            }
+        if (threadIdx.x == 64) tma_store_done();
+    }
+    tc_before_sync();
+    ok = __syncthreads_and(ok && !*abort_flag);
+    if (!ok && threadIdx.x == 0) report_error_lora(kErrLoraExpandWait);
+    if (warp == 1) {
+        tc_after_sync();
+        tmem_free(tmem, 2 * kBlk);
     }
 }
 
@@ -428,7 +643,7 @@ lora_expand_tc_kernel(const uint16_t *__restrict__ h, const uint16_t *__restrict
 // Schedules and order as lora_grad_kernel's: OWNER, every piece of an adapter in
 // order by one CTA, with two accumulators (where they fit), so that one piece's
 // leave while the next one's MMAs run, and the total in shared memory; otherwise a
-// CTA a piece.
+// CTA one or two pieces.
 //
 // Roles (192 threads): warp 0 lane 0 the copies, warp 1 the MMAs (and zeros for
 // the rows of a block past the sample's end, which may hold anything), warps 2
@@ -445,6 +660,7 @@ struct GradArgs {
     int B, S, R, NA, pieces;
     int Np;    // 3 R rounded up to 16
     int bufs;  // accumulators
+    int cta_pieces;  // pieces of a CTA (not OWNER)
     int stages, tmem_cols;
 };
 
@@ -468,18 +684,18 @@ lora_grad_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     const CUtensorMap *map_src = first ? &map_x : &map_d, *map_state = first ? &map_e : &map_h;
     const int c0 = ((int)blockIdx.x - (first ? 0 : g.o[0].blocks)) * kM;
     pdl_wait();
-    pdl_trigger();
     int samples = 1, s_begin = 0, s_most = g.S;
     const int a = OWNER ? (int)blockIdx.y : adapter_of(g.ids, g.is64, blockIdx.z, g.NA);
     if (!OWNER) {
-        s_begin = blockIdx.y * kLoraTcPiece;
-        s_most = s_begin + kLoraTcPiece;
+        s_begin = blockIdx.y * g.cta_pieces * kLoraTcPiece;
+        s_most = s_begin + g.cta_pieces * kLoraTcPiece;
         if (a < 0 || s_begin >= rows_of(g.lens, blockIdx.z, g.S)) return;
     }
     if (threadIdx.x == 0) bars_init(sm, 128);
     if (warp == 1) tmem_alloc(&sm.tmem, g.tmem_cols);
     tc_before_sync();
     __syncthreads();
+    pdl_trigger();
     tc_after_sync();
     const uint32_t tmem = sm.tmem;
 
@@ -615,10 +831,8 @@ lora_grad_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                                 }
                             }
                         }
-                        if (OWNER) {
-                            tc_before_sync();
-                            mbar_arrive(&sm.acc_empty[p]);
-                        }
+                        tc_before_sync();
+                        mbar_arrive(&sm.acc_empty[p]);
                     }
                 }
             }
@@ -731,16 +945,35 @@ cudaError_t lora_tc_shrink(const adaln_rows &src, const void *W, const LoraCall 
 
 cudaError_t lora_tc_expand(const void *h, const void *W, const LoraCall &c, int C, cudaStream_t stream,
                            const DeviceInfo &dev) {
-    const int run = ex_run(c.R);
-    const size_t smem = (size_t)c.R * kExWPitch + (size_t)2 * c.R * ex_h_pitch(run);
+    ExpandArgs g = {};
+    g.ids = c.ids, g.is64 = c.ids_are_64, g.lens = c.lens;
+    g.base = static_cast<const uint16_t *>(c.base.data), g.base_batch = c.base.batch, g.base_token = c.base.token;
+    g.out = static_cast<uint16_t *>(c.out.data), g.batch = c.out.batch, g.token = c.out.token;
+    g.S = c.S, g.C = C, g.R = c.R, g.NA = c.NA;
+    g.copies = c.R % 16 == 0 ? 1 : 2;
+    // a broadcast base has strides that no tensor map takes
+    const bool broadcast = (c.B > 1 && c.base.batch == 0) || (c.S > 1 && c.base.token == 0);
+    g.kind = !g.base ? kNoBase : broadcast ? kBaseByRow : kBaseByTma;
+    const int Sp = padded_tokens(c.S);
+    CUtensorMap map_h, map_w, map_y, map_o;
+    // the first two parts of the state: 2 R of its 3 R rows; without adapters nothing reads it or them
+    const void *any = c.out.data;
+    if (!make_map_3d(&map_h, c.NA > 0 ? h : any, Sp, 2 * c.R, c.B, Sp, (int64_t)3 * c.R * Sp, 2 * c.R) ||
+        !make_map_3d(&map_w, c.NA > 0 ? W : any, C, c.R, c.NA > 0 ? c.NA : 1, C, (int64_t)c.R * C, c.R) ||
+        !make_map_3d(&map_o, c.out.data, C, c.S, c.B, c.out.token, c.out.batch, kM) ||
+        !(g.kind == kBaseByTma ? make_map_3d(&map_y, c.base.data, C, c.S, c.B, c.base.token, c.base.batch, kM)
+                               : make_map_3d(&map_y, c.out.data, C, c.S, c.B, c.out.token, c.out.batch, kM)))
+        return cudaErrorInvalidValue;
+    g.B = c.B;
+    const int stage = kExTile + 4 * c.R * 128 + g.copies * c.R * 128;
+    g.stages = stages_for(stage, 0);
+    if (g.stages > kExStages) g.stages = kExStages;
+    const size_t smem = (size_t)g.stages * stage + kBarBytes + 1024;
+    const int per_sm = smem <= 113 * 1024 ? 2 : 1;
+    const long long most = (long long)((C + kBlk - 1) / kBlk) * ((c.S + kM - 1) / kM) * c.B, room = (long long)per_sm * dev.sm_count;
     cudaError_t err = ensure_smem_attr((const void *)lora_expand_tc_kernel, smem, dev);
     if (err != cudaSuccess) return err;
-    const dim3 grid((C + kExC - 1) / kExC, (c.S + run - 1) / run, c.B);
-    return launch_pdl(lora_expand_tc_kernel, grid, dim3(256), smem, stream, static_cast<const uint16_t *>(h),
-                      static_cast<const uint16_t *>(W), c.ids, c.ids_are_64, c.lens,
-                      static_cast<const uint16_t *>(c.base.data), (long long)c.base.batch, (long long)c.base.token,
-                      static_cast<uint16_t *>(c.out.data), (long long)c.out.batch, (long long)c.out.token, c.S,
-                      padded_tokens(c.S), C, c.R, c.NA, run);
+    return launch_pdl(lora_expand_tc_kernel, dim3((unsigned)(most < room ? most : room)), dim3(kExThreads), smem, stream, map_h, map_w, map_y, map_o, g);
 }
 
 cudaError_t lora_tc_grads(const GradOperand &o0, const GradOperand &o1, const LoraCall &c, bool in_parts,
@@ -752,7 +985,10 @@ cudaError_t lora_tc_grads(const GradOperand &o0, const GradOperand &o1, const Lo
     g.ids = c.ids, g.is64 = c.ids_are_64, g.lens = c.lens, g.accumulate = c.accumulate;
     g.B = c.B, g.S = c.S, g.R = c.R, g.NA = c.NA, g.pieces = (c.S + kLoraTcPiece - 1) / kLoraTcPiece;
     g.Np = (3 * c.R + 15) / 16 * 16;
-    g.bufs = !in_parts && g.Np <= 256 ? 2 : 1;
+    const unsigned x = (unsigned)(g.o[0].blocks + g.o[1].blocks);
+    // two pieces a CTA where that still gives every SM two: the CTA's start is paid once
+    g.cta_pieces = (long long)x * g.pieces * c.B >= 4ll * dev.sm_count ? 2 : 1;
+    g.bufs = (!in_parts || g.cta_pieces > 1) && g.Np <= 256 ? 2 : 1;
     const int stage = kRowTile + g.Np * kBlk * 2, extra = in_parts ? 0 : c.R * kM * 4;
     g.stages = stages_for(stage, extra);
     g.tmem_cols = tmem_columns(g.bufs * g.Np);
@@ -768,8 +1004,8 @@ cudaError_t lora_tc_grads(const GradOperand &o0, const GradOperand &o1, const Lo
     auto kern = in_parts ? lora_grad_tc_kernel<false> : lora_grad_tc_kernel<true>;
     cudaError_t err = ensure_smem_attr((const void *)kern, smem, dev);
     if (err != cudaSuccess) return err;
-    const unsigned x = (unsigned)(g.o[0].blocks + g.o[1].blocks);
-    const dim3 grid = in_parts ? dim3(x, (unsigned)g.pieces, (unsigned)c.B) : dim3(x, (unsigned)c.NA);
+    const dim3 grid = in_parts ? dim3(x, (unsigned)((g.pieces + g.cta_pieces - 1) / g.cta_pieces), (unsigned)c.B)
+                               : dim3(x, (unsigned)c.NA);
     return launch_pdl(kern, grid, dim3(kGradThreads), smem, stream, map_x, map_e, map_d, map_h, g);
 }
 
