@@ -12,6 +12,8 @@
 // h and e are held as three bf16 parts, whose sum is the fp32 number itself.  The
 // gradients, which are fp32, take all three (two would leave 2.5e-6 of error, more
 // than all the sums); out and dx are rounded to bf16 once more and take two (2^-17).
+#include <algorithm>
+
 #include "lora.cuh"
 #include "tc.cuh"
 
@@ -350,12 +352,13 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
 // copies: 36 us instead of XX for 4222 rows of 9216 channels at rank 32.  Each CTA a
 // run of one row of tiles: 45, the last CTAs alone on the device.)
 //
-// Roles (192 threads): warp 0 finds the tiles and lane 0 copies, warp 1 lane 0 the
-// MMAs, warps 2 to 5 a token a thread.
+// Roles (320 threads): warp 0 finds the tiles and lane 0 copies, warp 1 lane 0 the
+// MMAs, warps 2 to 5 and 6 to 9 every other tile, a token a thread.
 // --------------------------------------------------------------------------
-constexpr int kExThreads = 192;
+constexpr int kExThreads = 320;
 constexpr int kExTile = kM * kBlk * 2;  // 16 KB: 64 channels of the base
-constexpr int kExStages = 4;
+constexpr int kExStages = 4;   // most; 2 or 4, so that a stage is always the same group's
+constexpr int kExCtas = 3;     // most on an SM
 static_assert(kExStages <= kMaxStages, "barriers");
 
 enum BaseKind { kNoBase, kBaseByTma, kBaseByRow };
@@ -379,6 +382,7 @@ struct ExpandTile {  // what a stage holds
     int b, t0, c0;
     int n;  // rows of the sample from t0 on; 0: there are no more tiles
     int a;  // adapter, -1: none
+    int m;  // products before this one among the tiles of its group of warps
 };
 
 // The tiles x, x + step, ... of a call, for a warp.  Without lens every sample has
@@ -391,8 +395,10 @@ struct ExpandTiles {
     int w0;             // first sample of the window
     long long before;   // token tiles of the samples before it
     int rows, upto;     // this lane's sample: its rows, and the token tiles up to its end
+    bool over;
     __device__ __forceinline__ ExpandTiles(const ExpandArgs &args, int lane)
-        : g(args), u(blockIdx.x), step(gridDim.x), ct((args.C + kBlk - 1) / kBlk), w0(0), before(0) {
+        : g(args), u(blockIdx.x), step(gridDim.x), ct((args.C + kBlk - 1) / kBlk), w0(0), before(0), rows(0), upto(0),
+          over(false) {
         if (g.lens) window(lane);
     }
     __device__ __forceinline__ void window(int lane) {
@@ -404,25 +410,31 @@ struct ExpandTiles {
             if (lane >= d) upto += v;
         }
     }
-    // the next tile, n == 0 after the last; the same in every lane
+    // the next tile; after the last n == 0, as often as it is asked; the same in every lane
     __device__ __forceinline__ ExpandTile next(int lane) {
-        ExpandTile t = {0, 0, 0, 0, -1};
-        for (;; u += step) {
+        ExpandTile t = {0, 0, 0, 0, -1, 0};
+        for (; !over; u += step) {
             const long long tt = u / ct;  // token tile
             t.c0 = (int)(u - tt * ct) * kBlk;
             if (!g.lens) {
                 const int per = (g.S + kM - 1) / kM;
-                if (tt >= (long long)g.B * per) return t;
+                if (tt >= (long long)g.B * per) {
+                    over = true;
+                    break;
+                }
                 t.b = (int)(tt / per), t.t0 = (int)(tt - (long long)t.b * per) * kM, t.n = g.S - t.t0;
             } else {
                 unsigned past;
                 for (;;) {  // the first sample whose end lies beyond tt
                     past = __ballot_sync(0xFFFFFFFFu, before + upto > tt);
-                    if (past) break;
+                    if (past || w0 + 32 >= g.B) break;
                     before += __shfl_sync(0xFFFFFFFFu, upto, 31);
                     w0 += 32;
-                    if (w0 >= g.B) return t;
                     window(lane);
+                }
+                if (!past) {
+                    over = true;
+                    break;
                 }
                 const int i = __ffs(past) - 1, n = __shfl_sync(0xFFFFFFFFu, rows, i);
                 const int end = __shfl_sync(0xFFFFFFFFu, upto, i);
@@ -442,15 +454,13 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
                  "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
-__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// all but the last N stores have read their shared memory
-template <int N>
+// this thread's stores have read their shared memory
 __device__ __forceinline__ void tma_store_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 __device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-__global__ void __launch_bounds__(kExThreads)
+__global__ void __launch_bounds__(kExThreads, kExCtas)
 lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_o,
                       const ExpandArgs g) {
@@ -478,9 +488,12 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
     bool ok = true;
     if (warp == 0) {
         ExpandTiles tiles(g, lane);
-        int issued = 0;
-        for (int i = 0;; ++i) {
-            const ExpandTile t = tiles.next(lane);
+        int issued = 0, products[2] = {0, 0};
+        for (int i = 0, ends = 0; ends < 2; ++i) {  // the end is told twice, once to each group of warps
+            ExpandTile t = tiles.next(lane);
+            t.m = i & 1 ? products[1] : products[0];
+            if (t.n > 0 && t.a >= 0) (i & 1 ? products[1] : products[0]) += 1;
+            ends += t.n == 0;
             const int s = i % g.stages;
             // free: the tile's MMAs are done, and its store has read it
             if (i >= g.stages) ok = mbar_wait_or_abort(&sm.empty[s], (uint32_t)(i / g.stages - 1) & 1u, abort_flag);
@@ -503,7 +516,6 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
                 }
             }
             issued = i + 1;
-            if (t.n == 0) break;
         }
         // every copy issued lands before the CTA leaves
         if (lane == 0)
@@ -516,14 +528,15 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
         if (lane == 0) {
             const uint32_t idesc = f16_idesc(kBlk, true) | (1u << 16);  // B N-major
             bool go = first_wait(sm);
-            for (int i = 0, m = 0; go; ++i) {
-                const int s = i % g.stages, p = m & 1;
+            for (int i = 0; go; ++i) {
+                const int s = i % g.stages;
                 go = mbar_wait_or_abort(&sm.full[s], (uint32_t)(i / g.stages) & 1u, abort_flag);
                 if (!go || info[s].n == 0) break;
                 const bool add = info[s].a >= 0;
+                const int m = info[s].m, p = i & 1;  // an accumulator for each group
                 mbar_arrive(&sm.empty[s]);  // one of two; the other comes after the tile's accumulators were taken
                 if (!add) continue;
-                if (m >= 2) go = mbar_wait_or_abort(&sm.acc_empty[p], (uint32_t)(m / 2 - 1) & 1u, abort_flag);
+                if (m > 0) go = mbar_wait_or_abort(&sm.acc_empty[p], (uint32_t)(m - 1) & 1u, abort_flag);
                 if (!go) break;
                 tc_after_sync();
                 const uint32_t at = smem_u32(ring + (size_t)s * stage_bytes + kExTile);
@@ -536,7 +549,6 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
                     if (r >= g.copies * R) r -= g.copies * R;
                 }
                 mma_commit(&sm.acc_full[p]);
-                ++m;
             }
             if (!go) {
                 *abort_flag = 1;
@@ -548,15 +560,18 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
     } else {
         const int t = (warp & 3) * 32 + lane;  // a warp reads the tensor memory of lanes 32 (warp mod 4) ..
         const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        int held = -1;  // thread 64: the stage that the last store may still be reading
-        for (int i = 0, m = 0;; ++i) {
-            const int s = i % g.stages, p = m & 1;
+        const int group = (warp - 2) >> 2;
+        const bool leads = (threadIdx.x - 64) % 128 == 0;
+        for (int i = group;; i += 2) {
+            const int s = i % g.stages;
+            // the stages are even in number: this one's phases are all this group's
             ok = mbar_wait_or_abort(&sm.full[s], (uint32_t)(i / g.stages) & 1u, abort_flag);
             const ExpandTile e = info[s];
+            const int p = group;
             if (ok && e.n > 0 && e.a >= 0)
-                ok = mbar_wait_or_abort(&sm.acc_full[p], (uint32_t)(m / 2) & 1u, abort_flag);
-            // the four warps go on, or give up, together
-            if (!named_bar_and(1, 128, ok)) {
+                ok = mbar_wait_or_abort(&sm.acc_full[p], (uint32_t)e.m & 1u, abort_flag);
+            // the group's warps go on, or give up, together
+            if (!named_bar_and(1 + group, 128, ok)) {
                 ok = false;
                 *abort_flag = 1;
                 break;
@@ -600,30 +615,18 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
             if (e.a >= 0) {
                 tc_before_sync();
                 mbar_arrive(&sm.acc_empty[p]);
-                ++m;
             }
             if (whole) fence_proxy_async_smem();
-            named_bar(1, 128);
-            if (threadIdx.x == 64) {
+            named_bar(1 + group, 128);
+            if (leads) {
                 if (whole) {
                     tma_store_3d(&map_o, tile, e.c0, e.t0, e.b);
-                    tma_store_commit();
-                    if (held >= 0) {
-                        tma_store_read<1>();
-                        mbar_arrive(&sm.empty[held]);
-                    }
-                    held = s;
-                } else {
-                    if (held >= 0) {
-                        tma_store_read<0>();
-                        mbar_arrive(&sm.empty[held]);
-                    }
-                    held = -1;
-                    mbar_arrive(&sm.empty[s]);
+                    tma_store_read();
                 }
+                mbar_arrive(&sm.empty[s]);
             }
         }
-        if (threadIdx.x == 64) tma_store_done();
+        if (leads) tma_store_done();
     }
     tc_before_sync();
     ok = __syncthreads_and(ok && !*abort_flag);
@@ -966,10 +969,14 @@ cudaError_t lora_tc_expand(const void *h, const void *W, const LoraCall &c, int 
         return cudaErrorInvalidValue;
     g.B = c.B;
     const int stage = kExTile + 4 * c.R * 128 + g.copies * c.R * 128;
-    g.stages = stages_for(stage, 0);
-    if (g.stages > kExStages) g.stages = kExStages;
+    // 2 or 4 stages, whichever gives an SM more of them in all: 8 up to rank 16, 6 up
+    // to 32, 4 up to 64, 2 beyond 104
+    int per_sm = 0;
+    for (int n = 2; n <= kExStages; n += 2) {
+        const int ctas = std::min(kExCtas, 228 * 1024 / (n * stage + kBarBytes + 2 * 1024));
+        if (n * ctas > g.stages * per_sm) g.stages = n, per_sm = ctas;
+    }
     const size_t smem = (size_t)g.stages * stage + kBarBytes + 1024;
-    const int per_sm = smem <= 113 * 1024 ? 2 : 1;
     const long long most = (long long)((C + kBlk - 1) / kBlk) * ((c.S + kM - 1) / kM) * c.B, room = (long long)per_sm * dev.sm_count;
     cudaError_t err = ensure_smem_attr((const void *)lora_expand_tc_kernel, smem, dev);
     if (err != cudaSuccess) return err;
