@@ -18,6 +18,7 @@ struct Eight<uint16_t> {
     uint4 v;
     __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ void load(const uint16_t *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void load_kept(const uint16_t *p) { v = ldg16(p); }
     __device__ __forceinline__ uint32_t max_bits() const { return ckpt8_max(v); }
     __device__ __forceinline__ void pairs(px2 (&x)[4]) const {
         x[0] = px_bf16(v.x), x[1] = px_bf16(v.y), x[2] = px_bf16(v.z), x[3] = px_bf16(v.w);
@@ -39,6 +40,10 @@ struct Eight<float> {
         a = __ldcs(reinterpret_cast<const float4 *>(p));
         b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
     }
+    __device__ __forceinline__ void load_kept(const float *p) {
+        a = __ldg(reinterpret_cast<const float4 *>(p));
+        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    }
     __device__ __forceinline__ uint32_t max_bits() const { return ckpt8_max(a, b); }
     __device__ __forceinline__ void pairs(px2 (&x)[4]) const {
         x[0] = px_make(a.x, a.y), x[1] = px_make(a.z, a.w), x[2] = px_make(b.x, b.y), x[3] = px_make(b.z, b.w);
@@ -52,30 +57,35 @@ struct Eight<float> {
 
 constexpr int kVecs = 4;  // vectors of 8 channels a lane has in flight
 
-// A warp takes 32 kVecs vectors of a row; V is rounded up to whole groups.
+// A warp takes 32 kVecs vectors (part blockIdx.y) of a row; the rows go by 8.  The
+// arithmetic is 30 to 60 instructions a vector: with a division for the place of a
+// task, and the halves' largest value by emulated 16-bit maxima, pack issued 154.
 template <typename T>
 __global__ void __launch_bounds__(256)
 ckpt8_pack_kernel(const T *__restrict__ x, unsigned char *__restrict__ ckpt, long long rows, int D) {
     const int lane = threadIdx.x & 31;
-    const int V = D >> 3, Vg = (V + 3) & ~3, parts = (Vg + 32 * kVecs - 1) / (32 * kVecs), P = ckpt8_row_bytes(D);
+    const int V = D >> 3, Vg = (V + 3) & ~3, P = ckpt8_row_bytes(D), code_bytes = ckpt8_code_bytes(D);
+    const int w0 = blockIdx.y * 32 * kVecs, v0 = w0 + lane;
     pdl_wait();
     pdl_trigger();
-    for (long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); task < rows * parts;
-         task += (long long)gridDim.x * 8) {
-        const long long row = task / parts;
-        const int v0 = (int)(task - row * parts) * 32 * kVecs + lane;
+    for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (long long)gridDim.x * 8) {
+        const T *src = x + row * D + v0 * 8;
+        unsigned char *rec = ckpt + row * P;
         Eight<T> e[kVecs];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
             e[j].zero();
-            if (v0 + 32 * j < V) e[j].load(x + row * D + (size_t)(v0 + 32 * j) * 8);
+            if (v0 + 32 * j < V) e[j].load(src + 256 * j);
         }
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            if (v0 - lane + 32 * j >= Vg) break;  // the whole warp
+            if (w0 + 32 * j >= Vg) break;  // the whole warp
             px2 p[4];
             e[j].pairs(p);
-            ckpt8_put(ckpt + row * P, D, V, v0 + 32 * j, e[j].max_bits(), p);
+            if (w0 + 32 * j + 32 < V)  // not the row's end
+                ckpt8_put<true>(rec, code_bytes, V, v0 + 32 * j, e[j].max_bits(), p);
+            else
+                ckpt8_put<false>(rec, code_bytes, V, v0 + 32 * j, e[j].max_bits(), p);
         }
     }
 }
@@ -84,116 +94,123 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 ckpt8_unpack_kernel(const unsigned char *__restrict__ ckpt, T *__restrict__ x, long long rows, int D) {
     const int lane = threadIdx.x & 31;
-    const int V = D >> 3, parts = (V + 32 * kVecs - 1) / (32 * kVecs), P = ckpt8_row_bytes(D);
-    const int at = ckpt8_code_bytes(D);
+    const int V = D >> 3, P = ckpt8_row_bytes(D);
+    const int v0 = blockIdx.y * 32 * kVecs + lane, at = ckpt8_code_bytes(D) + (v0 >> 2);
     pdl_wait();
     pdl_trigger();
-    for (long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); task < rows * parts;
-         task += (long long)gridDim.x * 8) {
-        const long long row = task / parts;
-        const int v0 = (int)(task - row * parts) * 32 * kVecs + lane;
+    for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (long long)gridDim.x * 8) {
         const unsigned char *rec = ckpt + row * P;
+        T *dst = x + row * D + v0 * 8;
         uint2 c[kVecs];
         uint32_t s[kVecs];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int v = v0 + 32 * j;
             c[j] = make_uint2(0u, 0u), s[j] = 1u;
-            if (v < V) c[j] = __ldcs(reinterpret_cast<const uint2 *>(rec + (size_t)v * 8)), s[j] = rec[at + (v >> 2)];
+            if (v0 + 32 * j < V) {
+                c[j] = __ldcs(reinterpret_cast<const uint2 *>(rec + v0 * 8) + 32 * j);
+                s[j] = rec[at + 8 * j];
+            }
         }
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int v = v0 + 32 * j;
-            if (v >= V) continue;
+            if (v0 + 32 * j >= V) continue;
             const px2 step = px_splat(ckpt8_step(s[j]));
             px2 p[4];
             ckpt8_floats(c[j].x, p[0], p[1]);
             ckpt8_floats(c[j].y, p[2], p[3]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) p[q] = px_mul(p[q], step);
-            Eight<T>::store(x + row * D + (size_t)v * 8, p);
+            Eight<T>::store(dst + 256 * j, p);
         }
     }
 }
 
-// A lane keeps the modulation of one vector of 8 channels in registers for a run
-// of a sample's rows.
-constexpr int kAgainRows = 16;  // rows a warp takes
-constexpr int kAgainFlight = 4; // of them in flight
+// A warp takes kAgainRows rows of 256 channels, all requested at once; a lane keeps the
+// modulation of its 8 channels in registers, and lane i brings row i's statistics.
+// (16 rows, 4 of them requested at once: 21 us for 8192 rows of 3072 channels; the
+// modulation read and formed again for each row: 28, bound by issue.)
+constexpr int kAgainRows = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(256)
 ckpt8_again_kernel(const unsigned char *__restrict__ ckpt, const T *__restrict__ emb, const float *__restrict__ mean,
                    const float *__restrict__ rstd, T *__restrict__ out, int S, int D) {
-    const int V = D >> 3, P = ckpt8_row_bytes(D), at = ckpt8_code_bytes(D);
-    const int v = blockIdx.x * 32 + (threadIdx.x & 31);
-    const int b = blockIdx.z;
+    const int lane = threadIdx.x & 31;
+    const int V = D >> 3, P = ckpt8_row_bytes(D);
+    const int v = blockIdx.x * 32 + lane, b = blockIdx.z;
     const int s0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kAgainRows;
     pdl_wait();
     pdl_trigger();
-    if (v >= V || s0 >= S) return;
+    if (s0 >= S) return;  // the whole warp
+    const int n = min(kAgainRows, S - s0);
+    const bool live = v < V;
+    const size_t row0 = (size_t)b * S + s0;
+    const unsigned char *rec = ckpt + row0 * P + v * 8, *scales = ckpt + row0 * P + ckpt8_code_bytes(D) + (v >> 2);
+    uint2 c[kAgainRows];
+    uint32_t s[kAgainRows];
+#pragma unroll
+    for (int i = 0; i < kAgainRows; ++i) {
+        c[i] = make_uint2(0u, 0u), s[i] = 1u;
+        if (live && i < n) {
+            c[i] = __ldcs(reinterpret_cast<const uint2 *>(rec + (size_t)i * P));
+            s[i] = scales[(size_t)i * P];
+        }
+    }
+    float mu = 0.0f, rs = 0.0f;
+    if (lane < n) mu = mean[row0 + lane], rs = rstd[row0 + lane];
     px2 onep[4], shift[4];
     {
-        Eight<T> e;
-        e.load(emb + (size_t)b * 2 * D + (size_t)v * 8);
+        Eight<T> e, f;
+        e.zero(), f.zero();
+        if (live) {
+            e.load_kept(emb + (size_t)b * 2 * D + (size_t)v * 8);
+            f.load_kept(emb + (size_t)b * 2 * D + D + (size_t)v * 8);
+        }
         e.pairs(onep);
+        f.pairs(shift);
 #pragma unroll
         for (int q = 0; q < 4; ++q) onep[q] = Eight<T>::one_plus(onep[q]);
-        e.load(emb + (size_t)b * 2 * D + D + (size_t)v * 8);
-        e.pairs(shift);
     }
-    const int n = min(kAgainRows, S - s0);
-    for (int i0 = 0; i0 < n; i0 += kAgainFlight) {
-        uint2 c[kAgainFlight];
-        uint32_t s[kAgainFlight];
-        float mu[kAgainFlight], rs[kAgainFlight];
+    T *o = out + row0 * D + (size_t)v * 8;
 #pragma unroll
-        for (int i = 0; i < kAgainFlight; ++i) {
-            c[i] = make_uint2(0u, 0u), s[i] = 1u, mu[i] = rs[i] = 0.0f;
-            if (i0 + i < n) {
-                const size_t row = (size_t)b * S + s0 + i0 + i;
-                const unsigned char *rec = ckpt + row * P;
-                c[i] = __ldcs(reinterpret_cast<const uint2 *>(rec + (size_t)v * 8));
-                s[i] = rec[at + (v >> 2)];
-                mu[i] = mean[row], rs[i] = rstd[row];
-            }
-        }
+    for (int i = 0; i < kAgainRows; ++i) {
+        const px2 nmu = px_splat(-__shfl_sync(0xFFFFFFFFu, mu, i)), r2 = px_splat(__shfl_sync(0xFFFFFFFFu, rs, i)),
+                  step = px_splat(ckpt8_step(s[i]));
+        if (!live || i >= n) continue;
+        px2 p[4];
+        ckpt8_floats(c[i].x, p[0], p[1]);
+        ckpt8_floats(c[i].y, p[2], p[3]);
 #pragma unroll
-        for (int i = 0; i < kAgainFlight; ++i) {
-            if (i0 + i >= n) break;
-            const px2 step = px_splat(ckpt8_step(s[i])), nmu = px_splat(-mu[i]), r2 = px_splat(rs[i]);
-            px2 p[4];
-            ckpt8_floats(c[i].x, p[0], p[1]);
-            ckpt8_floats(c[i].y, p[2], p[3]);
+        for (int q = 0; q < 4; ++q) {
             // the value is code * step exactly, so the fused form is fp32(value - mean)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const px2 xhat = px_mul(px_fma(p[q], step, nmu), r2);
-                // rounded before the shift is added: scalar products, since a packed one may be fused into the add
-                const px2 m = px_make(__fmul_rn(px_lo(xhat), px_lo(onep[q])), __fmul_rn(px_hi(xhat), px_hi(onep[q])));
-                p[q] = px_add(m, shift[q]);
-            }
-            Eight<T>::store(out + ((size_t)b * S + s0 + i0 + i) * D + (size_t)v * 8, p);
+            const px2 xhat = px_mul(px_fma(p[q], step, nmu), r2);
+            // rounded before the shift is added: scalar products, since a packed one may be fused into the add
+            const px2 y = px_make(__fmul_rn(px_lo(xhat), px_lo(onep[q])), __fmul_rn(px_hi(xhat), px_hi(onep[q])));
+            p[q] = px_add(y, shift[q]);
         }
+        Eight<T>::store(o + (size_t)i * D, p);
     }
 }
 
-unsigned grid_of(long long ctas) { return (unsigned)(ctas < (1 << 30) ? ctas : (1 << 30)); }
+// rows by 8, in turns where they are more than a grid has room for
+dim3 rows_grid(int64_t rows, int parts) {
+    const int64_t x = (rows + 7) / 8;
+    return dim3((unsigned)(x < (1 << 30) ? x : (1 << 30)), (unsigned)parts);
+}
 
 }  // namespace
 
 template <typename T>
 cudaError_t launch_ckpt8_pack(const T *x, uint8_t *ckpt, int64_t rows, int D, cudaStream_t stream) {
     const int Vg = (D / 8 + 3) & ~3, parts = (Vg + 32 * kVecs - 1) / (32 * kVecs);
-    return launch_pdl(ckpt8_pack_kernel<T>, dim3(grid_of((rows * parts + 7) / 8)), dim3(256), 0, stream, x, ckpt,
-                      (long long)rows, D);
+    return launch_pdl(ckpt8_pack_kernel<T>, rows_grid(rows, parts), dim3(256), 0, stream, x, ckpt, (long long)rows, D);
 }
 
 template <typename T>
 cudaError_t launch_ckpt8_unpack(const uint8_t *ckpt, T *x, int64_t rows, int D, cudaStream_t stream) {
     const int parts = (D / 8 + 32 * kVecs - 1) / (32 * kVecs);
-    return launch_pdl(ckpt8_unpack_kernel<T>, dim3(grid_of((rows * parts + 7) / 8)), dim3(256), 0, stream, ckpt, x,
-                      (long long)rows, D);
+    return launch_pdl(ckpt8_unpack_kernel<T>, rows_grid(rows, parts), dim3(256), 0, stream, ckpt, x, (long long)rows,
+                      D);
 }
 
 template <typename T>

@@ -37,6 +37,17 @@ __device__ __forceinline__ uint32_t ckpt8_codes(px2 lo, px2 hi, px2 inv) {
     return __byte_perm(p, q, 0x5410);
 }
 
+// Four codes of a group with that scale byte (not 255)
+__device__ __forceinline__ uint32_t ckpt8_clamped(px2 (&x)[2], uint32_t scale) {
+    if (scale == kCkptLastScale) {  // values from 127.5 2^121 on would round to 128: 127
+        const float most = 127.0f * 0x1p121f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            x[q] = px_make(fminf(fmaxf(px_lo(x[q]), -most), most), fminf(fmaxf(px_hi(x[q]), -most), most));
+    }
+    return ckpt8_codes(x[0], x[1], px_splat(ckpt8_inverse(scale)));
+}
+
 // Four codes as exact fp32 pairs: byte + 128 in the low bits of 2^23, less 2^23 + 128
 __device__ __forceinline__ void ckpt8_floats(uint32_t w, px2 &lo, px2 &hi) {
     const uint32_t u = w ^ 0x80808080u;
@@ -48,10 +59,16 @@ __device__ __forceinline__ void ckpt8_floats(uint32_t w, px2 &lo, px2 &hi) {
 }
 
 // the largest magnitude's bits among 8 channels, bf16 (as 16-bit halves) or fp32
+// (a NaN wins, in either)
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 __device__ __forceinline__ uint32_t ckpt8_max(const uint4 &v) {
     const uint32_t m = 0x7FFF7FFFu;
-    const uint32_t a = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
-    return max(a & 0xFFFFu, a >> 16) << 16;
+    const uint32_t a = bf16x2_max(bf16x2_max(v.x & m, v.y & m), bf16x2_max(v.z & m, v.w & m));
+    return max(a << 16, a & 0xFFFF0000u);
 }
 __device__ __forceinline__ uint32_t ckpt8_max(const float4 &a, const float4 &b) {
     const uint32_t m = 0x7FFFFFFFu;
@@ -65,31 +82,44 @@ __device__ __forceinline__ uint32_t ckpt8_max(const float4 &a, const float4 &b) 
 // Vector v (8 channels) of a record, by the lane that holds it; four neighbouring
 // lanes, the first with v a multiple of 4, hold a group (lanes past the row's V
 // vectors give zeros, max_bits 0).  All four run this.  Fills the record's
-// padding as well.
-__device__ __forceinline__ void ckpt8_put(unsigned char *rec, int D, int V, int v, uint32_t max_bits,
-                                          px2 (&x)[4]) {
+// padding as well; INSIDE: the row does not end in this group.
+template <bool INSIDE = false>
+__device__ __forceinline__ void ckpt8_put(unsigned char *rec, int code_bytes, int V, int v, uint32_t max_bits,
+                                          const px2 (&x)[4]) {
     max_bits = max(max_bits, __shfl_xor_sync(0xFFFFFFFFu, max_bits, 1));
     max_bits = max(max_bits, __shfl_xor_sync(0xFFFFFFFFu, max_bits, 2));
     const uint32_t scale = ckpt8_scale(max_bits);
-    const int code_bytes = ckpt8_code_bytes(D);
-    if (v * 8 < code_bytes) {
+    if (INSIDE || v * 8 < code_bytes) {
         uint2 c = make_uint2(0u, 0u);
-        if (v < V && scale != 255u) {
-            const px2 inv = px_splat(ckpt8_inverse(scale));
-            if (scale == kCkptLastScale) {  // values from 127.5 2^121 on would round to 128: 127
-                const float most = 127.0f * 0x1p121f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    x[q] = px_make(fminf(fmaxf(px_lo(x[q]), -most), most), fminf(fmaxf(px_hi(x[q]), -most), most));
-            }
-            c = make_uint2(ckpt8_codes(x[0], x[1], inv), ckpt8_codes(x[2], x[3], inv));
+        if ((INSIDE || v < V) && scale != 255u) {
+            px2 lo[2] = {x[0], x[1]}, hi[2] = {x[2], x[3]};
+            c = make_uint2(ckpt8_clamped(lo, scale), ckpt8_clamped(hi, scale));
         }
         *reinterpret_cast<uint2 *>(rec + (size_t)v * 8) = c;
     }
-    if ((v & 3) == 0 && v < V) {
+    if ((v & 3) == 0 && (INSIDE || v < V)) {
         rec[code_bytes + (v >> 2)] = (unsigned char)scale;
-        if (v + 4 >= V)
+        if (!INSIDE && v + 4 >= V)
             for (int i = (v >> 2) + 1; i & 15; ++i) rec[code_bytes + i] = 0;
+    }
+}
+
+// The same for a lane that holds 4 channels, vector v of D / 4; eight neighbouring
+// lanes, the first with v a multiple of 8, hold a group.
+__device__ __forceinline__ void ckpt8_put4(unsigned char *rec, int D, int v, const float4 &x) {
+    const int V = D >> 2, code_bytes = ckpt8_code_bytes(D);
+    uint32_t max_bits = ckpt8_max(x, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) max_bits = max(max_bits, __shfl_xor_sync(0xFFFFFFFFu, max_bits, d));
+    const uint32_t scale = ckpt8_scale(max_bits);
+    if (v * 4 < code_bytes) {
+        px2 p[2] = {px_make(x.x, x.y), px_make(x.z, x.w)};
+        *reinterpret_cast<uint32_t *>(rec + (size_t)v * 4) = v < V && scale != 255u ? ckpt8_clamped(p, scale) : 0u;
+    }
+    if ((v & 7) == 0 && v < V) {
+        rec[code_bytes + (v >> 3)] = (unsigned char)scale;
+        if (v + 8 >= V)
+            for (int i = (v >> 3) + 1; i & 15; ++i) rec[code_bytes + i] = 0;
     }
 }
 

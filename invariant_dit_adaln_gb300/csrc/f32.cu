@@ -12,8 +12,10 @@
 //   d_emb  = the 32-way token trees of fp32(g * xhat) and g
 //   d_temb = fp32(d_silu * silu'(t)),          d_silu = sum_n e W, e = d_emb
 //   dW     = fma over samples ascending,        db = sum over samples ascending
+#include "ckpt8.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "tune.h"
 
 namespace adaln {
 
@@ -111,13 +113,15 @@ f32_proj_fwd_kernel(const float *__restrict__ u, const float *__restrict__ W, co
 // accumulator (packed fp32x2 instructions, explicit rounding), the halves
 // added, then the xor butterfly; mean = sum / D, var = sum (x - mean)^2 / D,
 // rstd = 1 / sqrt(var + eps), each operation rounded once.
+// CKPT: a lane also writes the 8-bit record's part of its vectors.
 // --------------------------------------------------------------------------
 constexpr int kF32FwdVPL = kF32MaxD / 128;  // 32 vectors per lane at most
 
-template <int VPL>
+template <int VPL, bool CKPT>
 __global__ void __launch_bounds__(256, VPL <= 24 ? 2 : 1)
 f32_out_fwd_kernel(const float *__restrict__ x, const float *__restrict__ emb, float *__restrict__ out,
-                   float *__restrict__ mean, float *__restrict__ rstd, int S, int D, float eps, int rows_per_cta) {
+                   float *__restrict__ mean, float *__restrict__ rstd, int S, int D, float eps, int rows_per_cta,
+                   unsigned char *__restrict__ ckpt) {
     extern __shared__ __align__(16) float tab_f32[];  // onep [D], shift [D]
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -144,6 +148,12 @@ f32_out_fwd_kernel(const float *__restrict__ x, const float *__restrict__ emb, f
         for (int j = 0; j < VPL; ++j) {
             const int v = lane + 32 * j;
             xv[j] = v < V ? ldf4_hint(xr + (size_t)v * 4, pol) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        if (CKPT) {
+            unsigned char *rec = ckpt + row * ckpt8_row_bytes(D);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (32 * j < V) ckpt8_put4(rec, D, lane + 32 * j, xv[j]);  // the whole warp
         }
         // sums by column pair (packed), the halves added, then the butterfly
         px2 s1 = 0ull;
@@ -197,14 +207,26 @@ f32_out_fwd_kernel(const float *__restrict__ x, const float *__restrict__ emb, f
 // All arithmetic on column pairs in packed fp32x2 instructions with explicit
 // rounding (a float4 of a row is two pairs as loaded).  Two CTAs per SM hide
 // the loads' latency.
+//
+// CKPT: x comes as 8-bit records.  A thread copies its own part of the rows
+// kF32Ahead rows ahead, asynchronously, into places of shared memory that no other
+// thread reads, so the rows in flight take no registers and no barrier.
 // --------------------------------------------------------------------------
+constexpr int kF32Ahead = 4;
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+
 // EXACT: D / 4 == blockDim.x * VPT, every thread's vectors inside the row (no tests)
-template <int VPT, int MAXNT, bool EXACT>
+template <int VPT, int MAXNT, bool EXACT, bool CKPT>
 __global__ void __launch_bounds__(MAXNT, 2)
-f32_out_bwd_tile_kernel(const float *__restrict__ dy, const float *__restrict__ x, const float *__restrict__ emb,
+f32_out_bwd_tile_kernel(const float *__restrict__ dy, const void *__restrict__ x_rows, const float *__restrict__ emb,
                         const float *__restrict__ mean, const float *__restrict__ rstd, float *__restrict__ dx,
                         float *__restrict__ ws_sig, float *__restrict__ ws_kap, int S, int D, int T) {
     __shared__ float2 red[2][32];
+    extern __shared__ __align__(16) unsigned char ahead_f32[];  // CKPT: [kF32Ahead][VPT][NT] dy (16 B), then codes and scales (8 B)
+    const float *x = static_cast<const float *>(x_rows);
     const int tid = threadIdx.x;
     const int NT = blockDim.x;
     const int nw = NT >> 5;
@@ -237,23 +259,66 @@ f32_out_bwd_tile_kernel(const float *__restrict__ dy, const float *__restrict__ 
     const int n = min(kTile, S - s0);
     const float Df = (float)D;
     const uint64_t pol = l2_evict_first();
+    uint4 *ahead_g = reinterpret_cast<uint4 *>(ahead_f32) + tid;
+    uint2 *ahead_c = reinterpret_cast<uint2 *>(ahead_f32 + (size_t)kF32Ahead * VPT * NT * 16) + tid;
+    const int P = ckpt8_row_bytes(D), code_bytes = ckpt8_code_bytes(D);
+    auto copy_row = [&](int i) {  // CKPT: this thread's part of row i, one group of copies (none past the tile's end)
+        if (i < n) {
+            const size_t row = (size_t)b * S + s0 + i;
+            const unsigned char *rec = static_cast<const unsigned char *>(x_rows) + row * P;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = tid + NT * j, at = ((i % kF32Ahead) * VPT + j) * NT;
+                if (EXACT || v < V) {
+                    copy_ahead<16>(ahead_g + at, dy + row * D + (size_t)v * 4);
+                    copy_ahead<4>(&ahead_c[at].x, rec + (size_t)v * 4);
+                    copy_ahead<4>(&ahead_c[at].y, rec + code_bytes + (v >> 5) * 4);  // four groups' scales
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float mu_l = 0.0f, rs_l = 0.0f;  // CKPT: lane i holds row i's statistics
+    if constexpr (CKPT) {
+        if (lane < n) mu_l = mean[(size_t)b * S + s0 + lane], rs_l = rstd[(size_t)b * S + s0 + lane];
+        for (int i = 0; i < kF32Ahead - 1; ++i) copy_row(i);
+    }
     for (int i = 0; i < n; ++i) {
         const size_t row = (size_t)b * S + s0 + i;
         px2 xp[VPT][2], gp[VPT][2];
+        if constexpr (CKPT) {
+            copy_row(i + kF32Ahead - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kF32Ahead - 1) : "memory");
+        }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + NT * j;
-            uint4 xw = make_uint4(0u, 0u, 0u, 0u), gw = xw;
-            if (EXACT || v < V) {
-                xw = ldg16_hint(x + row * D + (size_t)v * 4, pol);
-                gw = ldg16_hint(dy + row * D + (size_t)v * 4, pol);
+            uint4 gw = make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (CKPT) {
+                xp[j][0] = xp[j][1] = 0ull;
+                if (EXACT || v < V) {
+                    const int at = ((i % kF32Ahead) * VPT + j) * NT;
+                    gw = ahead_g[at];
+                    const uint2 c = ahead_c[at];
+                    const px2 step = px_splat(ckpt8_step((c.y >> ((v >> 3) & 3) * 8) & 0xFFu));
+                    ckpt8_floats(c.x, xp[j][0], xp[j][1]);
+                    xp[j][0] = px_mul(xp[j][0], step);
+                    xp[j][1] = px_mul(xp[j][1], step);
+                }
+            } else {
+                uint4 xw = make_uint4(0u, 0u, 0u, 0u);
+                if (EXACT || v < V) {
+                    xw = ldg16_hint(x + row * D + (size_t)v * 4, pol);
+                    gw = ldg16_hint(dy + row * D + (size_t)v * 4, pol);
+                }
+                xp[j][0] = px_make(__uint_as_float(xw.x), __uint_as_float(xw.y));
+                xp[j][1] = px_make(__uint_as_float(xw.z), __uint_as_float(xw.w));
             }
-            xp[j][0] = px_make(__uint_as_float(xw.x), __uint_as_float(xw.y));
-            xp[j][1] = px_make(__uint_as_float(xw.z), __uint_as_float(xw.w));
             gp[j][0] = px_make(__uint_as_float(gw.x), __uint_as_float(gw.y));
             gp[j][1] = px_make(__uint_as_float(gw.z), __uint_as_float(gw.w));
         }
-        const float mu = mean[row], rs = rstd[row];
+        const float mu = CKPT ? __shfl_sync(0xFFFFFFFFu, mu_l, i) : mean[row];
+        const float rs = CKPT ? __shfl_sync(0xFFFFFFFFu, rs_l, i) : rstd[row];
         const px2 mu2 = px_splat(mu), rs2 = px_splat(rs);
         // phase 1: x_hat, the tree products and this thread's row sums (column
         // pairs in packed fused multiply-adds, the halves added at the end)
@@ -466,8 +531,10 @@ cudaError_t launch_f32_proj_fwd(const float *temb, const float *W, const float *
                       emb, B, D);
 }
 
-cudaError_t launch_f32_out_fwd(const float *x, const float *emb, float *out, float *mean, float *rstd, int B, int S,
-                               int D, float eps, cudaStream_t stream, const DeviceInfo &dev) {
+template <bool CKPT>
+static cudaError_t launch_f32_out_fwd_rows(const float *x, const float *emb, float *out, float *mean, float *rstd,
+                                           uint8_t *ckpt, int B, int S, int D, float eps, cudaStream_t stream,
+                                           const DeviceInfo &dev) {
     const size_t smem = (size_t)2 * D * 4;
     // about four CTAs of 8 warps per SM over the batch
     int cps = (dev.sm_count * 4 + B - 1) / B;
@@ -475,21 +542,28 @@ cudaError_t launch_f32_out_fwd(const float *x, const float *emb, float *out, flo
     if (cps < 1) cps = 1;
     const int rows = (S + cps - 1) / cps;
     const dim3 grid((unsigned)((S + rows - 1) / rows), (unsigned)B);
-    if (D / 4 <= 32 * 24) {  // D <= 3072: 24 vectors per lane, two CTAs per SM
-        cudaError_t err = ensure_smem_attr((const void *)f32_out_fwd_kernel<24>, smem, dev);
-        if (err != cudaSuccess) return err;
-        return launch_pdl(f32_out_fwd_kernel<24>, grid, dim3(256), smem, stream, x, emb, out, mean, rstd, S, D, eps,
-                          rows);
-    }
-    auto kern = f32_out_fwd_kernel<kF32FwdVPL>;
+    // D <= 3072: 24 vectors per lane, two CTAs per SM
+    auto kern = D / 4 <= 32 * 24 ? f32_out_fwd_kernel<24, CKPT> : f32_out_fwd_kernel<kF32FwdVPL, CKPT>;
     cudaError_t err = ensure_smem_attr((const void *)kern, smem, dev);
     if (err != cudaSuccess) return err;
-    return launch_pdl(kern, grid, dim3(256), smem, stream, x, emb, out, mean, rstd, S, D, eps, rows);
+    return launch_pdl(kern, grid, dim3(256), smem, stream, x, emb, out, mean, rstd, S, D, eps, rows, ckpt);
 }
 
-cudaError_t launch_f32_out_bwd(const float *dy, const float *x, const float *emb, const float *mean,
-                               const float *rstd, float *dx, float *d_emb, void *ws, int B, int S, int D,
-                               cudaStream_t stream, const DeviceInfo &dev) {
+cudaError_t launch_f32_out_fwd(const float *x, const float *emb, float *out, float *mean, float *rstd, int B, int S,
+                               int D, float eps, cudaStream_t stream, const DeviceInfo &dev) {
+    return launch_f32_out_fwd_rows<false>(x, emb, out, mean, rstd, nullptr, B, S, D, eps, stream, dev);
+}
+
+cudaError_t launch_f32_out_fwd_ckpt8(const float *x, const float *emb, float *out, float *mean, float *rstd,
+                                     uint8_t *ckpt, int B, int S, int D, float eps, cudaStream_t stream,
+                                     const DeviceInfo &dev) {
+    return launch_f32_out_fwd_rows<true>(x, emb, out, mean, rstd, ckpt, B, S, D, eps, stream, dev);
+}
+
+template <bool CKPT>
+static cudaError_t launch_f32_out_bwd_rows(const float *dy, const void *x, const float *emb, const float *mean,
+                                           const float *rstd, float *dx, float *d_emb, void *ws, int B, int S, int D,
+                                           cudaStream_t stream, const DeviceInfo &dev) {
     if (S == 0) return launch_zero(d_emb, (size_t)B * 2 * D, stream);
     const int T = (S + kTile - 1) / kTile;
     const int H = 2 * D;
@@ -498,21 +572,31 @@ cudaError_t launch_f32_out_bwd(const float *dy, const float *x, const float *emb
     // two CTAs per SM: three vectors (12 columns: more independent TwoSum
     // chains per thread) per thread up to D = 3072 (at most 256 threads), four
     // up to D = 4096 (at most 256)
-    const int V = D / 4;
-    cudaError_t err;
-    if (V <= 768) {
-        const int nt = ((V + 2) / 3 + 31) / 32 * 32;
-        auto kern = nt * 3 == V ? f32_out_bwd_tile_kernel<3, 256, true> : f32_out_bwd_tile_kernel<3, 256, false>;
-        err = launch_pdl(kern, dim3((unsigned)T, (unsigned)B), dim3(nt), 0, stream, dy, x, emb, mean, rstd, dx, sig,
-                         kap, S, D, T);
-    } else {
-        const int nt = ((V + 3) / 4 + 31) / 32 * 32;
-        auto kern = f32_out_bwd_tile_kernel<4, 256, false>;  // the exact form spills at 128 registers
-        err = launch_pdl(kern, dim3((unsigned)T, (unsigned)B), dim3(nt), 0, stream, dy, x, emb, mean, rstd, dx, sig,
-                         kap, S, D, T);
-    }
+    const int V = D / 4, vpt = V <= 768 ? 3 : 4;
+    const int nt = ((V + vpt - 1) / vpt + 31) / 32 * 32;
+    // the exact form of four spills at 128 registers
+    auto kern = vpt == 4      ? f32_out_bwd_tile_kernel<4, 256, false, CKPT>
+                : nt * 3 == V ? f32_out_bwd_tile_kernel<3, 256, true, CKPT>
+                              : f32_out_bwd_tile_kernel<3, 256, false, CKPT>;
+    const size_t smem = CKPT ? (size_t)kF32Ahead * vpt * nt * 24 : 0;
+    cudaError_t err = ensure_smem_attr((const void *)kern, smem, dev);
+    if (err != cudaSuccess) return err;
+    err = launch_pdl(kern, dim3((unsigned)T, (unsigned)B), dim3(nt), smem, stream, dy, x, emb, mean, rstd, dx, sig, kap,
+                     S, D, T);
     if (err != cudaSuccess) return err;
     return launch_fold(sig, kap, d_emb, B, T, H, stream, dev);
+}
+
+cudaError_t launch_f32_out_bwd(const float *dy, const float *x, const float *emb, const float *mean,
+                               const float *rstd, float *dx, float *d_emb, void *ws, int B, int S, int D,
+                               cudaStream_t stream, const DeviceInfo &dev) {
+    return launch_f32_out_bwd_rows<false>(dy, x, emb, mean, rstd, dx, d_emb, ws, B, S, D, stream, dev);
+}
+
+cudaError_t launch_f32_out_bwd_ckpt8(const float *dy, const uint8_t *ckpt, const float *emb, const float *mean,
+                                     const float *rstd, float *dx, float *d_emb, void *ws, int B, int S, int D,
+                                     cudaStream_t stream, const DeviceInfo &dev) {
+    return launch_f32_out_bwd_rows<true>(dy, ckpt, emb, mean, rstd, dx, d_emb, ws, B, S, D, stream, dev);
 }
 
 size_t f32_proj_bwd_ws_bytes(int B, int D) {

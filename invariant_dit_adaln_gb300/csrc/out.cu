@@ -12,8 +12,10 @@
 //   mean, rstd       [B, S]    fp32
 //   d_emb            [B, 2D]   fp32     [d_scale | d_shift]
 //   tree partials    sigma [B, T, H] fp32 then kappa [B, T, H] fp32, T = ceil(S/32)
+#include "ckpt8.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "tune.h"
 
 namespace adaln {
 
@@ -293,14 +295,17 @@ out_fwd_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ emb,
 // and a lane forms r = bf16(residual + bf16(gate * x)) (eager bf16: each
 // operation's fp32 result rounded once) for its vectors as it takes them from
 // the stage, stores r, and normalises and modulates r as above.
+//
+// CKPT (the norm with its input kept in 8 bits): a lane also writes the record's
+// part of its vectors, four neighbouring lanes holding a group of 32 channels.
 // ==========================================================================
 // EXACT: V == 32 * VPL, every lane's vectors lie inside the row (no tests)
-template <int VPL, int MAXW, bool RES, bool EXACT>
+template <int VPL, int MAXW, bool RES, bool EXACT, bool CKPT>
 __global__ void __launch_bounds__(MAXW * 32, 1)
 out_fwd_row_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ emb, uint16_t *__restrict__ out,
                    float *__restrict__ mean, float *__restrict__ rstd, int S, int D, float eps, int cps, int NS,
                    int keep_out, const uint16_t *__restrict__ residual, const uint16_t *__restrict__ gate,
-                   uint16_t *__restrict__ r_out) {
+                   uint16_t *__restrict__ r_out, unsigned char *__restrict__ ckpt) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -433,6 +438,16 @@ out_fwd_row_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ 
                 if (EXACT || v < V) stg16_hint(rrow + (size_t)v * 8, xr[j], pol_r);
             }
         }
+        if (CKPT) {
+            unsigned char *rec = ckpt + r * ckpt8_row_bytes(D);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (EXACT || 32 * j < V) {  // the whole warp
+                    const px2 p[4] = {px_bf16(xr[j].x), px_bf16(xr[j].y), px_bf16(xr[j].z), px_bf16(xr[j].w)};
+                    // not the form without the row's end, which spills at 128 registers
+                    ckpt8_put(rec, ckpt8_code_bytes(D), V, lane + 32 * j, ckpt8_max(xr[j]), p);
+                }
+        }
         // mean (zero vectors past the row end add +0 and change nothing)
         float2 s1[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
@@ -495,11 +510,12 @@ out_fwd_row_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ 
     }
 }
 
-template <int VPL, int MAXW, bool RES = false>
+template <int VPL, int MAXW, bool RES = false, bool CKPT = false>
 static cudaError_t launch_out_fwd_row(const uint16_t *x, const uint16_t *emb, uint16_t *out, float *mean,
                                       float *rstd, int B, int S, int D, float eps, cudaStream_t stream,
                                       const DeviceInfo &dev, bool keep_out, const uint16_t *residual = nullptr,
-                                      const uint16_t *gate = nullptr, uint16_t *r_out = nullptr) {
+                                      const uint16_t *gate = nullptr, uint16_t *r_out = nullptr,
+                                      unsigned char *ckpt = nullptr) {
     constexpr size_t kSmemMax = 227 * 1024;
     const size_t stage = (size_t)D * 2 * (RES ? 2 : 1);
     auto smem_of = [&](int warps, int ns) { return 1024 + (size_t)D * (RES ? 10 : 8) + (size_t)warps * ns * stage; };
@@ -516,7 +532,8 @@ static cudaError_t launch_out_fwd_row(const uint16_t *x, const uint16_t *emb, ui
         if (smem_of(warps, ns) > kSmemMax) warps = 8;
     }
     const size_t smem = smem_of(warps, ns);
-    auto kern = D / 8 == 32 * VPL ? out_fwd_row_kernel<VPL, MAXW, RES, true> : out_fwd_row_kernel<VPL, MAXW, RES, false>;
+    auto kern = D / 8 == 32 * VPL ? out_fwd_row_kernel<VPL, MAXW, RES, true, CKPT>
+                                  : out_fwd_row_kernel<VPL, MAXW, RES, false, CKPT>;
     cudaError_t err = ensure_smem_attr((const void *)kern, smem, dev);
     if (err != cudaSuccess) return err;
     // about one CTA per SM in all; every CTA within one sample
@@ -525,7 +542,7 @@ static cudaError_t launch_out_fwd_row(const uint16_t *x, const uint16_t *emb, ui
     if (cps < 1) cps = 1;
     const long long grid = (long long)B * cps;
     return launch_pdl(kern, dim3((unsigned)grid), dim3(warps * 32), smem, stream, x, emb, out, mean, rstd, S, D, eps,
-                      cps, ns, keep_out ? 1 : 0, residual, gate, r_out);
+                      cps, ns, keep_out ? 1 : 0, residual, gate, r_out, ckpt);
 }
 
 template <int VPT, int BLK, int NST, int MINB>
@@ -591,6 +608,25 @@ cudaError_t launch_out_fwd_res(const uint16_t *x, const uint16_t *residual, cons
                                            r);
 }
 
+// The forward with the 8-bit records of x, in one pass where the row fits a warp's
+// registers (rows of up to 8 KB); longer rows take a second kernel, which finds x
+// in L2 as far as it fits.
+cudaError_t launch_out_fwd_ckpt8(const uint16_t *x, const uint16_t *emb, uint16_t *out, float *mean, float *rstd,
+                                 uint8_t *ckpt, int B, int S, int D, float eps, cudaStream_t stream,
+                                 const DeviceInfo &dev) {
+    const int V = D / 8;
+    auto go = [&](auto launch) {
+        return launch(x, emb, out, mean, rstd, B, S, D, eps, stream, dev, false, nullptr, nullptr, nullptr, ckpt);
+    };
+    if (V <= 128) return go(launch_out_fwd_row<4, 16, false, true>);
+    if (V <= 256) return go(launch_out_fwd_row<8, 16, false, true>);
+    if (V <= 384) return go(launch_out_fwd_row<12, 16, false, true>);
+    if (V <= 512) return go(launch_out_fwd_row<16, 8, false, true>);
+    const cudaError_t err = launch_out_fwd(x, emb, out, mean, rstd, B, S, D, eps, stream, dev);
+    if (err != cudaSuccess) return err;
+    return launch_ckpt8_pack<uint16_t>(x, ckpt, (int64_t)B * S, D, stream);
+}
+
 // ==========================================================================
 // Backward, kernel 1: one CTA per (sample b, 32-token tile t).
 //
@@ -613,6 +649,12 @@ cudaError_t launch_out_fwd_res(const uint16_t *x, const uint16_t *residual, cons
 // after one multiply.  The reduction order over d depends on D only.  A block's
 // stages are refilled by the last warp to finish its phase 2 (a counter per
 // block of stages), while the other warps go on.
+//
+// CKPT: x comes as 8-bit records (a stage holds a record and a dy row).  A value is
+// code * 2^k exactly, so x - mean is one fused multiply-add with the same bits.  (One
+// tree a thread, in two groups of warps that share the rows, twice the warps on an SM:
+// 60 instead of 43 us at B=2, S=4096, D=3072; what is shared is unpacked twice, 31
+// instead of 20 million instructions.)
 // ==========================================================================
 constexpr int kRowBlock = 4;        // most rows per block
 constexpr int kBwdMaxStages = 8;
@@ -657,9 +699,9 @@ __device__ __forceinline__ float warp_transposed_sum(const float (&in)[NV], int 
     return a[0];
 }
 
-template <int VPT, int MAXNT, int MINB, int RB, int NST, bool EXACT>
+template <int VPT, int MAXNT, int MINB, int RB, int NST, bool EXACT, bool CKPT>
 __global__ void __launch_bounds__(MAXNT, MINB)
-out_bwd_tile_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict__ x,
+out_bwd_tile_kernel(const uint16_t *__restrict__ dy, const void *__restrict__ x_rows,
                     const uint16_t *__restrict__ emb, const float *__restrict__ mean,
                     const float *__restrict__ rstd, uint16_t *__restrict__ dx, float *__restrict__ ws_sig,
                     float *__restrict__ ws_kap, int S, int D, int T, int keep_dx) {
@@ -670,7 +712,9 @@ out_bwd_tile_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict_
     volatile int *abort_flag = &sm.abort;
     unsigned char *stages = smem_raw + ((sizeof(BwdSmem) + 127) / 128) * 128;
     const int row_bytes = D * 2;
-    const int stage_bytes = 2 * row_bytes;  // x row, then dy row
+    const int x_bytes = CKPT ? ckpt8_row_bytes(D) : row_bytes;  // of an x row or its record
+    const int stage_bytes = x_bytes + row_bytes;                // x, then dy row
+    const unsigned char *x = static_cast<const unsigned char *>(x_rows);
 
     const int tile = blockIdx.x;
     const int b = blockIdx.y;
@@ -722,8 +766,8 @@ out_bwd_tile_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict_
         for (int i = 0; i < NST && i < n; ++i) {
             unsigned char *dst = stages + (size_t)i * stage_bytes;
             mbar_arrive_expect_tx(&sm.full[i], stage_bytes);
-            bulk_g2s(dst, x + (row0 + i) * D, row_bytes, &sm.full[i]);
-            bulk_g2s_hint(dst + row_bytes, dy + (row0 + i) * D, row_bytes, &sm.full[i], pol_stream);
+            bulk_g2s(dst, x + (row0 + i) * x_bytes, x_bytes, &sm.full[i]);
+            bulk_g2s_hint(dst + x_bytes, dy + (row0 + i) * D, row_bytes, &sm.full[i], pol_stream);
             sm.last[i] = i;
         }
     }
@@ -755,26 +799,36 @@ out_bwd_tile_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict_
         for (int q = 0; q < 4; ++q) sg_s[j][q] = kp_s[j][q] = sg_h[j][q] = kp_h[j][q] = 0ull;
     const float invD = __frcp_rn((float)D);  // c1, c2 only feed dx (tolerance-checked)
 
+    // CKPT: the 8 codes of vector v of a staged record, and the scale byte of their group
+    const int code_bytes = ckpt8_code_bytes(D);
+    auto load_codes = [&](const unsigned char *rec, int v) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(rec + (size_t)v * 8);
+        return make_uint4(w.x, w.y, rec[code_bytes + (v >> 2)], 0u);
+    };
+
     // phase 1 of one row, its sums into rsum[2 jr], rsum[2 jr + 1]; EXACT: every
     // thread's vectors lie inside the row (no bounds test, so the tree state
     // stays in the same registers on every path)
     auto phase1_row = [&](int i, int jr, float (&rsum)[2 * RB]) {
         const unsigned char *xs = stages + (size_t)(i % NST) * stage_bytes;
-        const unsigned char *gs = xs + row_bytes;
-        const px2 mu2 = px_splat(sm.mu[i]), rs2 = px_splat(sm.rs[i]);
+        const unsigned char *gs = xs + x_bytes;
+        const px2 mu2 = px_splat(sm.mu[i]), rs2 = px_splat(sm.rs[i]), nmu2 = px_splat(-sm.mu[i]);
         px2 a1 = 0ull, a2 = 0ull;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + NT * j;
             if (EXACT || v < V) {
-                const uint4 xw = *reinterpret_cast<const uint4 *>(xs + (size_t)v * 16);
+                const uint4 xw = CKPT ? load_codes(xs, v) : *reinterpret_cast<const uint4 *>(xs + (size_t)v * 16);
                 const uint4 gw = *reinterpret_cast<const uint4 *>(gs + (size_t)v * 16);
                 const uint32_t xa[4] = {xw.x, xw.y, xw.z, xw.w};
                 const uint32_t ga[4] = {gw.x, gw.y, gw.z, gw.w};
+                px2 c[4];
+                if (CKPT) ckpt8_floats(xa[0], c[0], c[1]), ckpt8_floats(xa[1], c[2], c[3]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const px2 g2 = px_bf16(ga[q]);
-                    const px2 xh = px_mul(px_sub(px_bf16(xa[q]), mu2), rs2);  // x_hat
+                    const px2 xc = CKPT ? px_fma(c[q], px_splat(ckpt8_step(xa[2])), nmu2) : px_sub(px_bf16(xa[q]), mu2);
+                    const px2 xh = px_mul(xc, rs2);  // x_hat
                     const px2 p = px_mul(g2, xh);  // rounded before it enters the tree
                     a1 = px_fma(g2, onep[j][q], a1);
                     a2 = px_fma(p, onep[j][q], a2);
@@ -790,22 +844,25 @@ out_bwd_tile_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict_
     // k3 = mean k2 - rstd c1
     auto phase2_row = [&](int i, float k2, float k3) {
         const unsigned char *xs = stages + (size_t)(i % NST) * stage_bytes;
-        const unsigned char *gs = xs + row_bytes;
+        const unsigned char *gs = xs + x_bytes;
         const px2 rs2 = px_splat(sm.rs[i]), nk2 = px_splat(-k2), k3v = px_splat(k3);
         uint16_t *drow = dx + (row0 + i) * D;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + NT * j;
             if (EXACT || v < V) {
-                const uint4 xw = *reinterpret_cast<const uint4 *>(xs + (size_t)v * 16);
+                const uint4 xw = CKPT ? load_codes(xs, v) : *reinterpret_cast<const uint4 *>(xs + (size_t)v * 16);
                 const uint4 gw = *reinterpret_cast<const uint4 *>(gs + (size_t)v * 16);
                 const uint32_t xa[4] = {xw.x, xw.y, xw.z, xw.w};
                 const uint32_t ga[4] = {gw.x, gw.y, gw.z, gw.w};
                 uint32_t o[4];
+                px2 c[4];
+                if (CKPT) ckpt8_floats(xa[0], c[0], c[1]), ckpt8_floats(xa[1], c[2], c[3]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const px2 gh = px_mul(px_bf16(ga[q]), onep[j][q]);
-                    const px2 t = px_fma(px_bf16(xa[q]), nk2, k3v);
+                    const px2 xv = CKPT ? px_mul(c[q], px_splat(ckpt8_step(xa[2]))) : px_bf16(xa[q]);
+                    const px2 t = px_fma(xv, nk2, k3v);
                     o[q] = px_to_bf16x2(px_fma(gh, rs2, t));
                 }
                 stg16_hint(drow + (size_t)v * 8, make_uint4(o[0], o[1], o[2], o[3]), pol_dx);
@@ -898,8 +955,8 @@ out_bwd_tile_kernel(const uint16_t *__restrict__ dy, const uint16_t *__restrict_
                     if (i + NST < n) {
                         unsigned char *dst = stages + (size_t)st * stage_bytes;
                         mbar_arrive_expect_tx(&sm.full[st], stage_bytes);
-                        bulk_g2s(dst, x + (row0 + i + NST) * D, row_bytes, &sm.full[st]);
-                        bulk_g2s_hint(dst + row_bytes, dy + (row0 + i + NST) * D, row_bytes, &sm.full[st],
+                        bulk_g2s(dst, x + (row0 + i + NST) * x_bytes, x_bytes, &sm.full[st]);
+                        bulk_g2s_hint(dst + x_bytes, dy + (row0 + i + NST) * D, row_bytes, &sm.full[st],
                                       pol_stream);
                         sm.last[st] = i + NST;
                     }
@@ -1137,16 +1194,17 @@ cudaError_t launch_zero(float *p, size_t n, cudaStream_t stream) {
     return launch_pdl(zero_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, p, n);
 }
 
-template <int VPT, int MAXNT, int MINB, int RB, int NST>
-static cudaError_t launch_out_bwd_t(const uint16_t *dy, const uint16_t *x, const uint16_t *emb, const float *mean,
+template <int VPT, int MAXNT, int MINB, int RB, int NST, bool CKPT>
+static cudaError_t launch_out_bwd_t(const uint16_t *dy, const void *x, const uint16_t *emb, const float *mean,
                                     const float *rstd, uint16_t *dx, float *sig, float *kap, int B, int S, int D,
                                     int T, cudaStream_t stream, const DeviceInfo &dev, bool keep_dx) {
     const int V = D / 8;
     const int nt = ((V + VPT - 1) / VPT + 31) / 32 * 32;
-    const size_t smem = ((sizeof(BwdSmem) + 127) / 128) * 128 + (size_t)NST * 4 * D;
+    const size_t smem =
+        ((sizeof(BwdSmem) + 127) / 128) * 128 + (size_t)NST * (2 * D + (CKPT ? ckpt8_row_bytes(D) : 2 * D));
     // every thread's vectors inside the row: the form without bounds tests
-    auto kern = nt * VPT == V ? out_bwd_tile_kernel<VPT, MAXNT, MINB, RB, NST, true>
-                              : out_bwd_tile_kernel<VPT, MAXNT, MINB, RB, NST, false>;
+    auto kern = nt * VPT == V ? out_bwd_tile_kernel<VPT, MAXNT, MINB, RB, NST, true, CKPT>
+                              : out_bwd_tile_kernel<VPT, MAXNT, MINB, RB, NST, false, CKPT>;
     cudaError_t err = ensure_smem_attr((const void *)kern, smem, dev);
     if (err != cudaSuccess) return err;
     return launch_pdl(kern, dim3(T, B), dim3(nt), smem, stream, dy, x, emb, mean, rstd, dx, sig, kap,
@@ -1157,24 +1215,36 @@ static cudaError_t launch_out_bwd_t(const uint16_t *dy, const uint16_t *x, const
 // threads per SM, blocks of 4 rows, 8 stages; up to 16 KB: one CTA of <= 256
 // threads per SM, the same ring; longer rows: 32 columns per thread, blocks of
 // 2 rows and 4 stages (at most 128 KB).
-cudaError_t launch_out_bwd(const uint16_t *dy, const uint16_t *x, const uint16_t *emb, const float *mean,
-                           const float *rstd, uint16_t *dx, float *d_emb, void *ws, int B, int S, int D,
-                           cudaStream_t stream, const DeviceInfo &dev, bool keep_dx) {
+template <bool CKPT>
+static cudaError_t launch_out_bwd_rows(const uint16_t *dy, const void *x, const uint16_t *emb, const float *mean,
+                                       const float *rstd, uint16_t *dx, float *d_emb, void *ws, int B, int S, int D,
+                                       cudaStream_t stream, const DeviceInfo &dev, bool keep_dx) {
     if (S == 0) return launch_zero(d_emb, (size_t)B * 2 * D, stream);
     const int T = (S + kTile - 1) / kTile;
     const int H = 2 * D;
     float *sig = static_cast<float *>(ws);
     float *kap = sig + (size_t)B * T * H;
     const int V = D / 8;
-    cudaError_t err;
-    if (V <= 384)
-        err = launch_out_bwd_t<2, 192, 2, 4, 8>(dy, x, emb, mean, rstd, dx, sig, kap, B, S, D, T, stream, dev, keep_dx);
-    else if (V <= 512)
-        err = launch_out_bwd_t<2, 256, 1, 4, 8>(dy, x, emb, mean, rstd, dx, sig, kap, B, S, D, T, stream, dev, keep_dx);
-    else
-        err = launch_out_bwd_t<4, 256, 1, 2, 4>(dy, x, emb, mean, rstd, dx, sig, kap, B, S, D, T, stream, dev, keep_dx);
+    auto go = [&](auto launch) {
+        return launch(dy, x, emb, mean, rstd, dx, sig, kap, B, S, D, T, stream, dev, keep_dx);
+    };
+    const cudaError_t err = V <= 384   ? go(launch_out_bwd_t<2, 192, 2, 4, 8, CKPT>)
+                            : V <= 512 ? go(launch_out_bwd_t<2, 256, 1, 4, 8, CKPT>)
+                                       : go(launch_out_bwd_t<4, 256, 1, 2, 4, CKPT>);
     if (err != cudaSuccess) return err;
     return launch_fold(sig, kap, d_emb, B, T, H, stream, dev);
+}
+
+cudaError_t launch_out_bwd(const uint16_t *dy, const uint16_t *x, const uint16_t *emb, const float *mean,
+                           const float *rstd, uint16_t *dx, float *d_emb, void *ws, int B, int S, int D,
+                           cudaStream_t stream, const DeviceInfo &dev, bool keep_dx) {
+    return launch_out_bwd_rows<false>(dy, x, emb, mean, rstd, dx, d_emb, ws, B, S, D, stream, dev, keep_dx);
+}
+
+cudaError_t launch_out_bwd_ckpt8(const uint16_t *dy, const uint8_t *ckpt, const uint16_t *emb, const float *mean,
+                                 const float *rstd, uint16_t *dx, float *d_emb, void *ws, int B, int S, int D,
+                                 cudaStream_t stream, const DeviceInfo &dev) {
+    return launch_out_bwd_rows<true>(dy, ckpt, emb, mean, rstd, dx, d_emb, ws, B, S, D, stream, dev, false);
 }
 
 cudaError_t launch_token_tree(const float *in, float *out, void *ws, int B, int S, int H, cudaStream_t stream,

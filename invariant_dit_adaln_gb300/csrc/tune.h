@@ -20,6 +20,20 @@ template <typename T>
 cudaError_t launch_ckpt8_again(const uint8_t *ckpt, const T *emb, const float *mean, const float *rstd, T *out, int B,
                                int S, int D, cudaStream_t stream);
 
+// out.cu, f32.cu: the modulated norm with records of its input
+cudaError_t launch_out_fwd_ckpt8(const uint16_t *x, const uint16_t *emb, uint16_t *out, float *mean, float *rstd,
+                                 uint8_t *ckpt, int B, int S, int D, float eps, cudaStream_t stream,
+                                 const DeviceInfo &dev);
+cudaError_t launch_out_bwd_ckpt8(const uint16_t *dy, const uint8_t *ckpt, const uint16_t *emb, const float *mean,
+                                 const float *rstd, uint16_t *dx, float *d_emb, void *ws, int B, int S, int D,
+                                 cudaStream_t stream, const DeviceInfo &dev);
+cudaError_t launch_f32_out_fwd_ckpt8(const float *x, const float *emb, float *out, float *mean, float *rstd,
+                                     uint8_t *ckpt, int B, int S, int D, float eps, cudaStream_t stream,
+                                     const DeviceInfo &dev);
+cudaError_t launch_f32_out_bwd_ckpt8(const float *dy, const uint8_t *ckpt, const float *emb, const float *mean,
+                                     const float *rstd, float *dx, float *d_emb, void *ws, int B, int S, int D,
+                                     cudaStream_t stream, const DeviceInfo &dev);
+
 // lora.cu ---------------------------------------------------------------------
 constexpr int kLoraMaxRank = 128;
 

@@ -74,13 +74,10 @@ adaln_status fwd_ckpt8(const T *x, const T *emb, T *out, float *mean, float *rst
     ADALN_ON_DEVICE(dev)
     if (rows == 0) return ADALN_OK;
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e;
     if constexpr (sizeof(T) == 2)
-        e = launch_out_fwd(x, emb, out, mean, rstd, B, S, D, eps, s, dev);
+        return from_cuda(launch_out_fwd_ckpt8(x, emb, out, mean, rstd, ckpt, B, S, D, eps, s, dev));
     else
-        e = launch_f32_out_fwd(x, emb, out, mean, rstd, B, S, D, eps, s, dev);
-    if (e == cudaSuccess) e = launch_ckpt8_pack<T>(x, ckpt, (int64_t)rows, D, s);
-    return from_cuda(e);
+        return from_cuda(launch_f32_out_fwd_ckpt8(x, emb, out, mean, rstd, ckpt, B, S, D, eps, s, dev));
 }
 
 template <typename T>
@@ -100,14 +97,10 @@ adaln_status bwd_ckpt8(const T *dy, const uint8_t *ckpt, const T *emb, const flo
     ADALN_ON_DEVICE(dev)
     if (B == 0) return ADALN_OK;
     cudaStream_t s = (cudaStream_t)stream;
-    T *x = reinterpret_cast<T *>(static_cast<char *>(workspace) + adaln_out_bwd_workspace_bytes(B, S, D));
-    cudaError_t e = rows ? launch_ckpt8_unpack<T>(ckpt, x, (int64_t)rows, D, s) : cudaSuccess;
-    if (e != cudaSuccess) return from_cuda(e);
     if constexpr (sizeof(T) == 2)
-        e = launch_out_bwd(dy, x, emb, mean, rstd, dx, d_emb, workspace, B, S, D, s, dev);
+        return from_cuda(launch_out_bwd_ckpt8(dy, ckpt, emb, mean, rstd, dx, d_emb, workspace, B, S, D, s, dev));
     else
-        e = launch_f32_out_bwd(dy, x, emb, mean, rstd, dx, d_emb, workspace, B, S, D, s, dev);
-    return from_cuda(e);
+        return from_cuda(launch_f32_out_bwd_ckpt8(dy, ckpt, emb, mean, rstd, dx, d_emb, workspace, B, S, D, s, dev));
 }
 
 template <typename T>
@@ -307,7 +300,7 @@ adaln_status adaln_f32_out_fwd_ckpt8(const float *x, const float *emb, float *ou
 
 size_t adaln_out_bwd_ckpt8_workspace_bytes(int B, int S, int D) {
     if (!valid_norm(B, S, D, kMaxD)) return 0;
-    return adaln_out_bwd_workspace_bytes(B, S, D) + round256((size_t)B * S * D * 4);
+    return adaln_out_bwd_workspace_bytes(B, S, D);
 }
 
 adaln_status adaln_out_bwd_ckpt8(const adaln_bf16 *dy, const uint8_t *ckpt, const adaln_bf16 *emb, const float *mean,
