@@ -64,8 +64,8 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 ckpt8_pack_kernel(const T *__restrict__ x, unsigned char *__restrict__ ckpt, long long rows, int D) {
     const int lane = threadIdx.x & 31;
-    const int V = D >> 3, Vg = (V + 3) & ~3, P = ckpt8_row_bytes(D), code_bytes = ckpt8_code_bytes(D);
-    const int w0 = blockIdx.y * 32 * kVecs, v0 = w0 + lane;
+    const int V = D >> 3, P = ckpt8_row_bytes(D), code_bytes = ckpt8_code_bytes(D);
+    const int v0 = blockIdx.y * 32 * kVecs + lane;
     pdl_wait();
     pdl_trigger();
     for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (long long)gridDim.x * 8) {
@@ -77,16 +77,10 @@ ckpt8_pack_kernel(const T *__restrict__ x, unsigned char *__restrict__ ckpt, lon
             e[j].zero();
             if (v0 + 32 * j < V) e[j].load(src + 256 * j);
         }
+        uint32_t top[kVecs];
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            if (w0 + 32 * j >= Vg) break;  // the whole warp
-            px2 p[4];
-            e[j].pairs(p);
-            if (w0 + 32 * j + 32 < V)  // not the row's end
-                ckpt8_put<true>(rec, code_bytes, V, v0 + 32 * j, e[j].max_bits(), p);
-            else
-                ckpt8_put<false>(rec, code_bytes, V, v0 + 32 * j, e[j].max_bits(), p);
-        }
+        for (int j = 0; j < kVecs; ++j) top[j] = e[j].max_bits();
+        ckpt8_put<kVecs, 8>(rec, code_bytes, V, v0, top, [&](int j, px2 (&p)[4]) { e[j].pairs(p); });
     }
 }
 

@@ -79,48 +79,66 @@ __device__ __forceinline__ uint32_t ckpt8_max(const float4 &a, const float4 &b) 
     return max(x, y);
 }
 
-// Vector v (8 channels) of a record, by the lane that holds it; four neighbouring
-// lanes, the first with v a multiple of 4, hold a group (lanes past the row's V
-// vectors give zeros, max_bits 0).  All four run this.  Fills the record's
-// padding as well; INSIDE: the row does not end in this group.
-template <bool INSIDE = false>
-__device__ __forceinline__ void ckpt8_put(unsigned char *rec, int code_bytes, int V, int v, uint32_t max_bits,
-                                          const px2 (&x)[4]) {
-    max_bits = max(max_bits, __shfl_xor_sync(0xFFFFFFFFu, max_bits, 1));
-    max_bits = max(max_bits, __shfl_xor_sync(0xFFFFFFFFu, max_bits, 2));
-    const uint32_t scale = ckpt8_scale(max_bits);
-    if (INSIDE || v * 8 < code_bytes) {
-        uint2 c = make_uint2(0u, 0u);
-        if ((INSIDE || v < V) && scale != 255u) {
-            px2 lo[2] = {x[0], x[1]}, hi[2] = {x[2], x[3]};
-            c = make_uint2(ckpt8_clamped(lo, scale), ckpt8_clamped(hi, scale));
-        }
-        *reinterpret_cast<uint2 *>(rec + (size_t)v * 8) = c;
-    }
-    if ((v & 3) == 0 && (INSIDE || v < V)) {
-        rec[code_bytes + (v >> 2)] = (unsigned char)scale;
-        if (!INSIDE && v + 4 >= V)
-            for (int i = (v >> 2) + 1; i & 15; ++i) rec[code_bytes + i] = 0;
-    }
-}
-
-// The same for a lane that holds 4 channels, vector v of D / 4; eight neighbouring
-// lanes, the first with v a multiple of 8, hold a group.
-__device__ __forceinline__ void ckpt8_put4(unsigned char *rec, int D, int v, const float4 &x) {
-    const int V = D >> 2, code_bytes = ckpt8_code_bytes(D);
-    uint32_t max_bits = ckpt8_max(x, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+// Parts of a record, by the lanes of a warp that hold the row: vector v0 + 32 j (j <
+// N, v0 mod 32 the lane) has E channels, LANES = 32 / E neighbouring lanes, the first
+// with v a multiple of LANES, hold a group; V vectors in the row, past them
+// max_bits[j] is 0 and pairs(j, p) gives zeros.  The whole warp runs this; steps j
+// with 32 j past the row's last group do nothing.  Fills the record's padding as well.
+//
+// A step's chain (maximum, exchanges, scale, codes) is long and its work short, so the
+// N chains run side by side, without branches, but where a group holds an infinity,
+// a NaN or ends at the last scale: then the row's part is written one by one.
+template <int N, int E, typename F>
+__device__ __forceinline__ void ckpt8_put(unsigned char *rec, int code_bytes, int V, int v0, uint32_t (&max_bits)[N],
+                                          F pairs) {
+    constexpr int LANES = kCkptGroup / E;
+    static_assert(E == 8 || E == 4, "8 bytes of codes a lane, or 4");
 #pragma unroll
-    for (int d = 1; d < 8; d *= 2) max_bits = max(max_bits, __shfl_xor_sync(0xFFFFFFFFu, max_bits, d));
-    const uint32_t scale = ckpt8_scale(max_bits);
-    if (v * 4 < code_bytes) {
-        px2 p[2] = {px_make(x.x, x.y), px_make(x.z, x.w)};
-        *reinterpret_cast<uint32_t *>(rec + (size_t)v * 4) = v < V && scale != 255u ? ckpt8_clamped(p, scale) : 0u;
+    for (int d = 1; d < LANES; d *= 2)
+#pragma unroll
+        for (int j = 0; j < N; ++j) max_bits[j] = max(max_bits[j], __shfl_xor_sync(0xFFFFFFFFu, max_bits[j], d));
+    uint32_t scale[N], most = 0u;
+#pragma unroll
+    for (int j = 0; j < N; ++j) scale[j] = ckpt8_scale(max_bits[j]), most = max(most, scale[j]);
+    auto store = [&](int j, const uint32_t (&c)[E / 4]) {
+        const int v = v0 + 32 * j;
+        if (v * E < code_bytes) {
+            if (E == 8)
+                *reinterpret_cast<uint2 *>(rec + (size_t)v * E) = make_uint2(c[0], c[E / 4 - 1]);
+            else
+                *reinterpret_cast<uint32_t *>(rec + (size_t)v * E) = c[0];
+        }
+        if (v % LANES == 0 && v < V) rec[code_bytes + v / LANES] = (unsigned char)scale[j];
+    };
+    if (!__any_sync(0xFFFFFFFFu, most >= kCkptLastScale)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            px2 x[E / 2];
+            pairs(j, x);
+            const px2 inv = px_splat(ckpt8_inverse(scale[j]));
+            uint32_t c[E / 4];
+#pragma unroll
+            for (int q = 0; q < E / 4; ++q) c[q] = ckpt8_codes(x[2 * q], x[2 * q + 1], inv);
+            store(j, c);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            px2 x[E / 2];
+            pairs(j, x);
+            uint32_t c[E / 4];
+#pragma unroll
+            for (int q = 0; q < E / 4; ++q) {
+                px2 y[2] = {x[2 * q], x[2 * q + 1]};
+                c[q] = scale[j] == 255u ? 0u : ckpt8_clamped(y, scale[j]);
+            }
+            store(j, c);
+        }
     }
-    if ((v & 7) == 0 && v < V) {
-        rec[code_bytes + (v >> 3)] = (unsigned char)scale;
-        if (v + 8 >= V)
-            for (int i = (v >> 3) + 1; i & 15; ++i) rec[code_bytes + i] = 0;
-    }
+    // the scales' padding, by the lane of the last group
+    const int last = (V - 1) / LANES * LANES;
+    if (last >= v0 && (last - v0) % 32 == 0 && (last - v0) / 32 < N)
+        for (int i = last / LANES + 1; i & 15; ++i) rec[code_bytes + i] = 0;
 }
 
 }  // namespace adaln

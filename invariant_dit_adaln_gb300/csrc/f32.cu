@@ -151,9 +151,18 @@ f32_out_fwd_kernel(const float *__restrict__ x, const float *__restrict__ emb, f
         }
         if (CKPT) {
             unsigned char *rec = ckpt + row * ckpt8_row_bytes(D);
+            const int code_bytes = ckpt8_code_bytes(D);
+            constexpr int kSide = 8;  // steps side by side
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (32 * j < V) ckpt8_put4(rec, D, lane + 32 * j, xv[j]);  // the whole warp
+            for (int j0 = 0; j0 < VPL; j0 += kSide)
+                if (128 * j0 < code_bytes) {  // the whole warp
+                    uint32_t top[kSide];
+#pragma unroll
+                    for (int j = 0; j < kSide; ++j) top[j] = ckpt8_max(xv[j0 + j], make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+                    ckpt8_put<kSide, 4>(rec, code_bytes, V, lane + 32 * j0, top, [&](int j, px2 (&p)[2]) {
+                        p[0] = px_make(xv[j0 + j].x, xv[j0 + j].y), p[1] = px_make(xv[j0 + j].z, xv[j0 + j].w);
+                    });
+                }
         }
         // sums by column pair (packed), the halves added, then the butterfly
         px2 s1 = 0ull;
@@ -207,26 +216,14 @@ f32_out_fwd_kernel(const float *__restrict__ x, const float *__restrict__ emb, f
 // All arithmetic on column pairs in packed fp32x2 instructions with explicit
 // rounding (a float4 of a row is two pairs as loaded).  Two CTAs per SM hide
 // the loads' latency.
-//
-// CKPT: x comes as 8-bit records.  A thread copies its own part of the rows
-// kF32Ahead rows ahead, asynchronously, into places of shared memory that no other
-// thread reads, so the rows in flight take no registers and no barrier.
 // --------------------------------------------------------------------------
-constexpr int kF32Ahead = 4;
-template <int BYTES>
-__device__ __forceinline__ void copy_ahead(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
-}
-
 // EXACT: D / 4 == blockDim.x * VPT, every thread's vectors inside the row (no tests)
-template <int VPT, int MAXNT, bool EXACT, bool CKPT>
+template <int VPT, int MAXNT, bool EXACT>
 __global__ void __launch_bounds__(MAXNT, 2)
-f32_out_bwd_tile_kernel(const float *__restrict__ dy, const void *__restrict__ x_rows, const float *__restrict__ emb,
+f32_out_bwd_tile_kernel(const float *__restrict__ dy, const float *__restrict__ x, const float *__restrict__ emb,
                         const float *__restrict__ mean, const float *__restrict__ rstd, float *__restrict__ dx,
                         float *__restrict__ ws_sig, float *__restrict__ ws_kap, int S, int D, int T) {
     __shared__ float2 red[2][32];
-    extern __shared__ __align__(16) unsigned char ahead_f32[];  // CKPT: [kF32Ahead][VPT][NT] dy (16 B), then codes and scales (8 B)
-    const float *x = static_cast<const float *>(x_rows);
     const int tid = threadIdx.x;
     const int NT = blockDim.x;
     const int nw = NT >> 5;
@@ -259,66 +256,23 @@ f32_out_bwd_tile_kernel(const float *__restrict__ dy, const void *__restrict__ x
     const int n = min(kTile, S - s0);
     const float Df = (float)D;
     const uint64_t pol = l2_evict_first();
-    uint4 *ahead_g = reinterpret_cast<uint4 *>(ahead_f32) + tid;
-    uint2 *ahead_c = reinterpret_cast<uint2 *>(ahead_f32 + (size_t)kF32Ahead * VPT * NT * 16) + tid;
-    const int P = ckpt8_row_bytes(D), code_bytes = ckpt8_code_bytes(D);
-    auto copy_row = [&](int i) {  // CKPT: this thread's part of row i, one group of copies (none past the tile's end)
-        if (i < n) {
-            const size_t row = (size_t)b * S + s0 + i;
-            const unsigned char *rec = static_cast<const unsigned char *>(x_rows) + row * P;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int v = tid + NT * j, at = ((i % kF32Ahead) * VPT + j) * NT;
-                if (EXACT || v < V) {
-                    copy_ahead<16>(ahead_g + at, dy + row * D + (size_t)v * 4);
-                    copy_ahead<4>(&ahead_c[at].x, rec + (size_t)v * 4);
-                    copy_ahead<4>(&ahead_c[at].y, rec + code_bytes + (v >> 5) * 4);  // four groups' scales
-                }
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    float mu_l = 0.0f, rs_l = 0.0f;  // CKPT: lane i holds row i's statistics
-    if constexpr (CKPT) {
-        if (lane < n) mu_l = mean[(size_t)b * S + s0 + lane], rs_l = rstd[(size_t)b * S + s0 + lane];
-        for (int i = 0; i < kF32Ahead - 1; ++i) copy_row(i);
-    }
     for (int i = 0; i < n; ++i) {
         const size_t row = (size_t)b * S + s0 + i;
         px2 xp[VPT][2], gp[VPT][2];
-        if constexpr (CKPT) {
-            copy_row(i + kF32Ahead - 1);
-            asm volatile("cp.async.wait_group %0;" ::"n"(kF32Ahead - 1) : "memory");
-        }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + NT * j;
-            uint4 gw = make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (CKPT) {
-                xp[j][0] = xp[j][1] = 0ull;
-                if (EXACT || v < V) {
-                    const int at = ((i % kF32Ahead) * VPT + j) * NT;
-                    gw = ahead_g[at];
-                    const uint2 c = ahead_c[at];
-                    const px2 step = px_splat(ckpt8_step((c.y >> ((v >> 3) & 3) * 8) & 0xFFu));
-                    ckpt8_floats(c.x, xp[j][0], xp[j][1]);
-                    xp[j][0] = px_mul(xp[j][0], step);
-                    xp[j][1] = px_mul(xp[j][1], step);
-                }
-            } else {
-                uint4 xw = make_uint4(0u, 0u, 0u, 0u);
-                if (EXACT || v < V) {
-                    xw = ldg16_hint(x + row * D + (size_t)v * 4, pol);
-                    gw = ldg16_hint(dy + row * D + (size_t)v * 4, pol);
-                }
-                xp[j][0] = px_make(__uint_as_float(xw.x), __uint_as_float(xw.y));
-                xp[j][1] = px_make(__uint_as_float(xw.z), __uint_as_float(xw.w));
+            uint4 xw = make_uint4(0u, 0u, 0u, 0u), gw = xw;
+            if (EXACT || v < V) {
+                xw = ldg16_hint(x + row * D + (size_t)v * 4, pol);
+                gw = ldg16_hint(dy + row * D + (size_t)v * 4, pol);
             }
+            xp[j][0] = px_make(__uint_as_float(xw.x), __uint_as_float(xw.y));
+            xp[j][1] = px_make(__uint_as_float(xw.z), __uint_as_float(xw.w));
             gp[j][0] = px_make(__uint_as_float(gw.x), __uint_as_float(gw.y));
             gp[j][1] = px_make(__uint_as_float(gw.z), __uint_as_float(gw.w));
         }
-        const float mu = CKPT ? __shfl_sync(0xFFFFFFFFu, mu_l, i) : mean[row];
-        const float rs = CKPT ? __shfl_sync(0xFFFFFFFFu, rs_l, i) : rstd[row];
+        const float mu = mean[row], rs = rstd[row];
         const px2 mu2 = px_splat(mu), rs2 = px_splat(rs);
         // phase 1: x_hat, the tree products and this thread's row sums (column
         // pairs in packed fused multiply-adds, the halves added at the end)
@@ -368,6 +322,173 @@ f32_out_bwd_tile_kernel(const float *__restrict__ dy, const void *__restrict__ x
     for (int j = 0; j < VPT; ++j) {
         const int v = tid + NT * j;
         if (EXACT || v < V) {
+            const size_t node = ((size_t)b * T + t) * H + (size_t)v * 4;
+            stg16f(ws_sig + node, make_float4(px_lo(ss[j][0]), px_hi(ss[j][0]), px_lo(ss[j][1]), px_hi(ss[j][1])));
+            stg16f(ws_kap + node, make_float4(px_lo(ks[j][0]), px_hi(ks[j][0]), px_lo(ks[j][1]), px_hi(ks[j][1])));
+            stg16f(ws_sig + node + D, make_float4(px_lo(sh[j][0]), px_hi(sh[j][0]), px_lo(sh[j][1]), px_hi(sh[j][1])));
+            stg16f(ws_kap + node + D, make_float4(px_lo(kh[j][0]), px_hi(kh[j][0]), px_lo(kh[j][1]), px_hi(kh[j][1])));
+        }
+    }
+}
+
+// --------------------------------------------------------------------------
+// The same from 8-bit records of x: columns, orders and roundings of the kernel above
+// (so the same bits), the rows in blocks of RB.  A thread copies its own part of the
+// rows ahead, asynchronously, into places of shared memory that no other thread
+// reads, and reads them again for dx; so rows in flight take no registers, and a
+// block has one barrier.  (Row by row with a barrier each, as above: 41 us for 51
+// tiles of 1160 columns, a chain of 2300 cycles a row; this form XX.)
+// --------------------------------------------------------------------------
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+
+template <int VPT, int MAXNT, int MINB, int RB, int RING>
+__global__ void __launch_bounds__(MAXNT, MINB)
+f32_out_bwd_ckpt8_kernel(const float *__restrict__ dy, const unsigned char *__restrict__ ckpt,
+                         const float *__restrict__ emb, const float *__restrict__ mean,
+                         const float *__restrict__ rstd, float *__restrict__ dx, float *__restrict__ ws_sig,
+                         float *__restrict__ ws_kap, int S, int D, int T) {
+    static_assert(RING >= 2 * RB && RING % RB == 0 && (2 * RB <= 32), "two blocks of rows in flight");
+    __shared__ float red[2][2 * RB][32];  // [block parity][sum g onep, sum p onep of each row][warp]
+    extern __shared__ __align__(16) unsigned char ahead_f32[];  // [RING][VPT][NT] dy (16 B), then codes and scales (8 B)
+    const int tid = threadIdx.x, NT = blockDim.x, nw = NT >> 5, warp = tid >> 5, lane = tid & 31;
+    const int t = blockIdx.x, b = blockIdx.y;
+    const int V = D / 4, P = ckpt8_row_bytes(D), code_bytes = ckpt8_code_bytes(D);
+    const int s0 = t * kTile, n = min(kTile, S - s0);
+    const size_t row0 = (size_t)b * S + s0;
+    uint4 *ahead_g = reinterpret_cast<uint4 *>(ahead_f32) + tid;
+    uint2 *ahead_c = reinterpret_cast<uint2 *>(ahead_f32 + (size_t)RING * VPT * NT * 16) + tid;
+    pdl_wait();
+    pdl_trigger();
+    // this thread's part of the RB rows from i on, one group of copies (none past the tile's end)
+    auto copy_block = [&](int i0) {
+        for (int i = i0; i < i0 + RB && i < n; ++i) {
+            const unsigned char *rec = ckpt + (row0 + i) * P;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = tid + NT * j, at = ((i % RING) * VPT + j) * NT;
+                if (v < V) {
+                    copy_ahead<16>(ahead_g + at, dy + (row0 + i) * D + (size_t)v * 4);
+                    copy_ahead<4>(&ahead_c[at].x, rec + (size_t)v * 4);
+                    copy_ahead<4>(&ahead_c[at].y, rec + code_bytes + (v >> 5) * 4);  // four groups' scales
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // lane i holds row i's statistics; requested before the rows
+    float mu_l = 0.0f, rs_l = 0.0f;
+    if (lane < n) mu_l = mean[row0 + lane], rs_l = rstd[row0 + lane];
+    px2 onep[VPT][2];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = tid + NT * j;
+        float4 sc = make_float4(-1.0f, -1.0f, -1.0f, -1.0f);
+        if (v < V) sc = reinterpret_cast<const float4 *>(emb + (size_t)b * 2 * D)[v];
+        onep[j][0] = px_make(__fadd_rn(1.0f, sc.x), __fadd_rn(1.0f, sc.y));
+        onep[j][1] = px_make(__fadd_rn(1.0f, sc.z), __fadd_rn(1.0f, sc.w));
+    }
+    constexpr int kBlocksAhead = RING / RB - 1;
+#pragma unroll
+    for (int k = 0; k < kBlocksAhead; ++k) copy_block(k * RB);
+    px2 ss[VPT][2], ks[VPT][2], sh[VPT][2], kh[VPT][2];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) ss[j][c] = ks[j][c] = sh[j][c] = kh[j][c] = 0ull;
+    const float Df = (float)D;
+    const uint64_t pol = l2_evict_first();
+    // vector j of row i: x and g by column pair
+    auto load = [&](int i, int j, px2 (&xp)[2], px2 (&gp)[2]) {
+        const int v = tid + NT * j, at = ((i % RING) * VPT + j) * NT;
+        const uint4 gw = ahead_g[at];
+        const uint2 c = ahead_c[at];
+        const px2 step = px_splat(ckpt8_step((c.y >> ((v >> 3) & 3) * 8) & 0xFFu));
+        ckpt8_floats(c.x, xp[0], xp[1]);
+        xp[0] = px_mul(xp[0], step);
+        xp[1] = px_mul(xp[1], step);
+        gp[0] = px_make(__uint_as_float(gw.x), __uint_as_float(gw.y));
+        gp[1] = px_make(__uint_as_float(gw.z), __uint_as_float(gw.w));
+    };
+    for (int i0 = 0, par = 0; i0 < n; i0 += RB, par ^= 1) {
+        copy_block(i0 + kBlocksAhead * RB);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kBlocksAhead) : "memory");
+        // phase 1: x_hat, the tree products and this thread's row sums
+        float sums[2 * RB];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            px2 a1 = 0ull, a2 = 0ull;
+            const px2 mu2 = px_splat(__shfl_sync(0xFFFFFFFFu, mu_l, (i0 + r) & 31)),
+                      rs2 = px_splat(__shfl_sync(0xFFFFFFFFu, rs_l, (i0 + r) & 31));
+            if (i0 + r < n) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    if (tid + NT * j < V) {
+                        px2 xp[2], gp[2];
+                        load(i0 + r, j, xp, gp);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const px2 p = px_mul(gp[c], px_mul(px_sub(xp[c], mu2), rs2));
+                            px_twosum(ss[j][c], ks[j][c], p);
+                            px_twosum(sh[j][c], kh[j][c], gp[c]);
+                            a1 = px_fma(gp[c], onep[j][c], a1);
+                            a2 = px_fma(p, onep[j][c], a2);
+                        }
+                    }
+                }
+            }
+            sums[2 * r] = __fadd_rn(px_lo(a1), px_hi(a1));
+            sums[2 * r + 1] = __fadd_rn(px_lo(a2), px_hi(a2));
+        }
+        // the butterflies of warp_sum, side by side
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+            for (int q = 0; q < 2 * RB; ++q) sums[q] = __fadd_rn(sums[q], __shfl_xor_sync(0xFFFFFFFFu, sums[q], off));
+        if (lane == 0)
+#pragma unroll
+            for (int q = 0; q < 2 * RB; ++q) red[par][q][warp] = sums[q];
+        __syncthreads();
+        // lane q: quantity q mod 2 of row q / 2, the warps in ascending order
+        float cs = 0.0f;
+        if (lane < 2 * RB) {
+            cs = red[par][lane][0];
+            for (int w = 1; w < nw; ++w) cs = __fadd_rn(cs, red[par][lane][w]);
+            cs = __fdiv_rn(cs, Df);
+        }
+        // phase 2: dx = fp32(rstd * fp32(fp32(gh - c1) - fp32(x_hat * c2))), gh = fp32(g * onep)
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            const px2 mu2 = px_splat(__shfl_sync(0xFFFFFFFFu, mu_l, (i0 + r) & 31)),
+                      rs2 = px_splat(__shfl_sync(0xFFFFFFFFu, rs_l, (i0 + r) & 31)),
+                      c1 = px_splat(__shfl_sync(0xFFFFFFFFu, cs, 2 * r)),
+                      c2 = px_splat(__shfl_sync(0xFFFFFFFFu, cs, 2 * r + 1));
+            if (i0 + r >= n) continue;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = tid + NT * j;
+                if (v < V) {
+                    px2 xp[2], gp[2], o[2];
+                    load(i0 + r, j, xp, gp);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const px2 xh = px_mul(px_sub(xp[c], mu2), rs2), gh = px_mul(gp[c], onep[j][c]);
+                        o[c] = px_mul(rs2, px_sub(px_sub(gh, c1), px_mul(xh, c2)));
+                    }
+                    stg16f_hint(dx + (row0 + i0 + r) * D + (size_t)v * 4,
+                                make_float4(px_lo(o[0]), px_hi(o[0]), px_lo(o[1]), px_hi(o[1])), pol);
+                }
+            }
+        }
+        // red[par] is written again two blocks later, after the next barrier
+    }
+    const int H = 2 * D;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = tid + NT * j;
+        if (v < V) {
             const size_t node = ((size_t)b * T + t) * H + (size_t)v * 4;
             stg16f(ws_sig + node, make_float4(px_lo(ss[j][0]), px_hi(ss[j][0]), px_lo(ss[j][1]), px_hi(ss[j][1])));
             stg16f(ws_kap + node, make_float4(px_lo(ks[j][0]), px_hi(ks[j][0]), px_lo(ks[j][1]), px_hi(ks[j][1])));
@@ -560,10 +681,9 @@ cudaError_t launch_f32_out_fwd_ckpt8(const float *x, const float *emb, float *ou
     return launch_f32_out_fwd_rows<true>(x, emb, out, mean, rstd, ckpt, B, S, D, eps, stream, dev);
 }
 
-template <bool CKPT>
-static cudaError_t launch_f32_out_bwd_rows(const float *dy, const void *x, const float *emb, const float *mean,
-                                           const float *rstd, float *dx, float *d_emb, void *ws, int B, int S, int D,
-                                           cudaStream_t stream, const DeviceInfo &dev) {
+cudaError_t launch_f32_out_bwd(const float *dy, const float *x, const float *emb, const float *mean,
+                               const float *rstd, float *dx, float *d_emb, void *ws, int B, int S, int D,
+                               cudaStream_t stream, const DeviceInfo &dev) {
     if (S == 0) return launch_zero(d_emb, (size_t)B * 2 * D, stream);
     const int T = (S + kTile - 1) / kTile;
     const int H = 2 * D;
@@ -572,31 +692,47 @@ static cudaError_t launch_f32_out_bwd_rows(const float *dy, const void *x, const
     // two CTAs per SM: three vectors (12 columns: more independent TwoSum
     // chains per thread) per thread up to D = 3072 (at most 256 threads), four
     // up to D = 4096 (at most 256)
-    const int V = D / 4, vpt = V <= 768 ? 3 : 4;
-    const int nt = ((V + vpt - 1) / vpt + 31) / 32 * 32;
-    // the exact form of four spills at 128 registers
-    auto kern = vpt == 4      ? f32_out_bwd_tile_kernel<4, 256, false, CKPT>
-                : nt * 3 == V ? f32_out_bwd_tile_kernel<3, 256, true, CKPT>
-                              : f32_out_bwd_tile_kernel<3, 256, false, CKPT>;
-    const size_t smem = CKPT ? (size_t)kF32Ahead * vpt * nt * 24 : 0;
-    cudaError_t err = ensure_smem_attr((const void *)kern, smem, dev);
-    if (err != cudaSuccess) return err;
-    err = launch_pdl(kern, dim3((unsigned)T, (unsigned)B), dim3(nt), smem, stream, dy, x, emb, mean, rstd, dx, sig, kap,
-                     S, D, T);
+    const int V = D / 4;
+    cudaError_t err;
+    if (V <= 768) {
+        const int nt = ((V + 2) / 3 + 31) / 32 * 32;
+        auto kern = nt * 3 == V ? f32_out_bwd_tile_kernel<3, 256, true> : f32_out_bwd_tile_kernel<3, 256, false>;
+        err = launch_pdl(kern, dim3((unsigned)T, (unsigned)B), dim3(nt), 0, stream, dy, x, emb, mean, rstd, dx, sig,
+                         kap, S, D, T);
+    } else {
+        const int nt = ((V + 3) / 4 + 31) / 32 * 32;
+        auto kern = f32_out_bwd_tile_kernel<4, 256, false>;  // the exact form spills at 128 registers
+        err = launch_pdl(kern, dim3((unsigned)T, (unsigned)B), dim3(nt), 0, stream, dy, x, emb, mean, rstd, dx, sig,
+                         kap, S, D, T);
+    }
     if (err != cudaSuccess) return err;
     return launch_fold(sig, kap, d_emb, B, T, H, stream, dev);
-}
-
-cudaError_t launch_f32_out_bwd(const float *dy, const float *x, const float *emb, const float *mean,
-                               const float *rstd, float *dx, float *d_emb, void *ws, int B, int S, int D,
-                               cudaStream_t stream, const DeviceInfo &dev) {
-    return launch_f32_out_bwd_rows<false>(dy, x, emb, mean, rstd, dx, d_emb, ws, B, S, D, stream, dev);
 }
 
 cudaError_t launch_f32_out_bwd_ckpt8(const float *dy, const uint8_t *ckpt, const float *emb, const float *mean,
                                      const float *rstd, float *dx, float *d_emb, void *ws, int B, int S, int D,
                                      cudaStream_t stream, const DeviceInfo &dev) {
-    return launch_f32_out_bwd_rows<true>(dy, ckpt, emb, mean, rstd, dx, d_emb, ws, B, S, D, stream, dev);
+    if (S == 0) return launch_zero(d_emb, (size_t)B * 2 * D, stream);
+    const int T = (S + kTile - 1) / kTile;
+    const int H = 2 * D;
+    float *sig = static_cast<float *>(ws);
+    float *kap = sig + (size_t)B * T * H;
+    // the columns of a thread as above, which fixes the order of dx's row sums; blocks
+    // of 4 rows and a ring of 8 where two CTAs' rings fit an SM (up to 192 threads)
+    const int V = D / 4, vpt = V <= 768 ? 3 : 4;
+    const int nt = ((V + vpt - 1) / vpt + 31) / 32 * 32;
+    auto go = [&](auto kern, int ring) {
+        const size_t smem = (size_t)ring * vpt * nt * 24;
+        const cudaError_t err = ensure_smem_attr((const void *)kern, smem, dev);
+        if (err != cudaSuccess) return err;
+        return launch_pdl(kern, dim3((unsigned)T, (unsigned)B), dim3(nt), smem, stream, dy, ckpt, emb, mean, rstd, dx,
+                          sig, kap, S, D, T);
+    };
+    const cudaError_t err = vpt == 4    ? go(f32_out_bwd_ckpt8_kernel<4, 256, 2, 2, 4>, 4)
+                            : nt <= 192 ? go(f32_out_bwd_ckpt8_kernel<3, 192, 2, 4, 8>, 8)
+                                        : go(f32_out_bwd_ckpt8_kernel<3, 256, 2, 2, 6>, 6);
+    if (err != cudaSuccess) return err;
+    return launch_fold(sig, kap, d_emb, B, T, H, stream, dev);
 }
 
 size_t f32_proj_bwd_ws_bytes(int B, int D) {

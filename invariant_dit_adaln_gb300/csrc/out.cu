@@ -440,13 +440,12 @@ out_fwd_row_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ 
         }
         if (CKPT) {
             unsigned char *rec = ckpt + r * ckpt8_row_bytes(D);
+            uint32_t top[VPL];
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (EXACT || 32 * j < V) {  // the whole warp
-                    const px2 p[4] = {px_bf16(xr[j].x), px_bf16(xr[j].y), px_bf16(xr[j].z), px_bf16(xr[j].w)};
-                    // not the form without the row's end, which spills at 128 registers
-                    ckpt8_put(rec, ckpt8_code_bytes(D), V, lane + 32 * j, ckpt8_max(xr[j]), p);
-                }
+            for (int j = 0; j < VPL; ++j) top[j] = ckpt8_max(xr[j]);
+            ckpt8_put<VPL, 8>(rec, ckpt8_code_bytes(D), V, lane, top, [&](int j, px2 (&p)[4]) {
+                p[0] = px_bf16(xr[j].x), p[1] = px_bf16(xr[j].y), p[2] = px_bf16(xr[j].z), p[3] = px_bf16(xr[j].w);
+            });
         }
         // mean (zero vectors past the row end add +0 and change nothing)
         float2 s1[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
