@@ -40,6 +40,7 @@ struct TcBars {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t done;
+    uint64_t kept_full, kept_empty;
     uint32_t tmem;
     int abort;
 #ifdef ADALN_TEST_WAIT_NEVER_NS
@@ -95,10 +96,13 @@ __device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&v)[8]) {
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "r"(addr));
 }
-__device__ __forceinline__ void tmem_ld4(uint32_t addr, uint32_t (&v)[4]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "r"(addr));
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr));
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&v)[32]) {
     asm volatile(
@@ -133,6 +137,10 @@ __device__ __forceinline__ bool named_bar_and(int id, int count, bool flag) {
     return r != 0;
 }
 
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -147,6 +155,8 @@ __device__ __forceinline__ void bars_init(TcBars &sm, int acc_arrivals, int empt
         mbar_init(&sm.acc_empty[p], acc_arrivals);
     }
     mbar_init(&sm.done, 1);
+    mbar_init(&sm.kept_full, 1);
+    mbar_init(&sm.kept_empty, 1);
     sm.abort = 0;
 #ifdef ADALN_TEST_WAIT_NEVER_NS
     mbar_init(&sm.never, 1);
@@ -186,6 +196,8 @@ __device__ __forceinline__ void three_parts(float v, uint16_t (&p)[3]) {
 // Roles (128 threads): warp 0 lane 0 the copies, warp 1 lane 0 the MMAs, then
 // thread t holds token t.
 // --------------------------------------------------------------------------
+constexpr int kPartPitch = kM + 4;  // floats of a rank's tokens
+
 struct ShrinkArgs {
     const float *scale;
     const void *ids;
@@ -194,7 +206,7 @@ struct ShrinkArgs {
     uint16_t *h;
     int S, C, R, NA, Sp;
     int Rp;      // R rounded up to the MMA's multiple of 16
-    int ks;      // channel ranges: cluster size, 1, 2, 4 or 8, a divisor of Rp / 4
+    int ks;      // channel ranges: cluster size, 1, 2, 4 or 8, a divisor of Rp
     int stages, tmem_cols;
 };
 
@@ -205,8 +217,8 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
     const uint32_t raw = smem_u32(tc_smem_raw);
     unsigned char *ring = tc_smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const int w_tile = g.Rp * kBlk * 2, stage_bytes = kRowTile + w_tile;
-    float4 *part = reinterpret_cast<float4 *>(ring + (size_t)g.stages * stage_bytes);  // [ks][Rp / 4 / ks][128]
-    TcBars &sm = *reinterpret_cast<TcBars *>(reinterpret_cast<unsigned char *>(part) + (size_t)g.Rp * kM * 4);
+    float *part = reinterpret_cast<float *>(ring + (size_t)g.stages * stage_bytes);  // [ks][Rp / ks][kPartPitch]
+    TcBars &sm = *reinterpret_cast<TcBars *>(part + (size_t)g.Rp * kPartPitch);
     volatile int *abort_flag = &sm.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.y * kM, b = blockIdx.z;
@@ -291,16 +303,21 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
     ok = __syncthreads_and(ok);
     tc_after_sync();
     const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
-    const int slice = g.Rp / 4 / g.ks;  // ranks of a CTA, by four
-    float4 *mine = part + (int)rank * slice * kM + threadIdx.x;
-    for (int q = 0, c = 0; q < g.ks; ++q) {
-        const uint32_t at = g.ks > 1 ? map_to_rank(mine, (uint32_t)q) : smem_u32(mine);
-        for (int i = 0; i < slice; ++i, c += 4) {
-            uint32_t v[4];
-            tmem_ld4(trow + (uint32_t)c, v);
-            tmem_ld_done();
-            st_cluster_v4(at + (uint32_t)(i * kM * 16), make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]),
-                                                                   __uint_as_float(v[2]), __uint_as_float(v[3])));
+    const int slice = g.Rp / g.ks;  // ranks of a CTA
+    uint32_t at = g.ks > 1 ? map_to_rank(part + (int)rank * slice * kPartPitch + threadIdx.x, 0u)
+                           : smem_u32(part + threadIdx.x);  // place of the next rank
+    for (int c = 0, q = 0, i = 0; c < g.Rp; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(trow + (uint32_t)c, v);
+        tmem_ld_done();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            st_cluster_f32(at, __uint_as_float(v[k]));
+            at += kPartPitch * 4;
+            if (++i == slice && ++q < g.ks) {
+                i = 0;
+                at = map_to_rank(part + (int)rank * slice * kPartPitch + threadIdx.x, (uint32_t)q);
+            }
         }
     }
     tc_before_sync();
@@ -308,26 +325,31 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
         cluster_sync();
     else
         __syncthreads();
-    const int t = t0 + (int)threadIdx.x;
-    if (ok && t < g.Sp) {
-        uint16_t *h = g.h + (size_t)b * 3 * g.R * g.Sp + t;
-        for (int i = 0; i < slice; ++i) {
-            const int r = ((int)rank * slice + i) * 4;
-            if (r >= g.R) break;
-            float4 s = part[i * kM + threadIdx.x];
-            for (int q = 1; q < g.ks; ++q) {
-                const float4 v = part[(q * slice + i) * kM + threadIdx.x];
-                s = make_float4(__fadd_rn(s.x, v.x), __fadd_rn(s.y, v.y), __fadd_rn(s.z, v.z), __fadd_rn(s.w, v.w));
-            }
-            const float f[4] = {s.x, s.y, s.z, s.w};
+    // a thread joins 8 tokens of a rank: 16 bytes of each part of the state
+    uint16_t *h = g.h + (size_t)b * 3 * g.R * g.Sp + t0;
+    for (int k = threadIdx.x; ok && k < slice * (kM / 8); k += 128) {
+        const int i = k / (kM / 8), t = k % (kM / 8) * 8, r = (int)rank * slice + i;
+        if (r >= g.R || t0 + t >= g.Sp) continue;
+        float s[8];
+        for (int q = 0; q < g.ks; ++q) {
+            const float4 *p = reinterpret_cast<const float4 *>(part + (q * slice + i) * kPartPitch + t);
+            const float4 x = p[0], y = p[1];
+            const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint16_t p[3] = {0, 0, 0};  // rows past the sample's end: zero, which grad relies on
-                if (t < n) three_parts(__fmul_rn(scale, f[j]), p);
-#pragma unroll
-                for (int k = 0; k < 3; ++k) h[(size_t)(k * g.R + r + j) * g.Sp] = p[k];
-            }
+            for (int j = 0; j < 8; ++j) s[j] = q == 0 ? f[j] : __fadd_rn(s[j], f[j]);
         }
+        uint32_t w[3][4];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            uint16_t lo[3] = {0, 0, 0}, hi[3] = {0, 0, 0};  // rows past the sample's end: zero, which grad relies on
+            if (t0 + t + j < n) three_parts(__fmul_rn(scale, s[j]), lo);
+            if (t0 + t + j + 1 < n) three_parts(__fmul_rn(scale, s[j + 1]), hi);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) w[m][j / 2] = (uint32_t)lo[m] | (uint32_t)hi[m] << 16;
+        }
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+            stg16(h + (size_t)(m * g.R + r) * g.Sp + t, make_uint4(w[m][0], w[m][1], w[m][2], w[m][3]));
     }
     if (warp == 1) {
         tc_after_sync();
@@ -348,7 +370,9 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
 // same rows.  A tile's base, state and adapter come by TMA into a stage of a ring;
 // two accumulators; a thread adds row t's accumulators to the base in shared memory,
 // from where the tile leaves by TMA.  A tile that the sample's end crosses leaves by
-// row.  (One tile a CTA, of 128 channels, four CTAs an SM, each waiting for its own
+// row.  Above rank 32, where the state is the most of a stage, a CTA takes a run of
+// tiles instead, and keeps the state of its tokens beside the ring (rank 128, 2042
+// rows of 2560 channels: 16.8 us with the state in the stages, XX so).  (One tile a CTA, of 128 channels, four CTAs an SM, each waiting for its own
 // copies: 36 us instead of XX for 4222 rows of 9216 channels at rank 32.  Each CTA a
 // run of one row of tiles: 45, the last CTAs alone on the device.)
 //
@@ -376,6 +400,7 @@ struct ExpandArgs {
     int copies;  // of the adapter's rows
     int kind;    // of the base
     int stages;
+    int keep;    // the state lies beside the stages, for a run of tiles
 };
 
 struct ExpandTile {  // what a stage holds
@@ -383,23 +408,38 @@ struct ExpandTile {  // what a stage holds
     int n;  // rows of the sample from t0 on; 0: there are no more tiles
     int a;  // adapter, -1: none
     int m;  // products before this one among the tiles of its group of warps
+    int fresh;  // keep: the state of these tokens is to be loaded
 };
 
-// The tiles x, x + step, ... of a call, for a warp.  Without lens every sample has
+// The tiles x, x + gridDim.x, ... of a call, or (keep) the x-th of gridDim.x runs of
+// them, for a warp.  Without lens every sample has
 // the same number of token tiles; with them the warp goes through the samples, 32 at
 // a time.
 struct ExpandTiles {
     const ExpandArgs &g;
-    long long u, step;  // tile number
+    long long u, step, end;  // tile number
     int ct;             // channel tiles
     int w0;             // first sample of the window
     long long before;   // token tiles of the samples before it
     int rows, upto;     // this lane's sample: its rows, and the token tiles up to its end
     bool over;
     __device__ __forceinline__ ExpandTiles(const ExpandArgs &args, int lane)
-        : g(args), u(blockIdx.x), step(gridDim.x), ct((args.C + kBlk - 1) / kBlk), w0(0), before(0), rows(0), upto(0),
-          over(false) {
+        : g(args), u(blockIdx.x), step(gridDim.x), end(0x7FFFFFFFFFFFFFFFll), ct((args.C + kBlk - 1) / kBlk), w0(0),
+          before(0), rows(0), upto(0), over(false) {
         if (g.lens) window(lane);
+        if (!g.keep) return;
+        long long all = (long long)g.B * ((g.S + kM - 1) / kM);
+        if (g.lens) {
+            all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+            while (w0 + 32 < g.B) {
+                w0 += 32;
+                window(lane);
+                all += __shfl_sync(0xFFFFFFFFu, upto, 31);
+            }
+            if (w0 > 0) w0 = 0, window(lane);
+        }
+        all *= ct;
+        u = all * blockIdx.x / gridDim.x, end = all * (blockIdx.x + 1) / gridDim.x, step = 1;
     }
     __device__ __forceinline__ void window(int lane) {
         rows = w0 + lane < g.B ? rows_of(g.lens, w0 + lane, g.S) : 0;
@@ -412,8 +452,12 @@ struct ExpandTiles {
     }
     // the next tile; after the last n == 0, as often as it is asked; the same in every lane
     __device__ __forceinline__ ExpandTile next(int lane) {
-        ExpandTile t = {0, 0, 0, 0, -1, 0};
+        ExpandTile t = {0, 0, 0, 0, -1, 0, 0};
         for (; !over; u += step) {
+            if (u >= end) {
+                over = true;
+                break;
+            }
             const long long tt = u / ct;  // token tile
             t.c0 = (int)(u - tt * ct) * kBlk;
             if (!g.lens) {
@@ -469,8 +513,9 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
     const uint32_t raw = smem_u32(tc_smem_raw);
     unsigned char *ring = tc_smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const int R = g.R, h_box = 2 * R * 128, w_rows = R * 128, w_tile = g.copies * w_rows;
-    const int stage_bytes = kExTile + 2 * h_box + w_tile;  // base, state, adapter
-    TcBars &sm = *reinterpret_cast<TcBars *>(ring + (size_t)g.stages * stage_bytes);
+    const int w_at = kExTile + (g.keep ? 0 : 2 * h_box), stage_bytes = w_at + w_tile;  // base, state, adapter
+    unsigned char *kept = ring + (size_t)g.stages * stage_bytes;
+    TcBars &sm = *reinterpret_cast<TcBars *>(kept + (g.keep ? 2 * h_box : 0));
     volatile int *abort_flag = &sm.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -488,15 +533,18 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
     bool ok = true;
     if (warp == 0) {
         ExpandTiles tiles(g, lane);
-        int issued = 0, products[2] = {0, 0};
+        int issued = 0, products[2] = {0, 0}, b = -1, t0 = -1, loads = 0;  // keep: tokens of the state, loads of it
         for (int i = 0, ends = 0; ends < 2; ++i) {  // the end is told twice, once to each group of warps
             ExpandTile t = tiles.next(lane);
             t.m = i & 1 ? products[1] : products[0];
             if (t.n > 0 && t.a >= 0) (i & 1 ? products[1] : products[0]) += 1;
             ends += t.n == 0;
+            t.fresh = t.n > 0 && t.a >= 0 && (t.b != b || t.t0 != t0);
+            if (t.fresh) b = t.b, t0 = t.t0;
             const int s = i % g.stages;
             // free: the tile's MMAs are done, and its store has read it
-            if (i >= g.stages) ok = mbar_wait_or_abort(&sm.empty[s], (uint32_t)(i / g.stages - 1) & 1u, abort_flag);
+            if (i >= g.stages)
+                ok = ok && mbar_wait_or_abort(&sm.empty[s], (uint32_t)(i / g.stages - 1) & 1u, abort_flag);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 *abort_flag = 1;
                 ok = false;
@@ -505,19 +553,32 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
             if (lane == 0) {
                 unsigned char *p = ring + (size_t)s * stage_bytes;
                 info[s] = t;
-                const int bytes = t.n == 0 ? 0 : (by_tma ? kExTile : 0) + (t.a >= 0 ? 2 * h_box + w_tile : 0);
+                const int bytes = t.n == 0 ? 0 : (by_tma ? kExTile : 0) + (t.a >= 0 ? stage_bytes - kExTile : 0);
                 mbar_arrive_expect_tx(&sm.full[s], (uint32_t)bytes);
                 if (t.n > 0 && by_tma) tma_load_3d(p, &map_y, t.c0, t.t0, t.b, &sm.full[s]);
                 if (t.n > 0 && t.a >= 0) {
-                    for (int k = 0; k < 2; ++k)
-                        tma_load_3d(p + kExTile + k * h_box, &map_h, t.t0 + k * kBlk, 0, t.b, &sm.full[s]);
                     for (int k = 0; k < g.copies; ++k)
-                        tma_load_3d(p + kExTile + 2 * h_box + k * w_rows, &map_w, t.c0, 0, t.a, &sm.full[s]);
+                        tma_load_3d(p + w_at + k * w_rows, &map_w, t.c0, 0, t.a, &sm.full[s]);
+                    if (!g.keep)
+                        for (int k = 0; k < 2; ++k)
+                            tma_load_3d(p + kExTile + k * h_box, &map_h, t.t0 + k * kBlk, 0, t.b, &sm.full[s]);
+                }
+                if (g.keep && t.fresh) {
+                    // once the MMAs that read the last tokens' state are done
+                    if (loads > 0) ok = mbar_wait_or_abort(&sm.kept_empty, (uint32_t)(loads - 1) & 1u, abort_flag);
+                    if (ok) {
+                        mbar_arrive_expect_tx(&sm.kept_full, (uint32_t)(2 * h_box));
+                        for (int k = 0; k < 2; ++k)
+                            tma_load_3d(kept + k * h_box, &map_h, t.t0 + k * kBlk, 0, t.b, &sm.kept_full);
+                        ++loads;
+                    }
                 }
             }
             issued = i + 1;
         }
         // every copy issued lands before the CTA leaves
+        if (lane == 0 && loads > 0 && !mbar_wait_bounded(&sm.kept_full, (uint32_t)(loads - 1) & 1u, kDrainNs))
+            report_error_lora(kErrDrainFailed);
         if (lane == 0)
             for (int s = 0; s < g.stages && s < issued; ++s) {
                 const int last = s + g.stages * ((issued - 1 - s) / g.stages);
@@ -528,20 +589,26 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
         if (lane == 0) {
             const uint32_t idesc = f16_idesc(kBlk, true) | (1u << 16);  // B N-major
             bool go = first_wait(sm);
-            for (int i = 0; go; ++i) {
+            for (int i = 0, loads = 0; go; ++i) {
                 const int s = i % g.stages;
                 go = mbar_wait_or_abort(&sm.full[s], (uint32_t)(i / g.stages) & 1u, abort_flag);
                 if (!go || info[s].n == 0) break;
                 const bool add = info[s].a >= 0;
                 const int m = info[s].m, p = i & 1;  // an accumulator for each group
+                const bool fresh = info[s].fresh;
                 mbar_arrive(&sm.empty[s]);  // one of two; the other comes after the tile's accumulators were taken
                 if (!add) continue;
                 if (m > 0) go = mbar_wait_or_abort(&sm.acc_empty[p], (uint32_t)(m - 1) & 1u, abort_flag);
+                if (go && g.keep && fresh) {
+                    if (loads > 0) mma_commit(&sm.kept_empty);  // arrives when the MMAs so far are done
+                    go = mbar_wait_or_abort(&sm.kept_full, (uint32_t)loads & 1u, abort_flag);
+                    ++loads;
+                }
                 if (!go) break;
                 tc_after_sync();
-                const uint32_t at = smem_u32(ring + (size_t)s * stage_bytes + kExTile);
-                const uint64_t hd = sw128_desc(at, (uint32_t)h_box, 1024),
-                               wd = sw128_desc(at + 2 * (uint32_t)h_box, 0, 1024);
+                const uint32_t at = smem_u32(ring + (size_t)s * stage_bytes);
+                const uint64_t hd = sw128_desc(g.keep ? smem_u32(kept) : at + kExTile, (uint32_t)h_box, 1024),
+                               wd = sw128_desc(at + (uint32_t)w_at, 0, 1024);
                 for (int k = 0, r = 0; k < R / 8; ++k) {  // rows 16 k .. of the state, r .. of the adapter
                     mma_f16(tmem + (uint32_t)(p * kBlk), hd + (2048u >> 4) * k, wd + (uint32_t)(r * 128 >> 4), idesc,
                             k > 0);
@@ -916,8 +983,7 @@ cudaError_t lora_tc_shrink(const adaln_rows &src, const void *W, const LoraCall 
     g.Rp = (c.R + 15) / 16 * 16;
     const int KB = (C + kBlk - 1) / kBlk;
     g.ks = KB <= 12 ? 1 : KB <= 24 ? 2 : KB <= 48 ? 4 : 8;
-    while (g.Rp / 4 % g.ks != 0) g.ks /= 2;
-    const int stage = kRowTile + g.Rp * kBlk * 2, part = g.Rp * kM * 4;
+    const int stage = kRowTile + g.Rp * kBlk * 2, part = g.Rp * kPartPitch * 4;
     g.stages = stages_for(stage, part);
     g.tmem_cols = tmem_columns(g.Rp);
     CUtensorMap map_x, map_w;
@@ -968,15 +1034,17 @@ cudaError_t lora_tc_expand(const void *h, const void *W, const LoraCall &c, int 
                                : make_map_3d(&map_y, c.out.data, C, c.S, c.B, c.out.token, c.out.batch, kM)))
         return cudaErrorInvalidValue;
     g.B = c.B;
-    const int stage = kExTile + 4 * c.R * 128 + g.copies * c.R * 128;
+    g.keep = c.R > 32;
+    const int state = 4 * c.R * 128, stage = kExTile + g.copies * c.R * 128 + (g.keep ? 0 : state);
+    const int beside = (g.keep ? state : 0) + kBarBytes + 1024;
     // 2 or 4 stages, whichever gives an SM more of them in all: 8 up to rank 16, 6 up
-    // to 32, 4 up to 64, 2 beyond 104
+    // to 48, 4 beyond
     int per_sm = 0;
     for (int n = 2; n <= kExStages; n += 2) {
-        const int ctas = std::min(kExCtas, 228 * 1024 / (n * stage + kBarBytes + 2 * 1024));
+        const int ctas = std::min(kExCtas, 228 * 1024 / (n * stage + beside + 1024));
         if (n * ctas > g.stages * per_sm) g.stages = n, per_sm = ctas;
     }
-    const size_t smem = (size_t)g.stages * stage + kBarBytes + 1024;
+    const size_t smem = (size_t)g.stages * stage + beside;
     const long long most = (long long)((C + kBlk - 1) / kBlk) * ((c.S + kM - 1) / kM) * c.B, room = (long long)per_sm * dev.sm_count;
     cudaError_t err = ensure_smem_attr((const void *)lora_expand_tc_kernel, smem, dev);
     if (err != cudaSuccess) return err;
