@@ -448,6 +448,21 @@ lora_join_kernel(const GradOperand o0, const GradOperand o1, const void *ids, in
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     bool any = false;
     const int lane = threadIdx.x & 31;
+    constexpr int kSide = 8;  // pieces requested at once, of one sample or of several
+    const float4 *at[kSide];
+    int k = 0;
+    auto add = [&] {
+        float4 v[kSide];
+#pragma unroll
+        for (int j = 0; j < kSide; ++j)
+            if (live && j < k) v[j] = __ldcs(at[j]);
+#pragma unroll
+        for (int j = 0; j < kSide; ++j)
+            if (j < k)
+                s = make_float4(__fadd_rn(s.x, v[j].x), __fadd_rn(s.y, v[j].y), __fadd_rn(s.z, v[j].z),
+                                __fadd_rn(s.w, v[j].w));
+        k = 0;
+    };
     for (int b0 = 0; b0 < B; b0 += 32) {
         // the samples of adapter a among the next 32, and their rows, by a lane each
         const int mine = b0 + lane;
@@ -455,18 +470,19 @@ lora_join_kernel(const GradOperand o0, const GradOperand o1, const void *ids, in
         const int n = mine < B ? rows_of(lens, mine, S) : 0;
         for (; left; left &= left - 1) {
             const int b = b0 + __ffs(left) - 1;
-            const int k = (__shfl_sync(0xFFFFFFFFu, n, b - b0) + piece_rows - 1) / piece_rows;
-            if (!live) continue;
-            if (!any && accumulate) s = *p;
+            const int here = (__shfl_sync(0xFFFFFFFFu, n, b - b0) + piece_rows - 1) / piece_rows;
+            if (!any && accumulate && live) s = *p;
             any = true;
             const float4 *q = reinterpret_cast<const float4 *>(o.part + (long long)b * pieces * size) + i;
-#pragma unroll 8
-            for (int j = 0; j < k; ++j) {
-                const float4 v = __ldcs(q + j * (size / 4));
-                s = make_float4(__fadd_rn(s.x, v.x), __fadd_rn(s.y, v.y), __fadd_rn(s.z, v.z), __fadd_rn(s.w, v.w));
+            for (int j = 0; j < here; ++j, q += size / 4) {
+#pragma unroll
+                for (int m = 0; m < kSide; ++m)
+                    if (m == k) at[m] = q;
+                if (++k == kSide) add();
             }
         }
     }
+    add();
     if (!live) return;
     if (any || !accumulate) *p = s;
 }

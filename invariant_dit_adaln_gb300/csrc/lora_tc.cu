@@ -137,6 +137,11 @@ __device__ __forceinline__ bool named_bar_and(int id, int count, bool flag) {
     return r != 0;
 }
 
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(c0), "r"(c1),
+                 "r"(c2)
+                 : "memory");
+}
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -174,14 +179,17 @@ __device__ __forceinline__ bool first_wait(TcBars &sm) {
 #endif
 }
 
-// v as three bf16 parts (an infinity is the first)
-__device__ __forceinline__ void three_parts(float v, uint16_t (&p)[3]) {
-    p[0] = bf16_bits(v);
-    p[1] = p[2] = 0;
-    if ((p[0] & 0x7FFFu) == 0x7F80u) return;
-    const float rest = __fsub_rn(v, bf16f(p[0]));
-    p[1] = bf16_bits(rest);
-    p[2] = bf16_bits(__fsub_rn(rest, bf16f(p[1])));
+// A pair as three bf16x2 words, whose halves' sums are a and b (an infinity or a NaN
+// is the first part)
+__device__ __forceinline__ void three_parts(float a, float b, uint32_t (&p)[3]) {
+    auto rest = [](float v, float part) {
+        const float r = __fsub_rn(v, part);
+        return fabsf(r) <= 3.4e38f ? r : 0.0f;
+    };
+    p[0] = pack_bf16x2(a, b);
+    a = rest(a, bf16lo(p[0])), b = rest(b, bf16hi(p[0]));
+    p[1] = pack_bf16x2(a, b);
+    p[2] = pack_bf16x2(__fsub_rn(a, bf16lo(p[1])), __fsub_rn(b, bf16hi(p[1])));
 }
 
 // --------------------------------------------------------------------------
@@ -235,7 +243,6 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
     const int n = rows_of(g.lens, b, g.S);
     // no adapter, or no row of this tile: nothing reads its state (the whole cluster leaves)
     const bool idle = a < 0 || t0 >= n;
-    const float scale = idle ? 0.0f : g.scale[a];
     auto copy = [&](int i) {  // block i of this range
         const int s = i % g.stages;
         unsigned char *st = ring + (size_t)s * stage_bytes;
@@ -245,8 +252,11 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
     };
     // the first copies before the CTAs of the cluster meet
     const int early = idle ? 0 : min(nkb, g.stages);
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
         for (int i = 0; i < early; ++i) copy(i);
+        // the ring is short beside the latency: the rest is asked of memory at once, and found in L2
+        for (int i = early; i < (idle ? 0 : nkb); ++i) tma_prefetch_3d(&map_x, (kb0 + i) * kBlk, t0, b);
+    }
     tc_before_sync();
     if (g.ks > 1 && !idle)
         cluster_sync();  // also: the cluster's CTAs run, so their shared memory may be written
@@ -311,10 +321,11 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
         tmem_ld16(trow + (uint32_t)c, v);
         tmem_ld_done();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < 16; k += 2) {  // a slice is even
             st_cluster_f32(at, __uint_as_float(v[k]));
-            at += kPartPitch * 4;
-            if (++i == slice && ++q < g.ks) {
+            st_cluster_f32(at + kPartPitch * 4, __uint_as_float(v[k + 1]));
+            at += 2 * kPartPitch * 4;
+            if ((i += 2) == slice && ++q < g.ks) {
                 i = 0;
                 at = map_to_rank(part + (int)rank * slice * kPartPitch + threadIdx.x, (uint32_t)q);
             }
@@ -326,6 +337,7 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
     else
         __syncthreads();
     // a thread joins 8 tokens of a rank: 16 bytes of each part of the state
+    const float scale = g.scale[a];
     uint16_t *h = g.h + (size_t)b * 3 * g.R * g.Sp + t0;
     for (int k = threadIdx.x; ok && k < slice * (kM / 8); k += 128) {
         const int i = k / (kM / 8), t = k % (kM / 8) * 8, r = (int)rank * slice + i;
@@ -338,18 +350,17 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[j] = q == 0 ? f[j] : __fadd_rn(s[j], f[j]);
         }
-        uint32_t w[3][4];
+        if (t0 + t + 8 > n)  // rows past the sample's end: zero, which grad relies on
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            uint16_t lo[3] = {0, 0, 0}, hi[3] = {0, 0, 0};  // rows past the sample's end: zero, which grad relies on
-            if (t0 + t + j < n) three_parts(__fmul_rn(scale, s[j]), lo);
-            if (t0 + t + j + 1 < n) three_parts(__fmul_rn(scale, s[j + 1]), hi);
+            for (int j = 0; j < 8; ++j)
+                if (t0 + t + j >= n) s[j] = 0.0f;
+        uint32_t w[4][3];
 #pragma unroll
-            for (int m = 0; m < 3; ++m) w[m][j / 2] = (uint32_t)lo[m] | (uint32_t)hi[m] << 16;
-        }
+        for (int j = 0; j < 4; ++j) three_parts(__fmul_rn(scale, s[2 * j]), __fmul_rn(scale, s[2 * j + 1]), w[j]);
+        uint16_t *dst = h + (size_t)r * g.Sp + t;
 #pragma unroll
         for (int m = 0; m < 3; ++m)
-            stg16(h + (size_t)(m * g.R + r) * g.Sp + t, make_uint4(w[m][0], w[m][1], w[m][2], w[m][3]));
+            stg16(dst + (size_t)m * g.R * g.Sp, make_uint4(w[0][m], w[1][m], w[2][m], w[3][m]));
     }
     if (warp == 1) {
         tc_after_sync();
@@ -712,8 +723,10 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
 //
 // Schedules and order as lora_grad_kernel's: OWNER, every piece of an adapter in
 // order by one CTA, with two accumulators (where they fit), so that one piece's
-// leave while the next one's MMAs run, and the total in shared memory; otherwise a
-// CTA one or two pieces.
+// leave while the next one's MMAs run, and the total in shared memory; otherwise as
+// many CTAs as the device holds take every gridDim.x-th piece of every tile.  (A CTA a
+// piece or two: 30 us for 8192 rows of 3072 and 3072 channels at rank 16, a quarter of
+// it the last CTAs.)
 //
 // Roles (192 threads): warp 0 lane 0 the copies, warp 1 the MMAs (and zeros for
 // the rows of a block past the sample's end, which may hold anything), warps 2
@@ -730,8 +743,52 @@ struct GradArgs {
     int B, S, R, NA, pieces;
     int Np;    // 3 R rounded up to 16
     int bufs;  // accumulators
-    int cta_pieces;  // pieces of a CTA (not OWNER)
     int stages, tmem_cols;
+};
+
+// The pieces x, x + step, ... among those that are (samples with an adapter, rows),
+// for a warp: it goes through the samples 32 at a time, the next ones' ids and lengths
+// on their way.
+struct GradPieces {
+    const GradArgs &g;
+    int w0;           // first sample of the window
+    long long before; // pieces of the samples before it
+    int rows, upto;   // this lane's sample: its rows (0 without an adapter), and the pieces up to its end
+    int next_rows;    // the same of the next window's
+    __device__ __forceinline__ GradPieces(const GradArgs &args, int lane) : g(args), w0(0), before(0) {
+        next_rows = rows_at(lane);
+        window(lane);
+    }
+    __device__ __forceinline__ int rows_at(int b) const {
+        return b < g.B && adapter_of(g.ids, g.is64, b, g.NA) >= 0 ? rows_of(g.lens, b, g.S) : 0;
+    }
+    __device__ __forceinline__ void window(int lane) {
+        rows = next_rows;
+        next_rows = rows_at(w0 + 32 + lane);
+        upto = (rows + kLoraTcPiece - 1) / kLoraTcPiece;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d) upto += v;
+        }
+    }
+    // piece u (u ascending from call to call): rows [s0, s1) of sample b; false: there are not that many
+    __device__ __forceinline__ bool find(long long u, int lane, int &b, int &s0, int &s1) {
+        unsigned past;
+        for (;;) {  // the first sample whose end lies beyond u
+            past = __ballot_sync(0xFFFFFFFFu, before + upto > u);
+            if (past || w0 + 32 >= g.B) break;
+            before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+            w0 += 32;
+            window(lane);
+        }
+        if (!past) return false;
+        const int i = __ffs(past) - 1, n = __shfl_sync(0xFFFFFFFFu, rows, i), end = __shfl_sync(0xFFFFFFFFu, upto, i);
+        b = w0 + i;
+        s0 = (int)(u - before - (end - (n + kLoraTcPiece - 1) / kLoraTcPiece)) * kLoraTcPiece;
+        s1 = min(n, s0 + kLoraTcPiece);
+        return true;
+    }
 };
 
 template <bool OWNER>
@@ -749,45 +806,151 @@ lora_grad_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     __shared__ int count[kGradThreads / 32];
     volatile int *abort_flag = &sm.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool first = (int)blockIdx.x < g.o[0].blocks;
-    const GradOperand &o = g.o[first ? 0 : 1];
-    const CUtensorMap *map_src = first ? &map_x : &map_d, *map_state = first ? &map_e : &map_h;
-    const int c0 = ((int)blockIdx.x - (first ? 0 : g.o[0].blocks)) * kM;
-    pdl_wait();
-    int samples = 1, s_begin = 0, s_most = g.S;
-    const int a = OWNER ? (int)blockIdx.y : adapter_of(g.ids, g.is64, blockIdx.z, g.NA);
-    if (!OWNER) {
-        s_begin = blockIdx.y * g.cta_pieces * kLoraTcPiece;
-        s_most = s_begin + g.cta_pieces * kLoraTcPiece;
-        if (a < 0 || s_begin >= rows_of(g.lens, blockIdx.z, g.S)) return;
+    const int tiles = g.o[0].blocks + g.o[1].blocks;
+    if (threadIdx.x == 0) {
+        prefetch_map(&map_x), prefetch_map(&map_e), prefetch_map(&map_d), prefetch_map(&map_h);
+        bars_init(sm, 128);
     }
-    if (threadIdx.x == 0) bars_init(sm, 128);
     if (warp == 1) tmem_alloc(&sm.tmem, g.tmem_cols);
+    pdl_wait();
     tc_before_sync();
     __syncthreads();
     pdl_trigger();
     tc_after_sync();
     const uint32_t tmem = sm.tmem;
 
-    // this thread's channel (warps 2 to 5; a warp reads the tensor memory of lanes 32 (warp mod 4) ..)
+    // warps 2 to 5: this thread's channel of a tile (a warp reads the tensor memory of lanes 32 (warp mod 4) ..)
     const int lane_row = (warp & 3) * 32 + lane;
-    const int c = c0 + lane_row;
-    const bool holds = warp >= 2 && c < o.C;
     int blk = 0, unit = 0, issued = 0;  // blocks and pieces taken so far, by each role
-    bool any = false, ok = true;
+    bool ok = true;
     const int Na = Np <= 256 ? Np : 256;  // columns of the first MMA; the second's, if any: Np - Na
     const uint32_t idesc = f16_idesc(Na, true), idesc_b = f16_idesc(Np - Na, true);
 
-    for (int b0 = 0; b0 < (OWNER ? g.B : 1); b0 += kGradThreads) {
-        if (OWNER) {
+    // One piece: rows [s0, s1) of sample b, channels from c0 of operand o.  Each role does its part.
+    auto piece = [&](const GradOperand &o, bool x_side, int c0, int b, int s0, int s1) {
+        const int nblk = (s1 - s0 + kBlk - 1) / kBlk;
+        const int p = unit % g.bufs, use = unit / g.bufs;  // accumulator
+        if (warp == 0) {
+            const CUtensorMap *map_src = x_side ? &map_x : &map_d, *map_state = x_side ? &map_e : &map_h;
+            if (lane == 0)
+                for (int k = 0; k < nblk; ++k, ++blk) {
+                    const int st = blk % g.stages;
+                    if (blk >= g.stages &&
+                        !mbar_wait_or_abort(&sm.empty[st], (uint32_t)(blk / g.stages - 1) & 1u, abort_flag)) {
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                    unsigned char *q = ring + (size_t)st * stage_bytes;
+                    const int s = s0 + k * kBlk;
+                    mbar_arrive_expect_tx(&sm.full[st], (uint32_t)stage_bytes);
+                    tma_load_3d(q, map_src, c0, s, b, &sm.full[st]);
+                    tma_load_3d(q + kRowTile / 2, map_src, c0 + kBlk, s, b, &sm.full[st]);
+                    tma_load_3d(q + kRowTile, map_state, s, 0, b, &sm.full[st]);
+                    if (Np > 256) tma_load_3d(q + kRowTile + h_tile / 2, map_state, s, Np / 2, b, &sm.full[st]);
+                    issued = blk + 1;
+                }
+        } else if (warp == 1) {
+            const uint32_t acc = tmem + (uint32_t)(p * Np);
+            bool go = unit > 0 || first_wait(sm);
+            if (use > 0) go = go && mbar_wait_or_abort(&sm.acc_empty[p], (uint32_t)(use - 1) & 1u, abort_flag);
+            go = __all_sync(0xFFFFFFFFu, go);
+            for (int k = 0; k < nblk && go; ++k, ++blk) {
+                const int st = blk % g.stages;
+                go = mbar_wait_or_abort(&sm.full[st], (uint32_t)(blk / g.stages) & 1u, abort_flag);
+                go = __all_sync(0xFFFFFFFFu, go);
+                if (!go) break;
+                unsigned char *tile = ring + (size_t)st * stage_bytes;
+                const int left = s1 - s0 - k * kBlk;
+                if (left < kBlk && s1 < g.S) {
+                    // rows past the sample's end: their state is zero, and zero times NaN is not
+                    for (int z = left * 8 + lane; z < kBlk * 8; z += 32) {
+                        stg16(tile + z * 16, make_uint4(0u, 0u, 0u, 0u));
+                        stg16(tile + kRowTile / 2 + z * 16, make_uint4(0u, 0u, 0u, 0u));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    tc_after_sync();
+                    const uint32_t at = smem_u32(tile);
+                    // 16 tokens further: two groups of 8 rows of A, 32 bytes of B
+                    const uint64_t ad = sw128_desc(at, kRowTile / 2, 1024), hd = sw128_desc(at + kRowTile, 16, 1024);
+#pragma unroll
+                    for (int q = 0; q < kBlk / 16; ++q) {
+                        mma_f16(acc, ad + (2048u >> 4) * q, hd + 2u * q, idesc, k > 0 || q > 0);
+                        if (Np > Na)
+                            mma_f16(acc + (uint32_t)Na, ad + (2048u >> 4) * q,
+                                    hd + (uint32_t)(Na * kBlk * 2 >> 4) + 2u * q, idesc_b, k > 0 || q > 0);
+                    }
+                    mma_commit(&sm.empty[st]);
+                }
+                __syncwarp();
+            }
+            if (!go) {
+                *abort_flag = 1;
+                ok = false;
+            } else if (lane == 0) {
+                mma_commit(&sm.acc_full[p]);
+            }
+        } else {
+            ok = mbar_wait_or_abort(&sm.acc_full[p], (uint32_t)use & 1u, abort_flag) && !*abort_flag;
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) {
+                *abort_flag = 1;
+            } else {
+                tc_after_sync();
+                const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(p * Np);
+                const int c = c0 + lane_row;
+                float *dst = o.part + (b * (long long)g.pieces + s0 / kLoraTcPiece) * R * o.C + c;
+                for (int r = 0; r < R; r += 8) {
+                    uint32_t hi[8], mid[8], lo[8];
+                    tmem_ld8(at + (uint32_t)r, hi);
+                    tmem_ld8(at + (uint32_t)(R + r), mid);
+                    tmem_ld8(at + (uint32_t)(2 * R + r), lo);
+                    tmem_ld_done();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float v = __fadd_rn(__uint_as_float(hi[j]),
+                                                  __fadd_rn(__uint_as_float(mid[j]), __uint_as_float(lo[j])));
+                        if (OWNER) {
+                            float *t = total + (r + j) * kM + lane_row;
+                            *t = __fadd_rn(*t, v);
+                        } else if (c < o.C) {
+                            dst[(long long)(r + j) * o.C] = v;
+                        }
+                    }
+                }
+                tc_before_sync();
+                mbar_arrive(&sm.acc_empty[p]);
+            }
+        }
+        ++unit;
+    };
+
+    if constexpr (!OWNER) {
+        GradPieces pieces(g, lane);
+        for (long long u = blockIdx.x; __all_sync(0xFFFFFFFFu, ok); u += gridDim.x) {
+            const long long v = u / tiles;
+            const int tile = (int)(u - v * tiles);
+            int b, s0, s1;
+            if (!pieces.find(v, lane, b, s0, s1)) break;
+            const bool x_side = tile < g.o[0].blocks;
+            piece(g.o[x_side ? 0 : 1], x_side, (tile - (x_side ? 0 : g.o[0].blocks)) * kM, b, s0, s1);
+        }
+    } else {
+        const bool x_side = (int)blockIdx.x < g.o[0].blocks;
+        const GradOperand &o = g.o[x_side ? 0 : 1];
+        const int c0 = ((int)blockIdx.x - (x_side ? 0 : g.o[0].blocks)) * kM, c = c0 + lane_row, a = blockIdx.y;
+        bool any = false;
+        for (int b0 = 0; b0 < g.B; b0 += kGradThreads) {
             // the samples of adapter a among the next ones, in order
             const int b = b0 + threadIdx.x;
             const bool mine = b < g.B && adapter_of(g.ids, g.is64, b, g.NA) == a;
             const unsigned vote = __ballot_sync(0xFFFFFFFFu, mine);
             if (lane == 0) count[warp] = __popc(vote);
             __syncthreads();
-            int before = 0;
-            samples = 0;
+            int before = 0, samples = 0;
             for (int w = 0; w < kGradThreads / 32; ++w) {
                 if (w < warp) before += count[w];
                 samples += count[w];
@@ -801,117 +964,18 @@ lora_grad_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                         total[r * kM + lane_row] =
                             g.accumulate && c < o.C ? o.acc[((long long)a * R + r) * o.C + c] : 0.0f;
             }
-        }
-        for (int i = 0; i < samples && ok; ++i) {
-            const int b = OWNER ? found[i] : (int)blockIdx.z;
-            const int n = rows_of(g.lens, b, g.S);
-            for (int s0 = s_begin; s0 < min(n, s_most) && ok; s0 += kLoraTcPiece, ++unit) {
-                const int s1 = min(n, s0 + kLoraTcPiece), nblk = (s1 - s0 + kBlk - 1) / kBlk;
-                if (warp == 0) {
-                    if (lane == 0)
-                        for (int k = 0; k < nblk; ++k, ++blk) {
-                            const int st = blk % g.stages;
-                            if (blk >= g.stages &&
-                                !mbar_wait_or_abort(&sm.empty[st], (uint32_t)(blk / g.stages - 1) & 1u, abort_flag)) {
-                                *abort_flag = 1;
-                                ok = false;
-                                break;
-                            }
-                            unsigned char *p = ring + (size_t)st * stage_bytes;
-                            const int s = s0 + k * kBlk;
-                            mbar_arrive_expect_tx(&sm.full[st], (uint32_t)stage_bytes);
-                            tma_load_3d(p, map_src, c0, s, b, &sm.full[st]);
-                            tma_load_3d(p + kRowTile / 2, map_src, c0 + kBlk, s, b, &sm.full[st]);
-                            tma_load_3d(p + kRowTile, map_state, s, 0, b, &sm.full[st]);
-                            if (Np > 256) tma_load_3d(p + kRowTile + h_tile / 2, map_state, s, Np / 2, b, &sm.full[st]);
-                            issued = blk + 1;
-                        }
-                } else if (warp == 1) {
-                    const int p = unit % g.bufs, use = unit / g.bufs;
-                    const uint32_t acc = tmem + (uint32_t)(p * Np);
-                    bool go = unit > 0 || first_wait(sm);
-                    if (use > 0)
-                        go = go && mbar_wait_or_abort(&sm.acc_empty[p], (uint32_t)(use - 1) & 1u, abort_flag);
-                    go = __all_sync(0xFFFFFFFFu, go);
-                    for (int k = 0; k < nblk && go; ++k, ++blk) {
-                        const int st = blk % g.stages;
-                        go = mbar_wait_or_abort(&sm.full[st], (uint32_t)(blk / g.stages) & 1u, abort_flag);
-                        go = __all_sync(0xFFFFFFFFu, go);
-                        if (!go) break;
-                        unsigned char *tile = ring + (size_t)st * stage_bytes;
-                        const int left = s1 - s0 - k * kBlk;
-                        if (left < kBlk && s0 + k * kBlk + left < g.S) {
-                            // rows past the sample's end: their state is zero, and zero times NaN is not
-                            for (int z = left * 8 + lane; z < kBlk * 8; z += 32) {
-                                stg16(tile + z * 16, make_uint4(0u, 0u, 0u, 0u));
-                                stg16(tile + kRowTile / 2 + z * 16, make_uint4(0u, 0u, 0u, 0u));
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                        if (lane == 0) {
-                            tc_after_sync();
-                            const uint32_t at = smem_u32(tile);
-                            // 16 tokens further: two groups of 8 rows of A, 32 bytes of B
-                            const uint64_t ad = sw128_desc(at, kRowTile / 2, 1024),
-                                           hd = sw128_desc(at + kRowTile, 16, 1024);
-#pragma unroll
-                            for (int q = 0; q < kBlk / 16; ++q) {
-                                mma_f16(acc, ad + (2048u >> 4) * q, hd + 2u * q, idesc, k > 0 || q > 0);
-                                if (Np > Na)
-                                    mma_f16(acc + (uint32_t)Na, ad + (2048u >> 4) * q,
-                                            hd + (uint32_t)(Na * kBlk * 2 >> 4) + 2u * q, idesc_b, k > 0 || q > 0);
-                            }
-                            mma_commit(&sm.empty[st]);
-                        }
-                        __syncwarp();
-                    }
-                    if (!go) {
-                        *abort_flag = 1;
-                        ok = false;
-                    } else if (lane == 0) {
-                        mma_commit(&sm.acc_full[p]);
-                    }
-                } else {
-                    const int p = unit % g.bufs;
-                    ok = mbar_wait_or_abort(&sm.acc_full[p], (uint32_t)(unit / g.bufs) & 1u, abort_flag) &&
-                         !*abort_flag;
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) {
-                        *abort_flag = 1;
-                    } else {
-                        tc_after_sync();
-                        const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(p * Np);
-                        float *dst = o.part + ((long long)(b * (long long)g.pieces + s0 / kLoraTcPiece) * R) * o.C + c;
-                        for (int r = 0; r < R; r += 8) {
-                            uint32_t hi[8], mid[8], lo[8];
-                            tmem_ld8(at + (uint32_t)r, hi);
-                            tmem_ld8(at + (uint32_t)(R + r), mid);
-                            tmem_ld8(at + (uint32_t)(2 * R + r), lo);
-                            tmem_ld_done();
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float v = __fadd_rn(__uint_as_float(hi[j]), __fadd_rn(__uint_as_float(mid[j]),
-                                                                                           __uint_as_float(lo[j])));
-                                if (OWNER) {
-                                    float *t = total + (r + j) * kM + lane_row;
-                                    *t = __fadd_rn(*t, v);
-                                } else if (holds) {
-                                    dst[(long long)(r + j) * o.C] = v;
-                                }
-                            }
-                        }
-                        tc_before_sync();
-                        mbar_arrive(&sm.acc_empty[p]);
-                    }
-                }
+            for (int i = 0; i < samples && ok; ++i) {
+                const int n = rows_of(g.lens, found[i], g.S);
+                for (int s0 = 0; s0 < n && ok; s0 += kLoraTcPiece)
+                    piece(o, x_side, c0, found[i], s0, min(n, s0 + kLoraTcPiece));
             }
-        }
-        if (OWNER) {
             // found[] is written again; a role that gave up takes the others with it
             ok = __syncthreads_and(ok && !*abort_flag);
             if (!ok) break;
         }
+        if (ok && warp >= 2 && c < o.C && (any || !g.accumulate))
+            for (int r = 0; r < R; ++r)
+                o.acc[((long long)a * R + r) * o.C + c] = any ? total[r * kM + lane_row] : 0.0f;
     }
     // every copy issued lands and every MMA ends before the CTA leaves
     if (warp == 0 && lane == 0) {
@@ -925,8 +989,6 @@ lora_grad_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         if (!mbar_wait_bounded(&sm.done, 0u, kDrainNs)) report_error_lora(kErrDrainFailed);
     }
     __syncwarp();
-    if (OWNER && ok && holds && (any || !g.accumulate))
-        for (int r = 0; r < R; ++r) o.acc[((long long)a * R + r) * o.C + c] = any ? total[r * kM + lane_row] : 0.0f;
     tc_before_sync();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) report_error_lora(kErrLoraGradWait);
@@ -1060,12 +1122,12 @@ cudaError_t lora_tc_grads(const GradOperand &o0, const GradOperand &o1, const Lo
     g.ids = c.ids, g.is64 = c.ids_are_64, g.lens = c.lens, g.accumulate = c.accumulate;
     g.B = c.B, g.S = c.S, g.R = c.R, g.NA = c.NA, g.pieces = (c.S + kLoraTcPiece - 1) / kLoraTcPiece;
     g.Np = (3 * c.R + 15) / 16 * 16;
-    const unsigned x = (unsigned)(g.o[0].blocks + g.o[1].blocks);
-    // two pieces a CTA where that still gives every SM two: the CTA's start is paid once
-    g.cta_pieces = (long long)x * g.pieces * c.B >= 4ll * dev.sm_count ? 2 : 1;
-    g.bufs = (!in_parts || g.cta_pieces > 1) && g.Np <= 256 ? 2 : 1;
     const int stage = kRowTile + g.Np * kBlk * 2, extra = in_parts ? 0 : c.R * kM * 4;
     g.stages = stages_for(stage, extra);
+    const size_t smem = (size_t)g.stages * stage + extra + kBarBytes + 1024;
+    const int per_sm = smem <= 113 * 1024 ? 2 : 1;
+    // two accumulators where the SM's CTAs all find room for them: one that did not would wait for another's end
+    g.bufs = 2 * g.Np <= 512 && tmem_columns(2 * g.Np) * per_sm <= 512 ? 2 : 1;
     g.tmem_cols = tmem_columns(g.bufs * g.Np);
     const int h_box = g.Np <= 256 ? g.Np : g.Np / 2;  // a box has at most 256 rows
     const int Sp = padded_tokens(c.S);
@@ -1075,12 +1137,12 @@ cudaError_t lora_tc_grads(const GradOperand &o0, const GradOperand &o1, const Lo
         !make_map_3d(&map_d, o1.src, o1.C, c.S, c.B, o1.token, o1.batch, kBlk) ||
         !make_map_3d(&map_h, o1.h, Sp, 3 * c.R, c.B, Sp, (int64_t)3 * c.R * Sp, h_box))
         return cudaErrorInvalidValue;
-    const size_t smem = (size_t)g.stages * stage + extra + kBarBytes + 1024;
     auto kern = in_parts ? lora_grad_tc_kernel<false> : lora_grad_tc_kernel<true>;
     cudaError_t err = ensure_smem_attr((const void *)kern, smem, dev);
     if (err != cudaSuccess) return err;
-    const dim3 grid = in_parts ? dim3(x, (unsigned)((g.pieces + g.cta_pieces - 1) / g.cta_pieces), (unsigned)c.B)
-                               : dim3(x, (unsigned)c.NA);
+    const int tiles = g.o[0].blocks + g.o[1].blocks;
+    const long long units = (long long)tiles * g.pieces * c.B, room = (long long)per_sm * dev.sm_count;
+    const dim3 grid = in_parts ? dim3((unsigned)std::min(units, room)) : dim3((unsigned)tiles, (unsigned)c.NA);
     return launch_pdl(kern, grid, dim3(kGradThreads), smem, stream, map_x, map_e, map_d, map_h, g);
 }
 
