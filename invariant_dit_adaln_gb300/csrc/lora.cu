@@ -71,22 +71,22 @@ __device__ __forceinline__ float scatter_sum(float (&a)[NV], int lane) {
 }
 
 // --------------------------------------------------------------------------
-// shrink: a warp (KS == 1) or the CTA's four warps (KS == 4, the channels split
-// among them) form kRB ranks of TOK tokens of a sample.  A lane takes the 16-byte
+// shrink: the CTA's KS warps, the channels split among them, form kRB ranks of TOK
+// tokens of a sample.  A lane takes the 16-byte
 // vectors of its share in ascending order (NV of them requested at once), even and
 // odd channels in the halves of a packed accumulator; halves, butterfly, warps
 // ascending.  State fp32 [B,S,R].
 // --------------------------------------------------------------------------
 template <typename T, int TOK, int KS, int NV>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(KS * 32)
 lora_shrink_kernel(const T *__restrict__ src, long long batch, long long token, const T *__restrict__ W,
                    const float *__restrict__ scale, const void *ids, int is64, const int *lens,
                    float *__restrict__ h, int S, int C, int R, int NA) {
-    constexpr int E = Vec<T>::E, V = TOK * kRB;
+    constexpr int E = Vec<T>::E, V = TOK * kRB, kStep = KS * 32;
     __shared__ float part[KS][V];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.z, r0 = blockIdx.y * kRB;
-    const int s0 = (KS == 4 ? blockIdx.x : blockIdx.x * 4 + warp) * TOK;
+    const int s0 = blockIdx.x * TOK;
     pdl_wait();
     pdl_trigger();
     const int a = adapter_of(ids, is64, b, NA);
@@ -98,8 +98,7 @@ lora_shrink_kernel(const T *__restrict__ src, long long batch, long long token, 
         for (int r = 0; r < kRB; ++r) acc[i][r] = 0ull;
     if (n > 0) {
         const T *w = W + ((long long)a * R + r0) * C, *x = src + b * batch + s0 * token;
-        constexpr int kStep = KS * 32;
-        for (int v0 = KS == 4 ? (int)threadIdx.x : lane; v0 < C / E; v0 += NV * kStep) {
+        for (int v0 = threadIdx.x; v0 < C / E; v0 += NV * kStep) {
             Vec<T> xv[NV][TOK], wv[NV][kRB];
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
@@ -139,13 +138,11 @@ lora_shrink_kernel(const T *__restrict__ src, long long batch, long long token, 
 #pragma unroll
         for (int r = 0; r < kRB; ++r) sum[i * kRB + r] = __fadd_rn(px_lo(acc[i][r]), px_hi(acc[i][r]));
     float mine = scatter_sum<V>(sum, lane);
-    if (KS == 4) {
-        if (lane < V) part[warp & (KS - 1)][lane] = mine;
-        __syncthreads();
-        if (warp > 0) return;
-        if (lane < V)
-            for (int k = 1; k < KS; ++k) mine = __fadd_rn(mine, part[k][lane]);
-    }
+    if (lane < V) part[warp][lane] = mine;
+    __syncthreads();
+    if (warp > 0) return;
+    if (lane < V)
+        for (int k = 1; k < KS; ++k) mine = __fadd_rn(mine, part[k][lane]);
     // every row of the state is written: zeros where there is no adapter or no row
     if (lane < V && s0 + lane / kRB < S) {
         const float c = a < 0 ? 0.0f : scale[a];
@@ -172,7 +169,14 @@ lora_expand_kernel(const float *__restrict__ h, const T *__restrict__ W, const v
     if (n <= 0) return;
     const int a = adapter_of(ids, is64, b, NA);
     if (a < 0 && base == out) return;
-    Vec<T> y[TOK];
+    // the base and the first ranks are requested before the state has come
+    const T *w = W + (long long)max(a, 0) * R * C + c0;
+    Vec<T> y[TOK], wv[kRB];
+#pragma unroll
+    for (int r = 0; r < kRB; ++r) {
+        wv[r].zero();
+        if (a >= 0 && c0 < C) wv[r].load(w + (long long)r * C);
+    }
 #pragma unroll
     for (int i = 0; i < TOK; ++i) {
         y[i].zero();
@@ -191,11 +195,10 @@ lora_expand_kernel(const float *__restrict__ h, const T *__restrict__ W, const v
 #pragma unroll
         for (int q = 0; q < E / 2; ++q) acc[i][q] = 0ull;
     if (a >= 0) {
-        const T *w = W + (long long)a * R * C + c0;
         for (int r0 = 0; r0 < R; r0 += kRB) {
-            Vec<T> wv[kRB];
+            if (r0 > 0)
 #pragma unroll
-            for (int r = 0; r < kRB; ++r) wv[r].load(w + (long long)(r0 + r) * C);
+                for (int r = 0; r < kRB; ++r) wv[r].load(w + (long long)(r0 + r) * C);
 #pragma unroll
             for (int r = 0; r < kRB; ++r) {
                 px2 wp[E / 2];
@@ -232,7 +235,7 @@ lora_expand_kernel(const float *__restrict__ h, const T *__restrict__ W, const v
 // channel of a piece moved twice.  lora_grad_owner_kernel: a thread takes every
 // piece of an adapter and writes the accumulator.
 // --------------------------------------------------------------------------
-constexpr int kFlight = 8;
+constexpr int kFlight = 16;  // rows of a warp requested at once
 
 template <typename T>
 struct Four;  // 4 channels of a row
@@ -251,40 +254,48 @@ struct Four<float> {
     __device__ __forceinline__ void pairs(px2 (&x)[2]) const { x[0] = px_make(v.x, v.y), x[1] = px_make(v.z, v.w); }
 };
 
-typedef px2 RankAcc[kRB][2];
-__device__ __forceinline__ void zero_acc(RankAcc &a) {
+// NR ranks of 4 channels
+template <int NR>
+using RankAcc = px2[NR][2];
+template <int NR>
+__device__ __forceinline__ void zero_acc(RankAcc<NR> &a) {
 #pragma unroll
-    for (int r = 0; r < kRB; ++r) a[r][0] = a[r][1] = 0ull;
+    for (int r = 0; r < NR; ++r) a[r][0] = a[r][1] = 0ull;
 }
-__device__ __forceinline__ void add_acc(RankAcc &a, const RankAcc &b) {
+template <int NR>
+__device__ __forceinline__ void add_acc(RankAcc<NR> &a, const RankAcc<NR> &b) {
 #pragma unroll
-    for (int r = 0; r < kRB; ++r) a[r][0] = px_add(a[r][0], b[r][0]), a[r][1] = px_add(a[r][1], b[r][1]);
+    for (int r = 0; r < NR; ++r) a[r][0] = px_add(a[r][0], b[r][0]), a[r][1] = px_add(a[r][1], b[r][1]);
 }
-// a row's products: x of 4 channels, h of kRB ranks in shared memory
-template <typename T>
-__device__ __forceinline__ void add_row(RankAcc &a, const Four<T> &x, const float *h) {
+// a row's products: x of 4 channels, h of NR ranks in shared memory
+template <int NR, typename T>
+__device__ __forceinline__ void add_row(RankAcc<NR> &a, const Four<T> &x, const float *h) {
     px2 xp[2];
     x.pairs(xp);
-    const float4 ha = *reinterpret_cast<const float4 *>(h), hb = *reinterpret_cast<const float4 *>(h + 4);
-    const float hr[kRB] = {ha.x, ha.y, ha.z, ha.w, hb.x, hb.y, hb.z, hb.w};
 #pragma unroll
-    for (int r = 0; r < kRB; ++r) {
-        const px2 e = px_splat(hr[r]);
-        a[r][0] = px_fma(e, xp[0], a[r][0]);
-        a[r][1] = px_fma(e, xp[1], a[r][1]);
+    for (int r4 = 0; r4 < NR; r4 += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(h + r4);
+        const float hr[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const px2 e = px_splat(hr[r]);
+            a[r4 + r][0] = px_fma(e, xp[0], a[r4 + r][0]);
+            a[r4 + r][1] = px_fma(e, xp[1], a[r4 + r][1]);
+        }
     }
 }
-__device__ __forceinline__ float4 of_acc(const RankAcc &a, int r) {
+template <int NR>
+__device__ __forceinline__ float4 of_acc(const RankAcc<NR> &a, int r) {
     return make_float4(px_lo(a[r][0]), px_hi(a[r][0]), px_lo(a[r][1]), px_hi(a[r][1]));
 }
 
-// the operand, rank block and first channel of a CTA; blocks of `width` channels
-__device__ __forceinline__ const GradOperand &grad_place(const GradOperand &o0, const GradOperand &o1, int rb, int width,
-                                                         int &r0, int &c0) {
+// the operand, rank block and first channel of a CTA; rb blocks of `ranks` ranks, blocks of `width` channels
+__device__ __forceinline__ const GradOperand &grad_place(const GradOperand &o0, const GradOperand &o1, int ranks, int rb,
+                                                         int width, int &r0, int &c0) {
     const bool first = (int)blockIdx.x < o0.blocks * rb;
     const GradOperand &o = first ? o0 : o1;
     const int at = first ? blockIdx.x : blockIdx.x - o0.blocks * rb;
-    r0 = at / o.blocks * kRB, c0 = at % o.blocks * width;
+    r0 = at / o.blocks * ranks, c0 = at % o.blocks * width;
     return o;
 }
 
@@ -296,7 +307,7 @@ lora_grad_parts_kernel(const GradOperand o0, const GradOperand o1, const void *i
     __shared__ float4 sums[3][kRB][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int r0, c0;
-    const GradOperand &o = grad_place(o0, o1, R / kRB, 128, r0, c0);
+    const GradOperand &o = grad_place(o0, o1, kRB, R / kRB, 128, r0, c0);
     c0 += lane * 4;
     pdl_wait();
     pdl_trigger();
@@ -308,8 +319,8 @@ lora_grad_parts_kernel(const GradOperand o0, const GradOperand o1, const void *i
         *reinterpret_cast<float4 *>(&hs[i >> 1][(i & 1) * 4]) =
             *reinterpret_cast<const float4 *>(h + (long long)(i >> 1) * R + (i & 1) * 4);
     __syncthreads();
-    RankAcc acc;
-    zero_acc(acc);
+    RankAcc<kRB> acc;
+    zero_acc<kRB>(acc);
     if (c0 < o.C) {
         const T *x = static_cast<const T *>(o.src) + b * o.batch + s0 * o.token + c0;
         for (int s = warp; s < n; s += 4 * kFlight) {
@@ -319,18 +330,18 @@ lora_grad_parts_kernel(const GradOperand o0, const GradOperand o1, const void *i
                 if (s + 4 * k < n) v[k].load(x + (s + 4 * k) * o.token);
 #pragma unroll
             for (int k = 0; k < kFlight; ++k)
-                if (s + 4 * k < n) add_row(acc, v[k], hs[s + 4 * k]);
+                if (s + 4 * k < n) add_row<kRB>(acc, v[k], hs[s + 4 * k]);
         }
     }
     if (warp > 0)
 #pragma unroll
-        for (int r = 0; r < kRB; ++r) sums[warp - 1][r][lane] = of_acc(acc, r);
+        for (int r = 0; r < kRB; ++r) sums[warp - 1][r][lane] = of_acc<kRB>(acc, r);
     __syncthreads();
     if (warp > 0 || c0 >= o.C) return;
     float *p = o.part + (((long long)b * pieces + blockIdx.y) * R + r0) * o.C + c0;
 #pragma unroll
     for (int r = 0; r < kRB; ++r) {
-        float4 v = of_acc(acc, r);
+        float4 v = of_acc<kRB>(acc, r);
 #pragma unroll
         for (int w = 0; w < 3; ++w) {
             const float4 u = sums[w][r][lane];
@@ -340,21 +351,25 @@ lora_grad_parts_kernel(const GradOperand o0, const GradOperand o1, const void *i
     }
 }
 
-// The rows of the adapter's samples, S for each, as one sequence, 64 at a time: h
-// of these goes through shared memory, and kFlight rows of x are requested at
-// once, of one sample or of several.  (With one row requested after the other, 257
-// samples of one token, 4 adapters of rank 16, 3072 to 6144 channels took 54 us.)
-constexpr int kWindow = 64;
-template <typename T>
+// The rows of the adapter's samples, S for each, as one sequence: 1024 samples are
+// looked through at a time, h of 128 rows goes through shared memory, and FLIGHT rows
+// of x are requested at once, of one sample or of several.  A thread holds 4 ranks: few
+// samples of an adapter make a chain of latencies, which more warps hide (257 samples of
+// one token, 4 adapters of rank 16, 3072 and 6144 channels: 54 us with one row requested
+// after the other, 30 with 8 rows and 8 ranks, 23 so).
+constexpr int kWindow = 128;
+constexpr int kLook = 1024;
+constexpr int kOwnerRanks = 4;  // of a thread
+template <typename T, int FLIGHT>
 __global__ void __launch_bounds__(128)
 lora_grad_owner_kernel(const GradOperand o0, const GradOperand o1, const void *ids, int is64, const int *lens,
                        int accumulate, int B, int S, int R, int NA) {
-    __shared__ __align__(16) float hs[kWindow][kRB];
+    __shared__ __align__(16) float hs[kWindow][kOwnerRanks];
     __shared__ int place_b[kWindow], place_s[kWindow];  // sample and row, -1 past its end
-    __shared__ int found[128], count[4];
+    __shared__ int found[kLook], count[4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int r0, c0;
-    const GradOperand &o = grad_place(o0, o1, R / kRB, 512, r0, c0);
+    const GradOperand &o = grad_place(o0, o1, kOwnerRanks, R / kOwnerRanks, 512, r0, c0);
     c0 += threadIdx.x * 4;
     const bool live = c0 < o.C;
     pdl_wait();
@@ -362,73 +377,80 @@ lora_grad_owner_kernel(const GradOperand o0, const GradOperand o1, const void *i
     const int a = blockIdx.y;
     float *p = o.acc + ((long long)a * R + r0) * o.C + c0;
     const T *src = static_cast<const T *>(o.src) + c0;
-    RankAcc total, acc;
-    zero_acc(total);
+    RankAcc<kOwnerRanks> total, acc;
+    zero_acc<kOwnerRanks>(total);
     bool any = false, open = false;
-    for (int b0 = 0; b0 < B; b0 += 128) {
-        // the samples of adapter a among the next 128, in order
-        const int b = b0 + threadIdx.x;
-        const bool mine = b < B && adapter_of(ids, is64, b, NA) == a;
-        const unsigned vote = __ballot_sync(0xFFFFFFFFu, mine);
-        if (lane == 0) count[warp] = __popc(vote);
+    for (int b0 = 0; b0 < B; b0 += kLook) {
+        // the samples of adapter a among the next ones, in order; a warp looks through a quarter of them
+        unsigned mine[kLook / 128];
+        int here = 0;
+#pragma unroll
+        for (int j = 0; j < kLook / 128; ++j) {
+            const int b = b0 + warp * (kLook / 4) + j * 32 + lane;
+            mine[j] = __ballot_sync(0xFFFFFFFFu, b < B && adapter_of(ids, is64, b, NA) == a);
+            here += __popc(mine[j]);
+        }
+        if (lane == 0) count[warp] = here;
         __syncthreads();
         int before = 0, samples = 0;
         for (int w = 0; w < 4; ++w) {
             if (w < warp) before += count[w];
             samples += count[w];
         }
-        if (mine) found[before + __popc(vote & ((1u << lane) - 1u))] = b;
+#pragma unroll
+        for (int j = 0; j < kLook / 128; ++j) {
+            if (mine[j] >> lane & 1u)
+                found[before + __popc(mine[j] & ((1u << lane) - 1u))] = b0 + warp * (kLook / 4) + j * 32 + lane;
+            before += __popc(mine[j]);
+        }
         __syncthreads();
         if (samples > 0 && !any) {
             any = true;
             if (accumulate && live)
 #pragma unroll
-                for (int r = 0; r < kRB; ++r) {
+                for (int r = 0; r < kOwnerRanks; ++r) {
                     const float4 v = *reinterpret_cast<const float4 *>(p + (long long)r * o.C);
                     total[r][0] = px_make(v.x, v.y), total[r][1] = px_make(v.z, v.w);
                 }
         }
         for (long long i0 = 0; i0 < (long long)samples * S; i0 += kWindow) {
             const int rows = (int)min((long long)kWindow, (long long)samples * S - i0);
-            {
-                const int i = threadIdx.x >> 1, q = (threadIdx.x & 1) * 4;
-                if (i < rows) {
-                    const int bb = found[(i0 + i) / S], s = (int)((i0 + i) % S);
-                    const bool real = s < rows_of(lens, bb, S);
-                    if (q == 0) place_b[i] = bb, place_s[i] = real ? s : -1;
-                    if (real)
-                        *reinterpret_cast<float4 *>(&hs[i][q]) =
-                            *reinterpret_cast<const float4 *>(o.h + ((long long)bb * S + s) * R + r0 + q);
-                }
+            if (threadIdx.x < rows) {
+                const int i = threadIdx.x, bb = found[(i0 + i) / S], s = (int)((i0 + i) % S);
+                const bool real = s < rows_of(lens, bb, S);
+                place_b[i] = bb, place_s[i] = real ? s : -1;
+                if (real)
+                    *reinterpret_cast<float4 *>(hs[i]) =
+                        *reinterpret_cast<const float4 *>(o.h + ((long long)bb * S + s) * R + r0);
             }
             __syncthreads();
             if (live)
-                for (int i = 0; i < rows; i += kFlight) {
-                    Four<T> v[kFlight];
-                    int s[kFlight];
+                for (int i = 0; i < rows; i += FLIGHT) {
+                    Four<T> v[FLIGHT];
+                    int s[FLIGHT];
 #pragma unroll
-                    for (int k = 0; k < kFlight; ++k) {
+                    for (int k = 0; k < FLIGHT; ++k) {
                         s[k] = i + k < rows ? place_s[i + k] : -1;
                         if (s[k] >= 0) v[k].load(src + place_b[i + k] * o.batch + s[k] * o.token);
                     }
 #pragma unroll
-                    for (int k = 0; k < kFlight; ++k) {
+                    for (int k = 0; k < FLIGHT; ++k) {
                         if (s[k] < 0) continue;
                         if (s[k] % kGradPiece == 0) {  // a new piece
-                            if (open) add_acc(total, acc);
+                            if (open) add_acc<kOwnerRanks>(total, acc);
                             open = true;
-                            zero_acc(acc);
+                            zero_acc<kOwnerRanks>(acc);
                         }
-                        add_row(acc, v[k], hs[i + k]);
+                        add_row<kOwnerRanks>(acc, v[k], hs[i + k]);
                     }
                 }
             __syncthreads();
         }
     }
-    if (open) add_acc(total, acc);
+    if (open) add_acc<kOwnerRanks>(total, acc);
     if (live && (any || !accumulate))
 #pragma unroll
-        for (int r = 0; r < kRB; ++r) stg16f(p + (long long)r * o.C, of_acc(total, r));
+        for (int r = 0; r < kOwnerRanks; ++r) stg16f(p + (long long)r * o.C, of_acc<kOwnerRanks>(total, r));
 }
 
 // The pieces' sums onto the accumulators: a thread holds 4 channels of a rank.
@@ -494,12 +516,12 @@ template <typename T>
 cudaError_t shrink(const adaln_rows &src, const T *W, const LoraCall &c, int C, float *h, cudaStream_t stream) {
     const T *p = static_cast<const T *>(src.data);
     const dim3 grid(1, c.R / kRB, c.B);
-    auto go = [&](auto kern, int ctas) {
-        return launch_pdl(kern, dim3(ctas, grid.y, grid.z), dim3(128), 0, stream, p, (long long)src.batch,
+    auto go = [&](auto kern, int ctas, int warps) {
+        return launch_pdl(kern, dim3(ctas, grid.y, grid.z), dim3(32 * warps), 0, stream, p, (long long)src.batch,
                           (long long)src.token, W, c.scale, c.ids, c.ids_are_64, c.lens, h, c.S, C, c.R, c.NA);
     };
-    if (c.S == 1) return go(lora_shrink_kernel<T, 1, 4, 3>, 1);
-    return go(lora_shrink_kernel<T, 4, 4, 1>, (c.S + 3) / 4);
+    if (c.S == 1) return go(lora_shrink_kernel<T, 1, 4, 3>, 1, 4);
+    return go(lora_shrink_kernel<T, 4, 4, 1>, (c.S + 3) / 4, 4);
 }
 
 template <typename T>
@@ -531,13 +553,13 @@ int piece_rows(int S) { return on_tensor_cores<T>(S) ? kLoraTcPiece : kGradPiece
 template <typename T>
 cudaError_t grads(const float *h, const float *e, float *part, const LoraCall &c, cudaStream_t stream,
                   const DeviceInfo &dev) {
-    const int rows = piece_rows<T>(c.S), pieces = (c.S + rows - 1) / rows, rb = c.R / kRB;
+    const int rows = piece_rows<T>(c.S), pieces = (c.S + rows - 1) / rows;
     const bool in_parts = grad_in_parts(c.S, c.R, sizeof(T), rows);
     const int width = in_parts ? 128 : 512;  // channels of a CTA
     GradOperand o0 = {c.x.data, c.x.batch, c.x.token, e, c.dA, part, c.K, c.dA ? (c.K + width - 1) / width : 0};
     GradOperand o1 = {c.d_out.data, c.d_out.batch, c.d_out.token, h, c.dU,
                       part + (long long)c.B * pieces * c.R * c.K, c.N, c.dU ? (c.N + width - 1) / width : 0};
-    const unsigned x = (unsigned)((o0.blocks + o1.blocks) * rb);
+    const unsigned x = (unsigned)((o0.blocks + o1.blocks) * (c.R / (in_parts ? kRB : kOwnerRanks)));
     cudaError_t err;
     if (on_tensor_cores<T>(c.S))
         err = lora_tc_grads(o0, o1, c, in_parts, stream, dev);
@@ -545,7 +567,7 @@ cudaError_t grads(const float *h, const float *e, float *part, const LoraCall &c
         err = launch_pdl(lora_grad_parts_kernel<T>, dim3(x, pieces, c.B), dim3(128), 0, stream, o0, o1, c.ids,
                          c.ids_are_64, c.lens, c.S, c.R, c.NA, pieces);
     else
-        err = launch_pdl(lora_grad_owner_kernel<T>, dim3(x, c.NA), dim3(128), 0, stream, o0, o1, c.ids, c.ids_are_64, c.lens,
+        err = launch_pdl(lora_grad_owner_kernel<T, sizeof(T) == 2 ? 16 : 8>, dim3(x, c.NA), dim3(128), 0, stream, o0, o1, c.ids, c.ids_are_64, c.lens,
                          c.accumulate, c.B, c.S, c.R, c.NA);
     if (err != cudaSuccess || !in_parts) return err;
     const long long n = (long long)c.R * ((c.dA ? c.K : 0) + (c.dU ? c.N : 0)) / 4;
