@@ -1,7 +1,7 @@
 """The time-out path of the adapters' tensor-core kernels, run on the GPU
 without a fault: a test build sends the first wait of the MMA warp to an mbarrier
 that nothing arrives on (a 200 us limit).  shrink reports 0x401, the gradients'
-kernel 0x402; no drain runs out, and the context stays usable."""
+kernel 0x402, expand 0x403; no drain runs out, and the context stays usable."""
 
 from __future__ import annotations
 
@@ -15,7 +15,7 @@ from invariant_dit_adaln_gb300 import binding, build
 
 pytestmark = pytest.mark.gpu
 
-SHRINK_WAIT, GRAD_WAIT = 0x401, 0x402
+SHRINK_WAIT, GRAD_WAIT, EXPAND_WAIT = 0x401, 0x402, 0x403
 
 
 class Rows(ctypes.Structure):
@@ -54,6 +54,12 @@ def test_waits_that_run_out_report_and_return(B, S, K, N, R, NA):
     assert L.adaln_lora_bwd(rows(g), rows(x), before[1].data_ptr(), *w, None, None, None, dU.data_ptr(), 0,
                             ws.data_ptr(), ws.numel(), B, S, K, N, R, NA, st) == 0
     assert L.adaln_device_error() == GRAD_WAIT
+    # samples without an adapter: shrink has nothing to wait for, expand copies y
+    none = (*w[:3], torch.full_like(ids, -1), *w[4:])
+    y = torch.zeros_like(out)
+    assert L.adaln_lora_fwd(rows(x), *(v.data_ptr() if torch.is_tensor(v) else v for v in none), rows(y), rows(out),
+                            state.data_ptr(), state.numel(), B, S, K, N, R, NA, st) == 0
+    assert L.adaln_device_error() == EXPAND_WAIT
     assert L.adaln_device_error() == 0
     after = step()
     torch.cuda.synchronize()
