@@ -1024,12 +1024,20 @@ int tmem_columns(int need) {
     return cols;
 }
 
-// stages of `bytes` beside `extra` bytes: as many as let two CTAs share an SM, or
-// where that leaves fewer than three, as many as one CTA has room for
-int stages_for(int bytes, int extra) {
+// CTAs of `smem` bytes that share an SM (228 KB, 1 KB of it taken by each, and up to
+// 1 KB of static shared memory), at most 3
+constexpr int kSmOfOne = 225 * 1024, kSmOfTwo = 112 * 1024, kSmOfThree = 74 * 1024;
+int ctas_of(size_t smem) { return smem <= kSmOfThree ? 3 : smem <= kSmOfTwo ? 2 : 1; }
+
+// stages of `bytes` beside `extra` bytes: as many as let `ctas` CTAs share an SM, or
+// where that leaves fewer than three, one CTA less.  (Gradients of 4096 of 8192 rows,
+// 3072 and 3072 channels, rank 16: 28.5 us with two CTAs, 24.7 with three, whose
+// pieces are dealt more evenly; shrink's tiles are too few for three.)
+int stages_for(int bytes, int extra, int ctas) {
     const int fixed = extra + kBarBytes + 1024;
-    int n = (113 * 1024 - fixed) / bytes;
-    if (n < 3) n = (225 * 1024 - fixed) / bytes;
+    int n = ctas > 2 ? (kSmOfThree - fixed) / bytes : 0;
+    if (n < 3) n = (kSmOfTwo - fixed) / bytes;
+    if (n < 3) n = (kSmOfOne - fixed) / bytes;
     return n < kMaxStages ? n : kMaxStages;
 }
 static_assert(kRowTile + 3 * kLoraMaxRank * kBlk * 2 <= (225 * 1024 - kLoraMaxRank * kM * 4 - kBarBytes - 1024) / 2,
@@ -1046,7 +1054,7 @@ cudaError_t lora_tc_shrink(const adaln_rows &src, const void *W, const LoraCall 
     const int KB = (C + kBlk - 1) / kBlk;
     g.ks = KB <= 12 ? 1 : KB <= 24 ? 2 : KB <= 48 ? 4 : 8;
     const int stage = kRowTile + g.Rp * kBlk * 2, part = g.Rp * kPartPitch * 4;
-    g.stages = stages_for(stage, part);
+    g.stages = stages_for(stage, part, 2);
     g.tmem_cols = tmem_columns(g.Rp);
     CUtensorMap map_x, map_w;
     if (!make_map_3d(&map_x, src.data, C, c.S, c.B, src.token, src.batch, kM) ||
@@ -1123,9 +1131,9 @@ cudaError_t lora_tc_grads(const GradOperand &o0, const GradOperand &o1, const Lo
     g.B = c.B, g.S = c.S, g.R = c.R, g.NA = c.NA, g.pieces = (c.S + kLoraTcPiece - 1) / kLoraTcPiece;
     g.Np = (3 * c.R + 15) / 16 * 16;
     const int stage = kRowTile + g.Np * kBlk * 2, extra = in_parts ? 0 : c.R * kM * 4;
-    g.stages = stages_for(stage, extra);
+    g.stages = stages_for(stage, extra, 3);
     const size_t smem = (size_t)g.stages * stage + extra + kBarBytes + 1024;
-    const int per_sm = smem <= 113 * 1024 ? 2 : 1;
+    const int per_sm = ctas_of(smem);
     // two accumulators where the SM's CTAs all find room for them: one that did not would wait for another's end
     g.bufs = 2 * g.Np <= 512 && tmem_columns(2 * g.Np) * per_sm <= 512 ? 2 : 1;
     g.tmem_cols = tmem_columns(g.bufs * g.Np);
