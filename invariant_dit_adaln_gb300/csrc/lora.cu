@@ -25,6 +25,7 @@ struct Vec<uint16_t> {
     uint4 v;
     __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ void load(const uint16_t *p) { v = ldg16(p); }
+    __device__ __forceinline__ void load_l2(const uint16_t *p) { v = __ldcg(reinterpret_cast<const uint4 *>(p)); }
     __device__ __forceinline__ void pairs(px2 (&x)[4]) const {
         x[0] = px_bf16(v.x), x[1] = px_bf16(v.y), x[2] = px_bf16(v.z), x[3] = px_bf16(v.w);
     }
@@ -38,6 +39,7 @@ struct Vec<float> {
     uint4 v;
     __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ void load(const float *p) { v = ldg16(p); }
+    __device__ __forceinline__ void load_l2(const float *p) { v = __ldcg(reinterpret_cast<const uint4 *>(p)); }
     __device__ __forceinline__ void pairs(px2 (&x)[2]) const {
         x[0] = px_make(__uint_as_float(v.x), __uint_as_float(v.y));
         x[1] = px_make(__uint_as_float(v.z), __uint_as_float(v.w));
@@ -163,27 +165,26 @@ lora_expand_kernel(const float *__restrict__ h, const T *__restrict__ W, const v
     __shared__ float hs[TOK][kLoraMaxRank];
     const int b = blockIdx.z, s0 = blockIdx.y * TOK;
     const int c0 = (blockIdx.x * 128 + threadIdx.x) * E;
-    pdl_wait();
-    pdl_trigger();
-    const int n = min(TOK, rows_of(lens, b, S) - s0);
-    if (n <= 0) return;
-    const int a = adapter_of(ids, is64, b, NA);
-    if (a < 0 && base == out) return;
-    // the base and the first ranks are requested before the state has come
+    // With adapters this kernel follows shrink, which waited for all that came before:
+    // only the state is not there yet.
+    if (NA == 0) pdl_wait();
+    const int n = min(TOK, rows_of<true>(lens, b, S) - s0);
+    const int a = adapter_of<true>(ids, is64, b, NA);
     const T *w = W + (long long)max(a, 0) * R * C + c0;
     Vec<T> y[TOK], wv[kRB];
 #pragma unroll
     for (int r = 0; r < kRB; ++r) {
         wv[r].zero();
-        if (a >= 0 && c0 < C) wv[r].load(w + (long long)r * C);
+        if (a >= 0 && c0 < C) wv[r].load_l2(w + (long long)r * C);
     }
 #pragma unroll
     for (int i = 0; i < TOK; ++i) {
         y[i].zero();
-        // not the read-only path: base may be out
-        if (base && i < n && c0 < C)
-            y[i].v = *reinterpret_cast<const uint4 *>(base + b * base_batch + (s0 + i) * base_token + c0);
+        if (base && i < n && c0 < C) y[i].load_l2(base + b * base_batch + (s0 + i) * base_token + c0);
     }
+    if (NA > 0) pdl_wait();
+    pdl_trigger();
+    if (n <= 0 || (a < 0 && base == out)) return;
     if (a >= 0)
         for (int i = threadIdx.x; i < TOK * R; i += 128)
             hs[i / R][i % R] = i / R < n ? h[((long long)b * S + s0) * R + i] : 0.0f;
@@ -243,14 +244,14 @@ template <>
 struct Four<uint16_t> {
     uint2 v;
     __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
-    __device__ __forceinline__ void load(const uint16_t *p) { v = __ldg(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ void load(const uint16_t *p) { v = __ldcg(reinterpret_cast<const uint2 *>(p)); }
     __device__ __forceinline__ void pairs(px2 (&x)[2]) const { x[0] = px_bf16(v.x), x[1] = px_bf16(v.y); }
 };
 template <>
 struct Four<float> {
     float4 v;
     __device__ __forceinline__ void zero() { v = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-    __device__ __forceinline__ void load(const float *p) { v = __ldg(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void load(const float *p) { v = __ldcg(reinterpret_cast<const float4 *>(p)); }
     __device__ __forceinline__ void pairs(px2 (&x)[2]) const { x[0] = px_make(v.x, v.y), x[1] = px_make(v.z, v.w); }
 };
 
@@ -301,23 +302,26 @@ __device__ __forceinline__ const GradOperand &grad_place(const GradOperand &o0, 
 
 template <typename T>
 __global__ void __launch_bounds__(128)
-lora_grad_parts_kernel(const GradOperand o0, const GradOperand o1, const void *ids, int is64, const int *lens, int S,
-                       int R, int NA, int pieces) {
+lora_grad_parts_kernel(const GradOperand o0, const GradOperand o1, const void *ids, int is64, const int *lens, int early,
+                       int S, int R, int NA, int pieces) {
     __shared__ __align__(16) float hs[kGradPiece][kRB];
     __shared__ float4 sums[3][kRB][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int r0, c0;
     const GradOperand &o = grad_place(o0, o1, kRB, R / kRB, 128, r0, c0);
     c0 += lane * 4;
-    pdl_wait();
+    if (!early) pdl_wait();
     pdl_trigger();
     const int b = blockIdx.z, s0 = blockIdx.y * kGradPiece;
-    const int n = min(rows_of(lens, b, S) - s0, kGradPiece);
-    if (n <= 0 || adapter_of(ids, is64, b, NA) < 0) return;
+    const int n = min(rows_of<true>(lens, b, S) - s0, kGradPiece);
+    if (n <= 0 || adapter_of<true>(ids, is64, b, NA) < 0) {
+        pdl_wait();
+        return;
+    }
     const float *h = o.h + ((long long)b * S + s0) * R + r0;
     for (int i = threadIdx.x; i < n * 2; i += 128)
         *reinterpret_cast<float4 *>(&hs[i >> 1][(i & 1) * 4]) =
-            *reinterpret_cast<const float4 *>(h + (long long)(i >> 1) * R + (i & 1) * 4);
+            __ldcg(reinterpret_cast<const float4 *>(h + (long long)(i >> 1) * R + (i & 1) * 4));
     __syncthreads();
     RankAcc<kRB> acc;
     zero_acc<kRB>(acc);
@@ -336,6 +340,7 @@ lora_grad_parts_kernel(const GradOperand o0, const GradOperand o1, const void *i
     if (warp > 0)
 #pragma unroll
         for (int r = 0; r < kRB; ++r) sums[warp - 1][r][lane] = of_acc<kRB>(acc, r);
+    pdl_wait();  // in every CTA: the next kernel takes this one's end for that of all before it
     __syncthreads();
     if (warp > 0 || c0 >= o.C) return;
     float *p = o.part + (((long long)b * pieces + blockIdx.y) * R + r0) * o.C + c0;
@@ -363,7 +368,7 @@ constexpr int kOwnerRanks = 4;  // of a thread
 template <typename T, int FLIGHT>
 __global__ void __launch_bounds__(128)
 lora_grad_owner_kernel(const GradOperand o0, const GradOperand o1, const void *ids, int is64, const int *lens,
-                       int accumulate, int B, int S, int R, int NA) {
+                       int early, int accumulate, int B, int S, int R, int NA) {
     __shared__ __align__(16) float hs[kWindow][kOwnerRanks];
     __shared__ int place_b[kWindow], place_s[kWindow];  // sample and row, -1 past its end
     __shared__ int found[kLook], count[4];
@@ -372,7 +377,7 @@ lora_grad_owner_kernel(const GradOperand o0, const GradOperand o1, const void *i
     const GradOperand &o = grad_place(o0, o1, kOwnerRanks, R / kOwnerRanks, 512, r0, c0);
     c0 += threadIdx.x * 4;
     const bool live = c0 < o.C;
-    pdl_wait();
+    if (!early) pdl_wait();
     pdl_trigger();
     const int a = blockIdx.y;
     float *p = o.acc + ((long long)a * R + r0) * o.C + c0;
@@ -387,7 +392,7 @@ lora_grad_owner_kernel(const GradOperand o0, const GradOperand o1, const void *i
 #pragma unroll
         for (int j = 0; j < kLook / 128; ++j) {
             const int b = b0 + warp * (kLook / 4) + j * 32 + lane;
-            mine[j] = __ballot_sync(0xFFFFFFFFu, b < B && adapter_of(ids, is64, b, NA) == a);
+            mine[j] = __ballot_sync(0xFFFFFFFFu, b < B && adapter_of<true>(ids, is64, b, NA) == a);
             here += __popc(mine[j]);
         }
         if (lane == 0) count[warp] = here;
@@ -409,7 +414,7 @@ lora_grad_owner_kernel(const GradOperand o0, const GradOperand o1, const void *i
             if (accumulate && live)
 #pragma unroll
                 for (int r = 0; r < kOwnerRanks; ++r) {
-                    const float4 v = *reinterpret_cast<const float4 *>(p + (long long)r * o.C);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + (long long)r * o.C));
                     total[r][0] = px_make(v.x, v.y), total[r][1] = px_make(v.z, v.w);
                 }
         }
@@ -417,11 +422,11 @@ lora_grad_owner_kernel(const GradOperand o0, const GradOperand o1, const void *i
             const int rows = (int)min((long long)kWindow, (long long)samples * S - i0);
             if (threadIdx.x < rows) {
                 const int i = threadIdx.x, bb = found[(i0 + i) / S], s = (int)((i0 + i) % S);
-                const bool real = s < rows_of(lens, bb, S);
+                const bool real = s < rows_of<true>(lens, bb, S);
                 place_b[i] = bb, place_s[i] = real ? s : -1;
                 if (real)
                     *reinterpret_cast<float4 *>(hs[i]) =
-                        *reinterpret_cast<const float4 *>(o.h + ((long long)bb * S + s) * R + r0);
+                        __ldcg(reinterpret_cast<const float4 *>(o.h + ((long long)bb * S + s) * R + r0));
             }
             __syncthreads();
             if (live)
@@ -448,6 +453,7 @@ lora_grad_owner_kernel(const GradOperand o0, const GradOperand o1, const void *i
         }
     }
     if (open) add_acc<kOwnerRanks>(total, acc);
+    pdl_wait();
     if (live && (any || !accumulate))
 #pragma unroll
         for (int r = 0; r < kOwnerRanks; ++r) stg16f(p + (long long)r * o.C, of_acc<kOwnerRanks>(total, r));
@@ -565,10 +571,10 @@ cudaError_t grads(const float *h, const float *e, float *part, const LoraCall &c
         err = lora_tc_grads(o0, o1, c, in_parts, stream, dev);
     else if (in_parts)
         err = launch_pdl(lora_grad_parts_kernel<T>, dim3(x, pieces, c.B), dim3(128), 0, stream, o0, o1, c.ids,
-                         c.ids_are_64, c.lens, c.S, c.R, c.NA, pieces);
+                         c.ids_are_64, c.lens, c.grads_early, c.S, c.R, c.NA, pieces);
     else
         err = launch_pdl(lora_grad_owner_kernel<T, sizeof(T) == 2 ? 16 : 8>, dim3(x, c.NA), dim3(128), 0, stream, o0, o1, c.ids, c.ids_are_64, c.lens,
-                         c.accumulate, c.B, c.S, c.R, c.NA);
+                         c.grads_early, c.accumulate, c.B, c.S, c.R, c.NA);
     if (err != cudaSuccess || !in_parts) return err;
     const long long n = (long long)c.R * ((c.dA ? c.K : 0) + (c.dU ? c.N : 0)) / 4;
     return launch_pdl(lora_join_kernel, dim3((unsigned)((n + 127) / 128), c.NA), dim3(128), 0, stream, o0, o1, c.ids,
@@ -607,7 +613,11 @@ cudaError_t launch_lora_fwd(const LoraCall &c, cudaStream_t stream, const Device
 }
 
 template <typename T>
-cudaError_t launch_lora_bwd(const LoraCall &c, cudaStream_t stream, const DeviceInfo &dev) {
+cudaError_t launch_lora_bwd(const LoraCall &call, cudaStream_t stream, const DeviceInfo &dev) {
+    // Behind expand, which waited for shrink, which waited for all before it, the
+    // gradients find both states and their rows ready: they start beside expand's end.
+    LoraCall c = call;
+    c.grads_early = c.out.data != nullptr;
     const float *h = static_cast<const float *>(c.state);
     float *e = static_cast<float *>(c.ws);
     cudaError_t err = cudaSuccess;

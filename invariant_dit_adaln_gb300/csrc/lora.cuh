@@ -7,11 +7,19 @@
 namespace adaln {
 
 // the adapter of sample b, -1 for none
+// L2: from L2, not L1, which may hold what an earlier kernel left there: in kernels that
+// read before they have waited for the one they follow.
+template <bool L2 = false>
 __device__ __forceinline__ int adapter_of(const void *ids, int is64, int b, int NA) {
-    const long long i = is64 ? static_cast<const long long *>(ids)[b] : static_cast<const int *>(ids)[b];
+    const long long *p8 = static_cast<const long long *>(ids) + b;
+    const int *p4 = static_cast<const int *>(ids) + b;
+    const long long i = is64 ? (L2 ? __ldcg(p8) : *p8) : (L2 ? __ldcg(p4) : *p4);
     return i >= 0 && i < NA ? (int)i : -1;
 }
-__device__ __forceinline__ int rows_of(const int *lens, int b, int S) { return lens ? min(max(lens[b], 0), S) : S; }
+template <bool L2 = false>
+__device__ __forceinline__ int rows_of(const int *lens, int b, int S) {
+    return lens ? min(max(L2 ? __ldcg(lens + b) : lens[b], 0), S) : S;
+}
 
 // one side of the gradients: x with e for dA, d_out with h for dU
 struct GradOperand {

@@ -741,6 +741,7 @@ struct GradArgs {
     const int *lens;
     int accumulate;
     int B, S, R, NA, pieces;
+    int early; // what this kernel reads is there before the kernel it follows ends
     int Np;    // 3 R rounded up to 16
     int bufs;  // accumulators
     int stages, tmem_cols;
@@ -760,7 +761,7 @@ struct GradPieces {
         window(lane);
     }
     __device__ __forceinline__ int rows_at(int b) const {
-        return b < g.B && adapter_of(g.ids, g.is64, b, g.NA) >= 0 ? rows_of(g.lens, b, g.S) : 0;
+        return b < g.B && adapter_of<true>(g.ids, g.is64, b, g.NA) >= 0 ? rows_of<true>(g.lens, b, g.S) : 0;
     }
     __device__ __forceinline__ void window(int lane) {
         rows = next_rows;
@@ -812,7 +813,7 @@ lora_grad_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         bars_init(sm, 128);
     }
     if (warp == 1) tmem_alloc(&sm.tmem, g.tmem_cols);
-    pdl_wait();
+    if (!g.early) pdl_wait();
     tc_before_sync();
     __syncthreads();
     pdl_trigger();
@@ -900,6 +901,7 @@ lora_grad_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                 *abort_flag = 1;
             } else {
                 tc_after_sync();
+                if (!OWNER) pdl_wait();  // before the first store
                 const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(p * Np);
                 const int c = c0 + lane_row;
                 float *dst = o.part + (b * (long long)g.pieces + s0 / kLoraTcPiece) * R * o.C + c;
@@ -946,7 +948,7 @@ lora_grad_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         for (int b0 = 0; b0 < g.B; b0 += kGradThreads) {
             // the samples of adapter a among the next ones, in order
             const int b = b0 + threadIdx.x;
-            const bool mine = b < g.B && adapter_of(g.ids, g.is64, b, g.NA) == a;
+            const bool mine = b < g.B && adapter_of<true>(g.ids, g.is64, b, g.NA) == a;
             const unsigned vote = __ballot_sync(0xFFFFFFFFu, mine);
             if (lane == 0) count[warp] = __popc(vote);
             __syncthreads();
@@ -962,10 +964,10 @@ lora_grad_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
                 if (warp >= 2)
                     for (int r = 0; r < R; ++r)
                         total[r * kM + lane_row] =
-                            g.accumulate && c < o.C ? o.acc[((long long)a * R + r) * o.C + c] : 0.0f;
+                            g.accumulate && c < o.C ? __ldcg(o.acc + ((long long)a * R + r) * o.C + c) : 0.0f;
             }
             for (int i = 0; i < samples && ok; ++i) {
-                const int n = rows_of(g.lens, found[i], g.S);
+                const int n = rows_of<true>(g.lens, found[i], g.S);
                 for (int s0 = 0; s0 < n && ok; s0 += kLoraTcPiece)
                     piece(o, x_side, c0, found[i], s0, min(n, s0 + kLoraTcPiece));
             }
@@ -973,6 +975,7 @@ lora_grad_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             ok = __syncthreads_and(ok && !*abort_flag);
             if (!ok) break;
         }
+        pdl_wait();
         if (ok && warp >= 2 && c < o.C && (any || !g.accumulate))
             for (int r = 0; r < R; ++r)
                 o.acc[((long long)a * R + r) * o.C + c] = any ? total[r * kM + lane_row] : 0.0f;
@@ -989,6 +992,7 @@ lora_grad_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         if (!mbar_wait_bounded(&sm.done, 0u, kDrainNs)) report_error_lora(kErrDrainFailed);
     }
     __syncwarp();
+    pdl_wait();  // in every CTA: the next kernel takes this one's end for that of all before it
     tc_before_sync();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) report_error_lora(kErrLoraGradWait);
@@ -1129,6 +1133,7 @@ cudaError_t lora_tc_grads(const GradOperand &o0, const GradOperand &o1, const Lo
     g.o[1].blocks = o1.acc ? (o1.C + kM - 1) / kM : 0;
     g.ids = c.ids, g.is64 = c.ids_are_64, g.lens = c.lens, g.accumulate = c.accumulate;
     g.B = c.B, g.S = c.S, g.R = c.R, g.NA = c.NA, g.pieces = (c.S + kLoraTcPiece - 1) / kLoraTcPiece;
+    g.early = c.grads_early;
     g.Np = (3 * c.R + 15) / 16 * 16;
     const int stage = kRowTile + g.Np * kBlk * 2, extra = in_parts ? 0 : c.R * kM * 4;
     g.stages = stages_for(stage, extra, 3);

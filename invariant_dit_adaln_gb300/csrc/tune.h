@@ -48,6 +48,7 @@ struct LoraCall {
     void *state;             // h
     float *dA, *dU;          // backward: accumulators or NULL
     int accumulate;
+    int grads_early;  // the gradients may read before the kernel they follow ends
     void *ws;
     int B, S, K, N, R, NA;
 };
