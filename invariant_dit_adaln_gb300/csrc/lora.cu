@@ -465,7 +465,6 @@ lora_join_kernel(const GradOperand o0, const GradOperand o1, const void *ids, in
                  int B, int S, int R, int NA, int pieces, int piece_rows) {
     const int n0 = o0.acc ? R * (o0.C / 4) : 0, n1 = o1.acc ? R * (o1.C / 4) : 0;
     int i = blockIdx.x * 128 + threadIdx.x;
-    pdl_wait();
     pdl_trigger();
     const bool live = i < n0 + n1;
     const GradOperand &o = i < n0 ? o0 : o1;
@@ -480,6 +479,7 @@ lora_join_kernel(const GradOperand o0, const GradOperand o1, const void *ids, in
     const float4 *at[kSide];
     int k = 0;
     auto add = [&] {
+        pdl_wait();  // until here only what was there before the call is read
         float4 v[kSide];
 #pragma unroll
         for (int j = 0; j < kSide; ++j)
@@ -494,12 +494,12 @@ lora_join_kernel(const GradOperand o0, const GradOperand o1, const void *ids, in
     for (int b0 = 0; b0 < B; b0 += 32) {
         // the samples of adapter a among the next 32, and their rows, by a lane each
         const int mine = b0 + lane;
-        unsigned left = __ballot_sync(0xFFFFFFFFu, mine < B && adapter_of(ids, is64, mine, NA) == a);
-        const int n = mine < B ? rows_of(lens, mine, S) : 0;
+        unsigned left = __ballot_sync(0xFFFFFFFFu, mine < B && adapter_of<true>(ids, is64, mine, NA) == a);
+        const int n = mine < B ? rows_of<true>(lens, mine, S) : 0;
         for (; left; left &= left - 1) {
             const int b = b0 + __ffs(left) - 1;
             const int here = (__shfl_sync(0xFFFFFFFFu, n, b - b0) + piece_rows - 1) / piece_rows;
-            if (!any && accumulate && live) s = *p;
+            if (!any && accumulate && live) s = __ldcg(p);
             any = true;
             const float4 *q = reinterpret_cast<const float4 *>(o.part + (long long)b * pieces * size) + i;
             for (int j = 0; j < here; ++j, q += size / 4) {
