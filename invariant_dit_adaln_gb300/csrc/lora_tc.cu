@@ -7,7 +7,7 @@
 // shared memory, from where tcgen05.mma takes them; only their small results
 // leave tensor memory.  expand's rows come and leave by TMA as well; a thread adds
 // to 64 bytes of a row at a time.  (With mma.sync, rows in registers: 37 instead of
-// XX us for 4222 rows of 9216 channels at rank 32, bound by issue.)
+// 31.5 us for 4222 rows of 9216 channels at rank 32, bound by issue.)
 //
 // h and e are held as three bf16 parts, whose sum is the fp32 number itself.  The
 // gradients, which are fp32, take all three (two would leave 2.5e-6 of error, more
@@ -381,11 +381,13 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
 // same rows.  A tile's base, state and adapter come by TMA into a stage of a ring;
 // two accumulators; a thread adds row t's accumulators to the base in shared memory,
 // from where the tile leaves by TMA.  A tile that the sample's end crosses leaves by
-// row.  Above rank 32, where the state is the most of a stage, a CTA takes a run of
-// tiles instead, and keeps the state of its tokens beside the ring (rank 128, 2042
-// rows of 2560 channels: 16.8 us with the state in the stages, XX so).  (One tile a CTA, of 128 channels, four CTAs an SM, each waiting for its own
-// copies: 36 us instead of XX for 4222 rows of 9216 channels at rank 32.  Each CTA a
-// run of one row of tiles: 45, the last CTAs alone on the device.)
+// row.  Above rank 64, where the state is the most of a stage, a CTA takes a run of
+// tiles instead, and keeps the state of its tokens beside the ring (a forward call of
+// 4593 rows, 64 and 2560 channels, with the state in the stages and so: 20.7 and 22.5 us
+// at rank 64, 27.8 and 24.0 at 96, 30.1 and 26.8 at 128).  4222 rows of 9216 channels at
+// rank 32 take 31.5 us, 5.0 TB/s.  (One tile a CTA, of 128 channels, four CTAs an SM,
+// each waiting for its own copies: 36.5.  Each CTA a run of one row of tiles: 45, the last
+// CTAs alone on the device.)
 //
 // Roles (320 threads): warp 0 finds the tiles and lane 0 copies, warp 1 lane 0 the
 // MMAs, warps 2 to 5 and 6 to 9 every other tile, a token a thread.
@@ -1108,7 +1110,7 @@ cudaError_t lora_tc_expand(const void *h, const void *W, const LoraCall &c, int 
                                : make_map_3d(&map_y, c.out.data, C, c.S, c.B, c.out.token, c.out.batch, kM)))
         return cudaErrorInvalidValue;
     g.B = c.B;
-    g.keep = c.R > 32;
+    g.keep = c.R > 64;
     const int state = 4 * c.R * 128, stage = kExTile + g.copies * c.R * 128 + (g.keep ? 0 : state);
     const int beside = (g.keep ? state : 0) + kBarBytes + 1024;
     // 2 or 4 stages, whichever gives an SM more of them in all: 8 up to rank 16, 6 up
