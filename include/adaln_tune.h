@@ -12,7 +12,9 @@
  * owned buffers, asynchronous on `stream`, order of the checks, status codes),
  * with the differences stated at each call.  No call allocates or synchronizes
  * (the first one of a kernel on a device keeps a small record on the host), and
- * every call can be captured into a CUDA graph.
+ * every call can be captured into a CUDA graph.  Waits are bounded as in adaln.h;
+ * one of the adapters' kernels that runs out sets adaln_device_error's word: 0x401
+ * (x A^T or d_out U^T), 0x402 (gradients), 0x403 (out or dx).
  * Two calls (or two replayed graphs) that can run at the same time must not
  * share a workspace, a state or an output.
  */
@@ -153,8 +155,10 @@ size_t adaln_lora_state_bytes(int B, int S, int R);
  *   state             written: what adaln_lora_bwd needs, adaln_lora_state_bytes
  *
  * h is held in fp32; where S > 16 (bf16) the product with U takes it to 16
- * significant bits (2^-17 relative).  A row's result does not depend on the other
- * samples; its order depends on K, R and S only.
+ * significant bits (2^-17 relative; an |h| above bf16's largest finite number, 3.39e38,
+ * counts as infinite).  A row's result does not depend on the other samples; its order
+ * depends on K, R and S only.  What an infinity or a NaN enters is infinite or NaN, and
+ * nothing else changes.
  *
  * Sizes: K, N multiples of 8 in [8, 65536]; R a multiple of 8 in [8, 128] (fill
  * up smaller adapters with zeros); 0 <= NA <= 65535; B, S as in adaln.h; B * S *
@@ -181,7 +185,8 @@ size_t adaln_lora_bwd_workspace_bytes(int B, int S, int K, int N, int R);
 size_t adaln_f32_lora_bwd_workspace_bytes(int B, int S, int K, int N, int R);
 
 /*
- * adaln_lora_bwd — backward of adaln_lora_fwd, with the state that it left:
+ * adaln_lora_bwd — backward of adaln_lora_fwd, with the state that it left and its
+ * A, U, scale, ids and lens:
  *
  *   e[b,s,r]  = scale[a] * sum_n d_out[b,s,n] U[a,r,n]          fp32
  *   dx[b,s,k] = dx_base[b,s,k] + sum_r e[b,s,r] A[a,r,k]        as out

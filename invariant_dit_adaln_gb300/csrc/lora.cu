@@ -5,9 +5,13 @@
 //     shrink   h[b,s,:] = scale_a W_a src[b,s,:]           (x with A; d_out with U)
 //     expand   out[b,s,:] = base[b,s,:] + h[b,s,:] W_a     (h with U; e with A)
 //     grad     dW_a = sum over rows of h[b,s,:] src[b,s,:]^T
-// 2 R flop for each channel read or written: bound by memory for bf16 on the
-// tensor cores; on the CUDA cores (fp32, and samples of a few tokens) by issue
-// from R = 16 or so on.
+// 2 R flop for each channel read or written: from 17 tokens a sample on, in bf16, on
+// the tensor cores (lora_tc.cu); here on the CUDA cores, fp32 and samples of a few
+// tokens.  These calls are small, and a chain of latencies more than anything else:
+// what a kernel can read before the one it follows has ended, it does.  Cold, at 257
+// samples of a token, 3072 and 6144 channels, 4 adapters of rank 16: shrink 11 and 16 us,
+// expand 9 and 7, the gradients 17 to 20; at 64 samples replayed from a graph 7.0 for
+// both kernels of the forward.
 #include "lora.cuh"
 
 namespace adaln {
@@ -236,7 +240,7 @@ lora_expand_kernel(const float *__restrict__ h, const T *__restrict__ W, const v
 // channel of a piece moved twice.  lora_grad_owner_kernel: a thread takes every
 // piece of an adapter and writes the accumulator.
 // --------------------------------------------------------------------------
-constexpr int kFlight = 16;  // rows of a warp requested at once
+constexpr int kFlight = 16;  // rows of a warp requested at once (5 x 333 rows, fp32: 14 us; 8 rows 17)
 
 template <typename T>
 struct Four;  // 4 channels of a row
@@ -361,7 +365,9 @@ lora_grad_parts_kernel(const GradOperand o0, const GradOperand o1, const void *i
 // of x are requested at once, of one sample or of several.  A thread holds 4 ranks: few
 // samples of an adapter make a chain of latencies, which more warps hide (257 samples of
 // one token, 4 adapters of rank 16, 3072 and 6144 channels: 54 us with one row requested
-// after the other, 30 with 8 rows and 8 ranks, 23 so).
+// after the other, 30 with 8 rows and 8 ranks, 23 with 16 and 4.  A whole backward there,
+// and of 32 samples of 8 tokens: 28 and 22 us with 16 rows, 31 and 22 with 8, 27 and 26
+// with 32.)
 constexpr int kWindow = 128;
 constexpr int kLook = 1024;
 constexpr int kOwnerRanks = 4;  // of a thread
@@ -491,11 +497,14 @@ lora_join_kernel(const GradOperand o0, const GradOperand o1, const void *ids, in
                                 __fadd_rn(s.w, v[j].w));
         k = 0;
     };
+    // sample b's adapter and rows, by a lane each; the next 32 samples' on their way
+    auto id_of = [&](int b) { return b < B ? adapter_of<true>(ids, is64, b, NA) : -1; };
+    auto n_of = [&](int b) { return b < B ? rows_of<true>(lens, b, S) : 0; };
+    int next_id = id_of(lane), next_n = n_of(lane);
     for (int b0 = 0; b0 < B; b0 += 32) {
-        // the samples of adapter a among the next 32, and their rows, by a lane each
-        const int mine = b0 + lane;
-        unsigned left = __ballot_sync(0xFFFFFFFFu, mine < B && adapter_of<true>(ids, is64, mine, NA) == a);
-        const int n = mine < B ? rows_of<true>(lens, mine, S) : 0;
+        unsigned left = __ballot_sync(0xFFFFFFFFu, next_id == a);  // those of adapter a
+        const int n = next_n;
+        next_id = id_of(b0 + 32 + lane), next_n = n_of(b0 + 32 + lane);
         for (; left; left &= left - 1) {
             const int b = b0 + __ffs(left) - 1;
             const int here = (__shfl_sync(0xFFFFFFFFu, n, b - b0) + piece_rows - 1) / piece_rows;

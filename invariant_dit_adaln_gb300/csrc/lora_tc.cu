@@ -199,7 +199,9 @@ __device__ __forceinline__ void three_parts(float a, float b, uint32_t (&p)[3]) 
 // alone, one for each CTA of a cluster; CTA q joins the ranks of slice q: the
 // others write their accumulators of it into its shared memory, and it adds them
 // in range order.  About 12 blocks a range give two CTAs an SM, with 90 KB in
-// flight each, at 8192 tokens of 3072 channels.
+// flight each, at 8192 tokens of 3072 channels: 16.4 us cold, 3.1 TB/s; 13.8 for half of
+// them, 1.8 TB/s: a chain of latencies (the sample's id, the first blocks, the join) and
+// one ring's worth behind it.  (24 or 48 blocks a range, and rings of 225 KB: slower.)
 //
 // Roles (128 threads): warp 0 lane 0 the copies, warp 1 lane 0 the MMAs, then
 // thread t holds token t.
@@ -435,11 +437,12 @@ struct ExpandTiles {
     int w0;             // first sample of the window
     long long before;   // token tiles of the samples before it
     int rows, upto;     // this lane's sample: its rows, and the token tiles up to its end
+    int next_rows;      // the next window's, on their way
     bool over;
     __device__ __forceinline__ ExpandTiles(const ExpandArgs &args, int lane)
         : g(args), u(blockIdx.x), step(gridDim.x), end(0x7FFFFFFFFFFFFFFFll), ct((args.C + kBlk - 1) / kBlk), w0(0),
-          before(0), rows(0), upto(0), over(false) {
-        if (g.lens) window(lane);
+          before(0), rows(0), upto(0), next_rows(0), over(false) {
+        if (g.lens) first(lane);
         if (!g.keep) return;
         long long all = (long long)g.B * ((g.S + kM - 1) / kM);
         if (g.lens) {
@@ -449,13 +452,19 @@ struct ExpandTiles {
                 window(lane);
                 all += __shfl_sync(0xFFFFFFFFu, upto, 31);
             }
-            if (w0 > 0) w0 = 0, window(lane);
+            if (w0 > 0) w0 = 0, first(lane);
         }
         all *= ct;
         u = all * blockIdx.x / gridDim.x, end = all * (blockIdx.x + 1) / gridDim.x, step = 1;
     }
+    __device__ __forceinline__ int rows_at(int b) const { return b < g.B ? rows_of(g.lens, b, g.S) : 0; }
+    __device__ __forceinline__ void first(int lane) {
+        next_rows = rows_at(lane);
+        window(lane);
+    }
     __device__ __forceinline__ void window(int lane) {
-        rows = w0 + lane < g.B ? rows_of(g.lens, w0 + lane, g.S) : 0;
+        rows = next_rows;
+        next_rows = rows_at(w0 + 32 + lane);
         upto = (rows + kM - 1) / kM;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -726,9 +735,10 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
 // Schedules and order as lora_grad_kernel's: OWNER, every piece of an adapter in
 // order by one CTA, with two accumulators (where they fit), so that one piece's
 // leave while the next one's MMAs run, and the total in shared memory; otherwise as
-// many CTAs as the device holds take every gridDim.x-th piece of every tile.  (A CTA a
-// piece or two: 30 us for 8192 rows of 3072 and 3072 channels at rank 16, a quarter of
-// it the last CTAs.)
+// many CTAs as the device holds take every gridDim.x-th piece of every tile.  (8192 rows of
+// 3072 and 3072 channels at rank 16: 30 us with a CTA a piece or two, a quarter of it the
+// last CTAs, 24.7 so, 4.1 TB/s.)  At rank 128 the state is three quarters of what a tile
+// reads, from L2: 18 us for 3700 rows of 2048 and 2560 channels, 150 MB into shared memory.
 //
 // Roles (192 threads): warp 0 lane 0 the copies, warp 1 the MMAs (and zeros for
 // the rows of a block past the sample's end, which may hold anything), warps 2
