@@ -137,11 +137,6 @@ __device__ __forceinline__ bool named_bar_and(int id, int count, bool flag) {
     return r != 0;
 }
 
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int c0, int c1, int c2) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(c0), "r"(c1),
-                 "r"(c2)
-                 : "memory");
-}
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -199,9 +194,11 @@ __device__ __forceinline__ void three_parts(float a, float b, uint32_t (&p)[3]) 
 // alone, one for each CTA of a cluster; CTA q joins the ranks of slice q: the
 // others write their accumulators of it into its shared memory, and it adds them
 // in range order.  About 12 blocks a range give two CTAs an SM, with 90 KB in
-// flight each, at 8192 tokens of 3072 channels: 16.4 us cold, 3.1 TB/s; 13.8 for half of
-// them, 1.8 TB/s: a chain of latencies (the sample's id, the first blocks, the join) and
-// one ring's worth behind it.  (24 or 48 blocks a range, and rings of 225 KB: slower.)
+// flight each, at 8192 tokens of 3072 channels.  At 4096 a CTA has 0.5 us to its sample's
+// id, 2.7 to the first block, 4.2 at 5.6 TB/s, 0.7 to the last MMA's end, 1.8 for the join.
+// (24 or 48 blocks a range, and rings of 225 KB: slower.  The blocks that the ring has no
+// room for asked of memory at once: 1.6 us more, since the first ones come no sooner than
+// the last.)
 //
 // Roles (128 threads): warp 0 lane 0 the copies, warp 1 lane 0 the MMAs, then
 // thread t holds token t.
@@ -240,46 +237,33 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
         bars_init(sm, 1);
     }
     if (warp == 1) tmem_alloc(&sm.tmem, g.tmem_cols);
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = sm.tmem;
+    if (g.ks > 1) cluster_arrive();  // waited for where the others' shared memory is first written
     pdl_wait();
+    pdl_trigger();  // not before every CTA holds its tensor memory (tmem_alloc)
     const int a = adapter_of(g.ids, g.is64, b, g.NA);
     const int n = rows_of(g.lens, b, g.S);
     // no adapter, or no row of this tile: nothing reads its state (the whole cluster leaves)
-    const bool idle = a < 0 || t0 >= n;
-    auto copy = [&](int i) {  // block i of this range
-        const int s = i % g.stages;
-        unsigned char *st = ring + (size_t)s * stage_bytes;
-        mbar_arrive_expect_tx(&sm.full[s], (uint32_t)stage_bytes);
-        tma_load_3d(st, &map_x, (kb0 + i) * kBlk, t0, b, &sm.full[s]);
-        tma_load_3d(st + kRowTile, &map_w, (kb0 + i) * kBlk, 0, a, &sm.full[s]);
-    };
-    // the first copies before the CTAs of the cluster meet
-    const int early = idle ? 0 : min(nkb, g.stages);
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < early; ++i) copy(i);
-        // the ring is short beside the latency: the rest is asked of memory at once, and found in L2
-        for (int i = early; i < (idle ? 0 : nkb); ++i) tma_prefetch_3d(&map_x, (kb0 + i) * kBlk, t0, b);
-    }
-    tc_before_sync();
-    if (g.ks > 1 && !idle)
-        cluster_sync();  // also: the cluster's CTAs run, so their shared memory may be written
-    else
-        __syncthreads();
-    pdl_trigger();  // not before every CTA holds its tensor memory (tmem_alloc)
-    tc_after_sync();
-    const uint32_t tmem = sm.tmem;
-    if (idle) {
+    if (a < 0 || t0 >= n) {
+        if (g.ks > 1) cluster_wait();
         if (warp == 1) tmem_free(tmem, g.tmem_cols);
         return;
     }
-
     if (warp == 0 && lane == 0) {
-        int issued = early;
-        for (int i = early; i < nkb; ++i) {
-            if (!mbar_wait_or_abort(&sm.empty[i % g.stages], (uint32_t)(i / g.stages - 1) & 1u, abort_flag)) {
+        int issued = 0;
+        for (int i = 0; i < nkb; ++i) {
+            const int s = i % g.stages;
+            if (i >= g.stages && !mbar_wait_or_abort(&sm.empty[s], (uint32_t)(i / g.stages - 1) & 1u, abort_flag)) {
                 *abort_flag = 1;
                 break;
             }
-            copy(i);
+            unsigned char *st = ring + (size_t)s * stage_bytes;
+            mbar_arrive_expect_tx(&sm.full[s], (uint32_t)stage_bytes);
+            tma_load_3d(st, &map_x, (kb0 + i) * kBlk, t0, b, &sm.full[s]);
+            tma_load_3d(st + kRowTile, &map_w, (kb0 + i) * kBlk, 0, a, &sm.full[s]);
             issued = i + 1;
         }
         // every copy issued has landed before the CTA may leave
@@ -314,6 +298,7 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
     }
     ok = __syncthreads_and(ok);
     tc_after_sync();
+    if (g.ks > 1) cluster_wait();  // the cluster's CTAs run: their shared memory may be written
     const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
     const int slice = g.Rp / g.ks;  // ranks of a CTA
     uint32_t at = g.ks > 1 ? map_to_rank(part + (int)rank * slice * kPartPitch + threadIdx.x, 0u)
