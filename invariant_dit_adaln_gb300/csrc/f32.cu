@@ -113,12 +113,19 @@ f32_proj_fwd_kernel(const float *__restrict__ u, const float *__restrict__ W, co
 // accumulator (packed fp32x2 instructions, explicit rounding), the halves
 // added, then the xor butterfly; mean = sum / D, var = sum (x - mean)^2 / D,
 // rstd = 1 / sqrt(var + eps), each operation rounded once.
-// CKPT: a lane also writes the 8-bit record's part of its vectors.
+// CKPT: a lane also writes the 8-bit record's part of its vectors.  Its chains are
+// long, and steps past the row's end cost as much as others, so there are forms of
+// fewer vectors a lane, with more warps an SM
+// (104218 rows of 72 columns: 157 us with 24 vectors a lane, 41 with 2; 8000 rows of 1160:
+// 30, and 24 with 12).
 // --------------------------------------------------------------------------
 constexpr int kF32FwdVPL = kF32MaxD / 128;  // 32 vectors per lane at most
 
+// CTAs an SM holds
+constexpr int f32_fwd_ctas(int VPL) { return VPL <= 2 ? 6 : VPL <= 4 ? 5 : VPL <= 8 ? 4 : VPL <= 24 ? 2 : 1; }
+
 template <int VPL, bool CKPT>
-__global__ void __launch_bounds__(256, VPL <= 24 ? 2 : 1)
+__global__ void __launch_bounds__(256, f32_fwd_ctas(VPL))
 f32_out_fwd_kernel(const float *__restrict__ x, const float *__restrict__ emb, float *__restrict__ out,
                    float *__restrict__ mean, float *__restrict__ rstd, int S, int D, float eps, int rows_per_cta,
                    unsigned char *__restrict__ ckpt) {
@@ -152,7 +159,7 @@ f32_out_fwd_kernel(const float *__restrict__ x, const float *__restrict__ emb, f
         if (CKPT) {
             unsigned char *rec = ckpt + row * ckpt8_row_bytes(D);
             const int code_bytes = ckpt8_code_bytes(D);
-            constexpr int kSide = 8;  // steps side by side
+            constexpr int kSide = VPL == 12 ? 6 : VPL < 8 ? VPL : 8;  // steps side by side
 #pragma unroll
             for (int j0 = 0; j0 < VPL; j0 += kSide)
                 if (128 * j0 < code_bytes) {  // the whole warp
@@ -658,14 +665,26 @@ static cudaError_t launch_f32_out_fwd_rows(const float *x, const float *emb, flo
                                            uint8_t *ckpt, int B, int S, int D, float eps, cudaStream_t stream,
                                            const DeviceInfo &dev) {
     const size_t smem = (size_t)2 * D * 4;
-    // about four CTAs of 8 warps per SM over the batch
-    int cps = (dev.sm_count * 4 + B - 1) / B;
+    // D <= 3072: 24 vectors per lane, two CTAs per SM
+    const int V = D / 4;
+    auto kern = V <= 32 * 24 ? f32_out_fwd_kernel<24, CKPT> : f32_out_fwd_kernel<kF32FwdVPL, CKPT>;
+    int per_sm = 4;
+    if constexpr (CKPT) {
+        if (V <= 32 * 2)
+            kern = f32_out_fwd_kernel<2, true>, per_sm = f32_fwd_ctas(2);
+        else if (V <= 32 * 4)
+            kern = f32_out_fwd_kernel<4, true>, per_sm = f32_fwd_ctas(4);
+        else if (V <= 32 * 8)
+            kern = f32_out_fwd_kernel<8, true>;
+        else if (V <= 32 * 12)
+            kern = f32_out_fwd_kernel<12, true>;
+    }
+    // about four CTAs of 8 warps per SM over the batch, or as many as it holds
+    int cps = (dev.sm_count * per_sm + B - 1) / B;
     if (cps > (S + 7) / 8) cps = (S + 7) / 8;
     if (cps < 1) cps = 1;
     const int rows = (S + cps - 1) / cps;
     const dim3 grid((unsigned)((S + rows - 1) / rows), (unsigned)B);
-    // D <= 3072: 24 vectors per lane, two CTAs per SM
-    auto kern = D / 4 <= 32 * 24 ? f32_out_fwd_kernel<24, CKPT> : f32_out_fwd_kernel<kF32FwdVPL, CKPT>;
     cudaError_t err = ensure_smem_attr((const void *)kern, smem, dev);
     if (err != cudaSuccess) return err;
     return launch_pdl(kern, grid, dim3(256), smem, stream, x, emb, out, mean, rstd, S, D, eps, rows, ckpt);

@@ -724,6 +724,8 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
 // 3072 and 3072 channels at rank 16: 30 us with a CTA a piece or two, a quarter of it the
 // last CTAs, 24.7 so, 4.1 TB/s.)  At rank 128 the state is three quarters of what a tile
 // reads, from L2: 18 us for 3700 rows of 2048 and 2560 channels, 150 MB into shared memory.
+// (Two tiles a CTA beside one state, 90 MB, two stages: 7 us more; 4 less only from 8192
+// rows of 3072 channels on.)
 //
 // Roles (192 threads): warp 0 lane 0 the copies, warp 1 the MMAs (and zeros for
 // the rows of a block past the sample's end, which may hold anything), warps 2

@@ -127,6 +127,15 @@ def test_norm_with_records_long_rows(B, S, D):
     check_norm(torch.bfloat16, B, S, D)
 
 
+@pytest.mark.parametrize("t", TYPES, ids=NAME.get)
+@pytest.mark.parametrize("D", [8, 16, 72, 128, 248, 256, 264, 504, 512, 520, 1016, 1024, 1032, 1528, 1536, 1544, 2056])
+def test_norm_with_records_at_every_form(t, D):
+    """The ends of the forms that hold a row in 1, 2, 4, 8, ... vectors a lane; more rows
+    than the warps of one wave."""
+    check_norm(t, 3, 37, D)
+    check_norm(t, 2, 5001 if D <= 256 else 1201, D, seed=1)
+
+
 def test_norm_with_records_many_rows():
     check_norm(torch.bfloat16, 3, 2053, 3072)
     check_norm(torch.float32, 2, 1029, 3072)
