@@ -57,64 +57,91 @@ struct Eight<float> {
 
 constexpr int kVecs = 4;  // vectors of 8 channels a lane has in flight
 
-// A warp takes 32 kVecs vectors (part blockIdx.y) of a row; the rows go by 8.  The
-// arithmetic is 30 to 60 instructions a vector: with a division for the place of a
+// Where a lane's vectors lie.  In rows of more than 512 channels a warp takes 32 kVecs
+// vectors (part blockIdx.y) of a row (C == kVecs); in shorter ones C == 2 or 1 steps end
+// the row and the next rows follow, and up to 128 channels a row has 4, 8 or 16 lanes (2^lg)
+// and several rows share a step.  (104218 rows of 72 channels with a warp a row: pack 39
+// us, unpack 17, most of it empty lanes; 11 and 6 so.)
+template <int C>
+struct Place {
+    int sub, v0;           // this lane's row within a step, and its first vector
+    int rows;              // rows of a step
+    __device__ __forceinline__ explicit Place(int lg) {
+        const int lane = threadIdx.x & 31;
+        sub = C == 1 ? lane >> lg : 0, rows = C == 1 ? 32 >> lg : 1;
+        v0 = C == 1 ? lane & ((1 << lg) - 1) : C == kVecs ? blockIdx.y * 32 * kVecs + lane : lane;
+    }
+    // the warp's rows, from `first()` on by `step()`; there are `left` steps of rows at `row` (this lane's first)
+    __device__ __forceinline__ int taken() const { return kVecs / C * rows; }
+    __device__ __forceinline__ long long first() const {
+        return ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * taken() + sub;
+    }
+    __device__ __forceinline__ long long step() const { return (long long)gridDim.x * 8 * taken(); }
+    __device__ __forceinline__ int left(long long row, long long all) const {
+        const int n = (int)min(all - row, (long long)taken());
+        return (n + rows - 1) / rows;
+    }
+};
+
+// The arithmetic is 30 to 60 instructions a vector: with a division for the place of a
 // task, and the halves' largest value by emulated 16-bit maxima, pack issued 154.
-template <typename T>
+template <typename T, int C>
 __global__ void __launch_bounds__(256)
-ckpt8_pack_kernel(const T *__restrict__ x, unsigned char *__restrict__ ckpt, long long rows, int D) {
-    const int lane = threadIdx.x & 31;
+ckpt8_pack_kernel(const T *__restrict__ x, unsigned char *__restrict__ ckpt, long long rows, int D, int lg) {
     const int V = D >> 3, P = ckpt8_row_bytes(D), code_bytes = ckpt8_code_bytes(D);
-    const int v0 = blockIdx.y * 32 * kVecs + lane;
+    const Place<C> at(lg);
+    const int v0 = at.v0;
     pdl_wait();
     pdl_trigger();
-    for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (long long)gridDim.x * 8) {
+    for (long long row = at.first(); row - at.sub < rows; row += at.step()) {
+        const int left = C == kVecs ? 1 : at.left(row, rows);
         const T *src = x + row * D + v0 * 8;
-        unsigned char *rec = ckpt + row * P;
         Eight<T> e[kVecs];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
             e[j].zero();
-            if (v0 + 32 * j < V) e[j].load(src + 256 * j);
+            if (j / C < left && v0 + 32 * (j % C) < V) e[j].load(src + (long long)(j / C * at.rows) * D + 256 * (j % C));
         }
         uint32_t top[kVecs];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) top[j] = e[j].max_bits();
-        ckpt8_put<kVecs, 8>(rec, code_bytes, V, v0, top, [&](int j, px2 (&p)[4]) { e[j].pairs(p); });
+        ckpt8_put<kVecs, 8, C>(ckpt + row * P, code_bytes, V, v0, top, [&](int j, px2 (&p)[4]) { e[j].pairs(p); },
+                               (size_t)at.rows * P, left);
     }
 }
 
-template <typename T>
+template <typename T, int C>
 __global__ void __launch_bounds__(256)
-ckpt8_unpack_kernel(const unsigned char *__restrict__ ckpt, T *__restrict__ x, long long rows, int D) {
-    const int lane = threadIdx.x & 31;
+ckpt8_unpack_kernel(const unsigned char *__restrict__ ckpt, T *__restrict__ x, long long rows, int D, int lg) {
     const int V = D >> 3, P = ckpt8_row_bytes(D);
-    const int v0 = blockIdx.y * 32 * kVecs + lane, at = ckpt8_code_bytes(D) + (v0 >> 2);
+    const Place<C> place(lg);
+    const int v0 = place.v0, at = ckpt8_code_bytes(D) + (v0 >> 2);
     pdl_wait();
     pdl_trigger();
-    for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (long long)gridDim.x * 8) {
-        const unsigned char *rec = ckpt + row * P;
-        T *dst = x + row * D + v0 * 8;
+    for (long long row = place.first(); row - place.sub < rows; row += place.step()) {
+        const int left = C == kVecs ? 1 : place.left(row, rows);
         uint2 c[kVecs];
         uint32_t s[kVecs];
+        auto live = [&](int j) { return j / C < left && v0 + 32 * (j % C) < V; };
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
             c[j] = make_uint2(0u, 0u), s[j] = 1u;
-            if (v0 + 32 * j < V) {
-                c[j] = __ldcs(reinterpret_cast<const uint2 *>(rec + v0 * 8) + 32 * j);
-                s[j] = rec[at + 8 * j];
+            if (live(j)) {
+                const unsigned char *rec = ckpt + (row + j / C * place.rows) * P;
+                c[j] = __ldcs(reinterpret_cast<const uint2 *>(rec + v0 * 8) + 32 * (j % C));
+                s[j] = rec[at + 8 * (j % C)];
             }
         }
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            if (v0 + 32 * j >= V) continue;
+            if (!live(j)) continue;
             const px2 step = px_splat(ckpt8_step(s[j]));
             px2 p[4];
             ckpt8_floats(c[j].x, p[0], p[1]);
             ckpt8_floats(c[j].y, p[2], p[3]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) p[q] = px_mul(p[q], step);
-            Eight<T>::store(dst + 256 * j, p);
+            Eight<T>::store(x + (row + j / C * place.rows) * D + v0 * 8 + 256 * (j % C), p);
         }
     }
 }
@@ -186,25 +213,32 @@ ckpt8_again_kernel(const unsigned char *__restrict__ ckpt, const T *__restrict__
     }
 }
 
-// rows by 8, in turns where they are more than a grid has room for
-dim3 rows_grid(int64_t rows, int parts) {
-    const int64_t x = (rows + 7) / 8;
-    return dim3((unsigned)(x < (1 << 30) ? x : (1 << 30)), (unsigned)parts);
+// pack or unpack `rows` rows of V vectors (those of a record's groups included)
+template <typename K1, typename K2, typename K4, typename... Args>
+cudaError_t launch_rows(K1 k1, K2 k2, K4 k4, int64_t rows, int V, cudaStream_t stream, Args... args) {
+    int lg = 2;  // lanes of a row: 4 to 32
+    while (lg < 5 && (1 << lg) < V) ++lg;
+    const int steps = V <= 32 ? 1 : V <= 64 ? 2 : kVecs;  // of a row
+    const int taken = kVecs / steps * (steps == 1 ? 32 >> lg : 1);  // rows of a warp
+    const int64_t x = (rows + 8 * taken - 1) / (8 * taken);  // in turns where they are more than a grid has room for
+    const dim3 grid((unsigned)(x < (1 << 30) ? x : (1 << 30)), (unsigned)((V + 32 * kVecs - 1) / (32 * kVecs)));
+    auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(256), 0, stream, args..., lg); };
+    return steps == 1 ? go(k1) : steps == 2 ? go(k2) : go(k4);
 }
 
 }  // namespace
 
 template <typename T>
 cudaError_t launch_ckpt8_pack(const T *x, uint8_t *ckpt, int64_t rows, int D, cudaStream_t stream) {
-    const int Vg = (D / 8 + 3) & ~3, parts = (Vg + 32 * kVecs - 1) / (32 * kVecs);
-    return launch_pdl(ckpt8_pack_kernel<T>, rows_grid(rows, parts), dim3(256), 0, stream, x, ckpt, (long long)rows, D);
+    // whole groups: 8 bytes of padding behind the codes are a lane's too
+    return launch_rows(ckpt8_pack_kernel<T, 1>, ckpt8_pack_kernel<T, 2>, ckpt8_pack_kernel<T, kVecs>, rows,
+                       (D / 8 + 3) & ~3, stream, x, ckpt, (long long)rows, D);
 }
 
 template <typename T>
 cudaError_t launch_ckpt8_unpack(const uint8_t *ckpt, T *x, int64_t rows, int D, cudaStream_t stream) {
-    const int parts = (D / 8 + 32 * kVecs - 1) / (32 * kVecs);
-    return launch_pdl(ckpt8_unpack_kernel<T>, rows_grid(rows, parts), dim3(256), 0, stream, ckpt, x, (long long)rows,
-                      D);
+    return launch_rows(ckpt8_unpack_kernel<T, 1>, ckpt8_unpack_kernel<T, 2>, ckpt8_unpack_kernel<T, kVecs>, rows, D / 8,
+                       stream, ckpt, x, (long long)rows, D);
 }
 
 template <typename T>

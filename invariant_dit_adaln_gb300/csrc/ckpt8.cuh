@@ -85,12 +85,16 @@ __device__ __forceinline__ uint32_t ckpt8_max(const float4 &a, const float4 &b) 
 // max_bits[j] is 0 and pairs(j, p) gives zeros.  The whole warp runs this; steps j
 // with 32 j past the row's last group do nothing.  Fills the record's padding as well.
 //
+// C < N: the row ends after C steps, and the steps go on in the next row, row_step
+// bytes of records further; the first `left` of these N / C rows are there (the
+// others' max_bits 0, their pairs zeros).
+//
 // A step's chain (maximum, exchanges, scale, codes) is long and its work short, so the
 // N chains run side by side, without branches, but where a group holds an infinity,
 // a NaN or ends at the last scale: then the row's part is written one by one.
-template <int N, int E, typename F>
+template <int N, int E, int C = N, typename F>
 __device__ __forceinline__ void ckpt8_put(unsigned char *rec, int code_bytes, int V, int v0, uint32_t (&max_bits)[N],
-                                          F pairs) {
+                                          F pairs, size_t row_step = 0, int left = 1) {
     constexpr int LANES = kCkptGroup / E;
     static_assert(E == 8 || E == 4, "8 bytes of codes a lane, or 4");
 #pragma unroll
@@ -101,14 +105,16 @@ __device__ __forceinline__ void ckpt8_put(unsigned char *rec, int code_bytes, in
 #pragma unroll
     for (int j = 0; j < N; ++j) scale[j] = ckpt8_scale(max_bits[j]), most = max(most, scale[j]);
     auto store = [&](int j, const uint32_t (&c)[E / 4]) {
-        const int v = v0 + 32 * j;
+        if (C < N && j / C >= left) return;
+        unsigned char *to = rec + (j / C) * row_step;
+        const int v = v0 + 32 * (j % C);
         if (v * E < code_bytes) {
             if (E == 8)
-                *reinterpret_cast<uint2 *>(rec + (size_t)v * E) = make_uint2(c[0], c[E / 4 - 1]);
+                *reinterpret_cast<uint2 *>(to + (size_t)v * E) = make_uint2(c[0], c[E / 4 - 1]);
             else
-                *reinterpret_cast<uint32_t *>(rec + (size_t)v * E) = c[0];
+                *reinterpret_cast<uint32_t *>(to + (size_t)v * E) = c[0];
         }
-        if (v % LANES == 0 && v < V) rec[code_bytes + v / LANES] = (unsigned char)scale[j];
+        if (v % LANES == 0 && v < V) to[code_bytes + v / LANES] = (unsigned char)scale[j];
     };
     if (!__any_sync(0xFFFFFFFFu, most >= kCkptLastScale)) {
 #pragma unroll
@@ -137,8 +143,9 @@ __device__ __forceinline__ void ckpt8_put(unsigned char *rec, int code_bytes, in
     }
     // the scales' padding, by the lane of the last group
     const int last = (V - 1) / LANES * LANES;
-    if (last >= v0 && (last - v0) % 32 == 0 && (last - v0) / 32 < N)
-        for (int i = last / LANES + 1; i & 15; ++i) rec[code_bytes + i] = 0;
+    if (last >= v0 && (last - v0) % 32 == 0 && (last - v0) / 32 < C)
+        for (int r = 0; r < (C < N ? left : 1); ++r)
+            for (int i = last / LANES + 1; i & 15; ++i) rec[r * row_step + code_bytes + i] = 0;
 }
 
 }  // namespace adaln

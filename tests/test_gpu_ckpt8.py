@@ -60,6 +60,26 @@ def test_records(t, D):
 
 
 @pytest.mark.parametrize("t", TYPES, ids=NAME.get)
+@pytest.mark.parametrize("D", [8, 32, 40, 64, 72, 104, 120, 128, 136, 240, 256, 264, 504, 512, 520, 1048])
+def test_records_of_several_rows_a_warp(t, D):
+    """Any number of rows, and nothing written behind the last; groups that are not finite
+    among them."""
+    gen = torch.Generator("cuda").manual_seed(D)
+    P = binding.adaln_ckpt8_row_bytes(D)
+    for n in (1, 2, 5, 9, 31, 33, 67, 131, 1030):
+        x = rows(gen, t, n, D)
+        x[n // 2, D // 2] = float("nan")
+        x[-1, -1] = float("inf")
+        wide = torch.full((n + 40, P), 77, dtype=torch.uint8, device="cuda")
+        fn("ckpt8_pack", t)(x, wide[:n])
+        assert torch.equal(wide[:n].cpu(), record_of(x)) and (wide[n:] == 77).all()
+        out = torch.full((n + 40, D), 5.0, dtype=t, device="cuda")
+        fn("ckpt8_unpack", t)(wide[:n], D, out[:n])
+        want = value_of(wide[:n].cpu(), D)
+        assert torch.equal(out[:n].cpu().double().nan_to_num(7e30), want.nan_to_num(7e30)) and (out[n:] == 5).all()
+
+
+@pytest.mark.parametrize("t", TYPES, ids=NAME.get)
 def test_every_size_of_a_largest_value(t):
     """Largest magnitudes at and around each border, over the whole range; ties."""
     steps = [127.5, 127.0, 126.5, 64.0, 63.75, 63.5, 0.5, 1.5, 2.5]
