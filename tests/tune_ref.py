@@ -61,8 +61,8 @@ class Lora:
     h: a lane's chain holds K / 64 pairs (CUDA cores), a tensor-core range K / 16
     instructions of 16 products; 2 (K / 16 + 16) + 16 U is more than either, and
     the joins.  Held as two bf16 parts: 2^-17.  out: R products and the base, 2 U
-    each.  Gradients: a piece's rows (256 fused multiply-adds, or 1024 / 16
-    instructions: 2 (64 + 16) U), the pieces, the samples.
+    each.  Gradients: a piece's rows (256 fused multiply-adds and their join: 320 U is
+    more; 512 / 16 instructions: 2 (32 + 16) U), the pieces, the samples.
     """
 
     def __init__(self, x, A, Uw, scale, ids, y, lens, d_out=None, dx_base=None):
