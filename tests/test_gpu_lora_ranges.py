@@ -51,6 +51,15 @@ def test_drawn(t, seed):
     verify(t, c, run(t, c), f"{size}: ")
 
 
+@pytest.mark.parametrize("t", TYPES, ids=NAME.get)
+@pytest.mark.parametrize("S", range(1, 19))
+def test_few_tokens(t, S):
+    """Each number of tokens up to the tensor cores' first, alone and with lengths."""
+    for B, R, lens in ((5, 24, None), (40, 56, [i * 7 % (S + 1) for i in range(40)])):
+        c = inputs(t, B, S, 392, 200, R, 3, lens=lens)
+        verify(t, c, run(t, c), f"{B}: ")
+
+
 @pytest.mark.parametrize("R", range(8, 136, 8))
 def test_every_rank(R):
     """bf16 above 16 tokens: the stages, accumulators and schedules depend on R."""
