@@ -154,9 +154,9 @@ size_t adaln_lora_state_bytes(int B, int S, int R);
  *   out   [B, S, N]   bf16 rows    may describe exactly y's rows (in place)
  *   state             written: what adaln_lora_bwd needs, adaln_lora_state_bytes
  *
- * h is held in fp32; where S > 16 (bf16) the product with U takes it to 16
- * significant bits (2^-17 relative; an |h| above bf16's largest finite number, 3.39e38,
- * counts as infinite).  A row's result does not depend on the other samples; its order
+ * h is held in fp32; on the tensor cores (bf16, S >= 12 and S R >= 640) the product
+ * with U takes it to 16 significant bits (2^-17 relative; an |h| above bf16's largest
+ * finite number, 3.39e38, counts as infinite).  A row's result does not depend on the other samples; its order
  * depends on K, R and S only.  What an infinity or a NaN enters is infinite or NaN, and
  * nothing else changes.
  *

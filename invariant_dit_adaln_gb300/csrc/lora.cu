@@ -5,8 +5,8 @@
 //     shrink   h[b,s,:] = scale_a W_a src[b,s,:]           (x with A; d_out with U)
 //     expand   out[b,s,:] = base[b,s,:] + h[b,s,:] W_a     (h with U; e with A)
 //     grad     dW_a = sum over rows of h[b,s,:] src[b,s,:]^T
-// 2 R flop for each channel read or written: from 17 tokens a sample on, in bf16, on
-// the tensor cores (lora_tc.cu); here on the CUDA cores, fp32 and samples of a few
+// 2 R flop for each channel read or written: bf16 on the tensor cores where a sample
+// has work for them (lora_tc.cu); here on the CUDA cores, fp32 and samples of a few
 // tokens.  These calls are small, and a chain of latencies more than anything else:
 // what a kernel can read before the one it follows has ended, it does.  Cold, at 257
 // samples of a token, 3072 and 6144 channels, 4 adapters of rank 16: shrink 11 and 16 us,
@@ -561,7 +561,7 @@ cudaError_t expand(const float *h, const T *W, const LoraCall &c, int C, cudaStr
 }
 
 template <typename T>
-bool on_tensor_cores(int S) { return sizeof(T) == 2 && S >= kLoraTcMinTokens; }
+bool on_tensor_cores(int S, int R) { return sizeof(T) == 2 && lora_tc(S, R); }
 
 // Pieces in parallel, where their sums are no more than what is read anyway
 bool grad_in_parts(int S, int R, int es, int piece) {
@@ -570,12 +570,12 @@ bool grad_in_parts(int S, int R, int es, int piece) {
 
 // rows of a piece
 template <typename T>
-int piece_rows(int S) { return on_tensor_cores<T>(S) ? kLoraTcPiece : kGradPiece; }
+int piece_rows(int S, int R) { return on_tensor_cores<T>(S, R) ? kLoraTcPiece : kGradPiece; }
 
 template <typename T>
 cudaError_t grads(const float *h, const float *e, float *part, const LoraCall &c, cudaStream_t stream,
                   const DeviceInfo &dev) {
-    const int rows = piece_rows<T>(c.S), pieces = (c.S + rows - 1) / rows;
+    const int rows = piece_rows<T>(c.S, c.R), pieces = (c.S + rows - 1) / rows;
     const bool in_parts = grad_in_parts(c.S, c.R, sizeof(T), rows);
     const int width = in_parts ? 128 : 512;  // channels of a CTA
     GradOperand o0 = {c.x.data, c.x.batch, c.x.token, e, c.dA, part, c.K, c.dA ? (c.K + width - 1) / width : 0};
@@ -583,7 +583,7 @@ cudaError_t grads(const float *h, const float *e, float *part, const LoraCall &c
                       part + (long long)c.B * pieces * c.R * c.K, c.N, c.dU ? (c.N + width - 1) / width : 0};
     const unsigned x = (unsigned)((o0.blocks + o1.blocks) * (c.R / (in_parts ? kRB : kOwnerRanks)));
     cudaError_t err;
-    if (on_tensor_cores<T>(c.S))
+    if (on_tensor_cores<T>(c.S, c.R))
         err = lora_tc_grads(o0, o1, c, in_parts, stream, dev);
     else if (in_parts)
         err = launch_pdl(lora_grad_parts_kernel<T>, dim3(x, pieces, c.B), dim3(128), 0, stream, o0, o1, c.ids,
@@ -604,7 +604,7 @@ size_t lora_state_bytes(int B, int S, int R) { return (size_t)B * R * ((S + 7) /
 
 template <typename T>
 size_t lora_bwd_ws_bytes(int B, int S, int K, int N, int R) {
-    const int rows = piece_rows<T>(S);
+    const int rows = piece_rows<T>(S, R);
     const size_t pieces = grad_in_parts(S, R, sizeof(T), rows) ? (S + rows - 1) / rows : 0;
     return lora_state_bytes(B, S, R) + (size_t)B * pieces * R * ((size_t)K + N) * 4;
 }
@@ -613,12 +613,12 @@ template <typename T>
 static cudaError_t down(const adaln_rows &src, const void *W, const LoraCall &c, int C, void *h, cudaStream_t stream,
                  const DeviceInfo &dev) {
     if (c.NA == 0) return cudaSuccess;  // nothing reads h
-    if (on_tensor_cores<T>(c.S)) return lora_tc_shrink(src, W, c, C, h, stream, dev);
+    if (on_tensor_cores<T>(c.S, c.R)) return lora_tc_shrink(src, W, c, C, h, stream, dev);
     return shrink<T>(src, static_cast<const T *>(W), c, C, static_cast<float *>(h), stream);
 }
 template <typename T>
 static cudaError_t up(const void *h, const void *W, const LoraCall &c, int C, cudaStream_t stream, const DeviceInfo &dev) {
-    if (on_tensor_cores<T>(c.S)) return lora_tc_expand(h, W, c, C, stream, dev);
+    if (on_tensor_cores<T>(c.S, c.R)) return lora_tc_expand(h, W, c, C, stream, dev);
     return expand<T>(static_cast<const float *>(h), static_cast<const T *>(W), c, C, stream);
 }
 

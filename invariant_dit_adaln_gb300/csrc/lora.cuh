@@ -33,12 +33,20 @@ struct GradOperand {
 };
 
 // --------------------------------------------------------------------------
-// lora_tc.cu: the tensor-core forms, for bf16 rows and more than 16 tokens a
-// sample.  h and e are held as the exact sum of three bf16 parts, transposed:
+// lora_tc.cu: the tensor-core forms, for bf16 rows, by S and R (not by B, on which no
+// result may depend).  A tile is 128 tokens, so that samples of a few cost them as much
+// as long ones, and the CUDA cores' work grows with S R.  Forward and backward, us, on
+// the tensor cores and on the CUDA cores:
+//     64 samples, 3072 and 3072 channels   rank 8: 48 tokens 72 and 65, 64 tokens 73 and 81;
+//       rank 16: 24 tokens 72 and 84, 48 tokens 76 and 107;  rank 32: 16 tokens 71 and 76;
+//       rank 64: 8 tokens 118 and 75, 16 tokens 117 and 130;  rank 128: 8 tokens 178 and 131
+//     4 samples   rank 16: 24 tokens 32 and 18, 48 tokens 34 and 18, 96 tokens 34 and 22;
+//       rank 64: 16 tokens 43 and 26, 64 tokens 40 and 46
+// h and e are held as the exact sum of three bf16 parts, transposed:
 // [B][3R][Sp], the leading parts of the R ranks, the parts of the rests, theirs;
 // Sp = S rounded up to 8.
 // --------------------------------------------------------------------------
-constexpr int kLoraTcMinTokens = 17;
+inline bool lora_tc(int S, int R) { return S >= 12 && S * R >= 640; }
 // Consecutive rows of a sample that a gradient sums from +0.  The tensor core cuts
 // off what it adds: with 1024 rows the gradients' error was 1.07e-6 (rank 128), half
 // of it from there; the pieces' sums are joined with proper rounding.

@@ -1,5 +1,4 @@
-// The adapters' products on the tensor cores (lora.cuh says which calls): bf16
-// rows, more than 16 tokens a sample.
+// The adapters' products on the tensor cores (lora.cuh says which calls).
 //
 // Each operand row is read once from memory and R is small, so all three are
 // bound by memory; what matters is that the bytes flow without passing through

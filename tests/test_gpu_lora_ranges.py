@@ -60,6 +60,18 @@ def test_few_tokens(t, S):
         verify(t, c, run(t, c), f"{B}: ")
 
 
+@pytest.mark.parametrize("S,R", [(11, 64), (11, 128), (12, 48), (12, 56), (12, 128), (13, 48), (14, 48), (15, 40), (16, 40),
+                                 (19, 32), (20, 32), (26, 24), (27, 24), (39, 16), (40, 16), (79, 8), (80, 8)])
+def test_both_sides_of_the_tensor_cores(S, R):
+    t = torch.bfloat16
+    for B, lens in ((3, None), (37, [i * 5 % (S + 1) for i in range(37)])):
+        c = inputs(t, B, S, 200, 392, R, 3, lens=lens)
+        verify(t, c, run(t, c), f"{B}: ")
+        alone = {k: v if k in ("A", "U", "scale") else v[1:2].contiguous() for k, v in c.items() if v is not None}
+        alone.setdefault("lens", None)
+        assert all(same(a[0], b[1]) for a, b in zip(run(t, alone)[:2], run(t, c)[:2]))
+
+
 @pytest.mark.parametrize("R", range(8, 136, 8))
 def test_every_rank(R):
     """bf16 above 16 tokens: the stages, accumulators and schedules depend on R."""
