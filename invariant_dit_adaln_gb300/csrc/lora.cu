@@ -589,8 +589,8 @@ cudaError_t grads(const float *h, const float *e, float *part, const LoraCall &c
         err = launch_pdl(lora_grad_parts_kernel<T>, dim3(x, pieces, c.B), dim3(128), 0, stream, o0, o1, c.ids,
                          c.ids_are_64, c.lens, c.grads_early, c.S, c.R, c.NA, pieces);
     else
-        err = launch_pdl(lora_grad_owner_kernel<T, sizeof(T) == 2 ? 16 : 8>, dim3(x, c.NA), dim3(128), 0, stream, o0, o1, c.ids, c.ids_are_64, c.lens,
-                         c.grads_early, c.accumulate, c.B, c.S, c.R, c.NA);
+        err = launch_pdl(lora_grad_owner_kernel<T, sizeof(T) == 2 ? 16 : 8>, dim3(x, c.NA), dim3(128), 0, stream, o0,
+                         o1, c.ids, c.ids_are_64, c.lens, c.grads_early, c.accumulate, c.B, c.S, c.R, c.NA);
     if (err != cudaSuccess || !in_parts) return err;
     const long long n = (long long)c.R * ((c.dA ? c.K : 0) + (c.dU ? c.N : 0)) / 4;
     return launch_pdl(lora_join_kernel, dim3((unsigned)((n + 127) / 128), c.NA), dim3(128), 0, stream, o0, o1, c.ids,
@@ -617,7 +617,8 @@ static cudaError_t down(const adaln_rows &src, const void *W, const LoraCall &c,
     return shrink<T>(src, static_cast<const T *>(W), c, C, static_cast<float *>(h), stream);
 }
 template <typename T>
-static cudaError_t up(const void *h, const void *W, const LoraCall &c, int C, cudaStream_t stream, const DeviceInfo &dev) {
+static cudaError_t up(const void *h, const void *W, const LoraCall &c, int C, cudaStream_t stream,
+                      const DeviceInfo &dev) {
     if (on_tensor_cores<T>(c.S, c.R)) return lora_tc_expand(h, W, c, C, stream, dev);
     return expand<T>(static_cast<const float *>(h), static_cast<const T *>(W), c, C, stream);
 }

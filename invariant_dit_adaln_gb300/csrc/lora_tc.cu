@@ -716,7 +716,7 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
 // tokens of a piece in blocks of 64 (the MMA's k) through a ring of stages.  The
 // three parts' columns are added when they leave tensor memory.
 //
-// Schedules and order as lora_grad_kernel's: OWNER, every piece of an adapter in
+// Schedules and order as on the CUDA cores: OWNER, every piece of an adapter in
 // order by one CTA, with two accumulators (where they fit), so that one piece's
 // leave while the next one's MMAs run, and the total in shared memory; otherwise as
 // many CTAs as the device holds take every gridDim.x-th piece of every tile.  (8192 rows of
@@ -1117,10 +1117,12 @@ cudaError_t lora_tc_expand(const void *h, const void *W, const LoraCall &c, int 
         if (n * ctas > g.stages * per_sm) g.stages = n, per_sm = ctas;
     }
     const size_t smem = (size_t)g.stages * stage + beside;
-    const long long most = (long long)((C + kBlk - 1) / kBlk) * ((c.S + kM - 1) / kM) * c.B, room = (long long)per_sm * dev.sm_count;
+    const long long most = (long long)((C + kBlk - 1) / kBlk) * ((c.S + kM - 1) / kM) * c.B,
+                    room = (long long)per_sm * dev.sm_count;
     cudaError_t err = ensure_smem_attr((const void *)lora_expand_tc_kernel, smem, dev);
     if (err != cudaSuccess) return err;
-    return launch_pdl(lora_expand_tc_kernel, dim3((unsigned)(most < room ? most : room)), dim3(kExThreads), smem, stream, map_h, map_w, map_y, map_o, g);
+    return launch_pdl(lora_expand_tc_kernel, dim3((unsigned)std::min(most, room)), dim3(kExThreads), smem, stream,
+                      map_h, map_w, map_y, map_o, g);
 }
 
 cudaError_t lora_tc_grads(const GradOperand &o0, const GradOperand &o1, const LoraCall &c, bool in_parts,

@@ -60,8 +60,9 @@ def test_few_tokens(t, S):
         verify(t, c, run(t, c), f"{B}: ")
 
 
-@pytest.mark.parametrize("S,R", [(11, 64), (11, 128), (12, 48), (12, 56), (12, 128), (13, 48), (14, 48), (15, 40), (16, 40),
-                                 (19, 32), (20, 32), (26, 24), (27, 24), (39, 16), (40, 16), (79, 8), (80, 8)])
+@pytest.mark.parametrize("S,R", [(11, 64), (11, 128), (12, 48), (12, 56), (12, 128), (13, 48), (14, 48), (15, 40),
+                                 (16, 40), (19, 32), (20, 32), (26, 24), (27, 24), (39, 16), (40, 16), (79, 8),
+                                 (80, 8)])
 def test_both_sides_of_the_tensor_cores(S, R):
     t = torch.bfloat16
     for B, lens in ((3, None), (37, [i * 5 % (S + 1) for i in range(37)])):
