@@ -357,8 +357,9 @@ adaln_status adaln_f32_proj_fwd(const float *temb, const float *W, const float *
 
 /*
  * adaln_f32_out_fwd:  per row, mean = sum / D, rstd = 1 / sqrt(sum (x -
- * mean)^2 / D + eps) (fixed-order fp32 sums), xhat = fp32(fp32(x - mean) *
- * rstd), onep = fp32(1 + scale), out = fp32(fp32(xhat * onep) + shift).
+ * mean)^2 / D + eps) (fixed-order fp32 sums, the squares by fused multiply-
+ * adds), xhat = fp32(fp32(x - mean) * rstd), onep = fp32(1 + scale), out =
+ * fp32(fp32(xhat * onep) + shift).
  *   x [B,S,D], emb [B,2D] fp32 in;  out [B,S,D], mean, rstd [B,S] fp32 out.
  */
 adaln_status adaln_f32_out_fwd(const float *x, const float *emb, float *out, float *mean, float *rstd, int B, int S,

@@ -205,9 +205,7 @@ ckpt8_again_kernel(const unsigned char *__restrict__ ckpt, const T *__restrict__
         for (int q = 0; q < 4; ++q) {
             // the value is code * step exactly, so the fused form is fp32(value - mean)
             const px2 xhat = px_mul(px_fma(p[q], step, nmu), r2);
-            // rounded before the shift is added: scalar products, since a packed one may be fused into the add
-            const px2 y = px_make(__fmul_rn(px_lo(xhat), px_lo(onep[q])), __fmul_rn(px_hi(xhat), px_hi(onep[q])));
-            p[q] = px_add(y, shift[q]);
+            p[q] = px_add(px_mul_rounded(xhat, onep[q]), shift[q]);
         }
         Eight<T>::store(o + (size_t)i * D, p);
     }

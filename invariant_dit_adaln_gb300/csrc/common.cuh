@@ -78,10 +78,10 @@ __device__ __forceinline__ float2 f2sub(float2 a, float2 b) { return __ffma2_rn(
 // --------------------------------------------------------------------------
 // Packed fp32x2 in inline PTX, on a 64-bit register pair {lo, hi}.
 //
-// Every operation names its rounding (.rn), and PTX never contracts a
-// multiply or an add that carries an explicit rounding into a fused
-// multiply-add, so a product written here is always rounded before the add
-// that consumes it.  On this GPU a packed instruction occupies the FMA pipe for
+// Every operation names its rounding (.rn).  The caution above holds here as well: a
+// px_mul whose only use is a px_add or px_sub is merged into it, one rounding less
+// (seen in every bit of the fp32 norm's results while they were written so).
+// px_mul_rounded is for a product that must be rounded before it is added.  On this GPU a packed instruction occupies the FMA pipe for
 // two cycles (it does two lanes of work), so packing halves the issue slots of
 // fp32 arithmetic without changing its pipe time.
 // --------------------------------------------------------------------------
@@ -122,6 +122,10 @@ __device__ __forceinline__ float px_hi(px2 a) {
     float h;
     asm("{.reg .b32 l;\n\tmov.b64 {l, %0}, %1;}" : "=f"(h) : "l"(a));
     return h;
+}
+// a * b rounded, whatever is done with it (scalar products: never fused)
+__device__ __forceinline__ px2 px_mul_rounded(px2 a, px2 b) {
+    return px_make(__fmul_rn(px_lo(a), px_lo(b)), __fmul_rn(px_hi(a), px_hi(b)));
 }
 // a packed bf16x2 word (lo in the low half) as the exact fp32 pair, on the
 // integer pipe: the low half moved up by a byte permute, the high half masked

@@ -110,9 +110,9 @@ f32_proj_fwd_kernel(const float *__restrict__ u, const float *__restrict__ W, co
 // per CTA (onep and shift of the sample in shared memory).  Lane l holds the
 // float4 vectors l, l + 32, ... of the row in registers (D <= 4096).  Sums:
 // per lane in vector order, even and odd columns in the two halves of a packed
-// accumulator (packed fp32x2 instructions, explicit rounding), the halves
-// added, then the xor butterfly; mean = sum / D, var = sum (x - mean)^2 / D,
-// rstd = 1 / sqrt(var + eps), each operation rounded once.
+// accumulator (packed fp32x2 instructions, explicit rounding; the squares by
+// fused multiply-adds), the halves added, then the xor butterfly; mean = sum / D,
+// var = sum (x - mean)^2 / D, rstd = 1 / sqrt(var + eps), each operation rounded once.
 // CKPT: a lane also writes the 8-bit record's part of its vectors.  Its chains are
 // long, and steps past the row's end cost as much as others, so there are forms of
 // fewer vectors a lane, with more warps an SM
@@ -185,7 +185,7 @@ f32_out_fwd_kernel(const float *__restrict__ x, const float *__restrict__ emb, f
             if (lane + 32 * j < V) {
                 const px2 d0 = px_sub(px_make(xv[j].x, xv[j].y), mu2);
                 const px2 d1 = px_sub(px_make(xv[j].z, xv[j].w), mu2);
-                s2 = px_add(px_add(s2, px_mul(d0, d0)), px_mul(d1, d1));
+                s2 = px_fma(d1, d1, px_fma(d0, d0, s2));
             }
         const float var = __fdiv_rn(warp_sum(__fadd_rn(px_lo(s2), px_hi(s2))), Df);
         const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, eps)));
@@ -197,7 +197,8 @@ f32_out_fwd_kernel(const float *__restrict__ x, const float *__restrict__ emb, f
         float4 *orow = reinterpret_cast<float4 *>(out + row * D);
         // out = fp32(fp32(fp32(fp32(x - mean) * rstd) * onep) + shift)
         auto mod = [&](float a, float b, float on_a, float on_b, float sh_a, float sh_b) {
-            return px_add(px_mul(px_mul(px_sub(px_make(a, b), mu2), rs2), px_make(on_a, on_b)), px_make(sh_a, sh_b));
+            const px2 xh = px_mul(px_sub(px_make(a, b), mu2), rs2);
+            return px_add(px_mul_rounded(xh, px_make(on_a, on_b)), px_make(sh_a, sh_b));
         };
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
