@@ -292,7 +292,7 @@ f32_out_bwd_tile_kernel(const float *__restrict__ dy, const float *__restrict__ 
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     xh[j][c] = px_mul(px_sub(xp[j][c], mu2), rs2);
-                    const px2 p = px_mul(gp[j][c], xh[j][c]);
+                    const px2 p = px_mul(gp[j][c], xh[j][c]);  // of several uses: not merged
                     px_twosum(ss[j][c], ks[j][c], p);
                     px_twosum(sh[j][c], kh[j][c], gp[j][c]);
                     a1 = px_fma(gp[j][c], onep[j][c], a1);
@@ -317,8 +317,8 @@ f32_out_bwd_tile_kernel(const float *__restrict__ dy, const float *__restrict__ 
                 px2 o[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const px2 gh = px_mul(gp[j][c], onep[j][c]);
-                    o[c] = px_mul(rs2, px_sub(px_sub(gh, c1), px_mul(xh[j][c], c2)));
+                    const px2 gh = px_mul_rounded(gp[j][c], onep[j][c]);
+                    o[c] = px_mul(rs2, px_sub(px_sub(gh, c1), px_mul_rounded(xh[j][c], c2)));
                 }
                 stg16f_hint(dx + row * D + (size_t)v * 4, make_float4(px_lo(o[0]), px_hi(o[0]), px_lo(o[1]), px_hi(o[1])),
                             pol);
@@ -439,7 +439,7 @@ f32_out_bwd_ckpt8_kernel(const float *__restrict__ dy, const unsigned char *__re
                         load(i0 + r, j, xp, gp);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const px2 p = px_mul(gp[c], px_mul(px_sub(xp[c], mu2), rs2));
+                            const px2 p = px_mul(gp[c], px_mul(px_sub(xp[c], mu2), rs2));  // of several uses: not merged
                             px_twosum(ss[j][c], ks[j][c], p);
                             px_twosum(sh[j][c], kh[j][c], gp[c]);
                             a1 = px_fma(gp[c], onep[j][c], a1);
@@ -483,8 +483,8 @@ f32_out_bwd_ckpt8_kernel(const float *__restrict__ dy, const unsigned char *__re
                     load(i0 + r, j, xp, gp);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const px2 xh = px_mul(px_sub(xp[c], mu2), rs2), gh = px_mul(gp[c], onep[j][c]);
-                        o[c] = px_mul(rs2, px_sub(px_sub(gh, c1), px_mul(xh, c2)));
+                        const px2 xh = px_mul(px_sub(xp[c], mu2), rs2), gh = px_mul_rounded(gp[c], onep[j][c]);
+                        o[c] = px_mul(rs2, px_sub(px_sub(gh, c1), px_mul_rounded(xh, c2)));
                     }
                     stg16f_hint(dx + (row0 + i0 + r) * D + (size_t)v * 4,
                                 make_float4(px_lo(o[0]), px_hi(o[0]), px_lo(o[1]), px_hi(o[1])), pol);

@@ -54,3 +54,23 @@ def test_output(B, S, D):
         assert same(out8, out) and same(mean8, mean) and same(rstd8, rstd)
         if exact:
             assert same(binding.adaln_f32_out_again_ckpt8(ckpt, emb, mean, rstd), out)
+
+
+@pytest.mark.parametrize("B,S,D", SIZES + [(4, 77, 768), (1, 65, 2304), (1, 40, 2688)])
+def test_gradient(B, S, D):
+    """dx = fp32(rstd * fp32(fp32(gh - c1) - fp32(xhat * c2))), gh = fp32(g * onep), from x
+    and from its records.  One g that is not zero in a row, so that the row's sums have
+    one term: c1 = fp32(gh / D) and c2 = fp32(fp32(p * onep) / D), p = fp32(g * xhat)."""
+    x, emb = inputs(B, S, D)
+    gen = torch.Generator().manual_seed(S)
+    at = torch.randint(0, D, (B, S, 1), generator=gen)
+    dy = torch.zeros(B, S, D).scatter_(-1, at, torch.randn((B, S, 1), generator=gen))
+    _, mean, rstd, ckpt = binding.adaln_f32_out_fwd_ckpt8(x, emb)
+    for src, dx in ((x, binding.adaln_f32_out_bwd(dy.cuda(), x, emb, mean, rstd)[0]),
+                    (binding.adaln_f32_ckpt8_unpack(ckpt, D),
+                     binding.adaln_f32_out_bwd_ckpt8(dy.cuda(), ckpt, emb, mean, rstd)[0])):
+        xhat, onep, _ = parts(src, emb, mean, rstd)
+        gh, p = dy * onep, dy * xhat
+        c1 = gh.gather(-1, at) / D
+        c2 = (p * onep).gather(-1, at) / D
+        assert same(dx, rstd.cpu()[..., None] * ((gh - c1) - xhat * c2))
