@@ -220,11 +220,15 @@ lora_expand_kernel(const float *__restrict__ h, const T *__restrict__ W, const v
 #pragma unroll
     for (int i = 0; i < TOK; ++i) {
         if (i >= n) break;
-        px2 yp[E / 2];
-        y[i].pairs(yp);
+        uint4 o = y[i].v;  // without an adapter the base as it is (a zero added would lose the sign of -0)
+        if (a >= 0) {
+            px2 yp[E / 2];
+            y[i].pairs(yp);
 #pragma unroll
-        for (int q = 0; q < E / 2; ++q) acc[i][q] = px_add(yp[q], acc[i][q]);
-        stg16(out + b * batch + (s0 + i) * token + c0, Vec<T>::pack(acc[i]));
+            for (int q = 0; q < E / 2; ++q) acc[i][q] = px_add(yp[q], acc[i][q]);
+            o = Vec<T>::pack(acc[i]);
+        }
+        stg16(out + b * batch + (s0 + i) * token + c0, o);
     }
 }
 
