@@ -154,11 +154,13 @@ size_t adaln_lora_state_bytes(int B, int S, int R);
  *   out   [B, S, N]   bf16 rows    may describe exactly y's rows (in place)
  *   state             written: what adaln_lora_bwd needs, adaln_lora_state_bytes
  *
- * h is held in fp32; on the tensor cores (bf16, S >= 12 and S R >= 640) the product
- * with U takes it to 16 significant bits (2^-17 relative; an |h| above bf16's largest
- * finite number, 3.39e38, counts as infinite).  A row's result does not depend on the other samples; its order
- * depends on K, R and S only.  What an infinity or a NaN enters is infinite or NaN, and
- * nothing else changes.
+ * h is held in fp32.  On the tensor cores (bf16, S >= 12 and S R >= 640) what is added
+ * to a sum of up to 768 channels is cut off instead of rounded (8e-7 of h, rms, of random
+ * signs; these sums are added with rounding), the product with U takes h to 16
+ * significant bits (2^-17 relative), and an |h| above bf16's largest finite number,
+ * 3.39e38, counts as infinite.  A row's result does not depend on the other samples;
+ * its order depends on K, R and S only.  What an infinity or a NaN enters is infinite
+ * or NaN, and nothing else changes.
  *
  * Sizes: K, N multiples of 8 in [8, 65536]; R a multiple of 8 in [8, 128] (fill
  * up smaller adapters with zeros); 0 <= NA <= 65535; B, S as in adaln.h; B * S *

@@ -199,10 +199,22 @@ __device__ __forceinline__ void three_parts(float a, float b, uint32_t (&p)[3]) 
 // room for asked of memory at once: 1.6 us more, since the first ones come no sooner than
 // the last.)
 //
+// The tensor core cuts off what it adds, so an accumulator takes kChain blocks, the
+// next ones go to another beside it, and they are added with proper rounding: with one
+// accumulator for a whole range the relative error of h grew with the channels, 7e-7 at
+// 6144 (12 blocks), 2.1e-6 at 16384, 9.1e-6 at 65536 (3.5e-5 where all terms have one
+// sign).  Accumulators that do not fit a CTA's share of the SM's tensor memory (all that
+// share an SM find room for theirs: one that waits for columns holds up its cluster) are
+// taken in passes (LONG), whose sums a thread keeps in registers.  (Forward of 4096 rows of
+// 16384 channels at rank 128, three accumulators: 86.8 us, 84.7 with one; of 2048 rows of
+// 65536 in three passes: 139 and 111, at rank 16 without passes 58.7 and 57.9.  The next
+// pass's first blocks requested before this one's sums are taken: 144.)
+//
 // Roles (128 threads): warp 0 lane 0 the copies, warp 1 lane 0 the MMAs, then
 // thread t holds token t.
 // --------------------------------------------------------------------------
 constexpr int kPartPitch = kM + 4;  // floats of a rank's tokens
+constexpr int kChain = 12;          // blocks of channels that an accumulator takes
 
 struct ShrinkArgs {
     const float *scale;
@@ -213,9 +225,11 @@ struct ShrinkArgs {
     int S, C, R, NA, Sp;
     int Rp;      // R rounded up to the MMA's multiple of 16
     int ks;      // channel ranges: cluster size, 1, 2, 4 or 8, a divisor of Rp
+    int accs;    // accumulators of a pass
     int stages, tmem_cols;
 };
 
+template <bool LONG>
 __global__ void __launch_bounds__(128)
 lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                       const ShrinkArgs g) {
@@ -251,65 +265,100 @@ lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_co
         if (warp == 1) tmem_free(tmem, g.tmem_cols);
         return;
     }
-    if (warp == 0 && lane == 0) {
-        int issued = 0;
-        for (int i = 0; i < nkb; ++i) {
-            const int s = i % g.stages;
-            if (i >= g.stages && !mbar_wait_or_abort(&sm.empty[s], (uint32_t)(i / g.stages - 1) & 1u, abort_flag)) {
-                *abort_flag = 1;
-                break;
-            }
-            unsigned char *st = ring + (size_t)s * stage_bytes;
-            mbar_arrive_expect_tx(&sm.full[s], (uint32_t)stage_bytes);
-            tma_load_3d(st, &map_x, (kb0 + i) * kBlk, t0, b, &sm.full[s]);
-            tma_load_3d(st + kRowTile, &map_w, (kb0 + i) * kBlk, 0, a, &sm.full[s]);
-            issued = i + 1;
-        }
-        // every copy issued has landed before the CTA may leave
-        for (int s = 0; s < g.stages && s < issued; ++s) {
-            const int last = s + g.stages * ((issued - 1 - s) / g.stages);
-            if (!mbar_wait_bounded(&sm.full[s], (uint32_t)(last / g.stages) & 1u, kDrainNs))
-                report_error_lora(kErrDrainFailed);
-        }
-    } else if (warp == 1 && lane == 0) {
-        const uint32_t idesc = f16_idesc(g.Rp, false);
-        for (int i = 0; i < nkb; ++i) {
-            const int s = i % g.stages;
-            if ((i == 0 && !first_wait(sm)) ||
-                !mbar_wait_or_abort(&sm.full[s], (uint32_t)(i / g.stages) & 1u, abort_flag)) {
-                *abort_flag = 1;
-                break;
-            }
-            tc_after_sync();
-            const uint32_t st = smem_u32(ring + (size_t)s * stage_bytes);
-            const uint64_t ad = sw128_desc(st, 16, 1024), wd = sw128_desc(st + kRowTile, 16, 1024);
-#pragma unroll
-            for (int k = 0; k < kBlk / 16; ++k) mma_f16(tmem, ad + 2u * k, wd + 2u * k, idesc, i > 0 || k > 0);
-            mma_commit(&sm.empty[s]);
-        }
-        mma_commit(&sm.done);  // also after giving up: completes when every issued MMA has
-    }
-
-    bool ok = mbar_wait_or_abort(&sm.done, 0u, abort_flag) && !*abort_flag;
-    if (!ok && threadIdx.x == 0) {
-        report_error_lora(kErrLoraShrinkWait);
-        if (!mbar_wait_bounded(&sm.done, 0u, kDrainNs)) report_error_lora(kErrDrainFailed);
-    }
-    ok = __syncthreads_and(ok);
-    tc_after_sync();
-    if (g.ks > 1) cluster_wait();  // the cluster's CTAs run: their shared memory may be written
     const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+    // the accumulators of n blocks added up, ranks c .. c + 15 of this thread's token
+    auto chains = [&](int n, int c, float (&f)[16], bool from_zero) {
+        for (int q = 0; q * kChain < n; ++q) {
+            uint32_t v[16];
+            tmem_ld16(trow + (uint32_t)(q * g.Rp + c), v);
+            tmem_ld_done();
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                f[k] = from_zero && q == 0 ? __uint_as_float(v[k]) : __fadd_rn(f[k], __uint_as_float(v[k]));
+        }
+    };
+    float total[LONG ? kLoraMaxRank / 16 : 1][16];
+    const int span = LONG ? g.accs * kChain : nkb;  // blocks of a pass
+    bool ok = true;
+    for (int pass = 0, i0 = 0; i0 < nkb; ++pass, i0 += span) {
+        const int i1 = min(nkb, i0 + span);
+        if (warp == 0 && lane == 0) {
+            int issued = i0;
+            for (int i = i0; i < i1; ++i) {
+                const int s = i % g.stages;
+                if (i >= g.stages && !mbar_wait_or_abort(&sm.empty[s], (uint32_t)(i / g.stages - 1) & 1u, abort_flag)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                unsigned char *st = ring + (size_t)s * stage_bytes;
+                mbar_arrive_expect_tx(&sm.full[s], (uint32_t)stage_bytes);
+                tma_load_3d(st, &map_x, (kb0 + i) * kBlk, t0, b, &sm.full[s]);
+                tma_load_3d(st + kRowTile, &map_w, (kb0 + i) * kBlk, 0, a, &sm.full[s]);
+                issued = i + 1;
+            }
+            // every copy issued has landed before the CTA may leave
+            for (int s = 0; s < g.stages && s < issued; ++s) {
+                const int last = s + g.stages * ((issued - 1 - s) / g.stages);
+                if (!mbar_wait_bounded(&sm.full[s], (uint32_t)(last / g.stages) & 1u, kDrainNs))
+                    report_error_lora(kErrDrainFailed);
+            }
+        } else if (warp == 1 && lane == 0) {
+            const uint32_t idesc = f16_idesc(g.Rp, false);
+            if (LONG) tc_after_sync();  // the last pass's accumulators have been taken
+            for (int i = i0; i < i1; ++i) {
+                const int s = i % g.stages, q = (i - i0) / kChain;
+                if ((i == 0 && !first_wait(sm)) ||
+                    !mbar_wait_or_abort(&sm.full[s], (uint32_t)(i / g.stages) & 1u, abort_flag)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_after_sync();
+                const uint32_t st = smem_u32(ring + (size_t)s * stage_bytes);
+                const uint64_t ad = sw128_desc(st, 16, 1024), wd = sw128_desc(st + kRowTile, 16, 1024);
+                const uint32_t acc = tmem + (uint32_t)(q * g.Rp);
+#pragma unroll
+                for (int k = 0; k < kBlk / 16; ++k)
+                    mma_f16(acc, ad + 2u * k, wd + 2u * k, idesc, i - i0 > q * kChain || k > 0);
+                mma_commit(&sm.empty[s]);
+            }
+            mma_commit(&sm.done);  // also after giving up: completes when every issued MMA has
+        }
+
+        ok = mbar_wait_or_abort(&sm.done, (uint32_t)pass & 1u, abort_flag) && !*abort_flag;
+        if (!ok && threadIdx.x == 0) {
+            report_error_lora(kErrLoraShrinkWait);
+            if (!mbar_wait_bounded(&sm.done, (uint32_t)pass & 1u, kDrainNs)) report_error_lora(kErrDrainFailed);
+        }
+        ok = __syncthreads_and(ok);
+        tc_after_sync();
+        if (!ok) break;
+        if (LONG) {
+#pragma unroll
+            for (int c = 0; c < kLoraMaxRank / 16; ++c)
+                if (c * 16 < g.Rp) chains(i1 - i0, c * 16, total[c], pass == 0);
+            tc_before_sync();
+            __syncthreads();
+        }
+    }
+    if (g.ks > 1) cluster_wait();  // the cluster's CTAs run: their shared memory may be written
     const int slice = g.Rp / g.ks;  // ranks of a CTA
     uint32_t at = g.ks > 1 ? map_to_rank(part + (int)rank * slice * kPartPitch + threadIdx.x, 0u)
                            : smem_u32(part + threadIdx.x);  // place of the next rank
-    for (int c = 0, q = 0, i = 0; c < g.Rp; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(trow + (uint32_t)c, v);
-        tmem_ld_done();
+    int q = 0, i = 0;
+#pragma unroll(LONG ? kLoraMaxRank / 16 : 1)
+    for (int c = 0; c < (LONG ? kLoraMaxRank : g.Rp); c += 16) {
+        if (LONG && c >= g.Rp) break;
+        float v[16];
+        if constexpr (LONG) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = total[c / 16][k];
+        } else {
+            chains(nkb, c, v, true);
+        }
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {  // a slice is even
-            st_cluster_f32(at, __uint_as_float(v[k]));
-            st_cluster_f32(at + kPartPitch * 4, __uint_as_float(v[k + 1]));
+            st_cluster_f32(at, v[k]);
+            st_cluster_f32(at + kPartPitch * 4, v[k + 1]);
             at += 2 * kPartPitch * 4;
             if ((i += 2) == slice && ++q < g.ks) {
                 i = 0;
@@ -1057,13 +1106,20 @@ cudaError_t lora_tc_shrink(const adaln_rows &src, const void *W, const LoraCall 
     g.ks = KB <= 12 ? 1 : KB <= 24 ? 2 : KB <= 48 ? 4 : 8;
     const int stage = kRowTile + g.Rp * kBlk * 2, part = g.Rp * kPartPitch * 4;
     g.stages = stages_for(stage, part, 2);
-    g.tmem_cols = tmem_columns(g.Rp);
     CUtensorMap map_x, map_w;
     if (!make_map_3d(&map_x, src.data, C, c.S, c.B, src.token, src.batch, kM) ||
         !make_map_3d(&map_w, W, C, c.R, c.NA, C, (int64_t)c.R * C, g.Rp))
         return cudaErrorInvalidValue;
     const size_t smem = (size_t)g.stages * stage + part + kBarBytes + 1024;
-    cudaError_t err = ensure_smem_attr((const void *)lora_shrink_tc_kernel, smem, dev);
+    // one CTA an SM (above rank 64: 200 KB and more, beside which no other kernel with
+    // tensor memory fits), or two
+    const int cols = ctas_of(smem) == 1 ? 512 : 256;
+    const int most = (KB + g.ks - 1) / g.ks, chains = (most + kChain - 1) / kChain;  // of a range
+    const bool in_passes = chains * g.Rp > cols;
+    g.accs = in_passes ? cols / g.Rp : chains;
+    g.tmem_cols = tmem_columns(g.accs * g.Rp);
+    auto kern = in_passes ? lora_shrink_tc_kernel<true> : lora_shrink_tc_kernel<false>;
+    cudaError_t err = ensure_smem_attr((const void *)kern, smem, dev);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)g.ks, (unsigned)((c.S + kM - 1) / kM), (unsigned)c.B);
@@ -1081,7 +1137,7 @@ cudaError_t lora_tc_shrink(const adaln_rows &src, const void *W, const LoraCall 
     attr[2].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 3;
-    return cudaLaunchKernelEx(&cfg, lora_shrink_tc_kernel, map_x, map_w, g);
+    return cudaLaunchKernelEx(&cfg, kern, map_x, map_w, g);
 }
 
 cudaError_t lora_tc_expand(const void *h, const void *W, const LoraCall &c, int C, cudaStream_t stream,
