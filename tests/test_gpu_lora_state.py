@@ -67,3 +67,81 @@ def test_long_rows(K, R, sign):
     for got in states(t, x, A, scale):
         off = (got.double() - want).abs() / bound
         assert (off <= 1).all(), off.max()
+
+
+def whole_numbers(B, S, R, C, gen):
+    """src [B,S,C] and W [2,R,C] in bf16 whose products src W^T are whole numbers of 24 bits,
+    with a different number for most rows and ranks: 2^16 of 8 bits, 2^8 of two times 4, and
+    two times 4.  No sum of the terms needs more than 24 bits."""
+    def draw(lo, hi, *shape):
+        return torch.randint(lo, hi + 1, shape, generator=gen)
+
+    at = torch.randperm(C, generator=gen)[:3]
+    src, W = torch.zeros(B, S, C), torch.zeros(2, R, C)
+    src[..., at[0]] = 1
+    src[..., at[1:]] = draw(1, 15, B, S, 2).float()
+    W[..., at[0]] = draw(128, 255, 2, R).float() * 2 ** 16
+    W[..., at[1]] = draw(1, 15, 2, R).float() * 2 ** 8
+    W[..., at[2]] = draw(1, 15, 2, R).float()
+    return src.bfloat16().cuda(), W.bfloat16().cuda()
+
+
+@pytest.mark.parametrize("S,lens", [(150, None), (600, None), (700, [700, 513, 64])])
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 48, 56, 64, 72, 80, 88, 104, 120, 128])
+def test_every_part_of_a_state(R, S, lens):
+    """The gradients take h and e whole: with whole numbers of 24 bits, of which two bf16
+    parts hold 16 or 17, they are exact, in pieces and by owners."""
+    t = torch.bfloat16
+    B, C = 3, 72
+    gen = torch.Generator().manual_seed(R + S)
+    src, W = whole_numbers(B, S, R, C, gen)
+    ids = torch.tensor([1, 0, 1], dtype=torch.int32, device="cuda")
+    n = torch.tensor(lens or [S] * B)
+    N = (B * S + 7) // 8 * 8
+    one = torch.eye(B * S, N).view(B, S, N)  # row s of sample i: 1 or -2 in channel i S + s
+    one[1] *= -2
+    one = one.to(t).cuda()
+    other = torch.zeros((2, R, N), dtype=t, device="cuda")
+    scale = torch.tensor([1.0, 0.25], device="cuda")
+    kw = dict(lens=None if lens is None else n.int().cuda())
+    # what the sums are: one term each
+    s, w = src.cpu().double(), W.cpu().double()
+    want = torch.zeros(2, R, N, dtype=torch.float64)
+    for i, a in enumerate(ids.tolist()):
+        h = scale.cpu().double()[a] * (s[i] @ w[a].T)
+        hi = h.float().bfloat16().double()
+        mid = (h - hi).float().bfloat16().double()
+        assert ((hi + mid) != h).float().mean() > 0.3  # two parts are not enough
+        h[n[i]:] = 0
+        want[a][:, i * S:(i + 1) * S] = h.T * (-2 if i == 1 else 1)
+    _, state = b.adaln_lora_fwd(src, W, other, scale, ids, **kw)
+    dU = b.adaln_lora_bwd(one, src, state, W, other, scale, ids, **kw)[2]
+    assert torch.equal(dU.cpu().double(), want)
+    _, state = b.adaln_lora_fwd(one, other, W, scale, ids, **kw)
+    dA = b.adaln_lora_bwd(src, one, state, other, W, scale, ids, **kw)[1]
+    assert torch.equal(dA.cpu().double(), want)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=NAME.get)
+@pytest.mark.parametrize("S", [1, 2, 3, 9])
+@pytest.mark.parametrize("K,R", [(8, 8), (264, 16), (3080, 32), (9216, 8), (65536, 24)])
+def test_few_tokens(t, S, K, R):
+    """On the CUDA cores each of 128 threads sums its 16-byte vectors, even and odd
+    channels apart, by fused multiply-adds; then the halves, 32 lanes, 4 warps and the
+    scale: that many roundings of at most U."""
+    gen = torch.Generator("cuda").manual_seed(K + R + S)
+    for sign in (False, True):
+        x = torch.randn((1, S, K), generator=gen, device="cuda")
+        A = torch.randn((1, R, K), generator=gen, device="cuda") / K ** 0.5
+        if sign:
+            x, A = x.abs(), A.abs()
+        x, A = x.to(t), A.to(t)
+        scale = torch.tensor([0.7], device="cuda")
+        w = scale.double()
+        want = w * (x[0].double() @ A[0].double().T)
+        size = w * (x[0].double().abs() @ A[0].double().abs().T)
+        E = 16 // x.element_size()
+        steps = -(-K // (128 * E)) * E // 2 + 1 + 5 + 3 + 1
+        for got in states(t, x, A, scale):
+            off = (got.double() - want).abs() / (steps * 1.001 * U * size)
+            assert (off <= 1).all(), off.max()
