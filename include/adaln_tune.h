@@ -158,9 +158,9 @@ size_t adaln_lora_state_bytes(int B, int S, int R);
  * to a sum of up to 768 channels is cut off instead of rounded (8e-7 of h, rms, of random
  * signs; these sums are added with rounding), the product with U takes h to 16
  * significant bits (2^-17 relative), and an |h| above bf16's largest finite number,
- * 3.39e38, counts as infinite.  A row's result does not depend on the other samples;
- * its order depends on K, R and S only.  What an infinity or a NaN enters is infinite
- * or NaN, and nothing else changes.
+ * 3.39e38, counts as infinite (a small one is held to 2^-134).  A row's result does
+ * not depend on the other samples; its order depends on K, R and S only.  What an
+ * infinity or a NaN enters is infinite or NaN, and nothing else changes.
  *
  * Sizes: K, N multiples of 8 in [8, 65536]; R a multiple of 8 in [8, 128] (fill
  * up smaller adapters with zeros); 0 <= NA <= 65535; B, S as in adaln.h; B * S *
@@ -206,9 +206,11 @@ size_t adaln_f32_lora_bwd_workspace_bytes(int B, int S, int K, int N, int R);
  * dA and dU sum a sample's rows in an order fixed by S, R and the type, in pieces of
  * consecutive rows that each start from +0, and add the pieces, ascending, sample
  * by sample, onto the accumulator (accumulate ? its value : +0): bitwise
- * independent of how samples are split into accumulating calls.  With accumulate
- * only the adapters that occur are read and written; without it all are, with
- * zeros where an adapter does not occur.  Overlaps as adaln_lora_fwd.
+ * independent of how samples are split into accumulating calls.  On the tensor cores
+ * a piece has up to 512 rows, what is added to its sum is cut off instead of rounded,
+ * and h and e are what adaln_lora_fwd describes.  With accumulate only the adapters
+ * that occur are read and written; without it all are, with zeros where an adapter
+ * does not occur.  Overlaps as adaln_lora_fwd.
  * B * S == 0: the accumulators get their starting value.
  */
 adaln_status adaln_lora_bwd(const adaln_rows *d_out, const adaln_rows *x, const void *state, const adaln_bf16 *A,

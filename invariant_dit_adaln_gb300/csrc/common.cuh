@@ -81,9 +81,10 @@ __device__ __forceinline__ float2 f2sub(float2 a, float2 b) { return __ffma2_rn(
 // Every operation names its rounding (.rn).  The caution above holds here as well: a
 // px_mul whose only use is a px_add or px_sub is merged into it, one rounding less
 // (seen in every bit of the fp32 norm's results while they were written so).
-// px_mul_rounded is for a product that must be rounded before it is added.  On this GPU a packed instruction occupies the FMA pipe for
-// two cycles (it does two lanes of work), so packing halves the issue slots of
-// fp32 arithmetic without changing its pipe time.
+// px_mul_rounded is for a product that must be rounded before it is added.  On this
+// GPU a packed instruction occupies the FMA pipe for two cycles (it does two lanes of
+// work), so packing halves the issue slots of fp32 arithmetic without changing its
+// pipe time.
 // --------------------------------------------------------------------------
 typedef unsigned long long px2;
 

@@ -292,7 +292,7 @@ f32_out_bwd_tile_kernel(const float *__restrict__ dy, const float *__restrict__ 
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     xh[j][c] = px_mul(px_sub(xp[j][c], mu2), rs2);
-                    const px2 p = px_mul(gp[j][c], xh[j][c]);  // of several uses: not merged
+                    const px2 p = px_mul(gp[j][c], xh[j][c]);  // several uses: not merged into an add
                     px_twosum(ss[j][c], ks[j][c], p);
                     px_twosum(sh[j][c], kh[j][c], gp[j][c]);
                     a1 = px_fma(gp[j][c], onep[j][c], a1);
@@ -439,7 +439,8 @@ f32_out_bwd_ckpt8_kernel(const float *__restrict__ dy, const unsigned char *__re
                         load(i0 + r, j, xp, gp);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const px2 p = px_mul(gp[c], px_mul(px_sub(xp[c], mu2), rs2));  // of several uses: not merged
+                            // several uses: not merged into an add
+                            const px2 p = px_mul(gp[c], px_mul(px_sub(xp[c], mu2), rs2));
                             px_twosum(ss[j][c], ks[j][c], p);
                             px_twosum(sh[j][c], kh[j][c], gp[c]);
                             a1 = px_fma(gp[c], onep[j][c], a1);

@@ -8,7 +8,8 @@
 // to 64 bytes of a row at a time.  (With mma.sync, rows in registers: 37 instead of
 // 31.5 us for 4222 rows of 9216 channels at rank 32, bound by issue.)
 //
-// h and e are held as three bf16 parts, whose sum is the fp32 number itself.  The
+// h and e are held as three bf16 parts, whose sum is the fp32 number itself (below 2^-109
+// it is within 2^-134, half of bf16's smallest number).  The
 // gradients, which are fp32, take all three (two would leave 2.5e-6 of error, more
 // than all the sums); out and dx are rounded to bf16 once more and take two (2^-17).
 #include <algorithm>
@@ -768,9 +769,10 @@ lora_expand_tc_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_co
 // Schedules and order as on the CUDA cores: OWNER, every piece of an adapter in
 // order by one CTA, with two accumulators (where they fit), so that one piece's
 // leave while the next one's MMAs run, and the total in shared memory; otherwise as
-// many CTAs as the device holds take every gridDim.x-th piece of every tile.  (8192 rows of
-// 3072 and 3072 channels at rank 16: 30 us with a CTA a piece or two, a quarter of it the
-// last CTAs, 24.7 so, 4.1 TB/s.)  At rank 128 the state is three quarters of what a tile
+// many CTAs as the device holds take every gridDim.x-th piece of every tile.  (A call for
+// dA and dU alone on 4096 of 8192 rows of 3072 and 3072 channels at rank 16: 30 us with a
+// CTA a piece or two, a quarter of it the last CTAs, 24.7 so; this kernel by itself reads
+// 3.1 TB/s there.)  At rank 128 the state is three quarters of what a tile
 // reads, from L2: 18 us for 3700 rows of 2048 and 2560 channels, 150 MB into shared memory.
 // (Two tiles a CTA beside one state, 90 MB, two stages: 7 us more; 4 less only from 8192
 // rows of 3072 channels on.)
@@ -1166,7 +1168,9 @@ cudaError_t lora_tc_expand(const void *h, const void *W, const LoraCall &c, int 
     const int state = 4 * c.R * 128, stage = kExTile + g.copies * c.R * 128 + (g.keep ? 0 : state);
     const int beside = (g.keep ? state : 0) + kBarBytes + 1024;
     // 2 or 4 stages, whichever gives an SM more of them in all: 8 up to rank 16, 6 up
-    // to 48, 4 beyond
+    // to 32, 4 beyond, but 2 at ranks 56 and 120, whose adapter rows are there twice
+    // (4608 rows of 3072 and 3072 channels, forward: rank 48 28.9 us, 56 34.9, 64 30.1,
+    // 112 34.2, 120 40.9, 128 36.0)
     int per_sm = 0;
     for (int n = 2; n <= kExStages; n += 2) {
         const int ctas = std::min(kExCtas, 228 * 1024 / (n * stage + beside + 1024));
