@@ -645,6 +645,8 @@ struct TokenRows {
         }
         r = adaln_rows{x.data_ptr(), x.stride(0), x.stride(1)};
     }
+    // a tensor allocated here: what its size makes impossible the C ABI refuses by that size
+    explicit TokenRows(Tensor t) : x(std::move(t)), r{x.data_ptr(), x.stride(0), x.stride(1)} {}
     bool usable(bool positive) const {
         if (x.numel() == 0) return true;
         const int64_t step = 16 / x.element_size();
@@ -699,7 +701,7 @@ PyObject *lora_fwd(PyObject *const *a) {
     TokenRows y, out;
     if (given(a[6])) y = token_rows(a[6], "y", z.dev, z.t, {z.b, z.s, z.n}, a[6] != a[8], false);
     out = given(a[8]) ? token_rows(a[8], "out", z.dev, z.t, {z.b, z.s, z.n}, false, true)
-                      : TokenRows(z.fresh({z.b, z.s, z.n}), "out", false, true);
+                      : TokenRows(z.fresh({z.b, z.s, z.n}));
     const size_t need = lib.lora_state_bytes(z.B, z.S, z.R);
     Tensor state;
     if (given(a[9])) {
@@ -738,7 +740,7 @@ PyObject *lora_bwd(PyObject *const *a) {
     if (given(a[10]))
         dx = token_rows(a[10], "dx", z.dev, z.t, {z.b, z.s, z.k}, false, true);
     else if (want_x)
-        dx = TokenRows(z.fresh({z.b, z.s, z.k}), "dx", false, true);
+        dx = TokenRows(z.fresh({z.b, z.s, z.k}));
     // given accumulators are filled; want_w allocates the missing ones
     Tensor dA, dU;
     if (want_w && accumulate && (!given(a[11]) || !given(a[12])))
