@@ -1113,8 +1113,8 @@ cudaError_t lora_tc_shrink(const adaln_rows &src, const void *W, const LoraCall 
         !make_map_3d(&map_w, W, C, c.R, c.NA, C, (int64_t)c.R * C, g.Rp))
         return cudaErrorInvalidValue;
     const size_t smem = (size_t)g.stages * stage + part + kBarBytes + 1024;
-    // one CTA an SM (above rank 64: 200 KB and more, beside which no other kernel with
-    // tensor memory fits), or two
+    // one CTA an SM (above rank 64: 195 KB and more, beside which no other kernel with
+    // tensor memory fits), or two (no more: 92 KB and more each)
     const int cols = ctas_of(smem) == 1 ? 512 : 256;
     const int most = (KB + g.ks - 1) / g.ks, chains = (most + kChain - 1) / kChain;  // of a range
     const bool in_passes = chains * g.Rp > cols;
