@@ -98,3 +98,28 @@ def test_graphs_side_by_side(t):
         torch.cuda.synchronize()
         for g, buf, want, s, _ in made:
             assert all(same(p, q) for p, q in zip(buf, want))
+
+
+def test_long_rows_beside_others():
+    """Clusters that hold 64, 256 and 512 columns of tensor memory and the conditioning's
+    projection, on streams of their own."""
+    t = torch.bfloat16
+    cases = [inputs(t, 2, 300, *size, 2, seed=i) for i, size in enumerate(((65536, 264, 16), (20000, 136, 128),
+                                                                          (9216, 3080, 32)))]
+    want = [run(t, c) for c in cases]
+    gen = torch.Generator("cuda").manual_seed(1)
+    temb, W, bias = (torch.randn(s, generator=gen, device="cuda").to(t) for s in ((130, 1024), (2048, 1024), (2048,)))
+    emb = b.adaln_proj_fwd(temb, W, bias)[0]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got, embs = [[], [], []], []
+    for _ in range(10):
+        for i, c in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(t, c))
+        with torch.cuda.stream(streams[3]):
+            embs += [b.adaln_proj_fwd(temb, W, bias)[0] for _ in range(4)]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(same(p, q) for r in g for p, q in zip(r, w))
+    assert all(same(e, emb) for e in embs)
